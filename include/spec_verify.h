@@ -38,7 +38,8 @@
 extern "C" {
 #endif
 
-typedef enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1 } spec_dtype_t;
+/* E4M3: entries of a key-value cache only (spec_decode.h); logits are F32 or BF16 */
+typedef enum { SPEC_DTYPE_F32 = 0, SPEC_DTYPE_BF16 = 1, SPEC_DTYPE_E4M3 = 2 } spec_dtype_t;
 
 typedef enum {
   SPEC_OK = 0,

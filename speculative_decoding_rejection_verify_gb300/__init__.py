@@ -14,6 +14,9 @@ The C ABI is declared in ``include/spec_verify.h``; the names here mirror it:
   ``(tokens, num_accepted, chain, flags)``: several draft chains per request through
   ``spec_verify_multi``;
 * ``workspace_bytes(B, K, V, dtype, top_k)``;
+* ``kv_append``, ``paged_attention``, ``kv_keep``, ``process_logits``: the operators of a decode step around
+  the verify step (``decode.py``, ``include/spec_decode.h``, ``csrc/spec_kv.cu``, ``csrc/spec_attention.cu``,
+  ``csrc/spec_logits.cu``);
 * ``Controller(...)``: the host-side draft-length controller of ``include/spec_control.h``
   (2kiu.com/news/5895634 §4.4 and §7), fed with each batch's ``num_accepted``.
 
@@ -159,6 +162,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
             L = ctypes.POINTER(ctypes.c_int64)
             lib.spec_ctrl_totals.argtypes = [P, L, L, L]
             lib.spec_ctrl_totals.restype = None
+            decode.declare(lib)
             _lib = lib
     return _lib
 
@@ -493,3 +497,8 @@ def _host_i32(a) -> np.ndarray:
     if hasattr(a, "detach"):  # a torch tensor
         a = a.detach().cpu().numpy()
     return np.asarray(a, dtype=np.int32)
+
+
+from . import decode  # noqa: E402  (its functions use what is defined above)
+from .decode import (DECODE_EXPORTS, DTYPE_E4M3, FLAG_BAD_POSITION, FLAG_BAD_SLOT, kv_append, kv_keep,  # noqa: E402,F401
+                     paged_attention, process_logits)
