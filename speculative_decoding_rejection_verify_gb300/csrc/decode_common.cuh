@@ -75,7 +75,7 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
 // ------------------------------------------------------------------------------------------------
 inline bool heads_ok(const spec_heads_t* h) {
   return h && h->data && ((uintptr_t)h->data & 15u) == 0 && h->row_stride % 8 == 0 && h->token_stride % 8 == 0 &&
-         h->head_stride % 8 == 0;
+         h->head_stride % 8 == 0 && h->row_stride >= 0 && h->token_stride >= 0 && h->head_stride >= 0;
 }
 inline Heads heads_of(const spec_heads_t* h) {
   if (!h) return Heads{nullptr, 0, 0, 0};
@@ -84,13 +84,13 @@ inline Heads heads_of(const spec_heads_t* h) {
 
 inline spec_status_t check_cache(const spec_kv_cache_t* c, bool scales) {
   if (!c) return SPEC_ERR_INVALID_ARG;
-  if (c->layers < 1 || c->num_pages < 0 || c->heads < 1 || c->page_size < 1) return SPEC_ERR_INVALID_ARG;
+  if (c->layers < 1 || c->num_pages < 1 || c->heads < 1 || c->page_size < 1) return SPEC_ERR_INVALID_ARG;
   if (c->dtype != SPEC_DTYPE_BF16 && c->dtype != SPEC_DTYPE_E4M3) return SPEC_ERR_UNSUPPORTED;
   if (c->head_dim != 64 && c->head_dim != 128) return SPEC_ERR_UNSUPPORTED;
   if (c->page_size < 8 || c->page_size > SPEC_MAX_PAGE || (c->page_size & (c->page_size - 1)))
     return SPEC_ERR_UNSUPPORTED;
   if (c->heads > 65535) return SPEC_ERR_UNSUPPORTED;
-  if (c->num_pages > 0 && (!c->k || !c->v)) return SPEC_ERR_INVALID_ARG;
+  if (!c->k || !c->v) return SPEC_ERR_INVALID_ARG;
   const int vec = c->dtype == SPEC_DTYPE_BF16 ? 8 : 16;
   if (((uintptr_t)c->k & 15u) || ((uintptr_t)c->v & 15u) || c->layer_stride % vec || c->page_stride % vec ||
       c->slot_stride % vec || c->head_stride % vec)

@@ -1,88 +1,1033 @@
 // spec_attention.cu — spec_paged_attention: the new tokens of a step attend over the paged cache.
+//
+// A request's new tokens and the q heads of a group share every key and value they read: their
+// R = group * tokens rows are one small matrix against a long cache, so the work is a stream over the
+// cache with 2 R flops per byte (bf16), memory bound up to R ~ 280 on this part.  Per kv head:
+//
+//   S^T = K Q^T   [128 slots x R]    tcgen05.mma, K from a TMA-fed ring, the accumulator in TMEM
+//   P^T = exp2(c S^T - m)            one thread per slot, R columns in registers; fp32
+//   O^T += V^T P^T [head_dim x R]    tcgen05.mma, V and P^T read with their slots as the reduction
+//
+// Slots lie on the 128 rows of the matrix unit and query rows on its free N side, so few rows cost little
+// and nothing is padded to 128 query rows.  The maximum m of a row is taken over a tile only when
+// some score passes the one in use by 2^8 (a vote per tile; the first tile always): rescaling is
+// exact whatever m is, and this keeps the cross-thread reductions out of the stream.
+//
+// The tiles of all requests and heads form one line, cut into equal parts over the SMs (no part of the
+// plan needs the host to know a length).  An item (request, kv head, row group) that a cut splits
+// leaves its parts' (m, l, O) in the workspace, and a second kernel joins them.
+
+#include <cuda.h>
+
+#include <atomic>
 
 #include "decode_common.cuh"
 
 namespace sv {
 
-constexpr int kRowWarps = 4;
+constexpr int kTileSlots = 128;       // slots per tile = rows of the matrix unit
+constexpr int kMaxParts = 160;        // CTAs of the stream at most (one per SM), for the workspace's size
+constexpr int kMaxRows = 128;         // query rows of one item
+constexpr float kRescale = 8.0f;      // rescale when a score passes the maximum in use by 2^8
+constexpr int kSoftmaxWarps = 8;      // two warpgroups, each with every other chunk of columns
+constexpr int kConvertWarps = 4;      // E4M3 caches: E4M3 -> fp16
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
-  Heads q, out;
-  Cache cache;
+  CUtensorMap q_map, k_map, v_map;
+  Heads out;
+  Cache cache;                 // for the rare reads of single entries, and the scales
   Batch batch;
   const int64_t* mask;
-  int q_heads, group;
-  float scale;
+  int heads, group;
+  int tokens, row_groups;      // tokens per row group
+  int rows;                    // group * tokens
+  float scale_log2;            // scale * log2(e)
+  float* part;                 // [CTA][2][rows][D] unnormalised O
+  float2* part_ml;             // [CTA][2][rows] (m in log2 units, l)
+  int4* cut;                   // [CTA] (b, head * row_groups + row group, item's last tile + 1, total) of an
+                               //       item that begins in this CTA and ends in a later one; b = -1: none
 };
 
-// One block per query row; each warp takes every kRowWarps-th slot with its own running maximum, and the
-// warps' parts are joined at the end.
-template <int D, bool F8>
-__global__ void __launch_bounds__(kRowWarps * 32) attn_row_kernel(const __grid_constant__ AttnParams P) {
-  constexpr int E = D / 32;  // elements per lane
-  __shared__ float part[kRowWarps][D + 2];
-  const int h = blockIdx.x, t = blockIdx.y, b = blockIdx.z;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tb = batch_tokens(P.batch, b), ctx = batch_context(P.batch, b);
-  char* out = P.out.data + b * P.out.row + t * P.out.token + h * P.out.head;
-  float m = -INFINITY, l = 0.0f, o[E] = {};
-  if (t < tb) {
-    const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(P.q.data + b * P.q.row + t * P.q.token + h * P.q.head);
-    float x[E];
+// ------------------------------------------------------------------------------------------------
+// PTX
+// ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 10000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// Waits for the phase with a limit; a wait that runs out marks the block dead, which ends every other
+// wait in it soon after.  Nothing here waits on another block.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+  if (mbar_try(bar, parity)) return true;
+  for (int i = 0; i < (1 << 18); ++i) {
+    if (mbar_try(bar, parity)) return true;
+    if ((i & 255) == 0 && *dead) return false;
+  }
+  *dead = 1;
+  return false;
+}
+// the same for a whole warp that goes on together
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* dead) {
+  return __all_sync(~0u, mbar_wait(bar, parity, dead));
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// A load from TMEM and the wait for it, in one statement: nothing can use the registers in between.
+template <int N>
+__device__ __forceinline__ void tm_load(uint32_t addr, float (&x)[N]);
+template <>
+__device__ __forceinline__ void tm_load<8>(uint32_t addr, float (&x)[8]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr)
+               : "memory");
+}
+template <>
+__device__ __forceinline__ void tm_load<16>(uint32_t addr, float (&x)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tm_store(uint32_t addr, const float (&x)[N]);
+template <>
+__device__ __forceinline__ void tm_store<8>(uint32_t addr, const float (&x)[8]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+template <>
+__device__ __forceinline__ void tm_store<16>(uint32_t addr, const float (&x)[16]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 128 threads of one warpgroup
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Shared-memory matrix descriptors: 128-byte swizzle, strides in bytes.  Along a swizzled row of 128 bytes
+// lies the reduction (Q and K) or the free dimension (V^T and P^T, "transposed" in the instruction).
+__device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
+         1ull << 46 | 2ull << 61;
+}
+
+// ------------------------------------------------------------------------------------------------
+// the line of tiles
+// ------------------------------------------------------------------------------------------------
+struct Segment {
+  int b, head, row_group, index;  // index = head * row_groups + row group
+  int tile0, tile1, tiles;        // this part of the item's tiles
+  int ctx, tokens, end;           // context, valid new tokens, end of the slots
+};
+
+// Slots of a request that anything reads, and its tiles (one at least: its rows are written there).
+__device__ __forceinline__ int request_end(int ctx, int tokens, int slots) { return tokens > 0 ? min(ctx + tokens, slots) : 0; }
+__device__ __forceinline__ int request_tiles(int end) { return max(1, (end + kTileSlots - 1) / kTileSlots); }
+
+// Where CTA c's part of the line begins.
+__device__ __forceinline__ int line_cut(int total, int c, int ctas) { return (int)((int64_t)total * c / ctas); }
+
+// Every role of a CTA walks the same part of the line by itself.
+struct Walk {
+  const AttnParams& P;
+  int b, index, tile, left;
+  int ctx, tokens, next_ctx, next_tokens;
+
+  __device__ Walk(const AttnParams& p, int b0, int offset, int count) : P(p), b(b0), left(count) {
+    index = tile = ctx = tokens = next_ctx = next_tokens = 0;
+    if (left <= 0) return;
+    ctx = batch_context(P.batch, b);
+    tokens = batch_tokens(P.batch, b);
+    const int n = request_tiles(request_end(ctx, tokens, P.batch.slots));
+    index = offset / n;
+    tile = offset % n;
+    prefetch();
+  }
+  __device__ void prefetch() {
+    if (b + 1 < P.batch.B) {
+      next_ctx = batch_context(P.batch, b + 1);
+      next_tokens = batch_tokens(P.batch, b + 1);
+    }
+  }
+  __device__ bool next(Segment& s) {
+    if (left <= 0) return false;
+    s.b = b, s.index = index;
+    s.head = index / P.row_groups, s.row_group = index % P.row_groups;
+    s.ctx = ctx, s.tokens = tokens, s.end = request_end(ctx, tokens, P.batch.slots);
+    s.tiles = request_tiles(s.end);
+    const int n = min(s.tiles - tile, left);
+    s.tile0 = tile, s.tile1 = tile + n;
+    left -= n;
+    tile += n;
+    if (tile == s.tiles) {
+      tile = 0;
+      if (++index == P.heads * P.row_groups) {
+        index = 0;
+        ++b;
+        ctx = next_ctx, tokens = next_tokens;
+        prefetch();
+      }
+    }
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------------------------------------
+// shared memory
+// ------------------------------------------------------------------------------------------------
+template <int D, bool F8, int NT>
+struct Shape {
+  static constexpr int kHalves = D / 64;                          // 128-byte columns of a 16-bit row
+  static constexpr int kTile16 = kTileSlots * D * 2;              // a K or V tile in 16 bits
+  static constexpr int kRing = kTileSlots * D * (F8 ? 1 : 2);     // a ring slot: a tile as the cache holds it
+  static constexpr int kQ = NT * D * 2;                           // a Q buffer
+  static constexpr int kQBufs = NT > 64 ? 1 : 2;                  // two, where the ring stays deep enough
+  static constexpr int kP = kTileSlots * 128 * (NT > 64 ? 2 : 1); // P^T, 128 bytes a slot and 64 rows
+  static constexpr int kFixed = kQBufs * kQ + kP + (F8 ? 2 * kTile16 : 0);
+  static constexpr int kBudget = 232448 - 1024 - 6144;            // 227 KB, alignment, barriers and row states
+  static constexpr int kFit = (kBudget - kFixed) / kRing;
+  static constexpr int kSlots = kFit > 8 ? 8 : kFit;              // K and V tiles in flight
+  static_assert(kSlots >= 4, "the ring holds two tiles of K and V at least");
+  static constexpr int kThreads = (kSoftmaxWarps + 2 + (F8 ? kConvertWarps : 0)) * 32;
+  static constexpr int kColumns = 3 * NT <= 64 ? 64 : 3 * NT <= 128 ? 128 : 3 * NT <= 256 ? 256 : 512;
+  static constexpr int kChunk = NT >= 32 ? 16 : 8;                // columns a warpgroup takes at a time
+  static constexpr int kChunks = NT / (2 * kChunk);               // chunks of one warpgroup
+
+  struct State {
+    uint64_t ring_full[8], ring_empty[8];
+    uint64_t q_loaded[2], q_full[2], q_empty[2];
+    uint64_t k16_full, k16_empty, v16_full, v16_empty;
+    uint64_t s_full[2], s_empty[2], p_full, o_full;
+    uint32_t tmem;
+    int dead;
+    int start_b, start_offset, total;
+    uint32_t bad_value[2];           // segment + 1 whose new tokens hold a value that is not finite
+    int warp_sum[16];
+    alignas(16) float base[NT];      // what is subtracted: the row's maximum in use, 0 for none
+    alignas(16) float limit[NT];     // rescale beyond
+    alignas(16) float top[NT];       // the maximum in use, -inf for none
+    alignas(16) float factor[NT];    // a rescale's factor; 1 / l at the end
+    float red[4][NT];
+    uint64_t rule[NT];               // new tokens that the row attends to
+  };
+  static constexpr int kState = kFixed + kSlots * kRing;
+  static constexpr int kBytes = kState + (int)sizeof(State) + 1024;
+  static_assert(kBytes <= 232448, "shared memory");
+};
+
+// Over the 32 lanes, `op` of every one of N values: lane l ends with that of value l % N.
+template <int N, typename Op>
+__device__ __forceinline__ float fold_lanes(float (&x)[N], int lane, Op op) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = __bfloat162float(q[lane + 32 * i]);
-    const int kvh = h / P.group;
-    const float ks = F8 && P.cache.k_scale ? P.cache.k_scale[kvh] : 1.0f;
-    const float vs = F8 && P.cache.v_scale ? P.cache.v_scale[kvh] : 1.0f;
-    const uint64_t rule = P.mask ? (uint64_t)P.mask[(int64_t)b * P.batch.T + t] : (t >= 63 ? ~0ull : (2ull << t) - 1);
-    const int end = min(ctx + tb, P.batch.slots);
-    for (int s = warp; s < end; s += kRowWarps) {
-      if (s >= ctx && !((rule >> (s - ctx)) & 1)) continue;
-      const int page = P.batch.pages[(int64_t)b * P.batch.max_pages + (s >> P.cache.page_shift)];
-      const bool in = page >= 0 && page < P.cache.num_pages;
-      const int64_t at = page * P.cache.page + (s & ((1 << P.cache.page_shift) - 1)) * P.cache.slot + kvh * P.cache.head;
-      float dot = 0.0f, v[E];
+  for (int w = N / 2; w > 0; w /= 2) {
+    const bool up = lane & w;
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        float k = 0.0f;
-        v[i] = 0.0f;
+    for (int k = 0; k < w; ++k) {
+      const float keep = up ? x[k + w] : x[k], send = up ? x[k] : x[k + w];
+      x[k] = op(keep, __shfl_xor_sync(~0u, send, w));
+    }
+  }
+  float r = x[0];
+#pragma unroll
+  for (int w = N; w < 32; w *= 2) r = op(r, __shfl_xor_sync(~0u, r, w));
+  return r;
+}
+
+// ------------------------------------------------------------------------------------------------
+// the stream over the cache
+// ------------------------------------------------------------------------------------------------
+template <int D, bool F8, int NT>
+__global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams P) {
+  using S = Shape<D, F8, NT>;
+  extern __shared__ char raw_smem[];
+  char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+  char* q_buf = smem;                                     // [kQBufs][halves][NT][128 B]
+  char* p_buf = q_buf + S::kQBufs * S::kQ;                     // [NT > 64 ? 2 : 1][128][128 B]
+  char* t16 = p_buf + S::kP;                              // E4M3: K, V in fp16, [halves][128][128 B] each
+  char* ring = t16 + (F8 ? 2 * S::kTile16 : 0);
+  auto* st = reinterpret_cast<typename S::State*>(smem + S::kState);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kProducer = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // this CTA's part of the line: a scan over the requests' tiles
+  const int per_request = P.heads * P.row_groups;
+  const int chunk = (P.batch.B + S::kThreads - 1) / S::kThreads;
+  const int b_first = min((int)threadIdx.x * chunk, P.batch.B), b_last = min(b_first + chunk, P.batch.B);
+  int mine = 0;
+  for (int b = b_first; b < b_last; ++b)
+    mine += request_tiles(request_end(batch_context(P.batch, b), batch_tokens(P.batch, b), P.batch.slots)) * per_request;
+  int before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int x = __shfl_up_sync(~0u, before, d);
+    if (lane >= d) before += x;
+  }
+  if (lane == 31) st->warp_sum[warp] = before;
+  before -= mine;
+  if (threadIdx.x == 0) {
+    st->dead = 0;
+    st->bad_value[0] = st->bad_value[1] = 0;
+    const uint32_t full_count = 1;
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(smem_addr(&st->ring_full[i]), full_count);
+      mbar_init(smem_addr(&st->ring_empty[i]), F8 ? kConvertWarps : 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&st->q_loaded[i]), 1);
+      mbar_init(smem_addr(&st->q_full[i]), kConvertWarps);
+      mbar_init(smem_addr(&st->q_empty[i]), 1);
+      mbar_init(smem_addr(&st->s_full[i]), 1);
+      mbar_init(smem_addr(&st->s_empty[i]), kSoftmaxWarps);
+    }
+    mbar_init(smem_addr(&st->k16_full), kConvertWarps);
+    mbar_init(smem_addr(&st->k16_empty), 1);
+    mbar_init(smem_addr(&st->v16_full), kConvertWarps);
+    mbar_init(smem_addr(&st->v16_empty), 1);
+    mbar_init(smem_addr(&st->p_full), kSoftmaxWarps);
+    mbar_init(smem_addr(&st->o_full), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&st->tmem)),
+                 "r"(S::kColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < S::kThreads / 32; ++w) {
+    if (w < warp) before += st->warp_sum[w];
+    total += st->warp_sum[w];
+  }
+  const int ctas = min((int)gridDim.x, total);  // the others have no part
+  const int first = line_cut(total, min((int)blockIdx.x, ctas), ctas);
+  const int count = line_cut(total, min((int)blockIdx.x + 1, ctas), ctas) - first;
+  if (count > 0 && first >= before && first < before + mine) {
+    int b = b_first, rest = first - before;
+    for (;; ++b) {
+      const int n = request_tiles(request_end(batch_context(P.batch, b), batch_tokens(P.batch, b), P.batch.slots)) * per_request;
+      if (rest < n) break;
+      rest -= n;
+    }
+    st->start_b = b, st->start_offset = rest;
+  }
+  __syncthreads();
+  const uint32_t tmem = st->tmem;
+  volatile int* dead = &st->dead;
+  Walk walk(P, count > 0 ? st->start_b : 0, count > 0 ? st->start_offset : 0, count);
+  Segment s;
+
+  if (warp == kProducer) {
+    // ---- TMA: Q of every segment, K and V of every tile, page by page ----
+    const int page = 1 << P.cache.page_shift;
+    const int box = min(page, kTileSlots);                // slots of one copy
+    const int copies = kTileSlots / box;                  // copies of a tile (and half)
+    constexpr int kParts = F8 ? 1 : S::kHalves;
+    const int part = lane % kParts, copy = lane / kParts;
+    int slot = 0;
+    uint32_t phase = 0;  // of the ring
+    bool ok = true;
+    int issued = 0;
+    for (int seg = 0; ok && walk.next(s); ++seg) {
+      const int qb = seg % S::kQBufs;
+      ok = mbar_wait_warp(smem_addr(&st->q_empty[qb]), ((seg / S::kQBufs) & 1) ^ 1, dead);
+      if (!ok) break;
+      if (lane == 0) {
+        const uint32_t bar = smem_addr(&st->q_loaded[qb]);
+        mbar_expect(bar, P.rows * D * 2);
+        for (int h = 0; h < S::kHalves; ++h)
+          tma_load(smem_addr(q_buf + qb * S::kQ + h * NT * 128), &P.q_map, h * 64, s.head * P.group, s.row_group * P.tokens,
+                   s.b, bar);
+      }
+      const int32_t* table = P.batch.pages + (int64_t)s.b * P.batch.max_pages;
+      const auto entry = [&](int tile) {  // this lane's page of a tile; one past the pool reads as zeros
+        const int at = tile * kTileSlots + copy * box;
+        if (copy >= copies || at >= s.end) return P.cache.num_pages;
+        const int p = __ldg(table + (at >> P.cache.page_shift));
+        return p < 0 || p > P.cache.num_pages ? P.cache.num_pages : p;
+      };
+      int mine_page = entry(s.tile0);
+      for (int tile = s.tile0; ok && tile < s.tile1; ++tile) {
+        const int p = mine_page;
+        if (tile + 1 < s.tile1) mine_page = entry(tile + 1);
+        const int row = (tile * kTileSlots + copy * box) & (page - 1);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = ok && mbar_wait_warp(smem_addr(&st->ring_empty[slot]), phase ^ 1, dead);
+          if (!ok) break;
+          const uint32_t bar = smem_addr(&st->ring_full[slot]);
+          if (lane == 0) mbar_expect(bar, S::kRing);
+          __syncwarp();
+          if (copy < copies) {
+            const uint32_t dst = smem_addr(ring) + slot * S::kRing + (F8 ? copy * box * D : part * (kTileSlots * 128) + copy * box * 128);
+            tma_load(dst, kv ? &P.v_map : &P.k_map, part * 64, row, s.head, p, bar);
+          }
+          ++issued;
+          if (++slot == S::kSlots) slot = 0, phase ^= 1;
+        }
+      }
+    }
+    if (!ok)  // a wait ran out: see the copies in flight land before the block ends
+      for (int i = 0; i < min(issued, S::kSlots); ++i) {
+        if (--slot < 0) slot = S::kSlots - 1, phase ^= 1;
+        for (int n = 0; n < (1 << 16) && !mbar_try(smem_addr(&st->ring_full[slot]), phase); ++n) {
+        }
+      }
+  } else if (warp == kIssuer) {
+    // ---- matrix products ----
+    if (lane == 0) {
+      const uint32_t n16 = (P.rows + 15) / 16 * 16;
+      const uint32_t fmt = F8 ? 0u : 1u;  // fp16 or bf16 operands, fp32 accumulators, M = 128
+      const uint32_t idesc = 1u << 4 | fmt << 7 | fmt << 10 | (n16 >> 3) << 17 | (128u >> 4) << 24;
+      const uint32_t idesc_t = idesc | 1u << 15 | 1u << 16;  // both operands with the reduction outside
+      const uint32_t o_col = tmem + 2 * NT;
+      uint32_t it = 0;       // tiles so far
+      int k_slot = 0, v_slot = 0;
+      uint32_t k_phase = 0, v_phase = 0;
+      bool ok = true, o_any = false;
+      const auto advance = [&](int& slot, uint32_t& phase, int by) {
+        slot += by;
+        if (slot >= S::kSlots) slot -= S::kSlots, phase ^= 1;
+      };
+      advance(v_slot, v_phase, 1);
+
+      const auto scores = [&](int qb, uint32_t q_phase, bool first, bool last) {
+        if (first) ok = ok && mbar_wait(smem_addr(F8 ? &st->q_full[qb] : &st->q_loaded[qb]), q_phase, dead);
+        const int sb = it & 1;
+        ok = ok && mbar_wait(smem_addr(&st->s_empty[sb]), ((it >> 1) & 1) ^ 1, dead);
+        ok = ok && (F8 ? mbar_wait(smem_addr(&st->k16_full), it & 1, dead)
+                       : mbar_wait(smem_addr(&st->ring_full[k_slot]), k_phase, dead));
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t a = smem_addr(F8 ? t16 : ring + k_slot * S::kRing), b = smem_addr(q_buf + qb * S::kQ);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const int half = k / 4, in = (k % 4) * 32;
+          tc_mma(tmem + sb * NT, matrix_desc(a + half * (kTileSlots * 128) + in, 16, 1024),
+                 matrix_desc(b + half * (NT * 128) + in, 16, 1024), idesc, k > 0);
+        }
+        tc_commit(smem_addr(F8 ? &st->k16_empty : &st->ring_empty[k_slot]));
+        tc_commit(smem_addr(&st->s_full[sb]));
+        if (last) tc_commit(smem_addr(&st->q_empty[qb]));
+        advance(k_slot, k_phase, 2);
+      };
+      const auto values = [&](uint32_t i, bool first) {  // tile i, one behind the scores
+        ok = ok && (F8 ? mbar_wait(smem_addr(&st->v16_full), i & 1, dead)
+                       : mbar_wait(smem_addr(&st->ring_full[v_slot]), v_phase, dead));
+        ok = ok && mbar_wait(smem_addr(&st->p_full), i & 1, dead);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t a = smem_addr(F8 ? t16 + S::kTile16 : ring + v_slot * S::kRing), b = smem_addr(p_buf);
+        // head_dim 64: the instruction's rows 64..127 repeat rows 0..63 and are not read
+        const uint32_t lead = D == 128 ? kTileSlots * 128 : 0;
+#pragma unroll
+        for (int k = 0; k < kTileSlots / 16; ++k)
+          tc_mma(o_col, matrix_desc(a + k * 2048, lead, 1024), matrix_desc(b + k * 2048, kTileSlots * 128, 1024), idesc_t,
+                 !first || k > 0);
+        tc_commit(smem_addr(F8 ? &st->v16_empty : &st->ring_empty[v_slot]));
+        tc_commit(smem_addr(&st->o_full));
+        advance(v_slot, v_phase, 2);
+        o_any = true;
+      };
+      bool first_behind = false;
+      for (int seg = 0; ok && walk.next(s); ++seg)
+        for (int tile = s.tile0; ok && tile < s.tile1; ++tile) {
+          scores(seg % S::kQBufs, (seg / S::kQBufs) & 1, tile == s.tile0, tile + 1 == s.tile1);
+          if (it > 0 && ok) values(it - 1, first_behind);
+          first_behind = tile == s.tile0;
+          ++it;
+        }
+      if (ok && it > 0) values(it - 1, first_behind);
+      if (!ok && o_any)  // a wait ran out: let the products in flight end before TMEM is freed
+        for (int n = 0; n < (1 << 16); ++n) __nanosleep(20);
+    }
+    __syncwarp();
+  } else if (F8 && warp > kIssuer) {
+    // ---- E4M3 -> fp16 (exact), K and V into the swizzled layout that the matrix unit reads ----
+    const int tid = threadIdx.x - (kIssuer + 1) * 32;  // 0..127
+    int slot = 0;
+    uint32_t phase = 0, it = 0;
+    bool ok = true;
+    for (int seg = 0; ok && walk.next(s); ++seg) {
+      const int qb = seg % S::kQBufs;
+      ok = mbar_wait_warp(smem_addr(&st->q_loaded[qb]), (seg / S::kQBufs) & 1, dead);
+      if (!ok) break;
+      for (int i = tid; i < S::kQ / 16; i += kConvertWarps * 32) {  // q: bf16 -> fp16, in place
+        uint4* p = reinterpret_cast<uint4*>(q_buf + qb * S::kQ) + i;
+        uint4 w = *p;
+        uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __half2 h = __floats2half2_rn(bf16_low(u[j]), bf16_high(u[j]));
+          u[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *p = w;
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&st->q_full[qb]));
+      for (int tile = s.tile0; ok && tile < s.tile1; ++tile, ++it) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = ok && mbar_wait_warp(smem_addr(&st->ring_full[slot]), phase, dead);
+          ok = ok && mbar_wait_warp(smem_addr(kv ? &st->v16_empty : &st->k16_empty), (it & 1) ^ 1, dead);
+          if (!ok) break;
+          const char* src = ring + slot * S::kRing;
+          char* dst = t16 + kv * S::kTile16;
+          // V's slots past the end are zeroed: their weights are 0, but 0 times what they hold may not be.
+          // New tokens' values that are not finite are taken out here and added at the end to the rows
+          // that attend to them.
+          const int end = kv ? s.end - tile * kTileSlots : kTileSlots;
+          const int fresh = kv ? s.ctx - tile * kTileSlots : kTileSlots;
+          constexpr int kUnits = D / 16;
+#pragma unroll
+          for (int i = 0; i < kTileSlots * kUnits / 128; ++i) {
+            const int u = i * 128 + tid, row = u / kUnits, c = u % kUnits;
+            uint4 w = *reinterpret_cast<const uint4*>(src + u * 16);
+            uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+            if (row >= fresh) {
+              if (row >= end) {
+                w = make_uint4(0, 0, 0, 0);
+              } else {
+                bool bad = false;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {  // the code 0x7F of either sign is NaN
+                  const uint32_t nan = __vcmpeq4(x[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                  bad |= nan != 0;
+                  x[j] &= ~nan;
+                }
+                if (bad) st->bad_value[seg & 1] = seg + 1;
+              }
+            }
+            uint32_t h[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                  "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+                  : "=r"(h[2 * j]), "=r"(h[2 * j + 1])
+                  : "r"(x[j]));
+            }
+            char* out = dst + (c / 4) * (kTileSlots * 128) + row * 128;
+            const int sw = (row & 7) * 16, j0 = (c % 4) * 32;
+            // the two halves of a row start at the same banks: one of them stores its second vector first
+            const bool turn = c >= 4;
+            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4*>(out + ((j0 + (turn ? 16 : 0)) ^ sw)) = turn ? hi : lo;
+            *reinterpret_cast<uint4*>(out + ((j0 + (turn ? 0 : 16)) ^ sw)) = turn ? lo : hi;
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_addr(kv ? &st->v16_full : &st->k16_full));
+            mbar_arrive(smem_addr(&st->ring_empty[slot]));
+          }
+          if (++slot == S::kSlots) slot = 0, phase ^= 1;
+        }
+      }
+    }
+  } else if (warp < kSoftmaxWarps) {
+    // ---- softmax and output; no branch around a group_sync depends on anything but the plan and votes ----
+    const int wg = warp >> 2, quad = warp & 3, bar = 1 + wg;
+    const int key = quad * 32 + lane, wtid = threadIdx.x & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const int my_row = ((wtid / S::kChunk) * 2 + wg) * S::kChunk + wtid % S::kChunk;  // wtid < NT / 2
+    float l[S::kChunks][S::kChunk];
+    uint32_t it = 0;
+    int v_slot = 1;
+    uint32_t v_phase = 0;
+    const auto col = [&](int j) { return (2 * j + wg) * S::kChunk; };
+
+    for (int seg = 0; walk.next(s); ++seg) {
+      const int t0 = s.row_group * P.tokens;
+      const int rows = min(max((s.tokens - t0) * P.group, 0), P.rows);  // valid ones come first
+      float c = P.scale_log2;
+      if (F8 && P.cache.k_scale) c *= __ldg(P.cache.k_scale + s.head);
+      group_sync(bar);  // the last segment's row states are read
+      if (wtid < NT / 2) {
+        const bool in = my_row < rows;
+        st->top[my_row] = -INFINITY;
+        st->base[my_row] = 0.0f;
+        st->limit[my_row] = in ? -INFINITY : INFINITY;
+        uint64_t rule = 0;
         if (in) {
-          if constexpr (F8) {
-            k = (float)reinterpret_cast<const __nv_fp8_e4m3*>(P.cache.k + at)[lane + 32 * i] * ks;
-            v[i] = (float)reinterpret_cast<const __nv_fp8_e4m3*>(P.cache.v + at)[lane + 32 * i] * vs;
-          } else {
-            k = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(P.cache.k + at)[lane + 32 * i]);
-            v[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(P.cache.v + at)[lane + 32 * i]);
+          const int t = t0 + my_row / P.group;
+          rule = P.mask ? (uint64_t)__ldg(P.mask + (int64_t)s.b * P.batch.T + t) : t >= 63 ? ~0ull : (2ull << t) - 1;
+        }
+        st->rule[my_row] = rule;
+      }
+      group_sync(bar);
+#pragma unroll
+      for (int j = 0; j < S::kChunks; ++j)
+#pragma unroll
+        for (int i = 0; i < S::kChunk; ++i) l[j][i] = 0.0f;
+
+      for (int tile = s.tile0; tile < s.tile1; ++tile, ++it) {
+        const int sb = it & 1;
+        const uint32_t s_col = lanes + sb * NT;
+        const int slot = tile * kTileSlots + key;
+        const bool masked = (tile + 1) * kTileSlots > s.ctx;  // the tile reaches past the context
+        const int fresh = slot - s.ctx;                       // which new token, negative in the context
+        mbar_wait(smem_addr(&st->s_full[sb]), (it >> 1) & 1, dead);
+        __syncwarp();
+        tc_fence_after();
+        const auto sees = [&](int n) { return slot < s.end && (fresh < 0 || ((st->rule[n] >> fresh) & 1)); };
+
+        bool o_done = it == 0;
+        bool raise = tile == s.tile0;
+        if (!raise) {
+          float over = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < S::kChunks; ++j)
+            if (col(j) < rows) {
+              float x[S::kChunk];
+              tm_load<S::kChunk>(s_col + col(j), x);
+#pragma unroll
+              for (int i = 0; i < S::kChunk; ++i) {
+                const float z = fmaf(x[i], c, -st->limit[col(j) + i]);
+                if (!masked || sees(col(j) + i)) over = fmaxf(over, z);
+              }
+            }
+          raise = group_any(bar, over > 0.0f);
+        }
+        if (raise) {
+#pragma unroll
+          for (int j = 0; j < S::kChunks; ++j)
+            if (col(j) < rows) {
+              float x[S::kChunk];
+              tm_load<S::kChunk>(s_col + col(j), x);
+#pragma unroll
+              for (int i = 0; i < S::kChunk; ++i) x[i] = !masked || sees(col(j) + i) ? x[i] * c : -INFINITY;
+              const float m = fold_lanes<S::kChunk>(x, lane, [](float a, float b) { return fmaxf(a, b); });
+              if (lane < S::kChunk) st->red[quad][col(j) + lane] = m;
+            }
+          group_sync(bar);
+          if (wtid < NT / 2 && my_row < rows) {
+            const float old = st->top[my_row];
+            float top = old;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) top = fmaxf(top, st->red[w][my_row]);
+            st->factor[my_row] = old == -INFINITY ? 0.0f : exp2_approx(old - top);
+            st->top[my_row] = top;
+            st->base[my_row] = top == -INFINITY ? 0.0f : top;
+            st->limit[my_row] = top + kRescale;
+          }
+          group_sync(bar);
+          if (tile > s.tile0) {
+            mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
+            __syncwarp();
+            tc_fence_after();
+            o_done = true;
+#pragma unroll
+            for (int j = 0; j < S::kChunks; ++j)
+              if (col(j) < rows) {
+                float x[S::kChunk];
+                tm_load<S::kChunk>(lanes + 2 * NT + col(j), x);
+#pragma unroll
+                for (int i = 0; i < S::kChunk; ++i) {
+                  const float f = st->factor[col(j) + i];
+                  x[i] *= f;
+                  l[j][i] *= f;
+                }
+                tm_store<S::kChunk>(lanes + 2 * NT + col(j), x);
+              }
+            tm_wait_store();
           }
         }
-        dot += x[i] * k;
+        // the last product must have read P before it is written again
+        if (!o_done) mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < S::kChunks; ++j)
+          if (col(j) < rows) {
+            float x[S::kChunk];
+            tm_load<S::kChunk>(s_col + col(j), x);
+            uint32_t w[S::kChunk / 2];
+#pragma unroll
+            for (int i = 0; i < S::kChunk; ++i) {
+              float p = exp2_approx(fmaf(x[i], c, -st->base[col(j) + i]));
+              if (masked && !sees(col(j) + i)) p = 0.0f;
+              x[i] = p;
+              l[j][i] += p;
+            }
+            // the weights' rounding: bf16 to go with a bf16 cache (2^-9 of each), fp16 with an E4M3 one
+#pragma unroll
+            for (int i = 0; i < S::kChunk / 2; ++i) {
+              if constexpr (F8) {
+                const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+              } else {
+                w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+              }
+            }
+            char* row = p_buf + (col(j) / 64) * (kTileSlots * 128) + key * 128;
+#pragma unroll
+            for (int i = 0; i < S::kChunk / 8; ++i)
+              *reinterpret_cast<uint4*>(row + ((((col(j) % 64) + i * 8) * 2) ^ ((key & 7) * 16))) =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        tc_fence_before();
+        if constexpr (!F8) {
+          if (masked) {
+            // V's slots past the end are zeroed: their weights are 0, but 0 times what they hold may not
+            // be.  New tokens' values that are not finite are taken out here and added at the end to the
+            // rows that attend to them.
+            mbar_wait(smem_addr(&st->ring_full[v_slot]), v_phase, dead);
+            char* v = ring + v_slot * S::kRing;
+            const int from = max(s.ctx - tile * kTileSlots, 0), end = s.end - tile * kTileSlots;
+            constexpr int kVecs = D / 8;
+            for (int u = from * kVecs + (int)threadIdx.x; u < kTileSlots * kVecs; u += kSoftmaxWarps * 32) {
+              const int row = u / kVecs, vec = u % kVecs;
+              uint4* p = reinterpret_cast<uint4*>(v + (vec / 8) * (kTileSlots * 128) + row * 128 + (((vec % 8) ^ (row & 7)) * 16));
+              if (row >= end) {
+                *p = make_uint4(0, 0, 0, 0);
+              } else {
+                uint4 w = *p;
+                uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t odd = __vcmpeq2(x[i] & 0x7F807F80u, 0x7F807F80u);
+                  bad |= odd != 0;
+                  x[i] &= ~odd;
+                }
+                if (bad) {
+                  *p = w;
+                  st->bad_value[seg & 1] = seg + 1;
+                }
+              }
+            }
+          }
+          v_slot += 2;
+          if (v_slot >= S::kSlots) v_slot -= S::kSlots, v_phase ^= 1;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&st->s_empty[sb]));
+          mbar_arrive(smem_addr(&st->p_full));
+        }
+      }
+
+      // ---- the segment's end ----
+#pragma unroll
+      for (int j = 0; j < S::kChunks; ++j)
+        if (col(j) < rows) {
+          const float sum = fold_lanes<S::kChunk>(l[j], lane, [](float a, float b) { return a + b; });
+          if (lane < S::kChunk) st->red[quad][col(j) + lane] = sum;
+        }
+      mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
+      __syncwarp();
+      tc_fence_after();
+      group_sync(bar);
+      const bool whole = s.tile0 == 0 && s.tile1 == s.tiles;
+      // parts: slot 0 for an item that an earlier CTA began, slot 1 for one that a later one ends
+      const int64_t part_row = ((int64_t)blockIdx.x * 2 + (s.tile0 == 0)) * P.rows;
+      if (wtid < NT / 2 && my_row < rows) {
+        const float sum = st->red[0][my_row] + st->red[1][my_row] + st->red[2][my_row] + st->red[3][my_row];
+        if (whole) {
+          const float v = F8 && P.cache.v_scale ? __ldg(P.cache.v_scale + s.head) : 1.0f;
+          st->factor[my_row] = sum == 0.0f ? 0.0f : v / sum;
+        } else {
+          P.part_ml[part_row + my_row] = make_float2(st->top[my_row], sum);
+        }
+      }
+      group_sync(bar);
+      const bool bad = st->bad_value[seg & 1] == (uint32_t)seg + 1;
+      const bool lost = *dead != 0;
+      char* out = P.out.data + s.b * P.out.row + (int64_t)t0 * P.out.token + (int64_t)s.head * P.group * P.out.head;
+      const int rows_all = min(P.rows, (P.batch.T - t0) * P.group);
+#pragma unroll 1
+      for (int j = 0; j < S::kChunks; ++j) {
+        const int n0 = col(j);
+        if (n0 >= rows_all) continue;
+        float x[S::kChunk];
+#pragma unroll
+        for (int i = 0; i < S::kChunk; ++i) x[i] = 0.0f;
+        if (n0 < rows) {
+          tm_load<S::kChunk>(lanes + 2 * NT + n0, x);
+        }
+        if (key >= D) continue;
+        if (bad) {  // values that are not finite: each row takes those of the tokens it attends to
+          for (int i = max(s.tile0 * kTileSlots - s.ctx, 0); s.ctx + i < min(s.tile1 * kTileSlots, s.end); ++i) {
+            const int at = s.ctx + i;
+            const int pg = __ldg(P.batch.pages + (int64_t)s.b * P.batch.max_pages + (at >> P.cache.page_shift));
+            if (pg < 0 || pg >= P.cache.num_pages) continue;
+            const char* p = P.cache.v + pg * P.cache.page + (at & ((1 << P.cache.page_shift) - 1)) * P.cache.slot +
+                            s.head * P.cache.head + key * (F8 ? 1 : 2);
+            const float v = F8 ? ((*reinterpret_cast<const uint8_t*>(p) & 0x7F) == 0x7F ? NAN : 0.0f)
+                               : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
+            if (isfinite(v)) continue;
+#pragma unroll
+            for (int n = 0; n < S::kChunk; ++n)
+              if ((st->rule[n0 + n] >> i) & 1) x[n] += v;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < S::kChunk; ++i) {
+          const int n = n0 + i;
+          if (n >= rows_all) break;
+          float o = lost ? NAN : x[i];
+          if (whole) {
+            o = n < rows ? o * st->factor[n] : lost ? o : 0.0f;
+            reinterpret_cast<__nv_bfloat16*>(out + (n / P.group) * P.out.token + (n % P.group) * P.out.head)[key] =
+                __float2bfloat16(o);
+          } else if (n < rows) {
+            P.part[(part_row + n) * D + key] = o;
+          }
+        }
+      }
+      tc_fence_before();
+      if (threadIdx.x == 0) {
+        // the cut item begins here: who joins it finds it in this CTA's record
+        const bool begins = s.tile0 == 0 && s.tile1 < s.tiles;
+        if (begins || walk.left <= 0) {
+          // the place of the item's end in the line: this CTA's end, and the tiles behind it
+          const int end = first + count + (s.tiles - s.tile1);
+          P.cut[blockIdx.x] = begins ? make_int4(s.b, s.index, end, total) : make_int4(-1, 0, 0, 0);
+        }
+      }
+    }
+    if (count <= 0 && threadIdx.x == 0) P.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssuer) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kColumns));
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// the join of cut items
+// ------------------------------------------------------------------------------------------------
+constexpr int kJoinWarps = 8;
+
+// Block (x, y): the item that begins in CTA x and ends in a later one, rows 8 y .. 8 y + 7, a warp each.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams P, int ctas, bool f8) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int n = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const int4 cut = P.cut[c0];
+  if (cut.x < 0 || n >= P.rows) return;
+  const int b = cut.x, head = cut.y / P.row_groups, t0 = cut.y % P.row_groups * P.tokens;
+  const int end = cut.z, total = cut.w;
+  ctas = min(ctas, total);
+  const int t = t0 + n / P.group;
+  if (t >= P.batch.T) return;
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(P.out.data + b * P.out.row + t * P.out.token +
+                                                        (int64_t)(head * P.group + n % P.group) * P.out.head);
+  constexpr int E = D / 32;
+  float o[E] = {};
+  float sum = 0.0f;
+  if (t < batch_tokens(P.batch, b)) {
+    // the last CTA of the item: the one whose part of the line holds tile end - 1
+    int c1 = (int)(((int64_t)end * ctas - 1) / total);
+    while (c1 + 1 < ctas && line_cut(total, c1 + 1, ctas) < end) ++c1;
+    while (line_cut(total, c1, ctas) >= end) --c1;
+    const auto row_of = [&](int c) { return ((int64_t)c * 2 + (c == c0)) * P.rows + n; };
+    float top = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, P.part_ml[row_of(c)].x);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    const float base = top == -INFINITY ? 0.0f : top;
+    for (int c = c0; c <= c1; c += 32) {
+      float f = 0.0f, part = 0.0f;
+      if (c + lane <= c1) {
+        const float2 ml = P.part_ml[row_of(c + lane)];
+        f = exp2_approx(ml.x - base);
+        part = f * ml.y;
       }
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(~0u, dot, d);
-      const float z = dot * P.scale;
-      const float top = fmaxf(m, z), base = top == -INFINITY ? 0.0f : top;
-      const float keep = expf(m - base), w = expf(z - base);
-      l = l * keep + w;
+      for (int d = 16; d > 0; d /= 2) part += __shfl_xor_sync(~0u, part, d);
+      sum += part;
+      const int last = min(32, c1 + 1 - c);
+#pragma unroll 4
+      for (int i = 0; i < last; ++i) {
+        const float g = __shfl_sync(~0u, f, i);
+        const float* p = P.part + row_of(c + i) * D + lane * E;
+        float x[E];
+        if constexpr (E == 4) {
+          const float4 w = *reinterpret_cast<const float4*>(p);
+          x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+        } else {
+          const float2 w = *reinterpret_cast<const float2*>(p);
+          x[0] = w.x, x[1] = w.y;
+        }
 #pragma unroll
-      for (int i = 0; i < E; ++i) o[i] = o[i] * keep + w * v[i];
-      m = top;
+        for (int e = 0; e < E; ++e) o[e] += g * x[e];
+      }
     }
   }
+  const float v = f8 && P.cache.v_scale ? __ldg(P.cache.v_scale + head) : 1.0f;
+  const float inv = sum == 0.0f ? 0.0f : v / sum;
 #pragma unroll
-  for (int i = 0; i < E; ++i) part[warp][lane + 32 * i] = o[i];
-  if (lane == 0) part[warp][D] = m, part[warp][D + 1] = l;
-  __syncthreads();
-  for (int d = threadIdx.x; d < D; d += kRowWarps * 32) {
-    float top = -INFINITY, sum = 0.0f, acc = 0.0f;
-    for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, part[w][D]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    for (int w = 0; w < kRowWarps; ++w) {
-      const float f = expf(part[w][D] - base);
-      sum += f * part[w][D + 1];
-      acc += f * part[w][d];
-    }
-    reinterpret_cast<__nv_bfloat16*>(out)[d] = __float2bfloat16(sum == 0.0f ? 0.0f : acc / sum);
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(out + lane * E + e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
+}
+
+// ------------------------------------------------------------------------------------------------
+// host side
+// ------------------------------------------------------------------------------------------------
+// Tokens per row group: as few groups as 128 rows allow, of even size.
+static void row_groups(int T, int group, int* tokens, int* groups) {
+  const int most = kMaxRows / group;
+  *groups = (T + most - 1) / most;
+  *tokens = (T + *groups - 1) / *groups;
+  *groups = (T + *tokens - 1) / *tokens;
+}
+
+struct AttnLayout {
+  size_t part, ml, cut, bytes;
+};
+static AttnLayout attn_layout(int rows, int D) {
+  const auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  AttnLayout L;
+  L.part = 0;
+  L.ml = up(L.part + (size_t)kMaxParts * 2 * rows * D * sizeof(float));
+  L.cut = up(L.ml + (size_t)kMaxParts * 2 * rows * sizeof(float2));
+  L.bytes = up(L.cut + kMaxParts * sizeof(int4));
+  return L;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeFn encode_fn() {
+  static std::atomic<void*> cached{nullptr};
+  void* f = cached.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return nullptr;
+    cached.store(f, std::memory_order_release);
   }
+  return reinterpret_cast<EncodeFn>(f);
+}
+
+// A 4-d map with the given extents, byte strides of dimensions 1..3 and box.  The stride of a dimension of
+// one element is never used, and is set to a legal one.
+static bool encode(CUtensorMap* map, CUtensorMapDataType type, int es, void* data, const int64_t (&dim)[4],
+                   const int64_t (&stride)[3], const int (&box)[4], CUtensorMapSwizzle swizzle) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) d[i] = (cuuint64_t)dim[i], b[i] = (cuuint32_t)box[i];
+  for (int i = 0; i < 3; ++i) s[i] = dim[i + 1] == 1 ? (cuuint64_t)dim[0] * es : (cuuint64_t)stride[i];
+  return fn(map, type, 4, data, d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool F8, int NT>
+static cudaError_t launch_attention(const AttnParams& P, int ctas, cudaStream_t st) {
+  using S = Shape<D, F8, NT>;
+  auto kern = attn_kernel<D, F8, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, S::kThreads, S::kBytes, st>>>(P);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || ctas == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, (P.rows + kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, P, ctas, F8);
+}
+
+template <int D, bool F8>
+static cudaError_t launch_rows(const AttnParams& P, int ctas, cudaStream_t st) {
+  if (P.rows <= 16) return launch_attention<D, F8, 16>(P, ctas, st);
+  if (P.rows <= 32) return launch_attention<D, F8, 32>(P, ctas, st);
+  if (P.rows <= 64) return launch_attention<D, F8, 64>(P, ctas, st);
+  return launch_attention<D, F8, 128>(P, ctas, st);
 }
 
 }  // namespace sv
@@ -95,7 +1040,10 @@ size_t spec_paged_attention_workspace_bytes(int32_t B, int32_t T, int32_t q_head
   if (B < 0 || T < 0 || T > SPEC_MAX_NEW || heads < 1 || q_heads < 1 || q_heads % heads) return 0;
   if (q_heads / heads > SPEC_MAX_GROUP) return 0;
   if (head_dim != 64 && head_dim != 128) return 0;
-  return 256;
+  if (T == 0) return 256;
+  int tokens, groups;
+  row_groups(T, q_heads / heads, &tokens, &groups);
+  return attn_layout(tokens * (q_heads / heads), head_dim).bytes;
 }
 
 spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* out, int32_t q_heads,
@@ -109,20 +1057,51 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
   if (batch->T > SPEC_MAX_NEW || batch->B > 65535 || q_heads / cache->heads > SPEC_MAX_GROUP) return SPEC_ERR_UNSUPPORTED;
   if (batch->B == 0 || batch->T == 0) return SPEC_OK;
   if (!heads_ok(q) || !heads_ok(out)) return SPEC_ERR_INVALID_ARG;
-  const size_t need = spec_paged_attention_workspace_bytes(batch->B, batch->T, q_heads, cache->heads, cache->head_dim);
+  const int D = cache->head_dim, group = q_heads / cache->heads;
+  const size_t need = spec_paged_attention_workspace_bytes(batch->B, batch->T, q_heads, cache->heads, D);
   if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < need) return SPEC_ERR_WORKSPACE;
+
   AttnParams P = {};
-  P.q = heads_of(q), P.out = heads_of(out);
+  P.out = heads_of(out);
   P.cache = cache_of(cache);
   P.batch = batch_of(batch, cache);
   P.mask = mask;
-  P.q_heads = q_heads, P.group = q_heads / cache->heads;
-  P.scale = scale;
+  P.heads = cache->heads, P.group = group;
+  row_groups(batch->T, group, &P.tokens, &P.row_groups);
+  P.rows = group * P.tokens;
+  P.scale_log2 = scale * kLog2e;
+  const AttnLayout L = attn_layout(P.rows, D);
+  char* ws = static_cast<char*>(workspace);
+  P.part = reinterpret_cast<float*>(ws + L.part);
+  P.part_ml = reinterpret_cast<float2*>(ws + L.ml);
+  P.cut = reinterpret_cast<int4*>(ws + L.cut);
+
+  // tiles at most: what the page table could hold
+  const int64_t per = ((int64_t)P.batch.slots + kTileSlots - 1) / kTileSlots;
+  const int64_t most = (int64_t)batch->B * cache->heads * P.row_groups * (per > 0 ? per : 1);
+  if (most > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
+
   const bool f8 = cache->dtype == SPEC_DTYPE_E4M3;
-  auto kern = cache->head_dim == 128 ? (f8 ? attn_row_kernel<128, true> : attn_row_kernel<128, false>)
-                                     : (f8 ? attn_row_kernel<64, true> : attn_row_kernel<64, false>);
-  kern<<<dim3(q_heads, batch->T, batch->B), kRowWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  const int es = f8 ? 1 : 2;
+  const int box = cache->page_size < kTileSlots ? cache->page_size : kTileSlots;
+  const Heads hq = heads_of(q);
+  bool ok = encode(&P.q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, hq.data, {D, q_heads, batch->T, batch->B},
+                   {hq.head, hq.token, hq.row}, {64, group, P.tokens, 1}, CU_TENSOR_MAP_SWIZZLE_128B);
+  for (int kv = 0; kv < 2; ++kv)
+    ok = ok && encode(kv ? &P.v_map : &P.k_map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, es,
+                      kv ? P.cache.v : P.cache.k, {D, cache->page_size, cache->heads, cache->num_pages},
+                      {P.cache.slot, P.cache.head, P.cache.page}, {f8 ? D : 64, box, 1, 1},
+                      f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!ok) return SPEC_ERR_CUDA;
+  int sms = 0;
+  cudaError_t e = device_sms(&sms);
+  if (e != cudaSuccess) return SPEC_ERR_CUDA;
+  int ctas = sms < kMaxParts ? sms : kMaxParts;
+  if (most < ctas) ctas = (int)most;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  e = D == 128 ? (f8 ? launch_rows<128, true>(P, ctas, st) : launch_rows<128, false>(P, ctas, st))
+               : (f8 ? launch_rows<64, true>(P, ctas, st) : launch_rows<64, false>(P, ctas, st));
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // extern "C"
