@@ -20,6 +20,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "decode_common.cuh"
 
@@ -29,6 +30,7 @@ constexpr int kTileSlots = 128;       // slots per tile = rows of the matrix uni
 constexpr int kMaxParts = 160;        // CTAs of the stream at most (one per SM), for the workspace's size
 constexpr int kMaxRows = 128;         // query rows of one item
 constexpr float kRescale = 8.0f;      // rescale when a score passes the maximum in use by 2^8
+constexpr float kNone = 3e38f;        // shift of a row without a maximum yet: any score asks for one
 constexpr int kSoftmaxWarps = 8;      // two warpgroups, each with every other chunk of columns
 constexpr int kConvertWarps = 4;      // E4M3 caches: E4M3 -> fp16
 constexpr float kLog2e = 1.4426950408889634f;
@@ -67,7 +69,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 10000;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
       : "r"(bar), "r"(parity)
@@ -79,7 +81,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 // wait in it soon after.  Nothing here waits on another block.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
   if (mbar_try(bar, parity)) return true;
-  for (int i = 0; i < (1 << 18); ++i) {
+  for (int i = 0; i < (1 << 22); ++i) {
     if (mbar_try(bar, parity)) return true;
     if ((i & 255) == 0 && *dead) return false;
   }
@@ -173,6 +175,22 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
   return r != 0;
 }
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -263,10 +281,18 @@ struct Shape {
   static constexpr int kFit = (kBudget - kFixed) / kRing;
   static constexpr int kSlots = kFit > 8 ? 8 : kFit;              // K and V tiles in flight
   static_assert(kSlots >= 4, "the ring holds two tiles of K and V at least");
-  static constexpr int kThreads = (kSoftmaxWarps + 2 + (F8 ? kConvertWarps : 0)) * 32;
+  // Registers: the variants with many columns take more for the softmax warps than an even split of the
+  // SM's gives them, and less for the others.  Per warpgroup of 128 threads, of 512 in all:
+  // 3 x 168 = 504 = 2 x 208 + 88, and 4 x 128 = 512 = 2 x 176 + 2 x 80.
+  static constexpr bool kSplit = NT > 64 || (F8 && NT > 32);
+  static constexpr int kThreads = F8 ? 512 : 384;
+  static constexpr int kLaunchRegs = F8 ? 128 : 168, kMoreRegs = F8 ? 176 : 208, kFewRegs = F8 ? 80 : 88;
+  static_assert(2 * kMoreRegs + (kThreads / 128 - 2) * kFewRegs <= kThreads / 128 * kLaunchRegs, "register split");
   static constexpr int kColumns = 3 * NT <= 64 ? 64 : 3 * NT <= 128 ? 128 : 3 * NT <= 256 ? 256 : 512;
   static constexpr int kChunk = NT >= 32 ? 16 : 8;                // columns a warpgroup takes at a time
   static constexpr int kChunks = NT / (2 * kChunk);               // chunks of one warpgroup
+  static constexpr int kWords = NT > 64 ? 2 : 1;                  // 32-column words of one warpgroup
+  static constexpr bool kKeep = NT <= 64;                         // scores stay in registers over the vote
 
   struct State {
     uint64_t ring_full[8], ring_empty[8];
@@ -278,12 +304,12 @@ struct Shape {
     int start_b, start_offset, total;
     uint32_t bad_value[2];           // segment + 1 whose new tokens hold a value that is not finite
     int warp_sum[16];
-    alignas(16) float base[NT];      // what is subtracted: the row's maximum in use, 0 for none
-    alignas(16) float limit[NT];     // rescale beyond
+    alignas(16) float shift[NT];     // minus the row's maximum in use, what is added to a score (see kNone)
     alignas(16) float top[NT];       // the maximum in use, -inf for none
     alignas(16) float factor[NT];    // a rescale's factor; 1 / l at the end
     float red[4][NT];
-    uint64_t rule[NT];               // new tokens that the row attends to
+    int64_t place[NT];               // the row's offset in the item's output
+    uint64_t seen[2][SPEC_MAX_NEW];  // which columns of each warpgroup attend to a new token
   };
   static constexpr int kState = kFixed + kSlots * kRing;
   static constexpr int kBytes = kState + (int)sizeof(State) + 1024;
@@ -394,360 +420,407 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
   __syncthreads();
   const uint32_t tmem = st->tmem;
   volatile int* dead = &st->dead;
-  Walk walk(P, count > 0 ? st->start_b : 0, count > 0 ? st->start_offset : 0, count);
-  Segment s;
+  const int start_b = count > 0 ? st->start_b : 0, start_offset = count > 0 ? st->start_offset : 0;
 
-  if (warp == kProducer) {
-    // ---- TMA: Q of every segment, K and V of every tile, page by page ----
-    const int page = 1 << P.cache.page_shift;
-    const int box = min(page, kTileSlots);                // slots of one copy
-    const int copies = kTileSlots / box;                  // copies of a tile (and half)
-    constexpr int kParts = F8 ? 1 : S::kHalves;
-    const int part = lane % kParts, copy = lane / kParts;
-    int slot = 0;
-    uint32_t phase = 0;  // of the ring
-    bool ok = true;
-    int issued = 0;
-    for (int seg = 0; ok && walk.next(s); ++seg) {
-      const int qb = seg % S::kQBufs;
-      ok = mbar_wait_warp(smem_addr(&st->q_empty[qb]), ((seg / S::kQBufs) & 1) ^ 1, dead);
-      if (!ok) break;
-      if (lane == 0) {
-        const uint32_t bar = smem_addr(&st->q_loaded[qb]);
-        mbar_expect(bar, P.rows * D * 2);
-        for (int h = 0; h < S::kHalves; ++h)
-          tma_load(smem_addr(q_buf + qb * S::kQ + h * NT * 128), &P.q_map, h * 64, s.head * P.group, s.row_group * P.tokens,
-                   s.b, bar);
-      }
-      const int32_t* table = P.batch.pages + (int64_t)s.b * P.batch.max_pages;
-      const auto entry = [&](int tile) {  // this lane's page of a tile; one past the pool reads as zeros
-        const int at = tile * kTileSlots + copy * box;
-        if (copy >= copies || at >= s.end) return P.cache.num_pages;
-        const int p = __ldg(table + (at >> P.cache.page_shift));
-        return p < 0 || p > P.cache.num_pages ? P.cache.num_pages : p;
-      };
-      int mine_page = entry(s.tile0);
-      for (int tile = s.tile0; ok && tile < s.tile1; ++tile) {
-        const int p = mine_page;
-        if (tile + 1 < s.tile1) mine_page = entry(tile + 1);
-        const int row = (tile * kTileSlots + copy * box) & (page - 1);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          ok = ok && mbar_wait_warp(smem_addr(&st->ring_empty[slot]), phase ^ 1, dead);
-          if (!ok) break;
-          const uint32_t bar = smem_addr(&st->ring_full[slot]);
-          if (lane == 0) mbar_expect(bar, S::kRing);
-          __syncwarp();
-          if (copy < copies) {
-            const uint32_t dst = smem_addr(ring) + slot * S::kRing + (F8 ? copy * box * D : part * (kTileSlots * 128) + copy * box * 128);
-            tma_load(dst, kv ? &P.v_map : &P.k_map, part * 64, row, s.head, p, bar);
-          }
-          ++issued;
-          if (++slot == S::kSlots) slot = 0, phase ^= 1;
+  if (warp >= kSoftmaxWarps) {
+    if constexpr (S::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFewRegs));
+    Walk walk(P, start_b, start_offset, count);
+    Segment s;
+    if (warp == kProducer) {
+      // ---- TMA: Q of every segment, K and V of every tile, page by page ----
+      const int page = 1 << P.cache.page_shift;
+      const int box = min(page, kTileSlots);                // slots of one copy
+      const int copies = kTileSlots / box;                  // copies of a tile (and half)
+      constexpr int kParts = F8 ? 1 : S::kHalves;
+      const int part = lane % kParts, copy = lane / kParts;
+      int slot = 0;
+      uint32_t phase = 0;  // of the ring
+      bool ok = true;
+      int issued = 0;
+      for (int seg = 0; ok && walk.next(s); ++seg) {
+        const int qb = seg % S::kQBufs;
+        ok = mbar_wait_warp(smem_addr(&st->q_empty[qb]), ((seg / S::kQBufs) & 1) ^ 1, dead);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_addr(&st->q_loaded[qb]);
+          mbar_expect(bar, P.rows * D * 2);
+          for (int h = 0; h < S::kHalves; ++h)
+            tma_load(smem_addr(q_buf + qb * S::kQ + h * NT * 128), &P.q_map, h * 64, s.head * P.group, s.row_group * P.tokens,
+                     s.b, bar);
         }
-      }
-    }
-    if (!ok)  // a wait ran out: see the copies in flight land before the block ends
-      for (int i = 0; i < min(issued, S::kSlots); ++i) {
-        if (--slot < 0) slot = S::kSlots - 1, phase ^= 1;
-        for (int n = 0; n < (1 << 16) && !mbar_try(smem_addr(&st->ring_full[slot]), phase); ++n) {
-        }
-      }
-  } else if (warp == kIssuer) {
-    // ---- matrix products ----
-    if (lane == 0) {
-      const uint32_t n16 = (P.rows + 15) / 16 * 16;
-      const uint32_t fmt = F8 ? 0u : 1u;  // fp16 or bf16 operands, fp32 accumulators, M = 128
-      const uint32_t idesc = 1u << 4 | fmt << 7 | fmt << 10 | (n16 >> 3) << 17 | (128u >> 4) << 24;
-      const uint32_t idesc_t = idesc | 1u << 15 | 1u << 16;  // both operands with the reduction outside
-      const uint32_t o_col = tmem + 2 * NT;
-      uint32_t it = 0;       // tiles so far
-      int k_slot = 0, v_slot = 0;
-      uint32_t k_phase = 0, v_phase = 0;
-      bool ok = true, o_any = false;
-      const auto advance = [&](int& slot, uint32_t& phase, int by) {
-        slot += by;
-        if (slot >= S::kSlots) slot -= S::kSlots, phase ^= 1;
-      };
-      advance(v_slot, v_phase, 1);
-
-      const auto scores = [&](int qb, uint32_t q_phase, bool first, bool last) {
-        if (first) ok = ok && mbar_wait(smem_addr(F8 ? &st->q_full[qb] : &st->q_loaded[qb]), q_phase, dead);
-        const int sb = it & 1;
-        ok = ok && mbar_wait(smem_addr(&st->s_empty[sb]), ((it >> 1) & 1) ^ 1, dead);
-        ok = ok && (F8 ? mbar_wait(smem_addr(&st->k16_full), it & 1, dead)
-                       : mbar_wait(smem_addr(&st->ring_full[k_slot]), k_phase, dead));
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t a = smem_addr(F8 ? t16 : ring + k_slot * S::kRing), b = smem_addr(q_buf + qb * S::kQ);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const int half = k / 4, in = (k % 4) * 32;
-          tc_mma(tmem + sb * NT, matrix_desc(a + half * (kTileSlots * 128) + in, 16, 1024),
-                 matrix_desc(b + half * (NT * 128) + in, 16, 1024), idesc, k > 0);
-        }
-        tc_commit(smem_addr(F8 ? &st->k16_empty : &st->ring_empty[k_slot]));
-        tc_commit(smem_addr(&st->s_full[sb]));
-        if (last) tc_commit(smem_addr(&st->q_empty[qb]));
-        advance(k_slot, k_phase, 2);
-      };
-      const auto values = [&](uint32_t i, bool first) {  // tile i, one behind the scores
-        ok = ok && (F8 ? mbar_wait(smem_addr(&st->v16_full), i & 1, dead)
-                       : mbar_wait(smem_addr(&st->ring_full[v_slot]), v_phase, dead));
-        ok = ok && mbar_wait(smem_addr(&st->p_full), i & 1, dead);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t a = smem_addr(F8 ? t16 + S::kTile16 : ring + v_slot * S::kRing), b = smem_addr(p_buf);
-        // head_dim 64: the instruction's rows 64..127 repeat rows 0..63 and are not read
-        const uint32_t lead = D == 128 ? kTileSlots * 128 : 0;
-#pragma unroll
-        for (int k = 0; k < kTileSlots / 16; ++k)
-          tc_mma(o_col, matrix_desc(a + k * 2048, lead, 1024), matrix_desc(b + k * 2048, kTileSlots * 128, 1024), idesc_t,
-                 !first || k > 0);
-        tc_commit(smem_addr(F8 ? &st->v16_empty : &st->ring_empty[v_slot]));
-        tc_commit(smem_addr(&st->o_full));
-        advance(v_slot, v_phase, 2);
-        o_any = true;
-      };
-      bool first_behind = false;
-      for (int seg = 0; ok && walk.next(s); ++seg)
+        const int32_t* table = P.batch.pages + (int64_t)s.b * P.batch.max_pages;
+        const auto entry = [&](int tile) {  // this lane's page of a tile; one past the pool reads as zeros
+          const int at = tile * kTileSlots + copy * box;
+          if (copy >= copies || at >= s.end) return P.cache.num_pages;
+          const int p = __ldg(table + (at >> P.cache.page_shift));
+          return p < 0 || p > P.cache.num_pages ? P.cache.num_pages : p;
+        };
+        int mine_page = entry(s.tile0);
         for (int tile = s.tile0; ok && tile < s.tile1; ++tile) {
-          scores(seg % S::kQBufs, (seg / S::kQBufs) & 1, tile == s.tile0, tile + 1 == s.tile1);
-          if (it > 0 && ok) values(it - 1, first_behind);
-          first_behind = tile == s.tile0;
-          ++it;
+          const int p = mine_page;
+          if (tile + 1 < s.tile1) mine_page = entry(tile + 1);
+          const int row = (tile * kTileSlots + copy * box) & (page - 1);
+  #pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = ok && mbar_wait_warp(smem_addr(&st->ring_empty[slot]), phase ^ 1, dead);
+            if (!ok) break;
+            const uint32_t bar = smem_addr(&st->ring_full[slot]);
+            if (lane == 0) mbar_expect(bar, S::kRing);
+            __syncwarp();
+            if (copy < copies) {
+              const uint32_t dst = smem_addr(ring) + slot * S::kRing + (F8 ? copy * box * D : part * (kTileSlots * 128) + copy * box * 128);
+              tma_load(dst, kv ? &P.v_map : &P.k_map, part * 64, row, s.head, p, bar);
+            }
+            ++issued;
+            if (++slot == S::kSlots) slot = 0, phase ^= 1;
+          }
         }
-      if (ok && it > 0) values(it - 1, first_behind);
-      if (!ok && o_any)  // a wait ran out: let the products in flight end before TMEM is freed
-        for (int n = 0; n < (1 << 16); ++n) __nanosleep(20);
-    }
-    __syncwarp();
-  } else if (F8 && warp > kIssuer) {
-    // ---- E4M3 -> fp16 (exact), K and V into the swizzled layout that the matrix unit reads ----
-    const int tid = threadIdx.x - (kIssuer + 1) * 32;  // 0..127
-    int slot = 0;
-    uint32_t phase = 0, it = 0;
-    bool ok = true;
-    for (int seg = 0; ok && walk.next(s); ++seg) {
-      const int qb = seg % S::kQBufs;
-      ok = mbar_wait_warp(smem_addr(&st->q_loaded[qb]), (seg / S::kQBufs) & 1, dead);
-      if (!ok) break;
-      for (int i = tid; i < S::kQ / 16; i += kConvertWarps * 32) {  // q: bf16 -> fp16, in place
-        uint4* p = reinterpret_cast<uint4*>(q_buf + qb * S::kQ) + i;
-        uint4 w = *p;
-        uint32_t* u = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __half2 h = __floats2half2_rn(bf16_low(u[j]), bf16_high(u[j]));
-          u[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *p = w;
       }
-      fence_async_shared();
+      if (!ok)  // a wait ran out: see the copies in flight land before the block ends
+        for (int i = 0; i < min(issued, S::kSlots); ++i) {
+          if (--slot < 0) slot = S::kSlots - 1, phase ^= 1;
+          for (int n = 0; n < (1 << 16) && !mbar_try(smem_addr(&st->ring_full[slot]), phase); ++n) {
+          }
+        }
+    } else if (warp == kIssuer) {
+      // ---- matrix products ----
+      if (lane == 0) {
+        const uint32_t n16 = (P.rows + 15) / 16 * 16;
+        const uint32_t fmt = F8 ? 0u : 1u;  // fp16 or bf16 operands, fp32 accumulators, M = 128
+        const uint32_t idesc = 1u << 4 | fmt << 7 | fmt << 10 | (n16 >> 3) << 17 | (128u >> 4) << 24;
+        const uint32_t idesc_t = idesc | 1u << 15 | 1u << 16;  // both operands with the reduction outside
+        const uint32_t o_col = tmem + 2 * NT;
+        uint32_t it = 0;       // tiles so far
+        int k_slot = 0, v_slot = 0;
+        uint32_t k_phase = 0, v_phase = 0;
+        bool ok = true, o_any = false;
+        const auto advance = [&](int& slot, uint32_t& phase, int by) {
+          slot += by;
+          if (slot >= S::kSlots) slot -= S::kSlots, phase ^= 1;
+        };
+        advance(v_slot, v_phase, 1);
+
+        const auto scores = [&](int qb, uint32_t q_phase, bool first, bool last) {
+          if (first) ok = ok && mbar_wait(smem_addr(F8 ? &st->q_full[qb] : &st->q_loaded[qb]), q_phase, dead);
+          const int sb = it & 1;
+          ok = ok && mbar_wait(smem_addr(&st->s_empty[sb]), ((it >> 1) & 1) ^ 1, dead);
+          ok = ok && (F8 ? mbar_wait(smem_addr(&st->k16_full), it & 1, dead)
+                         : mbar_wait(smem_addr(&st->ring_full[k_slot]), k_phase, dead));
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t a = smem_addr(F8 ? t16 : ring + k_slot * S::kRing), b = smem_addr(q_buf + qb * S::kQ);
+  #pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const int half = k / 4, in = (k % 4) * 32;
+            tc_mma(tmem + sb * NT, matrix_desc(a + half * (kTileSlots * 128) + in, 16, 1024),
+                   matrix_desc(b + half * (NT * 128) + in, 16, 1024), idesc, k > 0);
+          }
+          tc_commit(smem_addr(F8 ? &st->k16_empty : &st->ring_empty[k_slot]));
+          tc_commit(smem_addr(&st->s_full[sb]));
+          if (last) tc_commit(smem_addr(&st->q_empty[qb]));
+          advance(k_slot, k_phase, 2);
+        };
+        const auto values = [&](uint32_t i, bool first) {  // tile i, one behind the scores
+          ok = ok && (F8 ? mbar_wait(smem_addr(&st->v16_full), i & 1, dead)
+                         : mbar_wait(smem_addr(&st->ring_full[v_slot]), v_phase, dead));
+          ok = ok && mbar_wait(smem_addr(&st->p_full), i & 1, dead);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t a = smem_addr(F8 ? t16 + S::kTile16 : ring + v_slot * S::kRing), b = smem_addr(p_buf);
+          // head_dim 64: the instruction's rows 64..127 repeat rows 0..63 and are not read
+          const uint32_t lead = D == 128 ? kTileSlots * 128 : 0;
+  #pragma unroll
+          for (int k = 0; k < kTileSlots / 16; ++k)
+            tc_mma(o_col, matrix_desc(a + k * 2048, lead, 1024), matrix_desc(b + k * 2048, kTileSlots * 128, 1024), idesc_t,
+                   !first || k > 0);
+          tc_commit(smem_addr(F8 ? &st->v16_empty : &st->ring_empty[v_slot]));
+          tc_commit(smem_addr(&st->o_full));
+          advance(v_slot, v_phase, 2);
+          o_any = true;
+        };
+        bool first_behind = false;
+        for (int seg = 0; ok && walk.next(s); ++seg)
+          for (int tile = s.tile0; ok && tile < s.tile1; ++tile) {
+            scores(seg % S::kQBufs, (seg / S::kQBufs) & 1, tile == s.tile0, tile + 1 == s.tile1);
+            if (it > 0 && ok) values(it - 1, first_behind);
+            first_behind = tile == s.tile0;
+            ++it;
+          }
+        if (ok && it > 0) values(it - 1, first_behind);
+        if (!ok && o_any)  // a wait ran out: let the products in flight end before TMEM is freed
+          for (int n = 0; n < (1 << 16); ++n) __nanosleep(20);
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&st->q_full[qb]));
-      for (int tile = s.tile0; ok && tile < s.tile1; ++tile, ++it) {
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          ok = ok && mbar_wait_warp(smem_addr(&st->ring_full[slot]), phase, dead);
-          ok = ok && mbar_wait_warp(smem_addr(kv ? &st->v16_empty : &st->k16_empty), (it & 1) ^ 1, dead);
-          if (!ok) break;
-          const char* src = ring + slot * S::kRing;
-          char* dst = t16 + kv * S::kTile16;
-          // V's slots past the end are zeroed: their weights are 0, but 0 times what they hold may not be.
-          // New tokens' values that are not finite are taken out here and added at the end to the rows
-          // that attend to them.
-          const int end = kv ? s.end - tile * kTileSlots : kTileSlots;
-          const int fresh = kv ? s.ctx - tile * kTileSlots : kTileSlots;
-          constexpr int kUnits = D / 16;
-#pragma unroll
-          for (int i = 0; i < kTileSlots * kUnits / 128; ++i) {
-            const int u = i * 128 + tid, row = u / kUnits, c = u % kUnits;
-            uint4 w = *reinterpret_cast<const uint4*>(src + u * 16);
-            uint32_t* x = reinterpret_cast<uint32_t*>(&w);
-            if (row >= fresh) {
-              if (row >= end) {
-                w = make_uint4(0, 0, 0, 0);
-              } else {
-                bool bad = false;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {  // the code 0x7F of either sign is NaN
-                  const uint32_t nan = __vcmpeq4(x[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                  bad |= nan != 0;
-                  x[j] &= ~nan;
+    } else if (F8 && warp > kIssuer && warp <= kIssuer + kConvertWarps) {
+      // ---- E4M3 -> fp16 (exact), K and V into the swizzled layout that the matrix unit reads ----
+      const int tid = threadIdx.x - (kIssuer + 1) * 32;  // 0..127
+      int slot = 0;
+      uint32_t phase = 0, it = 0;
+      bool ok = true;
+      for (int seg = 0; ok && walk.next(s); ++seg) {
+        const int qb = seg % S::kQBufs;
+        ok = mbar_wait_warp(smem_addr(&st->q_loaded[qb]), (seg / S::kQBufs) & 1, dead);
+        if (!ok) break;
+        for (int i = tid; i < S::kQ / 16; i += kConvertWarps * 32) {  // q: bf16 -> fp16, in place
+          uint4* p = reinterpret_cast<uint4*>(q_buf + qb * S::kQ) + i;
+          uint4 w = *p;
+          uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __half2 h = __floats2half2_rn(bf16_low(u[j]), bf16_high(u[j]));
+            u[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          *p = w;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&st->q_full[qb]));
+        for (int tile = s.tile0; ok && tile < s.tile1; ++tile, ++it) {
+  #pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = ok && mbar_wait_warp(smem_addr(&st->ring_full[slot]), phase, dead);
+            ok = ok && mbar_wait_warp(smem_addr(kv ? &st->v16_empty : &st->k16_empty), (it & 1) ^ 1, dead);
+            if (!ok) break;
+            char* src = ring + slot * S::kRing;
+            char* dst = t16 + kv * S::kTile16;
+            constexpr int kUnits = D / 16;
+            if (kv && (tile + 1) * kTileSlots > s.ctx) {
+              // V's slots past the end are zeroed: their weights are 0, but 0 times what they hold may not be.
+              // New tokens' values that are not finite are taken out here and added at the end to the rows
+              // that attend to them.  Every thread mends the units that it converts.
+              const int from = max(s.ctx - tile * kTileSlots, 0), end = s.end - tile * kTileSlots;
+              for (int u = tid; u < kTileSlots * kUnits; u += 128) {
+                const int row = u / kUnits;
+                if (row < from) continue;
+                uint4* p = reinterpret_cast<uint4*>(src + u * 16);
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (row < end) {
+                  w = *p;
+                  uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+                  bool bad = false;
+  #pragma unroll
+                  for (int j = 0; j < 4; ++j) {  // the code 0x7F of either sign is NaN
+                    const uint32_t nan = __vcmpeq4(x[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                    bad |= nan != 0;
+                    x[j] &= ~nan;
+                  }
+                  if (bad) st->bad_value[seg & 1] = seg + 1;
                 }
-                if (bad) st->bad_value[seg & 1] = seg + 1;
+                *p = w;
               }
             }
-            uint32_t h[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-                  "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-                  : "=r"(h[2 * j]), "=r"(h[2 * j + 1])
-                  : "r"(x[j]));
-            }
-            char* out = dst + (c / 4) * (kTileSlots * 128) + row * 128;
-            const int sw = (row & 7) * 16, j0 = (c % 4) * 32;
+            constexpr int kEach = kTileSlots * kUnits / 128;
+            uint4 raw[kEach];
+  #pragma unroll
+            for (int i = 0; i < kEach; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + (i * 128 + tid) * 16);
+            // a thread's units are 128 / kUnits rows apart: the same vector of the row and the same swizzle
+            const int row0 = tid / kUnits, c = tid % kUnits;
+            char* out = dst + (c / 4) * (kTileSlots * 128) + row0 * 128;
+            const int sw = (row0 & 7) * 16, j0 = (c % 4) * 32;
             // the two halves of a row start at the same banks: one of them stores its second vector first
             const bool turn = c >= 4;
-            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-            *reinterpret_cast<uint4*>(out + ((j0 + (turn ? 16 : 0)) ^ sw)) = turn ? hi : lo;
-            *reinterpret_cast<uint4*>(out + ((j0 + (turn ? 0 : 16)) ^ sw)) = turn ? lo : hi;
+            char* out0 = out + ((j0 + (turn ? 16 : 0)) ^ sw);
+            char* out1 = out + ((j0 + (turn ? 0 : 16)) ^ sw);
+  #pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+              const uint32_t* x = reinterpret_cast<const uint32_t*>(&raw[i]);
+              uint32_t h[8];
+  #pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                    "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+                    : "=r"(h[2 * j]), "=r"(h[2 * j + 1])
+                    : "r"(x[j]));
+              }
+              const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+              *reinterpret_cast<uint4*>(out0 + i * (128 / kUnits) * 128) = turn ? hi : lo;
+              *reinterpret_cast<uint4*>(out1 + i * (128 / kUnits) * 128) = turn ? lo : hi;
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(smem_addr(kv ? &st->v16_full : &st->k16_full));
+              mbar_arrive(smem_addr(&st->ring_empty[slot]));
+            }
+            if (++slot == S::kSlots) slot = 0, phase ^= 1;
           }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(smem_addr(kv ? &st->v16_full : &st->k16_full));
-            mbar_arrive(smem_addr(&st->ring_empty[slot]));
-          }
-          if (++slot == S::kSlots) slot = 0, phase ^= 1;
         }
       }
     }
-  } else if (warp < kSoftmaxWarps) {
+  } else {
+    if constexpr (S::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kMoreRegs));
+    Walk walk(P, start_b, start_offset, count);
+    Segment s;
     // ---- softmax and output; no branch around a group_sync depends on anything but the plan and votes ----
     const int wg = warp >> 2, quad = warp & 3, bar = 1 + wg;
     const int key = quad * 32 + lane, wtid = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const int my_row = ((wtid / S::kChunk) * 2 + wg) * S::kChunk + wtid % S::kChunk;  // wtid < NT / 2
-    float l[S::kChunks][S::kChunk];
+    constexpr int CK = S::kChunk;
+    const auto row_of = [&](int own) { return ((own / CK) * 2 + wg) * CK + own % CK; };  // of the warpgroup's columns
+    const int my_row = row_of(wtid);  // wtid < NT / 2
+    float l[S::kChunks][CK];
     uint32_t it = 0;
     int v_slot = 1;
     uint32_t v_phase = 0;
-    const auto col = [&](int j) { return (2 * j + wg) * S::kChunk; };
+    const auto col = [&](int j) { return (2 * j + wg) * CK; };
 
     for (int seg = 0; walk.next(s); ++seg) {
       const int t0 = s.row_group * P.tokens;
       const int rows = min(max((s.tokens - t0) * P.group, 0), P.rows);  // valid ones come first
-      float c = P.scale_log2;
+      float c = P.scale_log2, v_scale = 1.0f;
       if (F8 && P.cache.k_scale) c *= __ldg(P.cache.k_scale + s.head);
+      if (F8 && P.cache.v_scale) v_scale = __ldg(P.cache.v_scale + s.head);
       group_sync(bar);  // the last segment's row states are read
       if (wtid < NT / 2) {
-        const bool in = my_row < rows;
         st->top[my_row] = -INFINITY;
-        st->base[my_row] = 0.0f;
-        st->limit[my_row] = in ? -INFINITY : INFINITY;
-        uint64_t rule = 0;
-        if (in) {
-          const int t = t0 + my_row / P.group;
-          rule = P.mask ? (uint64_t)__ldg(P.mask + (int64_t)s.b * P.batch.T + t) : t >= 63 ? ~0ull : (2ull << t) - 1;
+        st->shift[my_row] = my_row < rows ? kNone : -INFINITY;  // rows that are none: weights 0, and no vote
+        const int t = my_row / P.group, g = my_row - t * P.group;
+        st->place[my_row] = (int64_t)t * P.out.token + (int64_t)g * P.out.head;
+      }
+      if (s.tile1 * kTileSlots > s.ctx) {  // new tokens among the slots: who attends to which
+        uint64_t rule[S::kWords];
+#pragma unroll
+        for (int w = 0; w < S::kWords; ++w) {
+          const int n = row_of(w * 32 + lane);
+          const int t = t0 + n / P.group;
+          rule[w] = 0;
+          if (w * 32 + lane < NT / 2 && n < rows)
+            rule[w] = P.mask ? (uint64_t)__ldg(P.mask + (int64_t)s.b * P.batch.T + t) : t >= 63 ? ~0ull : (2ull << t) - 1;
         }
-        st->rule[my_row] = rule;
+        for (int i = quad; i < s.tokens; i += 4) {
+          const uint32_t lo = __ballot_sync(~0u, (rule[0] >> i) & 1);
+          const uint32_t hi = S::kWords > 1 ? __ballot_sync(~0u, (rule[S::kWords - 1] >> i) & 1) : 0;
+          if (lane == 0) st->seen[wg][i] = lo | (uint64_t)hi << 32;
+        }
       }
       group_sync(bar);
 #pragma unroll
       for (int j = 0; j < S::kChunks; ++j)
 #pragma unroll
-        for (int i = 0; i < S::kChunk; ++i) l[j][i] = 0.0f;
+        for (int i = 0; i < CK; ++i) l[j][i] = 0.0f;
 
       for (int tile = s.tile0; tile < s.tile1; ++tile, ++it) {
         const int sb = it & 1;
         const uint32_t s_col = lanes + sb * NT;
-        const int slot = tile * kTileSlots + key;
-        const bool masked = (tile + 1) * kTileSlots > s.ctx;  // the tile reaches past the context
-        const int fresh = slot - s.ctx;                       // which new token, negative in the context
         mbar_wait(smem_addr(&st->s_full[sb]), (it >> 1) & 1, dead);
         __syncwarp();
         tc_fence_after();
-        const auto sees = [&](int n) { return slot < s.end && (fresh < 0 || ((st->rule[n] >> fresh) & 1)); };
 
-        bool o_done = it == 0;
-        bool raise = tile == s.tile0;
-        if (!raise) {
-          float over = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < S::kChunks; ++j)
-            if (col(j) < rows) {
-              float x[S::kChunk];
-              tm_load<S::kChunk>(s_col + col(j), x);
-#pragma unroll
-              for (int i = 0; i < S::kChunk; ++i) {
-                const float z = fmaf(x[i], c, -st->limit[col(j) + i]);
-                if (!masked || sees(col(j) + i)) over = fmaxf(over, z);
-              }
-            }
-          raise = group_any(bar, over > 0.0f);
-        }
-        if (raise) {
-#pragma unroll
-          for (int j = 0; j < S::kChunks; ++j)
-            if (col(j) < rows) {
-              float x[S::kChunk];
-              tm_load<S::kChunk>(s_col + col(j), x);
-#pragma unroll
-              for (int i = 0; i < S::kChunk; ++i) x[i] = !masked || sees(col(j) + i) ? x[i] * c : -INFINITY;
-              const float m = fold_lanes<S::kChunk>(x, lane, [](float a, float b) { return fmaxf(a, b); });
-              if (lane < S::kChunk) st->red[quad][col(j) + lane] = m;
-            }
-          group_sync(bar);
-          if (wtid < NT / 2 && my_row < rows) {
-            const float old = st->top[my_row];
-            float top = old;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) top = fmaxf(top, st->red[w][my_row]);
-            st->factor[my_row] = old == -INFINITY ? 0.0f : exp2_approx(old - top);
-            st->top[my_row] = top;
-            st->base[my_row] = top == -INFINITY ? 0.0f : top;
-            st->limit[my_row] = top + kRescale;
+        const auto weigh = [&](auto tag) {
+          constexpr bool MASKED = decltype(tag)::value;  // the tile reaches past the context
+          uint64_t see = ~0ull;                          // columns that attend to this thread's slot
+          if constexpr (MASKED) {
+            const int slot = tile * kTileSlots + key, fresh = slot - s.ctx;
+            see = slot >= s.end ? 0 : fresh < 0 ? ~0ull : st->seen[wg][fresh];
           }
-          group_sync(bar);
-          if (tile > s.tile0) {
-            mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
-            __syncwarp();
-            tc_fence_after();
-            o_done = true;
+          const auto sees = [&](int j, int i) { return !MASKED || ((see >> (j * CK + i)) & 1); };
+          const auto scores = [&](int j, float (&z)[CK]) {  // in log2 units, less the maximum in use
+            tm_load<CK>(s_col + col(j), z);
+#pragma unroll
+            for (int i = 0; i < CK; i += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(&st->shift[col(j) + i]);
+              const float2 a = fma2(make_float2(z[i], z[i + 1]), make_float2(c, c), make_float2(m.x, m.y));
+              const float2 b = fma2(make_float2(z[i + 2], z[i + 3]), make_float2(c, c), make_float2(m.z, m.w));
+              z[i] = a.x, z[i + 1] = a.y, z[i + 2] = b.x, z[i + 3] = b.y;
+            }
+          };
+          float z[S::kKeep ? S::kChunks : 1][CK];
+          const auto take = [&](int j) -> float (&)[CK] { return z[S::kKeep ? j : 0]; };
+
+          bool o_done = it == 0;
+          bool raise = tile == s.tile0;
+          if (!raise) {
+            float over = -INFINITY;
 #pragma unroll
             for (int j = 0; j < S::kChunks; ++j)
               if (col(j) < rows) {
-                float x[S::kChunk];
-                tm_load<S::kChunk>(lanes + 2 * NT + col(j), x);
+                auto& x = take(j);
+                scores(j, x);
 #pragma unroll
-                for (int i = 0; i < S::kChunk; ++i) {
-                  const float f = st->factor[col(j) + i];
-                  x[i] *= f;
-                  l[j][i] *= f;
+                for (int i = 0; i < CK; ++i) over = fmaxf(over, sees(j, i) ? x[i] : -INFINITY);
+              }
+            raise = group_any(bar, over > kRescale);
+          }
+          if (raise) {
+#pragma unroll
+            for (int j = 0; j < S::kChunks; ++j)
+              if (col(j) < rows) {
+                float x[CK];
+                tm_load<CK>(s_col + col(j), x);
+#pragma unroll
+                for (int i = 0; i < CK; ++i) x[i] = sees(j, i) ? x[i] * c : -INFINITY;
+                const float m = fold_lanes<CK>(x, lane, [](float a, float b) { return fmaxf(a, b); });
+                if (lane < CK) st->red[quad][col(j) + lane] = m;
+              }
+            group_sync(bar);
+            if (wtid < NT / 2 && my_row < rows) {
+              const float old = st->top[my_row];
+              float top = old;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) top = fmaxf(top, st->red[w][my_row]);
+              st->factor[my_row] = old == -INFINITY ? 0.0f : exp2_approx(old - top);
+              st->top[my_row] = top;
+              st->shift[my_row] = top == -INFINITY ? kNone : -top;
+            }
+            group_sync(bar);
+            if (tile > s.tile0) {
+              mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
+              __syncwarp();
+              tc_fence_after();
+              o_done = true;
+#pragma unroll
+              for (int j = 0; j < S::kChunks; ++j)
+                if (col(j) < rows) {
+                  float x[CK];
+                  tm_load<CK>(lanes + 2 * NT + col(j), x);
+#pragma unroll
+                  for (int i = 0; i < CK; ++i) {
+                    const float f = st->factor[col(j) + i];
+                    x[i] *= f;
+                    l[j][i] *= f;
+                  }
+                  tm_store<CK>(lanes + 2 * NT + col(j), x);
                 }
-                tm_store<S::kChunk>(lanes + 2 * NT + col(j), x);
-              }
-            tm_wait_store();
-          }
-        }
-        // the last product must have read P before it is written again
-        if (!o_done) mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < S::kChunks; ++j)
-          if (col(j) < rows) {
-            float x[S::kChunk];
-            tm_load<S::kChunk>(s_col + col(j), x);
-            uint32_t w[S::kChunk / 2];
-#pragma unroll
-            for (int i = 0; i < S::kChunk; ++i) {
-              float p = exp2_approx(fmaf(x[i], c, -st->base[col(j) + i]));
-              if (masked && !sees(col(j) + i)) p = 0.0f;
-              x[i] = p;
-              l[j][i] += p;
+              tm_wait_store();
             }
-            // the weights' rounding: bf16 to go with a bf16 cache (2^-9 of each), fp16 with an E4M3 one
+            if constexpr (S::kKeep) {
 #pragma unroll
-            for (int i = 0; i < S::kChunk / 2; ++i) {
-              if constexpr (F8) {
-                const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t*>(&h);
-              } else {
-                w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-              }
+              for (int j = 0; j < S::kChunks; ++j)
+                if (col(j) < rows) scores(j, z[j]);
             }
-            char* row = p_buf + (col(j) / 64) * (kTileSlots * 128) + key * 128;
-#pragma unroll
-            for (int i = 0; i < S::kChunk / 8; ++i)
-              *reinterpret_cast<uint4*>(row + ((((col(j) % 64) + i * 8) * 2) ^ ((key & 7) * 16))) =
-                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
           }
-        tc_fence_before();
-        if constexpr (!F8) {
-          if (masked) {
+          // the last product must have read P before it is written again
+          if (!o_done) mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < S::kChunks; ++j)
+            if (col(j) < rows) {
+              auto& x = take(j);
+              if constexpr (!S::kKeep) scores(j, x);
+              uint32_t w[CK / 2];
+#pragma unroll
+              for (int i = 0; i < CK; i += 2) {
+                float2 p = make_float2(exp2_approx(x[i]), exp2_approx(x[i + 1]));
+                if (!sees(j, i)) p.x = 0.0f;
+                if (!sees(j, i + 1)) p.y = 0.0f;
+                const float2 sum = add2(make_float2(l[j][i], l[j][i + 1]), p);
+                l[j][i] = sum.x, l[j][i + 1] = sum.y;
+                // the weights' rounding: bf16 to go with a bf16 cache (2^-8 of each at most), fp16 with E4M3
+                if constexpr (F8) {
+                  const __half2 h = __floats2half2_rn(p.x, p.y);
+                  w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                  w[i / 2] = pack_bf16(p.x, p.y);
+                }
+              }
+              char* row = p_buf + (col(j) / 64) * (kTileSlots * 128) + key * 128;
+#pragma unroll
+              for (int i = 0; i < CK / 8; ++i)
+                *reinterpret_cast<uint4*>(row + ((((col(j) % 64) + i * 8) * 2) ^ ((key & 7) * 16))) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
+          tc_fence_before();
+          if constexpr (!F8 && MASKED) {
             // V's slots past the end are zeroed: their weights are 0, but 0 times what they hold may not
             // be.  New tokens' values that are not finite are taken out here and added at the end to the
             // rows that attend to them.
@@ -777,6 +850,12 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
               }
             }
           }
+        };
+        if ((tile + 1) * kTileSlots > s.ctx)
+          weigh(std::true_type{});
+        else
+          weigh(std::false_type{});
+        if constexpr (!F8) {
           v_slot += 2;
           if (v_slot >= S::kSlots) v_slot -= S::kSlots, v_phase ^= 1;
         }
@@ -792,40 +871,39 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
 #pragma unroll
       for (int j = 0; j < S::kChunks; ++j)
         if (col(j) < rows) {
-          const float sum = fold_lanes<S::kChunk>(l[j], lane, [](float a, float b) { return a + b; });
-          if (lane < S::kChunk) st->red[quad][col(j) + lane] = sum;
+          const float sum = fold_lanes<CK>(l[j], lane, [](float a, float b) { return a + b; });
+          if (lane < CK) st->red[quad][col(j) + lane] = sum;
         }
-      mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
-      __syncwarp();
-      tc_fence_after();
       group_sync(bar);
       const bool whole = s.tile0 == 0 && s.tile1 == s.tiles;
       // parts: slot 0 for an item that an earlier CTA began, slot 1 for one that a later one ends
       const int64_t part_row = ((int64_t)blockIdx.x * 2 + (s.tile0 == 0)) * P.rows;
-      if (wtid < NT / 2 && my_row < rows) {
-        const float sum = st->red[0][my_row] + st->red[1][my_row] + st->red[2][my_row] + st->red[3][my_row];
-        if (whole) {
-          const float v = F8 && P.cache.v_scale ? __ldg(P.cache.v_scale + s.head) : 1.0f;
-          st->factor[my_row] = sum == 0.0f ? 0.0f : v / sum;
-        } else {
-          P.part_ml[part_row + my_row] = make_float2(st->top[my_row], sum);
+      if (wtid < NT / 2) {
+        float f = 0.0f;
+        if (my_row < rows) {
+          const float sum = st->red[0][my_row] + st->red[1][my_row] + st->red[2][my_row] + st->red[3][my_row];
+          f = sum == 0.0f ? 0.0f : v_scale / sum;
+          if (!whole) P.part_ml[part_row + my_row] = make_float2(st->top[my_row], sum);
         }
+        st->factor[my_row] = f;
       }
+      mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
+      __syncwarp();
+      tc_fence_after();
       group_sync(bar);
       const bool bad = st->bad_value[seg & 1] == (uint32_t)seg + 1;
       const bool lost = *dead != 0;
-      char* out = P.out.data + s.b * P.out.row + (int64_t)t0 * P.out.token + (int64_t)s.head * P.group * P.out.head;
+      char* out = P.out.data + s.b * P.out.row + (int64_t)t0 * P.out.token + (int64_t)s.head * P.group * P.out.head + key * 2;
+      float* part = P.part + part_row * D + key;
       const int rows_all = min(P.rows, (P.batch.T - t0) * P.group);
-#pragma unroll 1
+#pragma unroll
       for (int j = 0; j < S::kChunks; ++j) {
         const int n0 = col(j);
         if (n0 >= rows_all) continue;
-        float x[S::kChunk];
+        float x[CK];
 #pragma unroll
-        for (int i = 0; i < S::kChunk; ++i) x[i] = 0.0f;
-        if (n0 < rows) {
-          tm_load<S::kChunk>(lanes + 2 * NT + n0, x);
-        }
+        for (int i = 0; i < CK; ++i) x[i] = 0.0f;
+        if (n0 < rows) tm_load<CK>(lanes + 2 * NT + n0, x);
         if (key >= D) continue;
         if (bad) {  // values that are not finite: each row takes those of the tokens it attends to
           for (int i = max(s.tile0 * kTileSlots - s.ctx, 0); s.ctx + i < min(s.tile1 * kTileSlots, s.end); ++i) {
@@ -837,23 +915,28 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
             const float v = F8 ? ((*reinterpret_cast<const uint8_t*>(p) & 0x7F) == 0x7F ? NAN : 0.0f)
                                : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
             if (isfinite(v)) continue;
+            const uint64_t see = st->seen[wg][i];
 #pragma unroll
-            for (int n = 0; n < S::kChunk; ++n)
-              if ((st->rule[n0 + n] >> i) & 1) x[n] += v;
+            for (int n = 0; n < CK; ++n)
+              if ((see >> (j * CK + n)) & 1) x[n] += v;
           }
         }
+        if (lost) {
 #pragma unroll
-        for (int i = 0; i < S::kChunk; ++i) {
-          const int n = n0 + i;
-          if (n >= rows_all) break;
-          float o = lost ? NAN : x[i];
-          if (whole) {
-            o = n < rows ? o * st->factor[n] : lost ? o : 0.0f;
-            reinterpret_cast<__nv_bfloat16*>(out + (n / P.group) * P.out.token + (n % P.group) * P.out.head)[key] =
-                __float2bfloat16(o);
-          } else if (n < rows) {
-            P.part[(part_row + n) * D + key] = o;
-          }
+          for (int i = 0; i < CK; ++i) x[i] = NAN;
+        }
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < CK; ++i)
+            if (n0 + i < rows_all) {
+              // rows past the request's tokens are 0 (their products may hold anything)
+              const float o = n0 + i < rows || lost ? x[i] * (lost ? 1.0f : st->factor[n0 + i]) : 0.0f;
+              *reinterpret_cast<__nv_bfloat16*>(out + st->place[n0 + i]) = __float2bfloat16(o);
+            }
+        } else {
+#pragma unroll
+          for (int i = 0; i < CK; ++i)
+            if (n0 + i < rows) part[(n0 + i) * D] = x[i];
         }
       }
       tc_fence_before();
@@ -1007,6 +1090,12 @@ static cudaError_t launch_attention(const AttnParams& P, int ctas, cudaStream_t 
   auto kern = attn_kernel<D, F8, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
+  if constexpr (S::kSplit) {  // the split must not ask for more than the launch gets: the kernel would wait for it
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < S::kLaunchRegs) return cudaErrorInvalidConfiguration;
+  }
   kern<<<ctas, S::kThreads, S::kBytes, st>>>(P);
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
