@@ -129,7 +129,7 @@ size_t spec_paged_attention_workspace_bytes(int32_t B, int32_t T, int32_t q_head
  * Slots that a row does not attend to have no part in it, whatever they hold (NaN and infinities
  * among them).  A page outside the pool reads as zeros; slots past the page table are dropped.
  * Scores, weights and sums are fp32; the weights are rounded (bf16 for a bf16 cache, fp16 for E4M3)
- * where they multiply V.  With an E4M3 cache q is taken in fp16: |q| must be below 65504.
+ * where they multiply V.  With an E4M3 cache a query row that holds an infinity gives NaN.
  * The workspace (256-byte aligned) holds per-call scratch, needs no initialisation and must not be
  * used by two calls that may run at the same time.
  */

@@ -77,6 +77,18 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return done != 0;
 }
 
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {  // does not suspend
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Waits for the phase with a limit; a wait that runs out marks the block dead, which ends every other
 // wait in it soon after.  Nothing here waits on another block.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
@@ -108,13 +120,23 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+// kind::f16 (fp16 or bf16 operands) or kind::f8f6f4 (E4M3)
+template <bool F8>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
-      : "memory");
+  if constexpr (F8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
 }
 
 // A load from TMEM and the wait for it, in one statement: nothing can use the registers in between.
@@ -197,18 +219,20 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-// Shared-memory matrix descriptors: 128-byte swizzle, strides in bytes.  Along a swizzled row of 128 bytes
-// lies the reduction (Q and K) or the free dimension (V^T and P^T, "transposed" in the instruction).
+// Shared-memory matrix descriptors: 128-byte swizzle (or 64-byte: E4M3 rows of 64), strides in bytes.  Along
+// a swizzled row lies the reduction (Q and K) or the free dimension (V^T and P^T, "transposed" in the
+// instruction).
+template <int ROW = 128>
 __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
   return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
-         1ull << 46 | 2ull << 61;
+         1ull << 46 | (ROW == 128 ? 2ull : 4ull) << 61;
 }
 
 // ------------------------------------------------------------------------------------------------
 // the line of tiles
 // ------------------------------------------------------------------------------------------------
 struct Segment {
-  int b, head, row_group, index;  // index = head * row_groups + row group
+  int b, head, row_group;
   int tile0, tile1, tiles;        // this part of the item's tiles
   int ctx, tokens, end;           // context, valid new tokens, end of the slots
 };
@@ -223,17 +247,19 @@ __device__ __forceinline__ int line_cut(int total, int c, int ctas) { return (in
 // Every role of a CTA walks the same part of the line by itself.
 struct Walk {
   const AttnParams& P;
-  int b, index, tile, left;
+  int b, head, row_group, tile, left;
   int ctx, tokens, next_ctx, next_tokens;
 
   __device__ Walk(const AttnParams& p, int b0, int offset, int count) : P(p), b(b0), left(count) {
-    index = tile = ctx = tokens = next_ctx = next_tokens = 0;
+    head = row_group = tile = ctx = tokens = next_ctx = next_tokens = 0;
     if (left <= 0) return;
     ctx = batch_context(P.batch, b);
     tokens = batch_tokens(P.batch, b);
     const int n = request_tiles(request_end(ctx, tokens, P.batch.slots));
-    index = offset / n;
-    tile = offset % n;
+    const int index = offset / n;
+    tile = offset - index * n;
+    head = index / P.row_groups;
+    row_group = index - head * P.row_groups;
     prefetch();
   }
   __device__ void prefetch() {
@@ -244,8 +270,7 @@ struct Walk {
   }
   __device__ bool next(Segment& s) {
     if (left <= 0) return false;
-    s.b = b, s.index = index;
-    s.head = index / P.row_groups, s.row_group = index % P.row_groups;
+    s.b = b, s.head = head, s.row_group = row_group;
     s.ctx = ctx, s.tokens = tokens, s.end = request_end(ctx, tokens, P.batch.slots);
     s.tiles = request_tiles(s.end);
     const int n = min(s.tiles - tile, left);
@@ -254,8 +279,9 @@ struct Walk {
     tile += n;
     if (tile == s.tiles) {
       tile = 0;
-      if (++index == P.heads * P.row_groups) {
-        index = 0;
+      if (++row_group == P.row_groups) row_group = 0, ++head;
+      if (head == P.heads) {
+        head = 0;
         ++b;
         ctx = next_ctx, tokens = next_tokens;
         prefetch();
@@ -276,15 +302,15 @@ struct Shape {
   static constexpr int kQ = NT * D * 2;                           // a Q buffer
   static constexpr int kQBufs = NT > 64 ? 1 : 2;                  // two, where the ring stays deep enough
   static constexpr int kP = kTileSlots * 128 * (NT > 64 ? 2 : 1); // P^T, 128 bytes a slot and 64 rows
-  static constexpr int kFixed = kQBufs * kQ + kP + (F8 ? 2 * kTile16 : 0);
+  static constexpr int kFixed = kQBufs * kQ + kP + (F8 ? kTile16 : 0);
   static constexpr int kBudget = 232448 - 1024 - 6144;            // 227 KB, alignment, barriers and row states
   static constexpr int kFit = (kBudget - kFixed) / kRing;
-  static constexpr int kSlots = kFit > 8 ? 8 : kFit;              // K and V tiles in flight
+  static constexpr int kSlots = kFit > 8 ? 8 : F8 ? kFit / 2 * 2 : kFit;  // K and V tiles in flight (E4M3: V in odd slots)
   static_assert(kSlots >= 4, "the ring holds two tiles of K and V at least");
   // Registers: the variants with many columns take more for the softmax warps than an even split of the
   // SM's gives them, and less for the others.  Per warpgroup of 128 threads, of 512 in all:
   // 3 x 168 = 504 = 2 x 208 + 88, and 4 x 128 = 512 = 2 x 176 + 2 x 80.
-  static constexpr bool kSplit = NT > 64 || (F8 && NT > 32);
+  static constexpr bool kSplit = NT > 32 || (F8 && NT > 16);
   static constexpr int kThreads = F8 ? 512 : 384;
   static constexpr int kLaunchRegs = F8 ? 128 : 168, kMoreRegs = F8 ? 176 : 208, kFewRegs = F8 ? 80 : 88;
   static_assert(2 * kMoreRegs + (kThreads / 128 - 2) * kFewRegs <= kThreads / 128 * kLaunchRegs, "register split");
@@ -296,8 +322,8 @@ struct Shape {
 
   struct State {
     uint64_t ring_full[8], ring_empty[8];
-    uint64_t q_loaded[2], q_full[2], q_empty[2];
-    uint64_t k16_full, k16_empty, v16_full, v16_empty;
+    uint64_t q_loaded[2], q_full[2], q_empty[2], mult_full[2];
+    uint64_t v16_full, v16_empty;
     uint64_t s_full[2], s_empty[2], p_full, o_full;
     uint32_t tmem;
     int dead;
@@ -308,13 +334,28 @@ struct Shape {
     alignas(16) float top[NT];       // the maximum in use, -inf for none
     alignas(16) float factor[NT];    // a rescale's factor; 1 / l at the end
     float red[4][NT];
-    int64_t place[NT];               // the row's offset in the item's output
+    alignas(16) float mult[2][NT];   // E4M3: a score's factor to log2 units, by the segment's parity
+    alignas(16) int64_t place[NT];   // the row's offset in the item's output
     uint64_t seen[2][SPEC_MAX_NEW];  // which columns of each warpgroup attend to a new token
   };
   static constexpr int kState = kFixed + kSlots * kRing;
   static constexpr int kBytes = kState + (int)sizeof(State) + 1024;
   static_assert(kBytes <= 232448, "shared memory");
 };
+
+// Four E4M3 codes as fp16 pairs, exactly.
+__device__ __forceinline__ void e4m3_to_half(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+__device__ __forceinline__ float4 unpack_e4m3(uint32_t x) {
+  uint32_t lo, hi;
+  e4m3_to_half(x, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
 
 // Over the 32 lanes, `op` of every one of N values: lane l ends with that of value l % N.
 template <int N, typename Op>
@@ -344,8 +385,8 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
   char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
   char* q_buf = smem;                                     // [kQBufs][halves][NT][128 B]
   char* p_buf = q_buf + S::kQBufs * S::kQ;                     // [NT > 64 ? 2 : 1][128][128 B]
-  char* t16 = p_buf + S::kP;                              // E4M3: K, V in fp16, [halves][128][128 B] each
-  char* ring = t16 + (F8 ? 2 * S::kTile16 : 0);
+  char* v16 = p_buf + S::kP;                              // E4M3: V in fp16, [halves][128][128 B]
+  char* ring = v16 + (F8 ? S::kTile16 : 0);
   auto* st = reinterpret_cast<typename S::State*>(smem + S::kState);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kProducer = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1;
@@ -370,20 +411,18 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
   if (threadIdx.x == 0) {
     st->dead = 0;
     st->bad_value[0] = st->bad_value[1] = 0;
-    const uint32_t full_count = 1;
     for (int i = 0; i < S::kSlots; ++i) {
-      mbar_init(smem_addr(&st->ring_full[i]), full_count);
-      mbar_init(smem_addr(&st->ring_empty[i]), F8 ? kConvertWarps : 1);
+      mbar_init(smem_addr(&st->ring_full[i]), 1);
+      mbar_init(smem_addr(&st->ring_empty[i]), F8 && i % 2 ? kConvertWarps : 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&st->q_loaded[i]), 1);
       mbar_init(smem_addr(&st->q_full[i]), kConvertWarps);
+      mbar_init(smem_addr(&st->mult_full[i]), kConvertWarps);
       mbar_init(smem_addr(&st->q_empty[i]), 1);
       mbar_init(smem_addr(&st->s_full[i]), 1);
       mbar_init(smem_addr(&st->s_empty[i]), kSoftmaxWarps);
     }
-    mbar_init(smem_addr(&st->k16_full), kConvertWarps);
-    mbar_init(smem_addr(&st->k16_empty), 1);
     mbar_init(smem_addr(&st->v16_full), kConvertWarps);
     mbar_init(smem_addr(&st->v16_empty), 1);
     mbar_init(smem_addr(&st->p_full), kSoftmaxWarps);
@@ -483,167 +522,198 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
           }
         }
     } else if (warp == kIssuer) {
-      // ---- matrix products ----
+      // ---- matrix products: scores of the next tile or weighted values of an earlier one, as either is ready ----
       if (lane == 0) {
         const uint32_t n16 = (P.rows + 15) / 16 * 16;
-        const uint32_t fmt = F8 ? 0u : 1u;  // fp16 or bf16 operands, fp32 accumulators, M = 128
-        const uint32_t idesc = 1u << 4 | fmt << 7 | fmt << 10 | (n16 >> 3) << 17 | (128u >> 4) << 24;
-        const uint32_t idesc_t = idesc | 1u << 15 | 1u << 16;  // both operands with the reduction outside
+        const uint32_t shape = 1u << 4 | (n16 >> 3) << 17 | (128u >> 4) << 24;  // fp32 accumulators, M = 128
+        const uint32_t s_desc = shape | (F8 ? 0u : 1u << 7 | 1u << 10);         // E4M3 or bf16 operands
+        // fp16 or bf16 operands, both with the reduction outside
+        const uint32_t o_desc = shape | (F8 ? 0u : 1u << 7 | 1u << 10) | 1u << 15 | 1u << 16;
         const uint32_t o_col = tmem + 2 * NT;
-        uint32_t it = 0;       // tiles so far
-        int k_slot = 0, v_slot = 0;
-        uint32_t k_phase = 0, v_phase = 0;
-        bool ok = true, o_any = false;
-        const auto advance = [&](int& slot, uint32_t& phase, int by) {
-          slot += by;
+        const uint32_t p_addr = smem_addr(p_buf);
+        uint32_t s_it = 0, v_it = 0;  // tiles whose scores, and whose values, are issued
+        int k_slot = 0, v_slot = 1;
+        uint32_t k_phase = 0, v_phase = 0, first_bits = 0;
+        const auto advance = [&](int& slot, uint32_t& phase) {
+          slot += 2;
           if (slot >= S::kSlots) slot -= S::kSlots, phase ^= 1;
         };
-        advance(v_slot, v_phase, 1);
-
-        const auto scores = [&](int qb, uint32_t q_phase, bool first, bool last) {
-          if (first) ok = ok && mbar_wait(smem_addr(F8 ? &st->q_full[qb] : &st->q_loaded[qb]), q_phase, dead);
-          const int sb = it & 1;
-          ok = ok && mbar_wait(smem_addr(&st->s_empty[sb]), ((it >> 1) & 1) ^ 1, dead);
-          ok = ok && (F8 ? mbar_wait(smem_addr(&st->k16_full), it & 1, dead)
-                         : mbar_wait(smem_addr(&st->ring_full[k_slot]), k_phase, dead));
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t a = smem_addr(F8 ? t16 : ring + k_slot * S::kRing), b = smem_addr(q_buf + qb * S::kQ);
-  #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const int half = k / 4, in = (k % 4) * 32;
-            tc_mma(tmem + sb * NT, matrix_desc(a + half * (kTileSlots * 128) + in, 16, 1024),
-                   matrix_desc(b + half * (NT * 128) + in, 16, 1024), idesc, k > 0);
+        int seg = 0, tile = 0, idle = 0;
+        bool more = walk.next(s);
+        tile = s.tile0;
+        while (more || v_it < s_it) {
+          bool moved = false;
+          if (more && s_it - v_it < 2) {
+            const int qb = seg % S::kQBufs, sb = s_it & 1;
+            if (mbar_test(smem_addr(&st->ring_full[k_slot]), k_phase) &&
+                (tile != s.tile0 || mbar_test(smem_addr(F8 ? &st->q_full[qb] : &st->q_loaded[qb]), (seg / S::kQBufs) & 1)) &&
+                mbar_test(smem_addr(&st->s_empty[sb]), ((s_it >> 1) & 1) ^ 1)) {
+              tc_fence_after();
+              const uint32_t a = smem_addr(ring + k_slot * S::kRing), b = smem_addr(q_buf + qb * S::kQ);
+              if constexpr (F8) {
+                // q = (its 4 upper bits) + (the others), each in E4M3: see the split below
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                  const int part = k / (D / 32), in = (k % (D / 32)) * 32;
+                  tc_mma<true>(tmem + sb * NT, matrix_desc<D>(a + in, 16, 8 * D),
+                               matrix_desc(b + part * (D == 128 ? NT * 128 : 64) + in, 16, 1024), s_desc, k > 0);
+                }
+              } else {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                  const int half = k / 4, in = (k % 4) * 32;
+                  tc_mma<false>(tmem + sb * NT, matrix_desc(a + half * (kTileSlots * 128) + in, 16, 1024),
+                                matrix_desc(b + half * (NT * 128) + in, 16, 1024), s_desc, k > 0);
+                }
+              }
+              tc_commit(smem_addr(&st->ring_empty[k_slot]));
+              tc_commit(smem_addr(&st->s_full[sb]));
+              advance(k_slot, k_phase);
+              first_bits = (first_bits & ~(1u << sb)) | (uint32_t)(tile == s.tile0) << sb;
+              ++s_it;
+              if (++tile == s.tile1) {
+                tc_commit(smem_addr(&st->q_empty[qb]));
+                ++seg;
+                more = walk.next(s);
+                tile = s.tile0;
+              }
+              moved = true;
+            }
           }
-          tc_commit(smem_addr(F8 ? &st->k16_empty : &st->ring_empty[k_slot]));
-          tc_commit(smem_addr(&st->s_full[sb]));
-          if (last) tc_commit(smem_addr(&st->q_empty[qb]));
-          advance(k_slot, k_phase, 2);
-        };
-        const auto values = [&](uint32_t i, bool first) {  // tile i, one behind the scores
-          ok = ok && (F8 ? mbar_wait(smem_addr(&st->v16_full), i & 1, dead)
-                         : mbar_wait(smem_addr(&st->ring_full[v_slot]), v_phase, dead));
-          ok = ok && mbar_wait(smem_addr(&st->p_full), i & 1, dead);
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t a = smem_addr(F8 ? t16 + S::kTile16 : ring + v_slot * S::kRing), b = smem_addr(p_buf);
-          // head_dim 64: the instruction's rows 64..127 repeat rows 0..63 and are not read
-          const uint32_t lead = D == 128 ? kTileSlots * 128 : 0;
-  #pragma unroll
-          for (int k = 0; k < kTileSlots / 16; ++k)
-            tc_mma(o_col, matrix_desc(a + k * 2048, lead, 1024), matrix_desc(b + k * 2048, kTileSlots * 128, 1024), idesc_t,
-                   !first || k > 0);
-          tc_commit(smem_addr(F8 ? &st->v16_empty : &st->ring_empty[v_slot]));
-          tc_commit(smem_addr(&st->o_full));
-          advance(v_slot, v_phase, 2);
-          o_any = true;
-        };
-        bool first_behind = false;
-        for (int seg = 0; ok && walk.next(s); ++seg)
-          for (int tile = s.tile0; ok && tile < s.tile1; ++tile) {
-            scores(seg % S::kQBufs, (seg / S::kQBufs) & 1, tile == s.tile0, tile + 1 == s.tile1);
-            if (it > 0 && ok) values(it - 1, first_behind);
-            first_behind = tile == s.tile0;
-            ++it;
+          if (v_it < s_it && mbar_test(smem_addr(&st->p_full), v_it & 1) &&
+              (F8 ? mbar_test(smem_addr(&st->v16_full), v_it & 1) : mbar_test(smem_addr(&st->ring_full[v_slot]), v_phase))) {
+            tc_fence_after();
+            const bool first = (first_bits >> (v_it & 1)) & 1;
+            const uint32_t a = smem_addr(F8 ? v16 : ring + v_slot * S::kRing);
+            // head_dim 64: the instruction's rows 64..127 repeat rows 0..63 and are not read
+            const uint32_t lead = D == 128 ? kTileSlots * 128 : 0;
+#pragma unroll
+            for (int k = 0; k < kTileSlots / 16; ++k)
+              tc_mma<false>(o_col, matrix_desc(a + k * 2048, lead, 1024), matrix_desc(p_addr + k * 2048, kTileSlots * 128, 1024),
+                            o_desc, !first || k > 0);
+            tc_commit(smem_addr(F8 ? &st->v16_empty : &st->ring_empty[v_slot]));
+            tc_commit(smem_addr(&st->o_full));
+            advance(v_slot, v_phase);
+            ++v_it;
+            moved = true;
           }
-        if (ok && it > 0) values(it - 1, first_behind);
-        if (!ok && o_any)  // a wait ran out: let the products in flight end before TMEM is freed
+          if (moved) {
+            idle = 0;
+          } else if (++idle > (1 << 24) || ((idle & 255) == 0 && *dead)) {
+            *dead = 1;
+            break;
+          }
+        }
+        if (*dead && s_it > 0)  // a wait ran out: let the products in flight end before TMEM is freed
           for (int n = 0; n < (1 << 16); ++n) __nanosleep(20);
       }
       __syncwarp();
     } else if (F8 && warp > kIssuer && warp <= kIssuer + kConvertWarps) {
-      // ---- E4M3 -> fp16 (exact), K and V into the swizzled layout that the matrix unit reads ----
+      // ---- E4M3 caches: Q split for the product with K as it is; V to fp16 (exact) for that with P ----
       const int tid = threadIdx.x - (kIssuer + 1) * 32;  // 0..127
-      int slot = 0;
+      int slot = 1;
       uint32_t phase = 0, it = 0;
       bool ok = true;
       for (int seg = 0; ok && walk.next(s); ++seg) {
         const int qb = seg % S::kQBufs;
         ok = mbar_wait_warp(smem_addr(&st->q_loaded[qb]), (seg / S::kQBufs) & 1, dead);
         if (!ok) break;
-        for (int i = tid; i < S::kQ / 16; i += kConvertWarps * 32) {  // q: bf16 -> fp16, in place
-          uint4* p = reinterpret_cast<uint4*>(q_buf + qb * S::kQ) + i;
-          uint4 w = *p;
-          uint32_t* u = reinterpret_cast<uint32_t*>(&w);
-  #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __half2 h = __floats2half2_rn(bf16_low(u[j]), bf16_high(u[j]));
-            u[j] = *reinterpret_cast<const uint32_t*>(&h);
+        // A row is scaled by a power of two to a largest element in [128, 256), and its 8-bit significands
+        // split into E4M3's 4 bits and a remainder of 4: exact but for elements under 2^-9 of the largest,
+        // which are off by 2^-17 of it at most (q's own rounding to bf16 is 2^-8 of each element).  The
+        // scale goes into the row's factor.  The split overwrites the row: no other row's lines.
+        constexpr int kLanes = D / 16;  // threads per row, 16 elements each
+        const float c = P.scale_log2 * (P.cache.k_scale ? __ldg(P.cache.k_scale + s.head) : 1.0f);
+        char* q = q_buf + qb * S::kQ;
+        const int i = tid % kLanes;
+#pragma unroll 1
+        for (int row = tid / kLanes; row < NT; row += kConvertWarps * 32 / kLanes) {
+          const int sw = row & 7;
+          const char* src = q + (i * 16 / 64) * (NT * 128) + row * 128;
+          const int v0 = (i * 16 % 64) / 8;
+          float x[16];
+          unpack8(*reinterpret_cast<const uint4*>(src + ((v0 ^ sw) * 16)), reinterpret_cast<float(&)[8]>(x[0]));
+          unpack8(*reinterpret_cast<const uint4*>(src + (((v0 + 1) ^ sw) * 16)), reinterpret_cast<float(&)[8]>(x[8]));
+          uint32_t top = 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+#pragma unroll
+          for (int d = 1; d < kLanes; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
+          const int up = min(134 - (int)(top >> 23), 127);  // 7 minus the largest element's exponent
+          const float scale = __uint_as_float((uint32_t)(up + 127) << 23);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[e + k] *= scale;
+            hi[e / 4] = pack_e4m3(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            const float4 u = unpack_e4m3(hi[e / 4]);
+            lo[e / 4] = pack_e4m3(x[e] - u.x, x[e + 1] - u.y, x[e + 2] - u.z, x[e + 3] - u.w);
           }
-          *p = w;
+          __syncwarp();  // the row is read
+          *reinterpret_cast<uint4*>(q + row * 128 + ((i ^ sw) * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          char* rest = D == 128 ? q + NT * 128 + row * 128 + ((i ^ sw) * 16) : q + row * 128 + (((i + 4) ^ sw) * 16);
+          *reinterpret_cast<uint4*>(rest) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if (i == 0) st->mult[seg & 1][row] = top >= 0x7F800000u ? NAN : ldexpf(c, -up);  // infinite or NaN: the row is NaN
         }
         fence_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&st->q_full[qb]));
+        if (lane == 0) {
+          mbar_arrive(smem_addr(&st->q_full[qb]));
+          mbar_arrive(smem_addr(&st->mult_full[seg & 1]));
+        }
+
         for (int tile = s.tile0; ok && tile < s.tile1; ++tile, ++it) {
-  #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            ok = ok && mbar_wait_warp(smem_addr(&st->ring_full[slot]), phase, dead);
-            ok = ok && mbar_wait_warp(smem_addr(kv ? &st->v16_empty : &st->k16_empty), (it & 1) ^ 1, dead);
-            if (!ok) break;
-            char* src = ring + slot * S::kRing;
-            char* dst = t16 + kv * S::kTile16;
-            constexpr int kUnits = D / 16;
-            if (kv && (tile + 1) * kTileSlots > s.ctx) {
-              // V's slots past the end are zeroed: their weights are 0, but 0 times what they hold may not be.
-              // New tokens' values that are not finite are taken out here and added at the end to the rows
-              // that attend to them.  Every thread mends the units that it converts.
-              const int from = max(s.ctx - tile * kTileSlots, 0), end = s.end - tile * kTileSlots;
-              for (int u = tid; u < kTileSlots * kUnits; u += 128) {
-                const int row = u / kUnits;
-                if (row < from) continue;
-                uint4* p = reinterpret_cast<uint4*>(src + u * 16);
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (row < end) {
-                  w = *p;
-                  uint32_t* x = reinterpret_cast<uint32_t*>(&w);
-                  bool bad = false;
-  #pragma unroll
-                  for (int j = 0; j < 4; ++j) {  // the code 0x7F of either sign is NaN
-                    const uint32_t nan = __vcmpeq4(x[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-                    bad |= nan != 0;
-                    x[j] &= ~nan;
-                  }
-                  if (bad) st->bad_value[seg & 1] = seg + 1;
-                }
-                *p = w;
+          ok = ok && mbar_wait_warp(smem_addr(&st->ring_full[slot]), phase, dead);
+          ok = ok && mbar_wait_warp(smem_addr(&st->v16_empty), (it & 1) ^ 1, dead);
+          if (!ok) break;
+          // a slot per thread: its vectors lie in different banks from its neighbours' by the swizzle, in the
+          // ring and in fp16
+          const int row = tid;
+          const char* src = ring + slot * S::kRing + row * D;
+          const int sw = D == 128 ? row & 7 : (row >> 1) & 3;
+          uint4 raw[D / 16];
+#pragma unroll
+          for (int v = 0; v < D / 16; ++v) raw[v] = *reinterpret_cast<const uint4*>(src + ((v ^ sw) * 16));
+          const int at = tile * kTileSlots + row;
+          if (at >= s.ctx) {
+            // Slots past the end are zeroed: their weights are 0, but 0 times what they hold may not be.  New
+            // tokens' values that are not finite are taken out here and added at the end to the rows that
+            // attend to them.
+            bool bad = false;
+#pragma unroll
+            for (int v = 0; v < D / 16; ++v) {
+              uint32_t* x = reinterpret_cast<uint32_t*>(&raw[v]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {  // the code 0x7F of either sign is NaN
+                const uint32_t nan = __vcmpeq4(x[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                bad |= nan != 0;
+                x[j] = at < s.end ? x[j] & ~nan : 0u;
               }
             }
-            constexpr int kEach = kTileSlots * kUnits / 128;
-            uint4 raw[kEach];
-  #pragma unroll
-            for (int i = 0; i < kEach; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + (i * 128 + tid) * 16);
-            // a thread's units are 128 / kUnits rows apart: the same vector of the row and the same swizzle
-            const int row0 = tid / kUnits, c = tid % kUnits;
-            char* out = dst + (c / 4) * (kTileSlots * 128) + row0 * 128;
-            const int sw = (row0 & 7) * 16, j0 = (c % 4) * 32;
-            // the two halves of a row start at the same banks: one of them stores its second vector first
-            const bool turn = c >= 4;
-            char* out0 = out + ((j0 + (turn ? 16 : 0)) ^ sw);
-            char* out1 = out + ((j0 + (turn ? 0 : 16)) ^ sw);
-  #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-              const uint32_t* x = reinterpret_cast<const uint32_t*>(&raw[i]);
-              uint32_t h[8];
-  #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-                    "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-                    : "=r"(h[2 * j]), "=r"(h[2 * j + 1])
-                    : "r"(x[j]));
-              }
-              const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-              *reinterpret_cast<uint4*>(out0 + i * (128 / kUnits) * 128) = turn ? hi : lo;
-              *reinterpret_cast<uint4*>(out1 + i * (128 / kUnits) * 128) = turn ? lo : hi;
-            }
-            fence_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(smem_addr(kv ? &st->v16_full : &st->k16_full));
-              mbar_arrive(smem_addr(&st->ring_empty[slot]));
-            }
-            if (++slot == S::kSlots) slot = 0, phase ^= 1;
+            if (bad && at < s.end) st->bad_value[seg & 1] = seg + 1;
           }
+          char* out = v16 + row * 128;
+          const int sw16 = row & 7;
+#pragma unroll
+          for (int v = 0; v < D / 16; ++v) {
+            const uint32_t* x = reinterpret_cast<const uint32_t*>(&raw[v]);
+            uint32_t h[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e4m3_to_half(x[j], h[2 * j], h[2 * j + 1]);
+            char* o = out + (v / 4) * (kTileSlots * 128);
+            const int j0 = (v % 4) * 2;
+            *reinterpret_cast<uint4*>(o + ((j0 ^ sw16) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(o + (((j0 + 1) ^ sw16) * 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_addr(&st->v16_full));
+            mbar_arrive(smem_addr(&st->ring_empty[slot]));
+          }
+          slot += 2;
+          if (slot >= S::kSlots) slot -= S::kSlots, phase ^= 1;
         }
       }
     }
@@ -658,6 +728,16 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
     constexpr int CK = S::kChunk;
     const auto row_of = [&](int own) { return ((own / CK) * 2 + wg) * CK + own % CK; };  // of the warpgroup's columns
     const int my_row = row_of(wtid);  // wtid < NT / 2
+    if (wtid < NT / 2) {
+      const int t = my_row / P.group, g = my_row - t * P.group;
+      st->place[my_row] = (int64_t)t * P.out.token + (int64_t)g * P.out.head;
+    }
+    int rule_row[S::kWords], rule_token[S::kWords];  // this lane's columns and their tokens, for the ballots
+#pragma unroll
+    for (int w = 0; w < S::kWords; ++w) {
+      rule_row[w] = w * 32 + lane < NT / 2 ? row_of(w * 32 + lane) : kMaxRows;
+      rule_token[w] = rule_row[w] / P.group;
+    }
     float l[S::kChunks][CK];
     uint32_t it = 0;
     int v_slot = 1;
@@ -667,24 +747,21 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
     for (int seg = 0; walk.next(s); ++seg) {
       const int t0 = s.row_group * P.tokens;
       const int rows = min(max((s.tokens - t0) * P.group, 0), P.rows);  // valid ones come first
-      float c = P.scale_log2, v_scale = 1.0f;
-      if (F8 && P.cache.k_scale) c *= __ldg(P.cache.k_scale + s.head);
-      if (F8 && P.cache.v_scale) v_scale = __ldg(P.cache.v_scale + s.head);
+      const float c = P.scale_log2;
+      const float* mult = st->mult[seg & 1];
+      const float v_scale = F8 && P.cache.v_scale ? __ldg(P.cache.v_scale + s.head) : 1.0f;
       group_sync(bar);  // the last segment's row states are read
       if (wtid < NT / 2) {
         st->top[my_row] = -INFINITY;
         st->shift[my_row] = my_row < rows ? kNone : -INFINITY;  // rows that are none: weights 0, and no vote
-        const int t = my_row / P.group, g = my_row - t * P.group;
-        st->place[my_row] = (int64_t)t * P.out.token + (int64_t)g * P.out.head;
       }
       if (s.tile1 * kTileSlots > s.ctx) {  // new tokens among the slots: who attends to which
         uint64_t rule[S::kWords];
 #pragma unroll
         for (int w = 0; w < S::kWords; ++w) {
-          const int n = row_of(w * 32 + lane);
-          const int t = t0 + n / P.group;
+          const int t = t0 + rule_token[w];
           rule[w] = 0;
-          if (w * 32 + lane < NT / 2 && n < rows)
+          if (rule_row[w] < rows)
             rule[w] = P.mask ? (uint64_t)__ldg(P.mask + (int64_t)s.b * P.batch.T + t) : t >= 63 ? ~0ull : (2ull << t) - 1;
         }
         for (int i = quad; i < s.tokens; i += 4) {
@@ -693,6 +770,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
           if (lane == 0) st->seen[wg][i] = lo | (uint64_t)hi << 32;
         }
       }
+      if constexpr (F8) mbar_wait(smem_addr(&st->mult_full[seg & 1]), (seg >> 1) & 1, dead);
       group_sync(bar);
 #pragma unroll
       for (int j = 0; j < S::kChunks; ++j)
@@ -719,8 +797,9 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
 #pragma unroll
             for (int i = 0; i < CK; i += 4) {
               const float4 m = *reinterpret_cast<const float4*>(&st->shift[col(j) + i]);
-              const float2 a = fma2(make_float2(z[i], z[i + 1]), make_float2(c, c), make_float2(m.x, m.y));
-              const float2 b = fma2(make_float2(z[i + 2], z[i + 3]), make_float2(c, c), make_float2(m.z, m.w));
+              const float4 f = F8 ? *reinterpret_cast<const float4*>(&mult[col(j) + i]) : make_float4(c, c, c, c);
+              const float2 a = fma2(make_float2(z[i], z[i + 1]), make_float2(f.x, f.y), make_float2(m.x, m.y));
+              const float2 b = fma2(make_float2(z[i + 2], z[i + 3]), make_float2(f.z, f.w), make_float2(m.z, m.w));
               z[i] = a.x, z[i + 1] = a.y, z[i + 2] = b.x, z[i + 3] = b.y;
             }
           };
@@ -748,7 +827,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
                 float x[CK];
                 tm_load<CK>(s_col + col(j), x);
 #pragma unroll
-                for (int i = 0; i < CK; ++i) x[i] = sees(j, i) ? x[i] * c : -INFINITY;
+                for (int i = 0; i < CK; ++i) x[i] = sees(j, i) ? x[i] * (F8 ? mult[col(j) + i] : c) : -INFINITY;
                 const float m = fold_lanes<CK>(x, lane, [](float a, float b) { return fmaxf(a, b); });
                 if (lane < CK) st->red[quad][col(j) + lane] = m;
               }
@@ -926,13 +1005,18 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
           for (int i = 0; i < CK; ++i) x[i] = NAN;
         }
         if (whole) {
+          int64_t place[CK];
+#pragma unroll
+          for (int i = 0; i < CK; i += 2) {
+            const longlong2 w = *reinterpret_cast<const longlong2*>(&st->place[n0 + i]);
+            place[i] = w.x, place[i + 1] = w.y;
+          }
+#pragma unroll
+          for (int i = 0; i < CK; ++i)  // rows past the request's tokens are 0 (their products may hold anything)
+            x[i] = lost ? x[i] : n0 + i < rows ? x[i] * st->factor[n0 + i] : 0.0f;
 #pragma unroll
           for (int i = 0; i < CK; ++i)
-            if (n0 + i < rows_all) {
-              // rows past the request's tokens are 0 (their products may hold anything)
-              const float o = n0 + i < rows || lost ? x[i] * (lost ? 1.0f : st->factor[n0 + i]) : 0.0f;
-              *reinterpret_cast<__nv_bfloat16*>(out + st->place[n0 + i]) = __float2bfloat16(o);
-            }
+            if (n0 + i < rows_all) *reinterpret_cast<__nv_bfloat16*>(out + place[i]) = __float2bfloat16(x[i]);
         } else {
 #pragma unroll
           for (int i = 0; i < CK; ++i)
@@ -946,7 +1030,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
         if (begins || walk.left <= 0) {
           // the place of the item's end in the line: this CTA's end, and the tiles behind it
           const int end = first + count + (s.tiles - s.tile1);
-          P.cut[blockIdx.x] = begins ? make_int4(s.b, s.index, end, total) : make_int4(-1, 0, 0, 0);
+          P.cut[blockIdx.x] = begins ? make_int4(s.b, s.head * P.row_groups + s.row_group, end, total) : make_int4(-1, 0, 0, 0);
         }
       }
     }
@@ -1180,7 +1264,7 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
     ok = ok && encode(kv ? &P.v_map : &P.k_map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, es,
                       kv ? P.cache.v : P.cache.k, {D, cache->page_size, cache->heads, cache->num_pages},
                       {P.cache.slot, P.cache.head, P.cache.page}, {f8 ? D : 64, box, 1, 1},
-                      f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+                      f8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return SPEC_ERR_CUDA;
   int sms = 0;
   cudaError_t e = device_sms(&sms);
