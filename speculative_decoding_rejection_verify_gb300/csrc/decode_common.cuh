@@ -9,6 +9,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "spec_decode.h"
 
 namespace sv {
@@ -118,10 +120,18 @@ inline Batch batch_of(const spec_decode_batch_t* b, const spec_kv_cache_t* c) {
   return Batch{b->pages, b->ctx_len, b->t_per_row, b->B, b->T, b->max_pages, b->max_pages * c->page_size};
 }
 
-inline cudaError_t device_sms(int* sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+// The current device and its SMs (looked up once per device).
+constexpr int kMaxGpus = 64;
+inline cudaError_t device_sms(int* dev, int* sms) {
+  static std::atomic<int> known[kMaxGpus];
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  if (*dev < 0 || *dev >= kMaxGpus) return cudaErrorInvalidDevice;
+  *sms = known[*dev].load(std::memory_order_relaxed);
+  if (*sms == 0) {
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev);
+    if (e == cudaSuccess) known[*dev].store(*sms, std::memory_order_relaxed);
+  }
   return e;
 }
 

@@ -1169,16 +1169,21 @@ static bool encode(CUtensorMap* map, CUtensorMapDataType type, int es, void* dat
 }
 
 template <int D, bool F8, int NT>
-static cudaError_t launch_attention(const AttnParams& P, int ctas, cudaStream_t st) {
+static cudaError_t launch_attention(const AttnParams& P, int dev, int ctas, cudaStream_t st) {
   using S = Shape<D, F8, NT>;
   auto kern = attn_kernel<D, F8, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
-  if (e != cudaSuccess) return e;
-  if constexpr (S::kSplit) {  // the split must not ask for more than the launch gets: the kernel would wait for it
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kern);
+  static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory is set
+  cudaError_t e = cudaSuccess;
+  if (!((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs < S::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    if constexpr (S::kSplit) {  // the split must not ask for more than the launch gets: the kernel would wait for it
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kern);
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs < S::kLaunchRegs) return cudaErrorInvalidConfiguration;
+    }
+    ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   kern<<<ctas, S::kThreads, S::kBytes, st>>>(P);
   e = cudaGetLastError();
@@ -1196,11 +1201,11 @@ static cudaError_t launch_attention(const AttnParams& P, int ctas, cudaStream_t 
 }
 
 template <int D, bool F8>
-static cudaError_t launch_rows(const AttnParams& P, int ctas, cudaStream_t st) {
-  if (P.rows <= 16) return launch_attention<D, F8, 16>(P, ctas, st);
-  if (P.rows <= 32) return launch_attention<D, F8, 32>(P, ctas, st);
-  if (P.rows <= 64) return launch_attention<D, F8, 64>(P, ctas, st);
-  return launch_attention<D, F8, 128>(P, ctas, st);
+static cudaError_t launch_rows(const AttnParams& P, int dev, int ctas, cudaStream_t st) {
+  if (P.rows <= 16) return launch_attention<D, F8, 16>(P, dev, ctas, st);
+  if (P.rows <= 32) return launch_attention<D, F8, 32>(P, dev, ctas, st);
+  if (P.rows <= 64) return launch_attention<D, F8, 64>(P, dev, ctas, st);
+  return launch_attention<D, F8, 128>(P, dev, ctas, st);
 }
 
 }  // namespace sv
@@ -1266,14 +1271,14 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
                       {P.cache.slot, P.cache.head, P.cache.page}, {f8 ? D : 64, box, 1, 1},
                       f8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return SPEC_ERR_CUDA;
-  int sms = 0;
-  cudaError_t e = device_sms(&sms);
+  int dev = 0, sms = 0;
+  cudaError_t e = device_sms(&dev, &sms);
   if (e != cudaSuccess) return SPEC_ERR_CUDA;
   int ctas = sms < kMaxParts ? sms : kMaxParts;
   if (most < ctas) ctas = (int)most;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  e = D == 128 ? (f8 ? launch_rows<128, true>(P, ctas, st) : launch_rows<128, false>(P, ctas, st))
-               : (f8 ? launch_rows<64, true>(P, ctas, st) : launch_rows<64, false>(P, ctas, st));
+  e = D == 128 ? (f8 ? launch_rows<128, true>(P, dev, ctas, st) : launch_rows<128, false>(P, dev, ctas, st))
+               : (f8 ? launch_rows<64, true>(P, dev, ctas, st) : launch_rows<64, false>(P, dev, ctas, st));
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

@@ -19,9 +19,6 @@ struct AppendParams {
   int32_t* flags;
   int q_heads, heads;      // heads of q; heads of k (and of v)
   int rot, max_positions;  // rot = rot_dim
-  int per_task;            // heads that one thread takes in turn
-  int tasks;               // ceil((q_heads + 2 heads) / per_task)
-  int64_t total;           // B * T * tasks * units
 };
 
 // Where new token t of a request goes in the cache: its byte offset within a head, or -1.
@@ -32,55 +29,51 @@ __device__ __forceinline__ int64_t slot_offset(const Batch& b, const Cache& c, i
   return page * c.page + (slot & ((1 << c.page_shift) - 1)) * c.slot;
 }
 
-// 8 elements of a key or value into the cache.
+// 8 elements of a key or value into the cache.  E4M3: times the scale's reciprocal, which is within 2^-23 of
+// the quotient, 2^-19 of the rounding to 4 significant bits.
 template <bool F8>
-__device__ __forceinline__ void store_entry(char* p, float (&x)[8], float scale) {
+__device__ __forceinline__ void store_entry(char* p, float (&x)[8], float inv_scale) {
   if constexpr (F8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] / scale;
+    for (int i = 0; i < 8; ++i) x[i] *= inv_scale;
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_e4m3(x[0], x[1], x[2], x[3]), pack_e4m3(x[4], x[5], x[6], x[7]));
   } else {
     *reinterpret_cast<uint4*>(p) = pack8(x);
   }
 }
 
-// One thread owns one unit of the head dimension -- the 8 elements at `lo`, and with half-split rotation
-// also their partners at lo + rot/2 -- for per_task heads of one token, so a token's cos and sin are loaded
-// once for them, and an element's partner is always in the same thread (q_out may be q itself).
+// One block per token.  A thread owns one unit of the head dimension -- the 8 elements at `lo`, and with
+// half-split rotation also their partners at lo + rot/2 -- for every lanes-th head, so a token's cos and
+// sin are loaded once a thread and an element's partner is always in the same thread (q_out may be q
+// itself).  kAhead heads are loaded before the first is used.
 template <int D, bool F8, bool INTERLEAVED>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams P) {
+  constexpr int kAhead = 4;
   const int paired = INTERLEAVED ? 0 : P.rot / 16;  // units that hold a vector and its partner
-  const int units = D / 8 - paired;
-  const int64_t id = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x;
-  if (id >= P.total) return;
-  const int unit = (int)(id % units);
-  const int64_t rest = id / units;
-  const int task = (int)(rest % P.tasks);
-  const int64_t token = rest / P.tasks;
-  const int b = (int)(token / P.batch.T), t = (int)(token % P.batch.T);
-  const int h_end = min((task + 1) * P.per_task, P.q_heads + 2 * P.heads);
-  int h = task * P.per_task;
+  const int units = D / 8 - paired, lanes = kAppendThreads / units;
+  const int head0 = threadIdx.x / units, unit = threadIdx.x - head0 * units;
+  const int b = blockIdx.x / P.batch.T, t = blockIdx.x - b * P.batch.T;
+  if (head0 >= lanes) return;
 
   const bool pair = unit < paired;
   const int lo = pair || INTERLEAVED ? unit * 8 : P.rot + (unit - paired) * 8;
   const bool turns = pair || (INTERLEAVED && lo < P.rot);
-  const int tb = batch_tokens(P.batch, b);
+  const int far = P.rot / 2;  // distance to the partner
+  const int given = P.batch.t_per_row ? __ldg(P.batch.t_per_row + b) : P.batch.T;
+  const int held = __ldg(P.batch.ctx_len + b);
+  const int tb = min(max(given, 0), P.batch.T), ctx = min(max(held, 0), P.batch.slots);
+  int flag = given < 0 || given > P.batch.T ? SPEC_FLAG_BAD_K : 0;
   if (t >= tb) {  // a padded token: its rotated query is 0
-    for (; h < h_end && h < P.q_heads; ++h) {
+    for (int h = head0; h < P.q_heads; h += lanes) {
       char* o = P.q_out.data + b * P.q_out.row + t * P.q_out.token + h * P.q_out.head;
       *reinterpret_cast<uint4*>(o + lo * 2) = make_uint4(0, 0, 0, 0);
-      if (pair) *reinterpret_cast<uint4*>(o + (lo + P.rot / 2) * 2) = make_uint4(0, 0, 0, 0);
+      if (pair) *reinterpret_cast<uint4*>(o + (lo + far) * 2) = make_uint4(0, 0, 0, 0);
     }
-    if (P.flags && t == P.batch.T - 1 && task == 0 && unit == 0 && P.batch.t_per_row &&
-        __ldg(P.batch.t_per_row + b) < 0)
-      atomicOr(P.flags + b, SPEC_FLAG_BAD_K);
+    if (P.flags && flag && threadIdx.x == 0) atomicOr(P.flags + b, flag);
     return;
   }
-  const int ctx = batch_context(P.batch, b);
   const int64_t at = slot_offset(P.batch, P.cache, b, ctx + t);
-  int flag = at < 0 ? SPEC_FLAG_BAD_SLOT : 0;
-  if (P.flags && P.batch.t_per_row && __ldg(P.batch.t_per_row + b) > P.batch.T) flag |= SPEC_FLAG_BAD_K;
-  if (P.flags && __ldg(P.batch.ctx_len + b) < 0) flag |= SPEC_FLAG_BAD_SLOT;
+  if (at < 0 || held < 0) flag |= SPEC_FLAG_BAD_SLOT;
 
   // cos and sin of the unit: 8 pairs half-split, 4 pairs interleaved
   float co[8], si[8];
@@ -101,50 +94,59 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
       }
     }
   }
-  if (P.flags && flag && task == 0 && unit == 0) atomicOr(P.flags + b, flag);
+  if (P.flags && flag && threadIdx.x == 0) atomicOr(P.flags + b, flag);
 
-  const int far = P.rot / 2;  // distance to the partner
-  for (; h < h_end; ++h) {
-    const bool is_q = h < P.q_heads;
-    const bool is_k = !is_q && h < P.q_heads + P.heads;
-    const int hh = is_q ? h : is_k ? h - P.q_heads : h - P.q_heads - P.heads;
-    if (!is_q && at < 0) break;  // k and v heads follow the q heads
-    const Heads& in = is_q ? P.q : is_k ? P.k : P.v;
-    const char* p = in.data + b * in.row + t * in.token + hh * in.head;
-    const uint4 w0 = *reinterpret_cast<const uint4*>(p + lo * 2);
-    uint4 w1 = make_uint4(0, 0, 0, 0);
-    if (pair) w1 = *reinterpret_cast<const uint4*>(p + (lo + far) * 2);
-    float x[8], y[8];
-    unpack8(w0, x);
-    unpack8(w1, y);
-    if (turns && (is_q || is_k)) {
-      if constexpr (INTERLEAVED) {
+  const char* q = P.q.data + b * P.q.row + t * P.q.token;
+  const char* k = P.k.data + b * P.k.row + t * P.k.token;
+  const char* v = P.v.data + b * P.v.row + t * P.v.token;
+  char* o = P.q_out.data + b * P.q_out.row + t * P.q_out.token;
+  const int k_end = P.q_heads + P.heads, end = at < 0 ? P.q_heads : k_end + P.heads;
+  for (int h0 = head0; h0 < end; h0 += lanes * kAhead) {
+    uint4 w0[kAhead], w1[kAhead];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], c = x[2 * i + 1];
-          x[2 * i] = a * co[i] - c * si[i];
-          x[2 * i + 1] = c * co[i] + a * si[i];
-        }
-      } else {
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * lanes;
+      if (h >= end) break;
+      const char* p = h < P.q_heads ? q + h * P.q.head : h < k_end ? k + (h - P.q_heads) * P.k.head : v + (h - k_end) * P.v.head;
+      w0[i] = *reinterpret_cast<const uint4*>(p + lo * 2);
+      if (pair) w1[i] = *reinterpret_cast<const uint4*>(p + (lo + far) * 2);
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = x[i], c = y[i];
-          x[i] = a * co[i] - c * si[i];
-          y[i] = c * co[i] + a * si[i];
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * lanes;
+      if (h >= end) break;
+      float x[8], y[8];
+      unpack8(w0[i], x);
+      if (pair) unpack8(w1[i], y);
+      if (turns && h < k_end) {
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float a = x[2 * e], c = x[2 * e + 1];
+            x[2 * e] = a * co[e] - c * si[e];
+            x[2 * e + 1] = c * co[e] + a * si[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float a = x[e], c = y[e];
+            x[e] = a * co[e] - c * si[e];
+            y[e] = c * co[e] + a * si[e];
+          }
         }
       }
-    }
-    if (is_q) {
-      char* o = P.q_out.data + b * P.q_out.row + t * P.q_out.token + hh * P.q_out.head;
-      *reinterpret_cast<uint4*>(o + lo * 2) = pack8(x);
-      if (pair) *reinterpret_cast<uint4*>(o + (lo + far) * 2) = pack8(y);
-    } else {
-      constexpr int ES = F8 ? 1 : 2;
-      const float* scales = is_k ? P.cache.k_scale : P.cache.v_scale;
-      const float scale = F8 && scales ? __ldg(scales + hh) : 1.0f;
-      char* o = (is_k ? P.cache.k : P.cache.v) + at + hh * P.cache.head;
-      store_entry<F8>(o + lo * ES, x, scale);
-      if (pair) store_entry<F8>(o + (lo + far) * ES, y, scale);
+      if (h < P.q_heads) {
+        *reinterpret_cast<uint4*>(o + h * P.q_out.head + lo * 2) = pack8(x);
+        if (pair) *reinterpret_cast<uint4*>(o + h * P.q_out.head + (lo + far) * 2) = pack8(y);
+      } else {
+        constexpr int ES = F8 ? 1 : 2;
+        const int hh = h < k_end ? h - P.q_heads : h - k_end;
+        const float* scales = h < k_end ? P.cache.k_scale : P.cache.v_scale;
+        const float inv = F8 && scales ? 1.0f / __ldg(scales + hh) : 1.0f;
+        char* e = (h < k_end ? P.cache.k : P.cache.v) + at + hh * P.cache.head;
+        store_entry<F8>(e + lo * ES, x, inv);
+        if (pair) store_entry<F8>(e + (lo + far) * ES, y, inv);
+      }
     }
   }
 }
@@ -158,35 +160,48 @@ struct KeepParams {
   const int32_t* path;
   const int32_t* n_keep;
   int max_keep, heads, vecs;  // 16-byte vectors per head
-  int64_t total;              // layers * B * 2 * heads * vecs
+  int columns;                // layers * 2 * heads * vecs
 };
 
 constexpr int kKeepThreads = 256;
+constexpr int kKeepAhead = 8;   // entries a thread loads before it stores the first
+constexpr int kKeepRound = 64;  // moves whose places the block works out at a time
 
-// One thread owns one 16-byte column of one request's entries (layer, k or v, head, vector) and moves it
-// through the path in order.  A strictly increasing path has path[i] >= i, so what move i overwrites
-// (slot i) is never read by a later move: loads may run ahead of stores, and columns are independent.
+// Block (x, y): 256 columns of request y's entries.  A column is one 16-byte vector (layer, k or v, head,
+// vector) of every slot, and one thread moves it through the path in order.  A strictly increasing path
+// has path[i] >= i, so what move i overwrites (slot i) is never read by a later move: loads may run ahead
+// of stores, and columns are independent.
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constant__ KeepParams P) {
-  const int64_t id = (int64_t)blockIdx.x * kKeepThreads + threadIdx.x;
-  if (id >= P.total) return;
-  const int vec = (int)(id % P.vecs);
-  int64_t rest = id / P.vecs;
-  const int h = (int)(rest % P.heads);
-  rest /= P.heads;
-  const bool is_v = rest & 1;
-  rest >>= 1;
-  const int b = (int)(rest % P.batch.B);
-  const int64_t layer = rest / P.batch.B;
+  __shared__ int64_t from[kKeepRound], to[kKeepRound];  // -1: nothing to move
+  const int b = blockIdx.y;
   const int n = min(max(__ldg(P.n_keep + b), 0), P.max_keep);
   const int ctx = batch_context(P.batch, b);
-  char* column = (is_v ? P.cache.v : P.cache.k) + layer * P.cache.layer + h * P.cache.head + vec * 16;
-  for (int i = 0; i < n; ++i) {
-    const int from = __ldg(P.path + (int64_t)b * P.max_keep + i);
-    if (from == i || from < 0 || from >= P.batch.slots) continue;
-    const int64_t src = ctx + from >= 0 ? slot_offset(P.batch, P.cache, b, ctx + from) : -1;
-    const int64_t dst = slot_offset(P.batch, P.cache, b, ctx + i);
-    if (src < 0 || dst < 0) continue;
-    *reinterpret_cast<uint4*>(column + dst) = *reinterpret_cast<const uint4*>(column + src);
+  const int c = blockIdx.x * kKeepThreads + threadIdx.x;
+  const int head = c / P.vecs, vec = c - head * P.vecs;
+  const int side = head / P.heads, layer = side / 2;
+  char* column = (side % 2 ? P.cache.v : P.cache.k) + layer * P.cache.layer + (head - side * P.heads) * P.cache.head + vec * 16;
+  for (int i0 = 0; i0 < n; i0 += kKeepRound) {
+    const int round = min(kKeepRound, n - i0);
+    if ((int)threadIdx.x < round) {
+      const int i = i0 + threadIdx.x, p = __ldg(P.path + (int64_t)b * P.max_keep + i);
+      int64_t src = -1;
+      const int64_t dst = slot_offset(P.batch, P.cache, b, ctx + i);
+      if (p != i && p >= 0 && p < P.batch.slots && dst >= 0) src = slot_offset(P.batch, P.cache, b, ctx + p);
+      from[threadIdx.x] = src, to[threadIdx.x] = dst;
+    }
+    __syncthreads();
+    if (c < P.columns) {
+      for (int i = 0; i < round; i += kKeepAhead) {
+        uint4 w[kKeepAhead];
+#pragma unroll
+        for (int j = 0; j < kKeepAhead; ++j)
+          if (i + j < round && from[i + j] >= 0) w[j] = *reinterpret_cast<const uint4*>(column + from[i + j]);
+#pragma unroll
+        for (int j = 0; j < kKeepAhead; ++j)
+          if (i + j < round && from[i + j] >= 0) *reinterpret_cast<uint4*>(column + to[i + j]) = w[j];
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -225,13 +240,8 @@ spec_status_t spec_kv_append(const spec_heads_t* q, const spec_heads_t* k, const
   P.flags = out_flags;
   P.q_heads = q_heads, P.heads = cache->heads;
   const bool inter = rot > 0 && rotary->interleaved != 0;
-  const int units = cache->head_dim / 8 - (inter ? 0 : rot / 16);
-  const int all = q_heads + 2 * cache->heads;
-  P.per_task = 4;
-  P.tasks = (all + P.per_task - 1) / P.per_task;
-  P.total = (int64_t)batch->B * batch->T * P.tasks * units;
-  const int64_t blocks = (P.total + kAppendThreads - 1) / kAppendThreads;
-  if (blocks > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
+  const int64_t blocks = (int64_t)batch->B * batch->T;
+  if (blocks > 0x7fffffffll || q_heads > 65535) return SPEC_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f8 = cache->dtype == SPEC_DTYPE_E4M3;
   auto kern = cache->head_dim == 128
@@ -257,10 +267,11 @@ spec_status_t spec_kv_keep(const spec_kv_cache_t* cache, const spec_decode_batch
   P.path = path, P.n_keep = n_keep, P.max_keep = max_keep;
   P.heads = cache->heads;
   P.vecs = cache->head_dim * (cache->dtype == SPEC_DTYPE_BF16 ? 2 : 1) / 16;
-  P.total = (int64_t)cache->layers * batch->B * 2 * P.heads * P.vecs;
-  const int64_t blocks = (P.total + kKeepThreads - 1) / kKeepThreads;
-  if (blocks > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
-  keep_kernel<<<(unsigned)blocks, kKeepThreads, 0, static_cast<cudaStream_t>(stream)>>>(P);
+  const int64_t columns = (int64_t)cache->layers * 2 * P.heads * P.vecs;
+  if (columns > 0x7fffff00ll || batch->B > 65535) return SPEC_ERR_UNSUPPORTED;
+  P.columns = (int)columns;
+  const dim3 grid((unsigned)((columns + kKeepThreads - 1) / kKeepThreads), batch->B);
+  keep_kernel<<<grid, kKeepThreads, 0, static_cast<cudaStream_t>(stream)>>>(P);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

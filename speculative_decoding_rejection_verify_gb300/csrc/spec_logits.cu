@@ -12,7 +12,8 @@
 namespace sv {
 
 constexpr int kRuleThreads = 256;
-constexpr int kStretch = 8192;  // tokens of one block: 32 KB of counts, 6 blocks per SM
+constexpr int kRowsAhead = 4;            // positions whose logits a thread loads before it uses them
+constexpr int kStretches[] = {8192, 4096, 2048};  // tokens of one block
 
 // A token's word of counts: bit 31 = in the prompt, bits 20..30 = 1 + index of its bias entry (0: none),
 // bits 0..19 = times among the output tokens.
@@ -26,65 +27,100 @@ struct RuleParams {
   const void* logits;
   void* out;
   spec_logit_rules_t r;
-  int B, T, V, words;
+  int B, T, V, words, stretch;
 };
 
-template <typename T, int VEC>
-struct Pack;
+// VEC logits as one load and store of 2 to 16 bytes.  The loads are not read-only ones: out may be logits.
+template <int BYTES>
+struct Raw;
 template <>
-struct Pack<float, 4> {
-  using W = float4;
-  static __device__ __forceinline__ void get(const W& w, float (&x)[4]) { x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w; }
-  static __device__ __forceinline__ W put(const float (&x)[4]) { return make_float4(x[0], x[1], x[2], x[3]); }
+struct Raw<16> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const void* p) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+  }
+  __device__ __forceinline__ void store(void* p) const { *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]); }
 };
 template <>
-struct Pack<float, 1> {
-  using W = float;
-  static __device__ __forceinline__ void get(const W& w, float (&x)[1]) { x[0] = w; }
-  static __device__ __forceinline__ W put(const float (&x)[1]) { return x[0]; }
+struct Raw<8> {
+  uint32_t w[2];
+  __device__ __forceinline__ void load(const void* p) {
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+  }
+  __device__ __forceinline__ void store(void* p) const { *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]); }
 };
 template <>
-struct Pack<__nv_bfloat16, 8> {
-  using W = uint4;
-  static __device__ __forceinline__ void get(const W& w, float (&x)[8]) { unpack8(w, x); }
-  static __device__ __forceinline__ W put(const float (&x)[8]) { return pack8(x); }
+struct Raw<4> {
+  uint32_t w[1];
+  __device__ __forceinline__ void load(const void* p) { asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p)); }
+  __device__ __forceinline__ void store(void* p) const { *reinterpret_cast<uint32_t*>(p) = w[0]; }
 };
 template <>
-struct Pack<__nv_bfloat16, 1> {
-  using W = __nv_bfloat16;
-  static __device__ __forceinline__ void get(const W& w, float (&x)[1]) { x[0] = __bfloat162float(w); }
-  static __device__ __forceinline__ W put(const float (&x)[1]) { return __float2bfloat16(x[0]); }
+struct Raw<2> {
+  uint32_t w[1];
+  __device__ __forceinline__ void load(const void* p) {
+    uint16_t h;
+    asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(h) : "l"(p));
+    w[0] = h;
+  }
+  __device__ __forceinline__ void store(void* p) const { *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0]; }
 };
 
-template <typename T, int VEC>
+template <bool BF16, int VEC>
+__device__ __forceinline__ void unpack(const uint32_t* w, float (&x)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i)
+    x[i] = !BF16 ? __uint_as_float(w[i]) : i % 2 ? bf16_high(w[i / 2]) : bf16_low(w[i / 2]);
+}
+template <bool BF16, int VEC>
+__device__ __forceinline__ void pack(uint32_t* w, const float (&x)[VEC]) {
+  if constexpr (!BF16) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) w[i] = __float_as_uint(x[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 2) w[i / 2] = pack_bf16(x[i], i + 1 < VEC ? x[i + 1] : 0.0f);
+  }
+}
+
+// A thread takes GROUPS runs of VEC tokens, kRuleThreads * VEC apart, through all positions.
+template <bool BF16, int VEC, int GROUPS>
 __global__ void __launch_bounds__(kRuleThreads) rules_kernel(const __grid_constant__ RuleParams P) {
-  __shared__ __align__(16) uint32_t word[kStretch];
-  const int b = blockIdx.y, first = blockIdx.x * kStretch;
-  const int len = min(kStretch, P.V - first);
+  constexpr int ES = BF16 ? 2 : 4;
+  extern __shared__ __align__(16) uint32_t word[];  // [stretch]
+  __shared__ int draft[SPEC_MAX_NEW];               // relative to the stretch; -1: elsewhere
+  const int b = blockIdx.y, first = blockIdx.x * P.stretch;
+  const int len = min(P.stretch, P.V - first);
   const spec_logit_rules_t& R = P.r;
   const int rows = R.t_per_row ? min(max(__ldg(R.t_per_row + b), 0), P.T) : P.T;
   const float rep = R.repetition ? __ldg(R.repetition + b) : 1.0f;
   const float pre = R.presence ? __ldg(R.presence + b) : 0.0f;
   const float fre = R.frequency ? __ldg(R.frequency + b) : 0.0f;
+  const int held = R.history ? min(max(__ldg(R.history_len + b), 0), R.history_stride) : 0;
+  const int prompt = R.history && R.prompt_len ? __ldg(R.prompt_len + b) : 0;
   const bool penal = rep != 1.0f || pre != 0.0f || fre != 0.0f;
 
-  for (int i = threadIdx.x; i < kStretch; i += kRuleThreads) word[i] = 0;
+  for (int i = threadIdx.x; i < (len + 3) / 4; i += kRuleThreads) reinterpret_cast<uint4*>(word)[i] = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < SPEC_MAX_NEW) {
+    int d = -1;
+    if (penal && R.draft && (int)threadIdx.x < rows - 1) d = __ldg(R.draft + (int64_t)b * (P.T - 1) + threadIdx.x);
+    draft[threadIdx.x] = d >= first && d - first < len ? d - first : -1;
+  }
   __syncthreads();
   if (R.bias_n > 0) {  // of two entries with one id the later holds
     const int32_t* ids = R.bias_ids + (int64_t)b * R.bias_n;
     for (int i = threadIdx.x; i < R.bias_n; i += kRuleThreads) {
-      const int64_t v = (int64_t)__ldg(ids + i) - first;
-      if (v >= 0 && v < len) atomicMax(&word[v], (uint32_t)(i + 1) << kBiasShift);
+      const uint32_t v = (uint32_t)__ldg(ids + i) - (uint32_t)first;
+      if (v < (uint32_t)len) atomicMax(&word[v], (uint32_t)(i + 1) << kBiasShift);
     }
     __syncthreads();
   }
-  if (penal && R.history) {
-    const int held = min(max(__ldg(R.history_len + b), 0), R.history_stride);
-    const int prompt = R.prompt_len ? __ldg(R.prompt_len + b) : 0;
+  if (penal) {
     const int32_t* ids = R.history + (int64_t)b * R.history_stride;
+#pragma unroll 4
     for (int i = threadIdx.x; i < held; i += kRuleThreads) {
-      const int64_t v = (int64_t)__ldg(ids + i) - first;
-      if (v >= 0 && v < len) {
+      const uint32_t v = (uint32_t)__ldg(ids + i) - (uint32_t)first;
+      if (v < (uint32_t)len) {
         if (i < prompt)
           atomicOr(&word[v], kPromptBit);
         else
@@ -94,49 +130,100 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(const __grid_consta
   }
   __syncthreads();
 
-  using K = Pack<T, VEC>;
-  const int64_t base = (int64_t)b * P.T * P.V + first;
-  for (int v0 = threadIdx.x * VEC; v0 < len; v0 += kRuleThreads * VEC) {  // VEC > 1: V is a multiple of it
-    uint32_t c[VEC], any = 0;
+  const int64_t row_bytes = (int64_t)P.V * ES;
+  const int64_t base = ((int64_t)b * P.T * P.V + first) * ES;
+  const char* in = static_cast<const char*>(P.logits) + base;
+  char* out = static_cast<char*>(P.out) + base;
+  const int32_t* mask = R.mask ? R.mask + (int64_t)b * P.T * P.words + (first >> 5) : nullptr;
+  constexpr uint32_t kAll = VEC == 32 ? ~0u : (1u << VEC) - 1;
+  for (int v0 = threadIdx.x * VEC; v0 < len; v0 += kRuleThreads * VEC * GROUPS) {  // VEC divides V and the stretch
+    uint32_t c[GROUPS][VEC], any[GROUPS];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      c[i] = word[v0 + i];
-      any |= c[i];
+    for (int g = 0; g < GROUPS; ++g) {
+      const int v = v0 + g * kRuleThreads * VEC;
+      any[g] = 0;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        c[g][i] = v < len ? word[v + i] : 0;
+        any[g] |= c[g][i];
+      }
     }
-    for (int t = 0; t < rows; ++t) {
-      if (penal && R.draft && t > 0) {
-        const int64_t d = (int64_t)__ldg(R.draft + (int64_t)b * (P.T - 1) + t - 1) - first - v0;
-        if (d >= 0 && d < VEC) {
+    for (int t0 = 0; t0 < rows; t0 += kRowsAhead) {
+      uint32_t allowed[kRowsAhead][GROUPS];
+      Raw<VEC * ES> raw[kRowsAhead][GROUPS];
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) c[i] += i == (int)d;
-          any |= 1;
+      for (int r = 0; r < kRowsAhead; ++r)
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+          const int v = v0 + g * kRuleThreads * VEC;
+          allowed[r][g] = kAll;
+          if (mask && t0 + r < rows && v < len)
+            allowed[r][g] = ((uint32_t)__ldg(mask + (int64_t)(t0 + r) * P.words + (v >> 5)) >> (v & 31)) & kAll;
         }
-      }
-      const int64_t at = base + (int64_t)t * P.V + v0;
-      float x[VEC];
-      K::get(*reinterpret_cast<const typename K::W*>(static_cast<const T*>(P.logits) + at), x);
-      if (any) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const uint32_t count = c[i] & kCountMask;
-          if (penal) {
-            if (count > 0 || (c[i] & kPromptBit)) x[i] = x[i] > 0.0f ? x[i] / rep : x[i] * rep;
-            if (count > 0) x[i] = x[i] - fre * (float)count - pre;
+      for (int r = 0; r < kRowsAhead; ++r)
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+          const int v = v0 + g * kRuleThreads * VEC;
+#pragma unroll
+          for (int i = 0; i < (VEC * ES + 3) / 4; ++i) raw[r][g].w[i] = 0;
+          // a run that the mask forbids throughout is not read
+          if (allowed[r][g] && t0 + r < rows && v < len) raw[r][g].load(in + (t0 + r) * row_bytes + v * ES);
+        }
+#pragma unroll
+      for (int r = 0; r < kRowsAhead; ++r) {
+        const int t = t0 + r;
+        if (t >= rows) break;
+        const int d = t > 0 ? draft[t - 1] : -1;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+          const int v = v0 + g * kRuleThreads * VEC;
+          if (v >= len) continue;
+          if (d >= v && d < v + VEC) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) c[g][i] += i == d - v;
+            any[g] |= 1;
           }
-          const uint32_t e = (c[i] & ~kPromptBit) >> kBiasShift;
-          if (e) x[i] += __ldg(R.bias + (int64_t)b * R.bias_n + e - 1);
+          if (any[g] || allowed[r][g] != kAll) {
+            float x[VEC];
+            unpack<BF16, VEC>(raw[r][g].w, x);
+            if (any[g]) {
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) {
+                const uint32_t count = c[g][i] & kCountMask;
+                if (penal) {
+                  if (count > 0 || (c[g][i] & kPromptBit)) x[i] = x[i] > 0.0f ? x[i] / rep : x[i] * rep;
+                  if (count > 0) x[i] = x[i] - fre * (float)count - pre;
+                }
+                const uint32_t e = (c[g][i] & ~kPromptBit) >> kBiasShift;
+                if (e) x[i] += __ldg(R.bias + (int64_t)b * R.bias_n + e - 1);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+              if (!((allowed[r][g] >> i) & 1u)) x[i] = -INFINITY;
+            pack<BF16, VEC>(raw[r][g].w, x);
+          }
+          raw[r][g].store(out + t * row_bytes + v * ES);
         }
       }
-      if (R.mask) {
-        const uint32_t bits =
-            (uint32_t)__ldg(R.mask + ((int64_t)b * P.T + t) * P.words + ((first + v0) >> 5)) >> ((first + v0) & 31);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          if (!((bits >> i) & 1u)) x[i] = -INFINITY;
-      }
-      *reinterpret_cast<typename K::W*>(static_cast<T*>(P.out) + at) = K::put(x);
     }
   }
+}
+
+template <bool BF16>
+static cudaError_t launch_rules(const RuleParams& P, int align, cudaStream_t st) {
+  // the widest vector that divides the rows and their addresses; narrow ones take several runs a thread to
+  // keep as many bytes in flight
+  constexpr int ES = BF16 ? 2 : 4;
+  void (*kern)(RuleParams) = nullptr;
+  if (align % 16 == 0) kern = rules_kernel<BF16, 16 / ES, 1>;
+  else if (align % 8 == 0) kern = rules_kernel<BF16, 8 / ES, 2>;
+  else if (align % 4 == 0) kern = rules_kernel<BF16, 4 / ES, 4>;
+  else kern = rules_kernel<BF16, 1, 4>;
+  const dim3 grid((P.V + P.stretch - 1) / P.stretch, P.B);
+  kern<<<grid, kRuleThreads, P.stretch * sizeof(uint32_t), st>>>(P);
+  return cudaGetLastError();
 }
 
 }  // namespace sv
@@ -162,15 +249,18 @@ extern "C" spec_status_t spec_process_logits(const void* logits, void* out, cons
   RuleParams P = {};
   P.logits = logits, P.out = out, P.r = r;
   P.B = B, P.T = T, P.V = V, P.words = (V + 31) / 32;
-  const dim3 grid((V + kStretch - 1) / kStretch, B);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool vec = (uintptr_t)logits % 16 == 0 && (uintptr_t)out % 16 == 0 && (int64_t)V * es % 16 == 0;
-  if (dtype == SPEC_DTYPE_BF16) {
-    if (vec) rules_kernel<__nv_bfloat16, 8><<<grid, kRuleThreads, 0, st>>>(P);
-    else rules_kernel<__nv_bfloat16, 1><<<grid, kRuleThreads, 0, st>>>(P);
-  } else {
-    if (vec) rules_kernel<float, 4><<<grid, kRuleThreads, 0, st>>>(P);
-    else rules_kernel<float, 1><<<grid, kRuleThreads, 0, st>>>(P);
+  // A long stretch shares one scan of the history among more tokens; a shorter one is taken when there would
+  // be fewer than 8 blocks per SM.
+  int dev = 0, sms = 0;
+  if (device_sms(&dev, &sms) != cudaSuccess) return SPEC_ERR_CUDA;
+  for (int s : kStretches) {
+    P.stretch = s;
+    if ((int64_t)B * ((V + s - 1) / s) >= 8 * sms) break;
   }
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // the largest power of two that divides every row's address
+  const uint64_t bits = (uint64_t)(uintptr_t)logits | (uint64_t)(uintptr_t)out | (uint64_t)((int64_t)V * es) | 16u;
+  const int align = (int)(bits & (~bits + 1));
+  const cudaError_t e = dtype == SPEC_DTYPE_BF16 ? launch_rules<true>(P, align, st) : launch_rules<false>(P, align, st);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -17,6 +17,8 @@ says which page holds each stretch of a request's slots; the new tokens of a ste
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import Optional
 
 import speculative_decoding_rejection_verify_gb300 as sv
@@ -78,68 +80,104 @@ def declare(lib) -> None:
     lib.spec_process_logits.restype = _I
 
 
-def _heads(x, name, shape, device):
+# A small call's time is mostly this module's: the checks below look at a tensor once and say what is wrong
+# with it only when something is.
+_torch = None
+_raw_stream = None
+_PACK_CACHE = struct.Struct("PPqqqqiiiiiiPP").pack
+
+
+def _load():
+    """(torch, the library), and this module's shortcuts to them."""
+    global _torch, _raw_stream
+    lib = sv.load()
+    if _torch is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _torch = torch
+    return _torch, lib
+
+
+def _fits(t, name, shape, dtype, index) -> int:
+    """The address of a contiguous tensor of this shape and dtype on CUDA device ``index``."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        sv._check(t, name, shape, dtype, _torch.device("cuda", index))
+    return t.data_ptr()
+
+
+def _maybe(t, name, shape, dtype, index) -> Optional[int]:
+    return None if t is None else _fits(t, name, shape, dtype, index)
+
+
+def _heads(x, name, shape, index):
     """A [B, T, heads, head_dim] bfloat16 tensor of any strides with head_dim innermost."""
-    torch = sv._torch()
     if x.shape != shape:
         raise ValueError(f"{name}: shape {tuple(x.shape)} != {tuple(shape)}")
-    if x.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: dtype {x.dtype} != {torch.bfloat16}")
-    if x.device != device:
-        raise ValueError(f"{name}: on {x.device}, expected {device}")
-    s = x.stride()
-    if s[3] != 1:
+    if x.dtype is not _torch.bfloat16:
+        raise TypeError(f"{name}: dtype {x.dtype} != {_torch.bfloat16}")
+    if x.get_device() != index:
+        raise ValueError(f"{name}: on {x.device}, expected cuda:{index}")
+    row, token, head, one = x.stride()
+    if one != 1:
         raise ValueError(f"{name}: head_dim must be innermost")
-    return HeadsStruct(x.data_ptr(), s[0], s[1], s[2])
+    return HeadsStruct(x.data_ptr(), row, token, head)
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale):
-    torch = sv._torch()
-    shape, st = k_cache.shape, k_cache.stride()
-    dev = k_cache.device
-    if dev.type != "cuda":
+def _cache(k_cache, v_cache, k_scale, v_scale, layered):
+    """(the struct, heads, head_dim, the device's index)"""
+    shape, st, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
+    index = k_cache.get_device()
+    if index < 0:
         raise ValueError("k_cache must be a CUDA tensor")
-    if len(shape) != 4 and len(shape) != 5:
-        raise ValueError("k_cache must be [num_pages, page_size, heads, head_dim], or with layers in front of it")
+    if len(shape) != 4 and not (layered and len(shape) == 5):
+        raise ValueError("k_cache must be [num_pages, page_size, heads, head_dim]" +
+                         (", or with layers in front of it" if layered else ""))
     if v_cache.shape != shape or v_cache.stride() != st:
         raise ValueError("v_cache must have k_cache's shape and strides")
-    if v_cache.dtype != k_cache.dtype or v_cache.device != dev:
+    if v_cache.dtype is not dtype or v_cache.get_device() != index:
         raise ValueError("v_cache must have k_cache's dtype and device")
     if st[-1] != 1:
         raise ValueError("k_cache: head_dim must be innermost")
-    if k_cache.dtype == torch.bfloat16:
+    if dtype is _torch.bfloat16:
         dt = sv.DTYPE_BF16
-    elif k_cache.dtype == torch.float8_e4m3fn:
+    elif dtype is _torch.float8_e4m3fn:
         dt = DTYPE_E4M3
     else:
-        raise TypeError(f"k_cache must be bfloat16 or float8_e4m3fn, got {k_cache.dtype}")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t is not None:
-            sv._check(t, name, (shape[-2],), torch.float32, dev)
-    layers, lst = (1, 0) if len(shape) == 4 else (shape[0], st[0])
-    return CacheStruct(k_cache.data_ptr(), v_cache.data_ptr(), lst, st[-4], st[-3], st[-2], layers, shape[-4],
-                       shape[-3], shape[-2], shape[-1], dt, sv._ptr(k_scale), sv._ptr(v_scale))
+        raise TypeError(f"k_cache must be bfloat16 or float8_e4m3fn, got {dtype}")
+    layers, layer = (1, 0) if len(shape) == 4 else (shape[0], st[0])
+    num_pages, page, heads, D = shape[-4:]
+    ks = 0 if k_scale is None else _fits(k_scale, "k_scale", (heads,), _torch.float32, index)
+    vs = 0 if v_scale is None else _fits(v_scale, "v_scale", (heads,), _torch.float32, index)
+    packed = _PACK_CACHE(k_cache.data_ptr(), v_cache.data_ptr(), layer, st[-4], st[-3], st[-2], layers, num_pages, page,
+                         heads, D, dt, ks, vs)
+    return CacheStruct.from_buffer_copy(packed), heads, D, index
 
 
-def _batch(pages, ctx_len, t_per_row, T, device):
-    i32 = sv._torch().int32
+def _batch(pages, ctx_len, t_per_row, B, T, index):
+    i32 = _torch.int32
     if pages.dim() != 2:
         raise ValueError("pages must be [B, max_pages]")
-    B, max_pages = pages.shape
-    sv._check(pages, "pages", (B, max_pages), i32, device)
-    sv._check(ctx_len, "ctx_len", (B,), i32, device)
-    if t_per_row is not None:
-        sv._check(t_per_row, "t_per_row", (B,), i32, device)
-    return BatchStruct(pages.data_ptr(), ctx_len.data_ptr(), sv._ptr(t_per_row), B, T, max_pages)
+    max_pages = pages.shape[1]
+    return BatchStruct(_fits(pages, "pages", (B, max_pages), i32, index), _fits(ctx_len, "ctx_len", (B,), i32, index),
+                       _maybe(t_per_row, "t_per_row", (B,), i32, index), B, T, max_pages)
 
 
-def _empty(shape, dtype, device, stream):
-    """A new output, allocated on the stream that writes it."""
-    torch = sv._torch()
+def _like(x, stream):
+    """A new output of x's shape, allocated on the stream that writes it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty_like(x)
+    with _torch.cuda.stream(stream):
+        return _torch.empty_like(x)
+
+
+@functools.lru_cache(maxsize=None)
+def _attention_bytes(T: int, q_heads: int, heads: int, D: int) -> int:
+    """The workspace does not depend on the number of requests."""
+    n = sv.load().spec_paged_attention_workspace_bytes(1, T, q_heads, heads, D)
+    if n == 0:
+        raise sv.SpecVerifyError(1, "spec_paged_attention_workspace_bytes")
+    return n
 
 
 def kv_append(q, k, v, k_cache, v_cache, pages, ctx_len, cos=None, sin=None, t_per_row=None, positions=None,
@@ -149,45 +187,35 @@ def kv_append(q, k, v, k_cache, v_cache, pages, ctx_len, cos=None, sin=None, t_p
     be q itself).  ``q`` may be None.  ``cos``/``sin [max_positions, rot_dim / 2]``: None = no rotation;
     ``positions [B, T]``: None = ``ctx_len[b] + t``.  ``t_per_row [B]``: each request's valid tokens (the
     others' rotated q is 0).  ``flags [B]`` int32, cleared by the caller: FLAG_* bits are ORed into it."""
-    torch = sv._torch()
-    lib = sv.load()
-    c = _cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache: one layer, [num_pages, page_size, heads, head_dim]")
+    torch, lib = _load()
+    c, heads, D, index = _cache(k_cache, v_cache, k_scale, v_scale, False)
     if k.dim() != 4:
         raise ValueError("k must be [B, T, heads, head_dim]")
-    B, T = k.shape[0], k.shape[1]
-    b = _batch(pages, ctx_len, t_per_row, T, dev)
-    if b.B != B:
-        raise ValueError(f"pages: {b.B} rows for {B} requests")
-    shape = (B, T, c.heads, c.head_dim)
-    hk, hv = _heads(k, "k", shape, dev), _heads(v, "v", shape, dev)
+    B, T = k.shape[:2]
+    b = _batch(pages, ctx_len, t_per_row, B, T, index)
+    shape = (B, T, heads, D)
+    hk, hv = _heads(k, "k", shape, index), _heads(v, "v", shape, index)
     hq = ho = None
     n = 0
     if q is not None:
         if q.dim() != 4:
             raise ValueError("q must be [B, T, q_heads, head_dim]")
         n = q.shape[2]
-        qs = (B, T, n, c.head_dim)
-        hq = _heads(q, "q", qs, dev)
+        shape = (B, T, n, D)
+        hq = _heads(q, "q", shape, index)
         if out is None:
-            out = _empty(qs, q.dtype, dev, stream)
-        ho = _heads(out, "out", qs, dev)
+            out = _like(q, stream)
+        ho = _heads(out, "out", shape, index)
     r = None
     if cos is not None:
         if sin is None or cos.dim() != 2:
             raise ValueError("cos and sin must both be [max_positions, rot_dim / 2]")
-        sv._check(cos, "cos", cos.shape, torch.float32, dev)
-        sv._check(sin, "sin", cos.shape, torch.float32, dev)
-        if positions is not None:
-            sv._check(positions, "positions", (B, T), torch.int32, dev)
-        r = ctypes.byref(RotaryStruct(cos.data_ptr(), sin.data_ptr(), sv._ptr(positions), 2 * cos.shape[1],
-                                      cos.shape[0], int(interleaved)))
-    if flags is not None:
-        sv._check(flags, "flags", (B,), torch.int32, dev)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
-    rc = lib.spec_kv_append(hq, hk, hv, ho, n, c, b, r, sv._ptr(flags), st.cuda_stream)
+        table = tuple(cos.shape)
+        r = RotaryStruct(_fits(cos, "cos", table, torch.float32, index), _fits(sin, "sin", table, torch.float32, index),
+                         _maybe(positions, "positions", (B, T), torch.int32, index), 2 * table[1], table[0],
+                         1 if interleaved else 0)
+    f = _maybe(flags, "flags", (B,), torch.int32, index)
+    rc = lib.spec_kv_append(hq, hk, hv, ho, n, c, b, r, f, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != sv.SPEC_OK:
         raise sv.SpecVerifyError(rc, "spec_kv_append")
     return out
@@ -199,33 +227,26 @@ def paged_attention(q, k_cache, v_cache, pages, ctx_len, t_per_row=None, mask=No
     (spec_paged_attention, after ``kv_append``); returns ``out`` of q's shape.  ``mask [B, T]`` int64: bit i of
     ``mask[b, t]`` says whether new token t attends to new token i (None: causal); every token attends to the
     whole context.  ``scale``: None = head_dim ** -0.5."""
-    torch = sv._torch()
-    lib = sv.load()
-    c = _cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache: one layer, [num_pages, page_size, heads, head_dim]")
+    torch, lib = _load()
+    c, heads, D, index = _cache(k_cache, v_cache, k_scale, v_scale, False)
     if q.dim() != 4:
         raise ValueError("q must be [B, T, q_heads, head_dim]")
-    B, T, n, D = q.shape
-    b = _batch(pages, ctx_len, t_per_row, T, dev)
-    if b.B != B:
-        raise ValueError(f"pages: {b.B} rows for {B} requests")
-    hq = _heads(q, "q", (B, T, n, c.head_dim), dev)
+    B, T, n, _ = shape = q.shape
+    b = _batch(pages, ctx_len, t_per_row, B, T, index)
+    hq = _heads(q, "q", (B, T, n, D), index)
     if out is None:
-        out = _empty(q.shape, q.dtype, dev, stream)
-    ho = _heads(out, "out", q.shape, dev)
-    if mask is not None:
-        sv._check(mask, "mask", (B, T), torch.int64, dev)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
+        out = _like(q, stream)
+    ho = _heads(out, "out", shape, index)
+    m = _maybe(mask, "mask", (B, T), torch.int64, index)
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
     ws = workspace_tensor
     if ws is None:
-        nbytes = lib.spec_paged_attention_workspace_bytes(B, T, n, c.heads, D)
-        if nbytes == 0:
-            raise sv.SpecVerifyError(1, "spec_paged_attention_workspace_bytes")
-        ws = sv.workspace(nbytes, dev, st)
-    rc = lib.spec_paged_attention(hq, ho, n, c, b, sv._ptr(mask), D ** -0.5 if scale is None else scale,
-                                  ws.data_ptr(), ws.numel(), st.cuda_stream)
+        nbytes = _attention_bytes(T, n, heads, D)
+        ws = sv._ws_cache.get((index, handle))
+        if ws is None or ws.numel() < nbytes:
+            ws = sv.workspace(nbytes, k_cache.device, stream if stream is not None else torch.cuda.current_stream(index))
+    rc = lib.spec_paged_attention(hq, ho, n, c, b, m, D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(),
+                                  handle)
     if rc != sv.SPEC_OK:
         raise sv.SpecVerifyError(rc, "spec_paged_attention")
     return out
@@ -235,17 +256,15 @@ def kv_keep(k_cache, v_cache, pages, ctx_len, path, n_keep, stream=None) -> None
     """Move the accepted branch's entries up behind the context (spec_kv_keep): in every layer slot
     ``ctx_len[b] + i`` takes slot ``ctx_len[b] + path[b, i]`` for ``i < n_keep[b]``.  The cache may have a leading
     layer dimension; ``path [B, max_keep]`` holds strictly increasing indices of new tokens."""
-    torch = sv._torch()
-    lib = sv.load()
-    c = _cache(k_cache, v_cache, None, None)
-    dev = k_cache.device
-    b = _batch(pages, ctx_len, None, 0, dev)
+    torch, lib = _load()
+    c, _, _, index = _cache(k_cache, v_cache, None, None, True)
     if path.dim() != 2:
         raise ValueError("path must be [B, max_keep]")
-    sv._check(path, "path", (b.B, path.shape[1]), torch.int32, dev)
-    sv._check(n_keep, "n_keep", (b.B,), torch.int32, dev)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
-    rc = lib.spec_kv_keep(c, b, path.data_ptr(), n_keep.data_ptr(), path.shape[1], st.cuda_stream)
+    B, most = path.shape
+    b = _batch(pages, ctx_len, None, B, 0, index)
+    rc = lib.spec_kv_keep(c, b, _fits(path, "path", (B, most), torch.int32, index),
+                          _fits(n_keep, "n_keep", (B,), torch.int32, index), most,
+                          _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != sv.SPEC_OK:
         raise sv.SpecVerifyError(rc, "spec_kv_keep")
 
@@ -258,48 +277,40 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
     the prompt; ``draft [B, T-1]``: the drafts, which count at the positions behind them; ``repetition``,
     ``presence``, ``frequency [B]``; ``bias_ids``/``bias [B, n]``; ``mask [B, T, ceil(V / 32)]`` int32 words of allowed
     tokens.  Rows past ``t_per_row[b]`` are neither read nor written."""
-    torch = sv._torch()
-    lib = sv.load()
+    torch, lib = _load()
     if logits.dim() != 3:
         raise ValueError("logits must be [B, T, V]")
-    B, T, V = logits.shape
-    dev = logits.device
-    if dev.type != "cuda":
+    B, T, V = shape = logits.shape
+    index = logits.get_device()
+    if index < 0:
         raise ValueError("logits must be a CUDA tensor")
     dt = sv._dtype_code(logits)
     i32, f32 = torch.int32, torch.float32
-    sv._check(logits, "logits", (B, T, V), logits.dtype, dev)
+    z = _fits(logits, "logits", shape, logits.dtype, index)
     if out is None:
-        out = _empty(logits.shape, logits.dtype, dev, stream)
-    else:
-        sv._check(out, "out", (B, T, V), logits.dtype, dev)
+        out = _like(logits, stream)
+    o = _fits(out, "out", shape, logits.dtype, index)
     stride = nb = 0
+    hist = ids = bias_at = None
     if history is not None:
         if history.dim() != 2 or history_len is None:
             raise ValueError("history must be [B, n], with history_len")
         stride = history.shape[1]
-        sv._check(history, "history", (B, stride), i32, dev)
+        hist = _fits(history, "history", (B, stride), i32, index)
     if bias_ids is not None:
         if bias_ids.dim() != 2 or bias is None:
             raise ValueError("bias_ids must be [B, n], with bias")
         nb = bias_ids.shape[1]
-        sv._check(bias_ids, "bias_ids", (B, nb), i32, dev)
-        sv._check(bias, "bias", (B, nb), f32, dev)
-    for t, name in ((history_len, "history_len"), (prompt_len, "prompt_len"), (t_per_row, "t_per_row")):
-        if t is not None:
-            sv._check(t, name, (B,), i32, dev)
-    for t, name in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency")):
-        if t is not None:
-            sv._check(t, name, (B,), f32, dev)
-    if draft is not None:
-        sv._check(draft, "draft", (B, T - 1), i32, dev)
-    if mask is not None:
-        sv._check(mask, "mask", (B, T, (V + 31) // 32), i32, dev)
-    p = sv._ptr
-    r = RulesStruct(p(history), p(history_len), p(prompt_len), p(draft), p(t_per_row), p(repetition), p(presence),
-                    p(frequency), p(bias_ids), p(bias), p(mask), stride, nb)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
-    rc = lib.spec_process_logits(logits.data_ptr(), out.data_ptr(), r, B, T, V, dt, st.cuda_stream)
+        ids = _fits(bias_ids, "bias_ids", (B, nb), i32, index)
+        bias_at = _fits(bias, "bias", (B, nb), f32, index)
+    row = (B,)
+    r = RulesStruct(hist, _maybe(history_len, "history_len", row, i32, index),
+                    _maybe(prompt_len, "prompt_len", row, i32, index),
+                    _maybe(draft, "draft", (B, T - 1), i32, index), _maybe(t_per_row, "t_per_row", row, i32, index),
+                    _maybe(repetition, "repetition", row, f32, index), _maybe(presence, "presence", row, f32, index),
+                    _maybe(frequency, "frequency", row, f32, index), ids, bias_at,
+                    _maybe(mask, "mask", (B, T, (V + 31) // 32), i32, index), stride, nb)
+    rc = lib.spec_process_logits(z, o, r, B, T, V, dt, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != sv.SPEC_OK:
         raise sv.SpecVerifyError(rc, "spec_process_logits")
     return out
