@@ -136,16 +136,37 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(const __grid_consta
   char* out = static_cast<char*>(P.out) + base;
   const int32_t* mask = R.mask ? R.mask + (int64_t)b * P.T * P.words + (first >> 5) : nullptr;
   constexpr uint32_t kAll = VEC == 32 ? ~0u : (1u << VEC) - 1;
+  // What a token's word makes of its logit x: (seen ? x * (x > 0 ? 1 / rep : rep) : x) + off.  The reciprocal
+  // is within 2^-23 of the division, and the terms of off are summed before they meet the logit.
+  const float inv = 1.0f / rep;
+  const auto effect = [&](uint32_t w, bool& seen) {
+    const uint32_t count = w & kCountMask, e = (w & ~kPromptBit) >> kBiasShift;
+    seen = penal && (count > 0 || (w & kPromptBit));
+    float off = e ? __ldg(R.bias + (int64_t)b * R.bias_n + e - 1) : 0.0f;
+    if (count > 0) off = off - fre * (float)count - pre;
+    return off;
+  };
   for (int v0 = threadIdx.x * VEC; v0 < len; v0 += kRuleThreads * VEC * GROUPS) {  // VEC divides V and the stretch
-    uint32_t c[GROUPS][VEC], any[GROUPS];
+    float off[GROUPS][VEC];
+    uint32_t seen[GROUPS];  // bit i: token i is; bit 31: some token's logit changes
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
       const int v = v0 + g * kRuleThreads * VEC;
-      any[g] = 0;
+      uint32_t w[VEC], any = 0;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        c[g][i] = v < len ? word[v + i] : 0;
-        any[g] |= c[g][i];
+        w[i] = v < len ? word[v + i] : 0;
+        any |= w[i];
+        off[g][i] = 0.0f;
+      }
+      seen[g] = any ? 1u << 31 : 0;
+      if (any) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          bool s;
+          off[g][i] = effect(w[i], s);
+          seen[g] |= (uint32_t)s << i;
+        }
       }
     }
     for (int t0 = 0; t0 < rows; t0 += kRowsAhead) {
@@ -179,24 +200,23 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(const __grid_consta
         for (int g = 0; g < GROUPS; ++g) {
           const int v = v0 + g * kRuleThreads * VEC;
           if (v >= len) continue;
-          if (d >= v && d < v + VEC) {
+          if (d >= v && d < v + VEC) {  // this thread's word alone: from here on the draft counts
+            const uint32_t w = ++word[d];
+            bool s;
+            const float o = effect(w, s);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) c[g][i] += i == d - v;
-            any[g] |= 1;
+            for (int i = 0; i < VEC; ++i)
+              if (i == d - v) off[g][i] = o;
+            seen[g] |= 1u << 31 | 1u << (d - v);
           }
-          if (any[g] || allowed[r][g] != kAll) {
+          if (seen[g] || allowed[r][g] != kAll) {
             float x[VEC];
             unpack<BF16, VEC>(raw[r][g].w, x);
-            if (any[g]) {
+            if (seen[g]) {
 #pragma unroll
               for (int i = 0; i < VEC; ++i) {
-                const uint32_t count = c[g][i] & kCountMask;
-                if (penal) {
-                  if (count > 0 || (c[g][i] & kPromptBit)) x[i] = x[i] > 0.0f ? x[i] / rep : x[i] * rep;
-                  if (count > 0) x[i] = x[i] - fre * (float)count - pre;
-                }
-                const uint32_t e = (c[g][i] & ~kPromptBit) >> kBiasShift;
-                if (e) x[i] += __ldg(R.bias + (int64_t)b * R.bias_n + e - 1);
+                const float f = x[i] > 0.0f ? inv : rep;
+                x[i] = fmaf(x[i], (seen[g] >> i) & 1u ? f : 1.0f, off[g][i]);
               }
             }
 #pragma unroll
