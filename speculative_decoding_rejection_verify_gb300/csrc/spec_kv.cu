@@ -72,8 +72,22 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     if (P.flags && flag && threadIdx.x == 0) atomicOr(P.flags + b, flag);
     return;
   }
-  const int64_t at = slot_offset(P.batch, P.cache, b, ctx + t);
-  if (at < 0 || held < 0) flag |= SPEC_FLAG_BAD_SLOT;
+  const char* q = P.q.data + b * P.q.row + t * P.q.token;
+  const char* k = P.k.data + b * P.k.row + t * P.k.token;
+  const char* v = P.v.data + b * P.v.row + t * P.v.token;
+  const int k_end = P.q_heads + P.heads, end = k_end + P.heads;
+  uint4 w0[kAhead], w1[kAhead];
+  const auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * lanes;
+      if (h >= end) break;
+      const char* p = h < P.q_heads ? q + h * P.q.head : h < k_end ? k + (h - P.q_heads) * P.k.head : v + (h - k_end) * P.v.head;
+      w0[i] = *reinterpret_cast<const uint4*>(p + lo * 2);
+      if (pair) w1[i] = *reinterpret_cast<const uint4*>(p + (lo + far) * 2);
+    }
+  };
+  load(head0);  // before the page and the angles are known
 
   // cos and sin of the unit: 8 pairs half-split, 4 pairs interleaved
   float co[8], si[8];
@@ -94,23 +108,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
       }
     }
   }
+  const int64_t at = slot_offset(P.batch, P.cache, b, ctx + t);
+  if (at < 0 || held < 0) flag |= SPEC_FLAG_BAD_SLOT;
   if (P.flags && flag && threadIdx.x == 0) atomicOr(P.flags + b, flag);
 
-  const char* q = P.q.data + b * P.q.row + t * P.q.token;
-  const char* k = P.k.data + b * P.k.row + t * P.k.token;
-  const char* v = P.v.data + b * P.v.row + t * P.v.token;
   char* o = P.q_out.data + b * P.q_out.row + t * P.q_out.token;
-  const int k_end = P.q_heads + P.heads, end = at < 0 ? P.q_heads : k_end + P.heads;
   for (int h0 = head0; h0 < end; h0 += lanes * kAhead) {
-    uint4 w0[kAhead], w1[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int h = h0 + i * lanes;
-      if (h >= end) break;
-      const char* p = h < P.q_heads ? q + h * P.q.head : h < k_end ? k + (h - P.q_heads) * P.k.head : v + (h - k_end) * P.v.head;
-      w0[i] = *reinterpret_cast<const uint4*>(p + lo * 2);
-      if (pair) w1[i] = *reinterpret_cast<const uint4*>(p + (lo + far) * 2);
-    }
+    if (h0 > head0) load(h0);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int h = h0 + i * lanes;
@@ -138,7 +142,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
       if (h < P.q_heads) {
         *reinterpret_cast<uint4*>(o + h * P.q_out.head + lo * 2) = pack8(x);
         if (pair) *reinterpret_cast<uint4*>(o + h * P.q_out.head + (lo + far) * 2) = pack8(y);
-      } else {
+      } else if (at >= 0) {
         constexpr int ES = F8 ? 1 : 2;
         const int hh = h < k_end ? h - P.q_heads : h - k_end;
         const float* scales = h < k_end ? P.cache.k_scale : P.cache.v_scale;
@@ -164,41 +168,70 @@ struct KeepParams {
 };
 
 constexpr int kKeepThreads = 256;
-constexpr int kKeepAhead = 8;   // entries a thread loads before it stores the first
-constexpr int kKeepRound = 64;  // moves whose places the block works out at a time
+constexpr int kKeepColumns = 4;  // columns a thread takes together,
+constexpr int kKeepAhead = 4;    // and entries of each that it loads before it stores the first
+constexpr int kKeepRound = 64;   // moves whose places the block works out at a time
 
-// Block (x, y): 256 columns of request y's entries.  A column is one 16-byte vector (layer, k or v, head,
-// vector) of every slot, and one thread moves it through the path in order.  A strictly increasing path
-// has path[i] >= i, so what move i overwrites (slot i) is never read by a later move: loads may run ahead
-// of stores, and columns are independent.
+// Block (x, y): every gridDim.x-th run of 256 columns of request y's entries.  A column is one 16-byte
+// vector (layer, k or v, head, vector) of every slot, and one thread moves it through the path in order.  A
+// strictly increasing path has path[i] >= i, so what move i overwrites (slot i) is never read by a later
+// move: loads may run ahead of stores, and columns are independent.
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constant__ KeepParams P) {
-  __shared__ int64_t from[kKeepRound], to[kKeepRound];  // -1: nothing to move
+  __shared__ int64_t from[kKeepRound], to[kKeepRound];
+  __shared__ int moves;
   const int b = blockIdx.y;
   const int n = min(max(__ldg(P.n_keep + b), 0), P.max_keep);
   const int ctx = batch_context(P.batch, b);
-  const int c = blockIdx.x * kKeepThreads + threadIdx.x;
-  const int head = c / P.vecs, vec = c - head * P.vecs;
-  const int side = head / P.heads, layer = side / 2;
-  char* column = (side % 2 ? P.cache.v : P.cache.k) + layer * P.cache.layer + (head - side * P.heads) * P.cache.head + vec * 16;
   for (int i0 = 0; i0 < n; i0 += kKeepRound) {
-    const int round = min(kKeepRound, n - i0);
-    if ((int)threadIdx.x < round) {
-      const int i = i0 + threadIdx.x, p = __ldg(P.path + (int64_t)b * P.max_keep + i);
-      int64_t src = -1;
-      const int64_t dst = slot_offset(P.batch, P.cache, b, ctx + i);
-      if (p != i && p >= 0 && p < P.batch.slots && dst >= 0) src = slot_offset(P.batch, P.cache, b, ctx + p);
-      from[threadIdx.x] = src, to[threadIdx.x] = dst;
+    // the moves of this round that move something, in the path's order
+    if (threadIdx.x < 32) {
+      int count = 0;
+      for (int i1 = i0; i1 < min(n, i0 + kKeepRound); i1 += 32) {
+        const int i = i1 + threadIdx.x;
+        int64_t src = -1, dst = -1;
+        if (i < n) {
+          const int p = __ldg(P.path + (int64_t)b * P.max_keep + i);
+          if (p != i && p >= 0 && p < P.batch.slots) {
+            dst = slot_offset(P.batch, P.cache, b, ctx + i);
+            src = slot_offset(P.batch, P.cache, b, ctx + p);
+          }
+        }
+        const bool is = src >= 0 && dst >= 0;
+        const uint32_t all = __ballot_sync(~0u, is);
+        if (is) {
+          const int at = count + __popc(all & ((1u << threadIdx.x) - 1));
+          from[at] = src, to[at] = dst;
+        }
+        count += __popc(all);
+      }
+      if (threadIdx.x == 0) moves = count;
     }
     __syncthreads();
-    if (c < P.columns) {
+    const int round = moves;
+    for (int c0 = blockIdx.x * kKeepThreads * kKeepColumns + threadIdx.x; c0 < P.columns;
+         c0 += gridDim.x * kKeepThreads * kKeepColumns) {
+      char* column[kKeepColumns];
+#pragma unroll
+      for (int k = 0; k < kKeepColumns; ++k) {
+        const int c = c0 + k * kKeepThreads;
+        const int head = c / P.vecs, vec = c - head * P.vecs;
+        const int side = head / P.heads, layer = side / 2;
+        column[k] = c < P.columns ? (side % 2 ? P.cache.v : P.cache.k) + layer * P.cache.layer +
+                                        (head - side * P.heads) * P.cache.head + vec * 16
+                                  : nullptr;
+      }
       for (int i = 0; i < round; i += kKeepAhead) {
-        uint4 w[kKeepAhead];
+        uint4 w[kKeepColumns][kKeepAhead];
 #pragma unroll
-        for (int j = 0; j < kKeepAhead; ++j)
-          if (i + j < round && from[i + j] >= 0) w[j] = *reinterpret_cast<const uint4*>(column + from[i + j]);
+        for (int k = 0; k < kKeepColumns; ++k)
 #pragma unroll
-        for (int j = 0; j < kKeepAhead; ++j)
-          if (i + j < round && from[i + j] >= 0) *reinterpret_cast<uint4*>(column + to[i + j]) = w[j];
+          for (int j = 0; j < kKeepAhead; ++j)
+            if (column[k] && i + j < round) w[k][j] = *reinterpret_cast<const uint4*>(column[k] + from[i + j]);
+#pragma unroll
+        for (int k = 0; k < kKeepColumns; ++k)
+#pragma unroll
+          for (int j = 0; j < kKeepAhead; ++j)
+            if (column[k] && i + j < round) *reinterpret_cast<uint4*>(column[k] + to[i + j]) = w[k][j];
       }
     }
     __syncthreads();
@@ -268,9 +301,10 @@ spec_status_t spec_kv_keep(const spec_kv_cache_t* cache, const spec_decode_batch
   P.heads = cache->heads;
   P.vecs = cache->head_dim * (cache->dtype == SPEC_DTYPE_BF16 ? 2 : 1) / 16;
   const int64_t columns = (int64_t)cache->layers * 2 * P.heads * P.vecs;
-  if (columns > 0x7fffff00ll || batch->B > 65535) return SPEC_ERR_UNSUPPORTED;
+  if (columns > 0x40000000ll || batch->B > 65535) return SPEC_ERR_UNSUPPORTED;  // column indices stay in 32 bits
   P.columns = (int)columns;
-  const dim3 grid((unsigned)((columns + kKeepThreads - 1) / kKeepThreads), batch->B);
+  const int64_t run = kKeepThreads * kKeepColumns;
+  const dim3 grid((unsigned)((columns + run - 1) / run), batch->B);
   keep_kernel<<<grid, kKeepThreads, 0, static_cast<cudaStream_t>(stream)>>>(P);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

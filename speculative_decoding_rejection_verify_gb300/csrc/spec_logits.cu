@@ -117,15 +117,22 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(const __grid_consta
   }
   if (penal) {
     const int32_t* ids = R.history + (int64_t)b * R.history_stride;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < held; i += kRuleThreads) {
-      const uint32_t v = (uint32_t)__ldg(ids + i) - (uint32_t)first;
-      if (v < (uint32_t)len) {
-        if (i < prompt)
-          atomicOr(&word[v], kPromptBit);
-        else
-          atomicAdd(&word[v], 1u);
+    constexpr int kAhead = 8;  // entries a thread loads before it counts the first
+    for (int i0 = threadIdx.x; i0 < held; i0 += kRuleThreads * kAhead) {
+      uint32_t v[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j * kRuleThreads;
+        v[j] = i < held ? (uint32_t)__ldg(ids + i) - (uint32_t)first : ~0u;
       }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (v[j] < (uint32_t)len) {
+          if (i0 + j * kRuleThreads < prompt)
+            atomicOr(&word[v[j]], kPromptBit);
+          else
+            atomicAdd(&word[v[j]], 1u);
+        }
     }
   }
   __syncthreads();
