@@ -66,25 +66,31 @@ class RulesStruct(ctypes.Structure):
 
 
 def declare(lib) -> None:
-    """The entry points' argument types."""
-    H, C, B = ctypes.POINTER(HeadsStruct), ctypes.POINTER(CacheStruct), ctypes.POINTER(BatchStruct)
-    lib.spec_kv_append.argtypes = [H, H, H, H, _I, C, B, ctypes.POINTER(RotaryStruct), _P, _P]
+    """The entry points' argument types.  Structs go as packed bytes (or ctypes.byref of the classes above)."""
+    lib.spec_kv_append.argtypes = [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P]
     lib.spec_kv_append.restype = _I
     lib.spec_paged_attention_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
     lib.spec_paged_attention_workspace_bytes.restype = _Z
-    lib.spec_paged_attention.argtypes = [H, H, _I, C, B, _P, _F, _P, _Z, _P]
+    lib.spec_paged_attention.argtypes = [_P, _P, _I, _P, _P, _P, _F, _P, _Z, _P]
     lib.spec_paged_attention.restype = _I
-    lib.spec_kv_keep.argtypes = [C, B, _P, _P, _I, _P]
+    lib.spec_kv_keep.argtypes = [_P, _P, _P, _P, _I, _P]
     lib.spec_kv_keep.restype = _I
-    lib.spec_process_logits.argtypes = [_P, _P, ctypes.POINTER(RulesStruct), _I, _I, _I, _I, _P]
+    lib.spec_process_logits.argtypes = [_P, _P, _P, _I, _I, _I, _I, _P]
     lib.spec_process_logits.restype = _I
+
+
+# The structs as bytes, field by field as in the classes above (NULL is 0).
+_pack_heads = struct.Struct("Pqqq").pack
+_pack_cache = struct.Struct("PPqqqqiiiiiiPP").pack
+_pack_batch = struct.Struct("PPPiiixxxx").pack
+_pack_rotary = struct.Struct("PPPiiixxxx").pack
+_pack_rules = struct.Struct("11Pii").pack
 
 
 # A small call's time is mostly this module's: the checks below look at a tensor once and say what is wrong
 # with it only when something is.
 _torch = None
 _raw_stream = None
-_PACK_CACHE = struct.Struct("PPqqqqiiiiiiPP").pack
 
 
 def _load():
@@ -106,8 +112,8 @@ def _fits(t, name, shape, dtype, index) -> int:
     return t.data_ptr()
 
 
-def _maybe(t, name, shape, dtype, index) -> Optional[int]:
-    return None if t is None else _fits(t, name, shape, dtype, index)
+def _maybe(t, name, shape, dtype, index) -> int:
+    return 0 if t is None else _fits(t, name, shape, dtype, index)
 
 
 def _heads(x, name, shape, index):
@@ -121,7 +127,7 @@ def _heads(x, name, shape, index):
     row, token, head, one = x.stride()
     if one != 1:
         raise ValueError(f"{name}: head_dim must be innermost")
-    return HeadsStruct(x.data_ptr(), row, token, head)
+    return _pack_heads(x.data_ptr(), row, token, head)
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, layered):
@@ -149,9 +155,8 @@ def _cache(k_cache, v_cache, k_scale, v_scale, layered):
     num_pages, page, heads, D = shape[-4:]
     ks = 0 if k_scale is None else _fits(k_scale, "k_scale", (heads,), _torch.float32, index)
     vs = 0 if v_scale is None else _fits(v_scale, "v_scale", (heads,), _torch.float32, index)
-    packed = _PACK_CACHE(k_cache.data_ptr(), v_cache.data_ptr(), layer, st[-4], st[-3], st[-2], layers, num_pages, page,
-                         heads, D, dt, ks, vs)
-    return CacheStruct.from_buffer_copy(packed), heads, D, index
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), layer, st[-4], st[-3], st[-2], layers, num_pages, page,
+                       heads, D, dt, ks, vs), heads, D, index
 
 
 def _batch(pages, ctx_len, t_per_row, B, T, index):
@@ -159,7 +164,7 @@ def _batch(pages, ctx_len, t_per_row, B, T, index):
     if pages.dim() != 2:
         raise ValueError("pages must be [B, max_pages]")
     max_pages = pages.shape[1]
-    return BatchStruct(_fits(pages, "pages", (B, max_pages), i32, index), _fits(ctx_len, "ctx_len", (B,), i32, index),
+    return _pack_batch(_fits(pages, "pages", (B, max_pages), i32, index), _fits(ctx_len, "ctx_len", (B,), i32, index),
                        _maybe(t_per_row, "t_per_row", (B,), i32, index), B, T, max_pages)
 
 
@@ -211,7 +216,7 @@ def kv_append(q, k, v, k_cache, v_cache, pages, ctx_len, cos=None, sin=None, t_p
         if sin is None or cos.dim() != 2:
             raise ValueError("cos and sin must both be [max_positions, rot_dim / 2]")
         table = tuple(cos.shape)
-        r = RotaryStruct(_fits(cos, "cos", table, torch.float32, index), _fits(sin, "sin", table, torch.float32, index),
+        r = _pack_rotary(_fits(cos, "cos", table, torch.float32, index), _fits(sin, "sin", table, torch.float32, index),
                          _maybe(positions, "positions", (B, T), torch.int32, index), 2 * table[1], table[0],
                          1 if interleaved else 0)
     f = _maybe(flags, "flags", (B,), torch.int32, index)
@@ -291,7 +296,7 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
         out = _like(logits, stream)
     o = _fits(out, "out", shape, logits.dtype, index)
     stride = nb = 0
-    hist = ids = bias_at = None
+    hist = ids = bias_at = 0
     if history is not None:
         if history.dim() != 2 or history_len is None:
             raise ValueError("history must be [B, n], with history_len")
@@ -304,7 +309,7 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
         ids = _fits(bias_ids, "bias_ids", (B, nb), i32, index)
         bias_at = _fits(bias, "bias", (B, nb), f32, index)
     row = (B,)
-    r = RulesStruct(hist, _maybe(history_len, "history_len", row, i32, index),
+    r = _pack_rules(hist, _maybe(history_len, "history_len", row, i32, index),
                     _maybe(prompt_len, "prompt_len", row, i32, index),
                     _maybe(draft, "draft", (B, T - 1), i32, index), _maybe(t_per_row, "t_per_row", row, i32, index),
                     _maybe(repetition, "repetition", row, f32, index), _maybe(presence, "presence", row, f32, index),

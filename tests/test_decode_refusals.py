@@ -22,20 +22,20 @@ def lib():
 def heads(**kw):
     a = dict(data=4096, row_stride=4096, token_stride=1024, head_stride=128)
     a.update(kw)
-    return decode.HeadsStruct(*a.values())
+    return ctypes.byref(decode.HeadsStruct(*a.values()))
 
 
 def cache(**kw):
     a = dict(k=4096, v=4096, layer_stride=0, page_stride=16 * 1024, slot_stride=1024, head_stride=128, layers=1,
              num_pages=4, page_size=16, heads=8, head_dim=128, dtype=sv.DTYPE_BF16, k_scale=None, v_scale=None)
     a.update(kw)
-    return decode.CacheStruct(*a.values())
+    return ctypes.byref(decode.CacheStruct(*a.values()))
 
 
 def batch(**kw):
     a = dict(pages=4096, ctx_len=4096, t_per_row=None, B=1, T=2, max_pages=3)
     a.update(kw)
-    return decode.BatchStruct(*a.values())
+    return ctypes.byref(decode.BatchStruct(*a.values()))
 
 
 BAD_CACHES = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(k=4104), INVALID), (dict(v=4098), INVALID),
@@ -99,7 +99,7 @@ def test_append_arguments(lib):
     assert append(lib, k=heads(data=None)) == INVALID
     assert append(lib, v=heads(data=4100)) == INVALID
     assert append(lib, k=heads(token_stride=1022)) == INVALID
-    R = decode.RotaryStruct
+    R = lambda *a: ctypes.byref(decode.RotaryStruct(*a))  # noqa: E731
     for r in (R(4096, 4096, None, 24, 9, 0), R(4096, 4096, None, -16, 9, 0), R(4096, 4096, None, 144, 9, 0),
               R(None, 4096, None, 64, 9, 0), R(4096, None, None, 64, 9, 0), R(4096, 4100, None, 64, 9, 0),
               R(4096, 4096, None, 64, 0, 0)):
@@ -142,7 +142,7 @@ def rules(**kw):
     r = decode.RulesStruct()
     for k, x in kw.items():
         setattr(r, k, x)
-    return r
+    return ctypes.byref(r)
 
 
 def shape_logits(lib, r=None, z=4096, o=4096, B=1, T=1, V=64, dtype=0):
@@ -183,7 +183,7 @@ def test_header_and_binding_agree():
 
 
 def test_structs_match_the_header(tmp_path):
-    """The binding's struct sizes and last fields' offsets are the C compiler's."""
+    """The binding's struct sizes and fields' offsets are the C compiler's, and its packed bytes lie as they do."""
     import shutil
     import subprocess
     if shutil.which("gcc") is None:
@@ -200,6 +200,12 @@ def test_structs_match_the_header(tmp_path):
     got = [int(x) for x in subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split()]
     want = [n for _, s in pairs for n in [ctypes.sizeof(s)] + [getattr(s, f[0]).offset for f in s._fields_]]
     assert got == want
+    for pack, cls in ((decode._pack_heads, decode.HeadsStruct), (decode._pack_cache, decode.CacheStruct),
+                      (decode._pack_batch, decode.BatchStruct), (decode._pack_rotary, decode.RotaryStruct),
+                      (decode._pack_rules, decode.RulesStruct)):
+        values = list(range(1, len(cls._fields_) + 1))
+        s = cls.from_buffer_copy(pack(*values))
+        assert [getattr(s, f[0]) for f in cls._fields_] == values
 
 
 def test_binding_refuses_host_tensors_and_wrong_types(lib):
