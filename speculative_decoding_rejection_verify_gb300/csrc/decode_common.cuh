@@ -48,6 +48,11 @@ __device__ __forceinline__ int batch_context(const Batch& b, int row) {
   return min(max(__ldg(b.ctx_len + row), 0), b.slots);
 }
 
+// Programmatic dependent launch: a kernel lets the next one of the stream start launching, and waits
+// itself until the one before it has finished and its writes are visible.
+__device__ __forceinline__ void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -118,6 +123,19 @@ inline spec_status_t check_batch(const spec_decode_batch_t* b, const spec_kv_cac
 }
 inline Batch batch_of(const spec_decode_batch_t* b, const spec_kv_cache_t* c) {
   return Batch{b->pages, b->ctx_len, b->t_per_row, b->B, b->T, b->max_pages, b->max_pages * c->page_size};
+}
+
+// Launches a kernel that begins with pdl_wait: its blocks may come up while the kernel before it drains.
+template <typename P>
+inline cudaError_t launch_early(void (*kern)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const P& params) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid, cfg.blockDim = block, cfg.dynamicSmemBytes = smem, cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, params);
 }
 
 // The current device and its SMs (looked up once per device).

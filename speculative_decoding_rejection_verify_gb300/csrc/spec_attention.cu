@@ -27,6 +27,7 @@
 namespace sv {
 
 constexpr int kTileSlots = 128;       // slots per tile = rows of the matrix unit
+constexpr int kItemCost = 2;          // an item's beginning and end, in tiles
 constexpr int kMaxParts = 160;        // CTAs of the stream at most (one per SM), for the workspace's size
 constexpr int kMaxRows = 128;         // query rows of one item
 constexpr float kRescale = 8.0f;      // rescale when a score passes the maximum in use by 2^8
@@ -47,7 +48,7 @@ struct AttnParams {
   float scale_log2;            // scale * log2(e)
   float* part;                 // [CTA][2][rows][D] unnormalised O
   float2* part_ml;             // [CTA][2][rows] (m in log2 units, l)
-  int4* cut;                   // [CTA] (b, head * row_groups + row group, item's last tile + 1, total) of an
+  int4* cut;                   // [CTA] (b, head * row_groups + row group, item's end, total) on the line of an
                                //       item that begins in this CTA and ends in a later one; b = -1: none
 };
 
@@ -233,13 +234,18 @@ __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lead, ui
 // ------------------------------------------------------------------------------------------------
 struct Segment {
   int b, head, row_group;
-  int tile0, tile1, tiles;        // this part of the item's tiles
-  int ctx, tokens, end;           // context, valid new tokens, end of the slots
+  int tile0, tile1, tiles;  // this part of the item's tiles
+  int ctx, tokens, end;     // context, valid new tokens, end of the slots
+  int item_end;             // where the item ends on the line
 };
 
 // Slots of a request that anything reads, and its tiles (one at least: its rows are written there).
 __device__ __forceinline__ int request_end(int ctx, int tokens, int slots) { return tokens > 0 ? min(ctx + tokens, slots) : 0; }
 __device__ __forceinline__ int request_tiles(int end) { return max(1, (end + kTileSlots - 1) / kTileSlots); }
+// An item's length on the line: its tiles, behind what beginning and ending it costs.
+__device__ __forceinline__ int request_length(int ctx, int tokens, int slots) {
+  return request_tiles(request_end(ctx, tokens, slots)) + kItemCost;
+}
 
 // Where CTA c's part of the line begins.
 __device__ __forceinline__ int line_cut(int total, int c, int ctas) { return (int)((int64_t)total * c / ctas); }
@@ -247,17 +253,17 @@ __device__ __forceinline__ int line_cut(int total, int c, int ctas) { return (in
 // Every role of a CTA walks the same part of the line by itself.
 struct Walk {
   const AttnParams& P;
-  int b, head, row_group, tile, left;
+  int b, head, row_group, at, left, stop;  // at: within the item
   int ctx, tokens, next_ctx, next_tokens;
 
-  __device__ Walk(const AttnParams& p, int b0, int offset, int count) : P(p), b(b0), left(count) {
-    head = row_group = tile = ctx = tokens = next_ctx = next_tokens = 0;
+  __device__ Walk(const AttnParams& p, int b0, int offset, int first, int count) : P(p), b(b0), left(count), stop(first + count) {
+    head = row_group = at = ctx = tokens = next_ctx = next_tokens = 0;
     if (left <= 0) return;
     ctx = batch_context(P.batch, b);
     tokens = batch_tokens(P.batch, b);
-    const int n = request_tiles(request_end(ctx, tokens, P.batch.slots));
+    const int n = request_length(ctx, tokens, P.batch.slots);
     const int index = offset / n;
-    tile = offset - index * n;
+    at = offset - index * n;
     head = index / P.row_groups;
     row_group = index - head * P.row_groups;
     prefetch();
@@ -269,25 +275,28 @@ struct Walk {
     }
   }
   __device__ bool next(Segment& s) {
-    if (left <= 0) return false;
-    s.b = b, s.head = head, s.row_group = row_group;
-    s.ctx = ctx, s.tokens = tokens, s.end = request_end(ctx, tokens, P.batch.slots);
-    s.tiles = request_tiles(s.end);
-    const int n = min(s.tiles - tile, left);
-    s.tile0 = tile, s.tile1 = tile + n;
-    left -= n;
-    tile += n;
-    if (tile == s.tiles) {
-      tile = 0;
-      if (++row_group == P.row_groups) row_group = 0, ++head;
-      if (head == P.heads) {
-        head = 0;
-        ++b;
-        ctx = next_ctx, tokens = next_tokens;
-        prefetch();
+    while (left > 0) {
+      s.b = b, s.head = head, s.row_group = row_group;
+      s.ctx = ctx, s.tokens = tokens, s.end = request_end(ctx, tokens, P.batch.slots);
+      s.tiles = request_tiles(s.end);
+      const int n = min(s.tiles + kItemCost - at, left);
+      s.tile0 = max(at - kItemCost, 0), s.tile1 = max(at + n - kItemCost, 0);
+      left -= n;
+      at += n;
+      s.item_end = stop - left + s.tiles + kItemCost - at;
+      if (at == s.tiles + kItemCost) {
+        at = 0;
+        if (++row_group == P.row_groups) row_group = 0, ++head;
+        if (head == P.heads) {
+          head = 0;
+          ++b;
+          ctx = next_ctx, tokens = next_tokens;
+          prefetch();
+        }
       }
+      if (s.tile1 > s.tile0) return true;  // else it holds nothing but an item's cost
     }
-    return true;
+    return false;
   }
 };
 
@@ -391,23 +400,8 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kProducer = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_launch_next();
 
-  // this CTA's part of the line: a scan over the requests' tiles
-  const int per_request = P.heads * P.row_groups;
-  const int chunk = (P.batch.B + S::kThreads - 1) / S::kThreads;
-  const int b_first = min((int)threadIdx.x * chunk, P.batch.B), b_last = min(b_first + chunk, P.batch.B);
-  int mine = 0;
-  for (int b = b_first; b < b_last; ++b)
-    mine += request_tiles(request_end(batch_context(P.batch, b), batch_tokens(P.batch, b), P.batch.slots)) * per_request;
-  int before = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const int x = __shfl_up_sync(~0u, before, d);
-    if (lane >= d) before += x;
-  }
-  if (lane == 31) st->warp_sum[warp] = before;
-  before -= mine;
   if (threadIdx.x == 0) {
     st->dead = 0;
     st->bad_value[0] = st->bad_value[1] = 0;
@@ -435,6 +429,23 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  pdl_wait();  // nothing before this reads or writes global memory
+
+  // this CTA's part of the line: a scan over the requests' lengths
+  const int per_request = P.heads * P.row_groups;
+  const int chunk = (P.batch.B + S::kThreads - 1) / S::kThreads;
+  const int b_first = min((int)threadIdx.x * chunk, P.batch.B), b_last = min(b_first + chunk, P.batch.B);
+  int mine = 0;
+  for (int b = b_first; b < b_last; ++b)
+    mine += request_length(batch_context(P.batch, b), batch_tokens(P.batch, b), P.batch.slots) * per_request;
+  int before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int x = __shfl_up_sync(~0u, before, d);
+    if (lane >= d) before += x;
+  }
+  if (lane == 31) st->warp_sum[warp] = before;
+  before -= mine;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -450,7 +461,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
   if (count > 0 && first >= before && first < before + mine) {
     int b = b_first, rest = first - before;
     for (;; ++b) {
-      const int n = request_tiles(request_end(batch_context(P.batch, b), batch_tokens(P.batch, b), P.batch.slots)) * per_request;
+      const int n = request_length(batch_context(P.batch, b), batch_tokens(P.batch, b), P.batch.slots) * per_request;
       if (rest < n) break;
       rest -= n;
     }
@@ -463,7 +474,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
 
   if (warp >= kSoftmaxWarps) {
     if constexpr (S::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFewRegs));
-    Walk walk(P, start_b, start_offset, count);
+    Walk walk(P, start_b, start_offset, first, count);
     Segment s;
     if (warp == kProducer) {
       // ---- TMA: Q of every segment, K and V of every tile, page by page ----
@@ -719,7 +730,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
     }
   } else {
     if constexpr (S::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kMoreRegs));
-    Walk walk(P, start_b, start_offset, count);
+    Walk walk(P, start_b, start_offset, first, count);
     Segment s;
     // ---- softmax and output; no branch around a group_sync depends on anything but the plan and votes ----
     const int wg = warp >> 2, quad = warp & 3, bar = 1 + wg;
@@ -744,6 +755,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
     uint32_t v_phase = 0;
     const auto col = [&](int j) { return (2 * j + wg) * CK; };
 
+    if (threadIdx.x == 0) P.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
     for (int seg = 0; walk.next(s); ++seg) {
       const int t0 = s.row_group * P.tokens;
       const int rows = min(max((s.tokens - t0) * P.group, 0), P.rows);  // valid ones come first
@@ -906,8 +918,10 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
             mbar_wait(smem_addr(&st->ring_full[v_slot]), v_phase, dead);
             char* v = ring + v_slot * S::kRing;
             const int from = max(s.ctx - tile * kTileSlots, 0), end = s.end - tile * kTileSlots;
+            // pages behind the last one came as zeros
+            const int stop = min(kTileSlots, end + (-s.end & ((1 << P.cache.page_shift) - 1)));
             constexpr int kVecs = D / 8;
-            for (int u = from * kVecs + (int)threadIdx.x; u < kTileSlots * kVecs; u += kSoftmaxWarps * 32) {
+            for (int u = from * kVecs + (int)threadIdx.x; u < stop * kVecs; u += kSoftmaxWarps * 32) {
               const int row = u / kVecs, vec = u % kVecs;
               uint4* p = reinterpret_cast<uint4*>(v + (vec / 8) * (kTileSlots * 128) + row * 128 + (((vec % 8) ^ (row & 7)) * 16));
               if (row >= end) {
@@ -1024,17 +1038,10 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
         }
       }
       tc_fence_before();
-      if (threadIdx.x == 0) {
-        // the cut item begins here: who joins it finds it in this CTA's record
-        const bool begins = s.tile0 == 0 && s.tile1 < s.tiles;
-        if (begins || walk.left <= 0) {
-          // the place of the item's end in the line: this CTA's end, and the tiles behind it
-          const int end = first + count + (s.tiles - s.tile1);
-          P.cut[blockIdx.x] = begins ? make_int4(s.b, s.head * P.row_groups + s.row_group, end, total) : make_int4(-1, 0, 0, 0);
-        }
-      }
+      // an item that begins here and is cut: who joins it finds it in this CTA's record
+      if (threadIdx.x == 0 && s.tile0 == 0 && s.tile1 < s.tiles)
+        P.cut[blockIdx.x] = make_int4(s.b, s.head * P.row_groups + s.row_group, s.item_end, total);
     }
-    if (count <= 0 && threadIdx.x == 0) P.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
 
   tc_fence_before();
@@ -1050,17 +1057,28 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
 // ------------------------------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 
+struct JoinParams {
+  Heads out;
+  Batch batch;
+  const float* v_scale;
+  const float* part;
+  const float2* part_ml;
+  const int4* cut;
+  int group, tokens, row_groups, rows, ctas;
+};
+
 // Block (x, y): the item that begins in CTA x and ends in a later one, rows 8 y .. 8 y + 7, a warp each.
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttnParams P, int ctas, bool f8) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ JoinParams P) {
+  pdl_launch_next();
+  pdl_wait();
   const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const int n = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
   const int4 cut = P.cut[c0];
   if (cut.x < 0 || n >= P.rows) return;
   const int b = cut.x, head = cut.y / P.row_groups, t0 = cut.y % P.row_groups * P.tokens;
   const int end = cut.z, total = cut.w;
-  ctas = min(ctas, total);
+  const int ctas = min(P.ctas, total);
   const int t = t0 + n / P.group;
   if (t >= P.batch.T) return;
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(P.out.data + b * P.out.row + t * P.out.token +
@@ -1107,7 +1125,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
       }
     }
   }
-  const float v = f8 && P.cache.v_scale ? __ldg(P.cache.v_scale + head) : 1.0f;
+  const float v = P.v_scale ? __ldg(P.v_scale + head) : 1.0f;
   const float inv = sum == 0.0f ? 0.0f : v / sum;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
@@ -1185,19 +1203,11 @@ static cudaError_t launch_attention(const AttnParams& P, int dev, int ctas, cuda
     }
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  kern<<<ctas, S::kThreads, S::kBytes, st>>>(P);
-  e = cudaGetLastError();
+  e = launch_early(kern, dim3(ctas), dim3(S::kThreads), S::kBytes, st, P);
   if (e != cudaSuccess || ctas == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (P.rows + kJoinWarps - 1) / kJoinWarps);
-  cfg.blockDim = dim3(kJoinWarps * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, P, ctas, F8);
+  const JoinParams J = {P.out, P.batch, F8 ? P.cache.v_scale : nullptr, P.part, P.part_ml, P.cut, P.group, P.tokens,
+                        P.row_groups, P.rows, ctas};
+  return launch_early(join_kernel<D>, dim3(ctas, (P.rows + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0, st, J);
 }
 
 template <int D, bool F8>
@@ -1254,9 +1264,9 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
   P.part_ml = reinterpret_cast<float2*>(ws + L.ml);
   P.cut = reinterpret_cast<int4*>(ws + L.cut);
 
-  // tiles at most: what the page table could hold
+  // the line's length at most: what the page table could hold
   const int64_t per = ((int64_t)P.batch.slots + kTileSlots - 1) / kTileSlots;
-  const int64_t most = (int64_t)batch->B * cache->heads * P.row_groups * (per > 0 ? per : 1);
+  const int64_t most = (int64_t)batch->B * cache->heads * P.row_groups * ((per > 0 ? per : 1) + kItemCost);
   if (most > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
 
   const bool f8 = cache->dtype == SPEC_DTYPE_E4M3;

@@ -49,6 +49,8 @@ __device__ __forceinline__ void store_entry(char* p, float (&x)[8], float inv_sc
 template <int D, bool F8, bool INTERLEAVED>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams P) {
   constexpr int kAhead = 4;
+  pdl_launch_next();
+  pdl_wait();
   const int paired = INTERLEAVED ? 0 : P.rot / 16;  // units that hold a vector and its partner
   const int units = D / 8 - paired, lanes = kAppendThreads / units;
   const int head0 = threadIdx.x / units, unit = threadIdx.x - head0 * units;
@@ -179,6 +181,8 @@ constexpr int kKeepRound = 64;   // moves whose places the block works out at a 
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constant__ KeepParams P) {
   __shared__ int64_t from[kKeepRound], to[kKeepRound];
   __shared__ int moves;
+  pdl_launch_next();
+  pdl_wait();
   const int b = blockIdx.y;
   const int n = min(max(__ldg(P.n_keep + b), 0), P.max_keep);
   const int ctx = batch_context(P.batch, b);
@@ -282,8 +286,7 @@ spec_status_t spec_kv_append(const spec_heads_t* q, const spec_heads_t* k, const
                         : (inter ? append_kernel<128, false, true> : append_kernel<128, false, false>))
                   : (f8 ? (inter ? append_kernel<64, true, true> : append_kernel<64, true, false>)
                         : (inter ? append_kernel<64, false, true> : append_kernel<64, false, false>));
-  kern<<<(unsigned)blocks, kAppendThreads, 0, st>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return launch_early(kern, dim3((unsigned)blocks), dim3(kAppendThreads), 0, st, P) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 spec_status_t spec_kv_keep(const spec_kv_cache_t* cache, const spec_decode_batch_t* batch, const int32_t* path,
@@ -305,8 +308,8 @@ spec_status_t spec_kv_keep(const spec_kv_cache_t* cache, const spec_decode_batch
   P.columns = (int)columns;
   const int64_t run = kKeepThreads * kKeepColumns;
   const dim3 grid((unsigned)((columns + run - 1) / run), batch->B);
-  keep_kernel<<<grid, kKeepThreads, 0, static_cast<cudaStream_t>(stream)>>>(P);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return launch_early(keep_kernel, grid, dim3(kKeepThreads), 0, static_cast<cudaStream_t>(stream), P) == cudaSuccess ? SPEC_OK
+                                                                                                                    : SPEC_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -91,6 +91,9 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(const __grid_consta
   __shared__ int draft[SPEC_MAX_NEW];               // relative to the stretch; -1: elsewhere
   const int b = blockIdx.y, first = blockIdx.x * P.stretch;
   const int len = min(P.stretch, P.V - first);
+  pdl_launch_next();
+  for (int i = threadIdx.x; i < (len + 3) / 4; i += kRuleThreads) reinterpret_cast<uint4*>(word)[i] = make_uint4(0, 0, 0, 0);
+  pdl_wait();
   const spec_logit_rules_t& R = P.r;
   const int rows = R.t_per_row ? min(max(__ldg(R.t_per_row + b), 0), P.T) : P.T;
   const float rep = R.repetition ? __ldg(R.repetition + b) : 1.0f;
@@ -100,7 +103,6 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(const __grid_consta
   const int prompt = R.history && R.prompt_len ? __ldg(R.prompt_len + b) : 0;
   const bool penal = rep != 1.0f || pre != 0.0f || fre != 0.0f;
 
-  for (int i = threadIdx.x; i < (len + 3) / 4; i += kRuleThreads) reinterpret_cast<uint4*>(word)[i] = make_uint4(0, 0, 0, 0);
   if (threadIdx.x < SPEC_MAX_NEW) {
     int d = -1;
     if (penal && R.draft && (int)threadIdx.x < rows - 1) d = __ldg(R.draft + (int64_t)b * (P.T - 1) + threadIdx.x);
@@ -249,8 +251,7 @@ static cudaError_t launch_rules(const RuleParams& P, int align, cudaStream_t st)
   else if (align % 4 == 0) kern = rules_kernel<BF16, 4 / ES, 4>;
   else kern = rules_kernel<BF16, 1, 4>;
   const dim3 grid((P.V + P.stretch - 1) / P.stretch, P.B);
-  kern<<<grid, kRuleThreads, P.stretch * sizeof(uint32_t), st>>>(P);
-  return cudaGetLastError();
+  return launch_early(kern, grid, dim3(kRuleThreads), P.stretch * sizeof(uint32_t), st, P);
 }
 
 }  // namespace sv
