@@ -32,7 +32,6 @@ constexpr int kMaxParts = 160;        // CTAs of the stream at most (one per SM)
 constexpr int kMaxRows = 128;         // query rows of one item
 constexpr float kRescale = 8.0f;      // rescale when a score passes the maximum in use by 2^8
 constexpr float kNone = 3e38f;        // shift of a row without a maximum yet: any score asks for one
-constexpr int kSoftmaxWarps = 8;      // two warpgroups, each with every other chunk of columns
 constexpr int kConvertWarps = 4;      // E4M3 caches: E4M3 -> fp16
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -118,25 +117,34 @@ __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// Products are issued by one elected lane of a warp that goes through the code together: the descriptors then
+// stay in uniform registers (measured: 43 to 55 cycles per product of 128 x 16..80 x 32 bytes, against 90 to
+// 118 from a branch that one lane takes).
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 // kind::f16 (fp16 or bf16 operands) or kind::f8f6f4 (E4M3)
 template <bool F8>
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   if constexpr (F8)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -311,41 +319,48 @@ struct Shape {
   static constexpr int kQ = NT * D * 2;                           // a Q buffer
   static constexpr int kQBufs = NT > 64 ? 1 : 2;                  // two, where the ring stays deep enough
   static constexpr int kP = kTileSlots * 128 * (NT > 64 ? 2 : 1); // P^T, 128 bytes a slot and 64 rows
-  static constexpr int kFixed = kQBufs * kQ + kP + (F8 ? kTile16 : 0);
+  static constexpr int kFixed = kQBufs * kQ + kP + (F8 ? 2 * kTile16 : 0);
   static constexpr int kBudget = 232448 - 1024 - 6144;            // 227 KB, alignment, barriers and row states
   static constexpr int kFit = (kBudget - kFixed) / kRing;
   static constexpr int kSlots = kFit > 8 ? 8 : F8 ? kFit / 2 * 2 : kFit;  // K and V tiles in flight (E4M3: V in odd slots)
   static_assert(kSlots >= 4, "the ring holds two tiles of K and V at least");
-  // Registers: the variants with many columns take more for the softmax warps than an even split of the
-  // SM's gives them, and less for the others.  Per warpgroup of 128 threads, of 512 in all:
-  // 3 x 168 = 504 = 2 x 208 + 88, and 4 x 128 = 512 = 2 x 176 + 2 x 80.
-  static constexpr bool kSplit = NT > 32 || (F8 && NT > 16);
-  static constexpr int kThreads = F8 ? 512 : 384;
-  static constexpr int kLaunchRegs = F8 ? 128 : 168, kMoreRegs = F8 ? 176 : 208, kFewRegs = F8 ? 80 : 88;
-  static_assert(2 * kMoreRegs + (kThreads / 128 - 2) * kFewRegs <= kThreads / 128 * kLaunchRegs, "register split");
+  // Softmax warpgroups, each with every kGroups-th chunk of columns: a tile is a chain of short steps, and
+  // warps are what hides their latencies.
+  static constexpr int kGroups = NT >= 64 ? 4 : 2;
+  static constexpr int kSoftmaxWarps = 4 * kGroups;
+  static constexpr int kProducer = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1;
+  static constexpr int kThreads = kSoftmaxWarps * 32 + (F8 ? 256 : 128);
+  // Registers: the softmax warps take more than an even split of the SM's gives them, the others less.  Per
+  // warpgroup of 128 threads: 4 x 128 = 512 = 2 x 176 + 2 x 80 and 6 x 80 = 480 = 4 x 88 + 2 x 64 with E4M3;
+  // 5 x 96 = 480 = 4 x 104 + 64 with bf16.
+  static constexpr bool kSplit = kGroups == 4 || (F8 && NT > 16);
+  static constexpr int kLaunchRegs = kGroups == 4 ? (F8 ? 80 : 96) : F8 ? 128 : 168;
+  static constexpr int kMoreRegs = kGroups == 4 ? (F8 ? 88 : 104) : 176, kFewRegs = kGroups == 4 ? 64 : 80;
+  static_assert(!kSplit || kGroups * kMoreRegs + (kThreads / 128 - kGroups) * kFewRegs <= kThreads / 128 * kLaunchRegs,
+                "register split");
   static constexpr int kColumns = 3 * NT <= 64 ? 64 : 3 * NT <= 128 ? 128 : 3 * NT <= 256 ? 256 : 512;
-  static constexpr int kChunk = NT >= 32 ? 16 : 8;                // columns a warpgroup takes at a time
-  static constexpr int kChunks = NT / (2 * kChunk);               // chunks of one warpgroup
-  static constexpr int kWords = NT > 64 ? 2 : 1;                  // 32-column words of one warpgroup
-  static constexpr bool kKeep = NT <= 64;                         // scores stay in registers over the vote
+  static constexpr int kChunk = NT == 32 ? 16 : 8;                // columns a warpgroup takes at a time
+  static constexpr int kOwn = NT / kGroups;                       // columns of one warpgroup
+  static constexpr int kChunks = kOwn / kChunk;
+  static_assert(kOwn <= 32, "a warpgroup's columns fit a word");
 
   struct State {
     uint64_t ring_full[8], ring_empty[8];
     uint64_t q_loaded[2], q_full[2], q_empty[2], mult_full[2];
-    uint64_t v16_full, v16_empty;
+    uint64_t v16_full[2], v16_empty[2];
     uint64_t s_full[2], s_empty[2], p_full, o_full;
     uint32_t tmem;
     int dead;
     int start_b, start_offset, total;
-    uint32_t bad_value[2];           // segment + 1 whose new tokens hold a value that is not finite
-    int warp_sum[16];
-    alignas(16) float shift[NT];     // minus the row's maximum in use, what is added to a score (see kNone)
+    uint32_t bad_value[4];           // segment + 1 whose new tokens hold a value that is not finite, by segment % 4
+    int warp_sum[24];
+    alignas(16) float shift[NT];     // what is added to a score: minus the row's maximum in use (see kNone, kLift)
     alignas(16) float top[NT];       // the maximum in use, -inf for none
     alignas(16) float factor[NT];    // a rescale's factor; 1 / l at the end
     float red[4][NT];
     alignas(16) float mult[2][NT];   // E4M3: a score's factor to log2 units, by the segment's parity
     alignas(16) int64_t place[NT];   // the row's offset in the item's output
-    uint64_t seen[2][SPEC_MAX_NEW];  // which columns of each warpgroup attend to a new token
+    uint32_t seen[kGroups][SPEC_MAX_NEW];  // which columns of each warpgroup attend to a new token
   };
   static constexpr int kState = kFixed + kSlots * kRing;
   static constexpr int kBytes = kState + (int)sizeof(State) + 1024;
@@ -394,17 +409,17 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
   char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
   char* q_buf = smem;                                     // [kQBufs][halves][NT][128 B]
   char* p_buf = q_buf + S::kQBufs * S::kQ;                     // [NT > 64 ? 2 : 1][128][128 B]
-  char* v16 = p_buf + S::kP;                              // E4M3: V in fp16, [halves][128][128 B]
-  char* ring = v16 + (F8 ? S::kTile16 : 0);
+  char* v16 = p_buf + S::kP;                              // E4M3: V in fp16, [2][halves][128][128 B]
+  char* ring = v16 + (F8 ? 2 * S::kTile16 : 0);
   auto* st = reinterpret_cast<typename S::State*>(smem + S::kState);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kProducer = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1;
+  constexpr int kSoftmaxWarps = S::kSoftmaxWarps, kProducer = S::kProducer, kIssuer = S::kIssuer;
 
   pdl_launch_next();
 
   if (threadIdx.x == 0) {
     st->dead = 0;
-    st->bad_value[0] = st->bad_value[1] = 0;
+    for (int i = 0; i < 4; ++i) st->bad_value[i] = 0;
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(smem_addr(&st->ring_full[i]), 1);
       mbar_init(smem_addr(&st->ring_empty[i]), F8 && i % 2 ? kConvertWarps : 1);
@@ -416,9 +431,9 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
       mbar_init(smem_addr(&st->q_empty[i]), 1);
       mbar_init(smem_addr(&st->s_full[i]), 1);
       mbar_init(smem_addr(&st->s_empty[i]), kSoftmaxWarps);
+      mbar_init(smem_addr(&st->v16_full[i]), kConvertWarps);
+      mbar_init(smem_addr(&st->v16_empty[i]), 1);
     }
-    mbar_init(smem_addr(&st->v16_full), kConvertWarps);
-    mbar_init(smem_addr(&st->v16_empty), 1);
     mbar_init(smem_addr(&st->p_full), kSoftmaxWarps);
     mbar_init(smem_addr(&st->o_full), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -533,91 +548,91 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
           }
         }
     } else if (warp == kIssuer) {
-      // ---- matrix products: scores of the next tile or weighted values of an earlier one, as either is ready ----
-      if (lane == 0) {
-        const uint32_t n16 = (P.rows + 15) / 16 * 16;
-        const uint32_t shape = 1u << 4 | (n16 >> 3) << 17 | (128u >> 4) << 24;  // fp32 accumulators, M = 128
-        const uint32_t s_desc = shape | (F8 ? 0u : 1u << 7 | 1u << 10);         // E4M3 or bf16 operands
-        // fp16 or bf16 operands, both with the reduction outside
-        const uint32_t o_desc = shape | (F8 ? 0u : 1u << 7 | 1u << 10) | 1u << 15 | 1u << 16;
-        const uint32_t o_col = tmem + 2 * NT;
-        const uint32_t p_addr = smem_addr(p_buf);
-        uint32_t s_it = 0, v_it = 0;  // tiles whose scores, and whose values, are issued
-        int k_slot = 0, v_slot = 1;
-        uint32_t k_phase = 0, v_phase = 0, first_bits = 0;
-        const auto advance = [&](int& slot, uint32_t& phase) {
-          slot += 2;
-          if (slot >= S::kSlots) slot -= S::kSlots, phase ^= 1;
-        };
-        int seg = 0, tile = 0, idle = 0;
-        bool more = walk.next(s);
-        tile = s.tile0;
-        while (more || v_it < s_it) {
-          bool moved = false;
-          if (more && s_it - v_it < 2) {
-            const int qb = seg % S::kQBufs, sb = s_it & 1;
-            if (mbar_test(smem_addr(&st->ring_full[k_slot]), k_phase) &&
-                (tile != s.tile0 || mbar_test(smem_addr(F8 ? &st->q_full[qb] : &st->q_loaded[qb]), (seg / S::kQBufs) & 1)) &&
-                mbar_test(smem_addr(&st->s_empty[sb]), ((s_it >> 1) & 1) ^ 1)) {
-              tc_fence_after();
-              const uint32_t a = smem_addr(ring + k_slot * S::kRing), b = smem_addr(q_buf + qb * S::kQ);
+      // ---- matrix products: weighted values of a tile or scores of the next, as either is ready ----
+      const auto uniform = [](uint32_t x) { return __shfl_sync(~0u, x, 0); };
+      const auto ready = [](uint32_t bar, uint32_t parity) { return __all_sync(~0u, mbar_test(bar, parity)); };
+      const uint32_t n16 = uniform((P.rows + 15) / 16 * 16);
+      const uint32_t shape = 1u << 4 | (n16 >> 3) << 17 | (128u >> 4) << 24;  // fp32 accumulators, M = 128
+      const uint32_t s_idesc = shape | (F8 ? 0u : 1u << 7 | 1u << 10);        // E4M3 or bf16 operands
+      // fp16 or bf16 operands, both with the reduction outside
+      const uint32_t o_idesc = shape | (F8 ? 0u : 1u << 7 | 1u << 10) | 1u << 15 | 1u << 16;
+      const uint32_t base = uniform(smem_addr(smem)), cols = uniform(tmem), bars = uniform(smem_addr(st));
+      const auto bar_of = [&](const uint64_t* x) { return bars + (uint32_t)(reinterpret_cast<const char*>(x) - reinterpret_cast<const char*>(st)); };
+      const uint32_t ring_at = base + (uint32_t)(ring - smem), v16_at = base + (uint32_t)(v16 - smem);
+      const uint64_t q_desc = matrix_desc(base + (uint32_t)(q_buf - smem), 16, 1024);
+      const uint64_t k_desc = F8 ? matrix_desc<D>(ring_at, 16, 8 * D) : matrix_desc(ring_at, 16, 1024);
+      // head_dim 64: the instruction's rows 64..127 repeat rows 0..63 and are not read
+      const uint64_t v_desc = matrix_desc(F8 ? v16_at : ring_at, D == 128 ? kTileSlots * 128 : 0, 1024);
+      const uint64_t p_desc = matrix_desc(base + (uint32_t)(p_buf - smem), kTileSlots * 128, 1024);
+      const auto ahead = [](int bytes) { return (uint64_t)(bytes >> 4); };  // of a descriptor's address
+      uint32_t s_it = 0, v_it = 0;  // tiles whose scores, and whose values, are issued
+      int k_slot = 0, v_slot = 1;
+      uint32_t k_phase = 0, v_phase = 0, first_bits = 0;
+      const auto advance = [&](int& slot, uint32_t& phase) {
+        slot += 2;
+        if (slot >= S::kSlots) slot -= S::kSlots, phase ^= 1;
+      };
+      int seg = 0, idle = 0;
+      bool more = uniform(walk.next(s));
+      int tile0 = uniform(s.tile0), tile1 = uniform(s.tile1), tile = tile0;
+      while (more || v_it < s_it) {
+        bool moved = false;
+        if (v_it < s_it && ready(bar_of(&st->p_full), v_it & 1) &&
+            (F8 ? ready(bar_of(&st->v16_full[v_it & 1]), (v_it >> 1) & 1) : ready(bar_of(&st->ring_full[v_slot]), v_phase))) {
+          tc_fence_after();
+          const uint32_t add = ((first_bits >> (v_it & 1)) & 1) ^ 1;
+          const uint64_t a = v_desc + ahead(F8 ? (int)(v_it & 1) * S::kTile16 : v_slot * S::kRing);
+#pragma unroll
+          for (int k = 0; k < kTileSlots / 16; ++k)
+            tc_mma<false>(cols + 2 * NT, a + ahead(k * 2048), p_desc + ahead(k * 2048), o_idesc, k > 0 ? 1u : add);
+          tc_commit(bar_of(&st->o_full));
+          tc_commit(bar_of(F8 ? &st->v16_empty[v_it & 1] : &st->ring_empty[v_slot]));
+          advance(v_slot, v_phase);
+          ++v_it;
+          moved = true;
+        }
+        if (more && s_it - v_it < 2) {
+          const int qb = seg % S::kQBufs, sb = s_it & 1;
+          if (ready(bar_of(&st->ring_full[k_slot]), k_phase) &&
+              (tile != tile0 || ready(bar_of(F8 ? &st->q_full[qb] : &st->q_loaded[qb]), (seg / S::kQBufs) & 1)) &&
+              ready(bar_of(&st->s_empty[sb]), ((s_it >> 1) & 1) ^ 1)) {
+            tc_fence_after();
+            const uint64_t a = k_desc + ahead(k_slot * S::kRing), b = q_desc + ahead(qb * S::kQ);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
               if constexpr (F8) {
                 // q = (its 4 upper bits) + (the others), each in E4M3: see the split below
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                  const int part = k / (D / 32), in = (k % (D / 32)) * 32;
-                  tc_mma<true>(tmem + sb * NT, matrix_desc<D>(a + in, 16, 8 * D),
-                               matrix_desc(b + part * (D == 128 ? NT * 128 : 64) + in, 16, 1024), s_desc, k > 0);
-                }
+                const int part = k / (D / 32), in = (k % (D / 32)) * 32;
+                tc_mma<true>(cols + sb * NT, a + ahead(in), b + ahead(part * (D == 128 ? NT * 128 : 64) + in), s_idesc, k > 0);
               } else {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                  const int half = k / 4, in = (k % 4) * 32;
-                  tc_mma<false>(tmem + sb * NT, matrix_desc(a + half * (kTileSlots * 128) + in, 16, 1024),
-                                matrix_desc(b + half * (NT * 128) + in, 16, 1024), s_desc, k > 0);
-                }
+                const int half = k / 4, in = (k % 4) * 32;
+                tc_mma<false>(cols + sb * NT, a + ahead(half * (kTileSlots * 128) + in), b + ahead(half * (NT * 128) + in),
+                              s_idesc, k > 0);
               }
-              tc_commit(smem_addr(&st->ring_empty[k_slot]));
-              tc_commit(smem_addr(&st->s_full[sb]));
-              advance(k_slot, k_phase);
-              first_bits = (first_bits & ~(1u << sb)) | (uint32_t)(tile == s.tile0) << sb;
-              ++s_it;
-              if (++tile == s.tile1) {
-                tc_commit(smem_addr(&st->q_empty[qb]));
-                ++seg;
-                more = walk.next(s);
-                tile = s.tile0;
-              }
-              moved = true;
             }
-          }
-          if (v_it < s_it && mbar_test(smem_addr(&st->p_full), v_it & 1) &&
-              (F8 ? mbar_test(smem_addr(&st->v16_full), v_it & 1) : mbar_test(smem_addr(&st->ring_full[v_slot]), v_phase))) {
-            tc_fence_after();
-            const bool first = (first_bits >> (v_it & 1)) & 1;
-            const uint32_t a = smem_addr(F8 ? v16 : ring + v_slot * S::kRing);
-            // head_dim 64: the instruction's rows 64..127 repeat rows 0..63 and are not read
-            const uint32_t lead = D == 128 ? kTileSlots * 128 : 0;
-#pragma unroll
-            for (int k = 0; k < kTileSlots / 16; ++k)
-              tc_mma<false>(o_col, matrix_desc(a + k * 2048, lead, 1024), matrix_desc(p_addr + k * 2048, kTileSlots * 128, 1024),
-                            o_desc, !first || k > 0);
-            tc_commit(smem_addr(F8 ? &st->v16_empty : &st->ring_empty[v_slot]));
-            tc_commit(smem_addr(&st->o_full));
-            advance(v_slot, v_phase);
-            ++v_it;
+            tc_commit(bar_of(&st->s_full[sb]));
+            tc_commit(bar_of(&st->ring_empty[k_slot]));
+            advance(k_slot, k_phase);
+            first_bits = (first_bits & ~(1u << sb)) | (uint32_t)(tile == tile0) << sb;
+            ++s_it;
+            if (++tile == tile1) {
+              tc_commit(bar_of(&st->q_empty[qb]));
+              ++seg;
+              more = uniform(walk.next(s));
+              tile0 = uniform(s.tile0), tile1 = uniform(s.tile1), tile = tile0;
+            }
             moved = true;
           }
-          if (moved) {
-            idle = 0;
-          } else if (++idle > (1 << 24) || ((idle & 255) == 0 && *dead)) {
-            *dead = 1;
-            break;
-          }
         }
-        if (*dead && s_it > 0)  // a wait ran out: let the products in flight end before TMEM is freed
-          for (int n = 0; n < (1 << 16); ++n) __nanosleep(20);
+        if (moved) {
+          idle = 0;
+        } else if (++idle > (1 << 24) || ((idle & 255) == 0 && uniform(*dead))) {
+          *dead = 1;
+          break;
+        }
       }
+      if (uniform(*dead) && s_it > 0)  // a wait ran out: let the products in flight end before TMEM is freed
+        for (int n = 0; n < (1 << 16); ++n) __nanosleep(20);
       __syncwarp();
     } else if (F8 && warp > kIssuer && warp <= kIssuer + kConvertWarps) {
       // ---- E4M3 caches: Q split for the product with K as it is; V to fp16 (exact) for that with P ----
@@ -628,6 +643,8 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
       for (int seg = 0; ok && walk.next(s); ++seg) {
         const int qb = seg % S::kQBufs;
         ok = mbar_wait_warp(smem_addr(&st->q_loaded[qb]), (seg / S::kQBufs) & 1, dead);
+        // the tile before the last is done with: so are the factors of the segment before the last
+        ok = ok && mbar_wait_warp(smem_addr(&st->v16_empty[it & 1]), ((it >> 1) & 1) ^ 1, dead);
         if (!ok) break;
         // A row is scaled by a power of two to a largest element in [128, 256), and its 8-bit significands
         // split into E4M3's 4 bits and a remainder of 4: exact but for elements under 2^-9 of the largest,
@@ -676,7 +693,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
 
         for (int tile = s.tile0; ok && tile < s.tile1; ++tile, ++it) {
           ok = ok && mbar_wait_warp(smem_addr(&st->ring_full[slot]), phase, dead);
-          ok = ok && mbar_wait_warp(smem_addr(&st->v16_empty), (it & 1) ^ 1, dead);
+          ok = ok && mbar_wait_warp(smem_addr(&st->v16_empty[it & 1]), ((it >> 1) & 1) ^ 1, dead);
           if (!ok) break;
           // a slot per thread: its vectors lie in different banks from its neighbours' by the swizzle, in the
           // ring and in fp16
@@ -702,9 +719,9 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
                 x[j] = at < s.end ? x[j] & ~nan : 0u;
               }
             }
-            if (bad && at < s.end) st->bad_value[seg & 1] = seg + 1;
+            if (bad && at < s.end) st->bad_value[seg & 3] = seg + 1;
           }
-          char* out = v16 + row * 128;
+          char* out = v16 + (it & 1) * S::kTile16 + row * 128;
           const int sw16 = row & 7;
 #pragma unroll
           for (int v = 0; v < D / 16; ++v) {
@@ -720,7 +737,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(smem_addr(&st->v16_full));
+            mbar_arrive(smem_addr(&st->v16_full[it & 1]));
             mbar_arrive(smem_addr(&st->ring_empty[slot]));
           }
           slot += 2;
@@ -737,23 +754,21 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
     const int key = quad * 32 + lane, wtid = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     constexpr int CK = S::kChunk;
-    const auto row_of = [&](int own) { return ((own / CK) * 2 + wg) * CK + own % CK; };  // of the warpgroup's columns
-    const int my_row = row_of(wtid);  // wtid < NT / 2
-    if (wtid < NT / 2) {
+    const auto row_of = [&](int own) { return ((own / CK) * S::kGroups + wg) * CK + own % CK; };  // of the warpgroup's columns
+    const int my_row = row_of(wtid);  // wtid < kOwn
+    if (wtid < S::kOwn) {
       const int t = my_row / P.group, g = my_row - t * P.group;
       st->place[my_row] = (int64_t)t * P.out.token + (int64_t)g * P.out.head;
     }
-    int rule_row[S::kWords], rule_token[S::kWords];  // this lane's columns and their tokens, for the ballots
-#pragma unroll
-    for (int w = 0; w < S::kWords; ++w) {
-      rule_row[w] = w * 32 + lane < NT / 2 ? row_of(w * 32 + lane) : kMaxRows;
-      rule_token[w] = rule_row[w] / P.group;
-    }
+    // this lane's column and its token, for the ballots
+    const int rule_row = lane < S::kOwn ? row_of(lane) : kMaxRows, rule_token = rule_row / P.group;
+    // fp16 weights are lifted to a largest of 2^7 (2^15 before a rescale), so they reach down to 2^-31 of it
+    constexpr float kLift = F8 ? 7.0f : 0.0f;
     float l[S::kChunks][CK];
     uint32_t it = 0;
     int v_slot = 1;
     uint32_t v_phase = 0;
-    const auto col = [&](int j) { return (2 * j + wg) * CK; };
+    const auto col = [&](int j) { return (S::kGroups * j + wg) * CK; };
 
     if (threadIdx.x == 0) P.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
     for (int seg = 0; walk.next(s); ++seg) {
@@ -763,23 +778,18 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
       const float* mult = st->mult[seg & 1];
       const float v_scale = F8 && P.cache.v_scale ? __ldg(P.cache.v_scale + s.head) : 1.0f;
       group_sync(bar);  // the last segment's row states are read
-      if (wtid < NT / 2) {
+      if (wtid < S::kOwn) {
         st->top[my_row] = -INFINITY;
         st->shift[my_row] = my_row < rows ? kNone : -INFINITY;  // rows that are none: weights 0, and no vote
       }
       if (s.tile1 * kTileSlots > s.ctx) {  // new tokens among the slots: who attends to which
-        uint64_t rule[S::kWords];
-#pragma unroll
-        for (int w = 0; w < S::kWords; ++w) {
-          const int t = t0 + rule_token[w];
-          rule[w] = 0;
-          if (rule_row[w] < rows)
-            rule[w] = P.mask ? (uint64_t)__ldg(P.mask + (int64_t)s.b * P.batch.T + t) : t >= 63 ? ~0ull : (2ull << t) - 1;
-        }
+        uint64_t rule = 0;
+        const int t = t0 + rule_token;
+        if (rule_row < rows)
+          rule = P.mask ? (uint64_t)__ldg(P.mask + (int64_t)s.b * P.batch.T + t) : t >= 63 ? ~0ull : (2ull << t) - 1;
         for (int i = quad; i < s.tokens; i += 4) {
-          const uint32_t lo = __ballot_sync(~0u, (rule[0] >> i) & 1);
-          const uint32_t hi = S::kWords > 1 ? __ballot_sync(~0u, (rule[S::kWords - 1] >> i) & 1) : 0;
-          if (lane == 0) st->seen[wg][i] = lo | (uint64_t)hi << 32;
+          const uint32_t word = __ballot_sync(~0u, (rule >> i) & 1);
+          if (lane == 0) st->seen[wg][i] = word;
         }
       }
       if constexpr (F8) mbar_wait(smem_addr(&st->mult_full[seg & 1]), (seg >> 1) & 1, dead);
@@ -798,10 +808,10 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
 
         const auto weigh = [&](auto tag) {
           constexpr bool MASKED = decltype(tag)::value;  // the tile reaches past the context
-          uint64_t see = ~0ull;                          // columns that attend to this thread's slot
+          uint32_t see = ~0u;                            // columns that attend to this thread's slot
           if constexpr (MASKED) {
             const int slot = tile * kTileSlots + key, fresh = slot - s.ctx;
-            see = slot >= s.end ? 0 : fresh < 0 ? ~0ull : st->seen[wg][fresh];
+            see = slot >= s.end ? 0 : fresh < 0 ? ~0u : st->seen[wg][fresh];
           }
           const auto sees = [&](int j, int i) { return !MASKED || ((see >> (j * CK + i)) & 1); };
           const auto scores = [&](int j, float (&z)[CK]) {  // in log2 units, less the maximum in use
@@ -815,28 +825,55 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
               z[i] = a.x, z[i + 1] = a.y, z[i + 2] = b.x, z[i + 3] = b.y;
             }
           };
-          float z[S::kKeep ? S::kChunks : 1][CK];
-          const auto take = [&](int j) -> float (&)[CK] { return z[S::kKeep ? j : 0]; };
-
-          bool o_done = it == 0;
+          // One pass makes scores and weights with the maximum in use and adds the weights up; a vote on the
+          // largest weight then says whether they stand.
+          uint32_t p[S::kChunks][CK / 2];
+          uint32_t over = 0;  // two fp16 or bf16 weights
+          const auto weights = [&](int j) {
+            float z[CK];
+            scores(j, z);
+#pragma unroll
+            for (int i = 0; i < CK; i += 2) {
+              if (!sees(j, i)) z[i] = -INFINITY;
+              if (!sees(j, i + 1)) z[i + 1] = -INFINITY;
+              const float2 w = make_float2(exp2_approx(z[i]), exp2_approx(z[i + 1]));
+              const float2 sum = add2(make_float2(l[j][i], l[j][i + 1]), w);
+              l[j][i] = sum.x, l[j][i + 1] = sum.y;
+              // the weights' rounding: bf16 to go with a bf16 cache (2^-8 of each at most), fp16 with E4M3
+              if constexpr (F8) {
+                const __half2 h = __floats2half2_rn(w.x, w.y), m = __hmax2(h, *reinterpret_cast<const __half2*>(&over));
+                p[j][i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                over = *reinterpret_cast<const uint32_t*>(&m);
+              } else {
+                p[j][i / 2] = pack_bf16(w.x, w.y);
+                const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&p[j][i / 2]),
+                                                 *reinterpret_cast<const __nv_bfloat162*>(&over));
+                over = *reinterpret_cast<const uint32_t*>(&m);
+              }
+            }
+          };
           bool raise = tile == s.tile0;
           if (!raise) {
-            float over = -INFINITY;
 #pragma unroll
             for (int j = 0; j < S::kChunks; ++j)
-              if (col(j) < rows) {
-                auto& x = take(j);
-                scores(j, x);
-#pragma unroll
-                for (int i = 0; i < CK; ++i) over = fmaxf(over, sees(j, i) ? x[i] : -INFINITY);
-              }
-            raise = group_any(bar, over > kRescale);
+              if (col(j) < rows) weights(j);
+            // in either type a larger non-negative weight has the larger bits
+            const uint32_t most = F8 ? (uint32_t)(15 + kRescale + kLift) << 10 : (uint32_t)(127 + kRescale) << 7;
+            raise = group_any(bar, (over & 0xFFFF) > most || (over >> 16) > most);
           }
           if (raise) {
 #pragma unroll
             for (int j = 0; j < S::kChunks; ++j)
               if (col(j) < rows) {
                 float x[CK];
+                if (tile > s.tile0) {  // take the weights back; those over 2^100 leave nothing of what was there before
+                  scores(j, x);
+#pragma unroll
+                  for (int i = 0; i < CK; ++i) {
+                    const float w = sees(j, i) ? exp2_approx(x[i]) : 0.0f;
+                    l[j][i] = w < 0x1p100f ? l[j][i] - w : 0.0f;
+                  }
+                }
                 tm_load<CK>(s_col + col(j), x);
 #pragma unroll
                 for (int i = 0; i < CK; ++i) x[i] = sees(j, i) ? x[i] * (F8 ? mult[col(j) + i] : c) : -INFINITY;
@@ -844,21 +881,23 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
                 if (lane < CK) st->red[quad][col(j) + lane] = m;
               }
             group_sync(bar);
-            if (wtid < NT / 2 && my_row < rows) {
+            if (wtid < S::kOwn && my_row < rows) {
               const float old = st->top[my_row];
               float top = old;
 #pragma unroll
               for (int w = 0; w < 4; ++w) top = fmaxf(top, st->red[w][my_row]);
               st->factor[my_row] = old == -INFINITY ? 0.0f : exp2_approx(old - top);
               st->top[my_row] = top;
-              st->shift[my_row] = top == -INFINITY ? kNone : -top;
+              st->shift[my_row] = top == -INFINITY ? kNone : kLift - top;
             }
             group_sync(bar);
+          }
+          // the last product is done: P may be written again, and O rescaled
+          if (it > 0) mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
+          __syncwarp();
+          if (raise) {
             if (tile > s.tile0) {
-              mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
-              __syncwarp();
               tc_fence_after();
-              o_done = true;
 #pragma unroll
               for (int j = 0; j < S::kChunks; ++j)
                 if (col(j) < rows) {
@@ -874,41 +913,18 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
                 }
               tm_wait_store();
             }
-            if constexpr (S::kKeep) {
 #pragma unroll
-              for (int j = 0; j < S::kChunks; ++j)
-                if (col(j) < rows) scores(j, z[j]);
-            }
+            for (int j = 0; j < S::kChunks; ++j)
+              if (col(j) < rows) weights(j);
           }
-          // the last product must have read P before it is written again
-          if (!o_done) mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
-          __syncwarp();
 #pragma unroll
           for (int j = 0; j < S::kChunks; ++j)
             if (col(j) < rows) {
-              auto& x = take(j);
-              if constexpr (!S::kKeep) scores(j, x);
-              uint32_t w[CK / 2];
-#pragma unroll
-              for (int i = 0; i < CK; i += 2) {
-                float2 p = make_float2(exp2_approx(x[i]), exp2_approx(x[i + 1]));
-                if (!sees(j, i)) p.x = 0.0f;
-                if (!sees(j, i + 1)) p.y = 0.0f;
-                const float2 sum = add2(make_float2(l[j][i], l[j][i + 1]), p);
-                l[j][i] = sum.x, l[j][i + 1] = sum.y;
-                // the weights' rounding: bf16 to go with a bf16 cache (2^-8 of each at most), fp16 with E4M3
-                if constexpr (F8) {
-                  const __half2 h = __floats2half2_rn(p.x, p.y);
-                  w[i / 2] = *reinterpret_cast<const uint32_t*>(&h);
-                } else {
-                  w[i / 2] = pack_bf16(p.x, p.y);
-                }
-              }
               char* row = p_buf + (col(j) / 64) * (kTileSlots * 128) + key * 128;
 #pragma unroll
               for (int i = 0; i < CK / 8; ++i)
                 *reinterpret_cast<uint4*>(row + ((((col(j) % 64) + i * 8) * 2) ^ ((key & 7) * 16))) =
-                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                    make_uint4(p[j][4 * i], p[j][4 * i + 1], p[j][4 * i + 2], p[j][4 * i + 3]);
             }
           tc_fence_before();
           if constexpr (!F8 && MASKED) {
@@ -938,7 +954,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
                 }
                 if (bad) {
                   *p = w;
-                  st->bad_value[seg & 1] = seg + 1;
+                  st->bad_value[seg & 3] = seg + 1;
                 }
               }
             }
@@ -971,7 +987,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
       const bool whole = s.tile0 == 0 && s.tile1 == s.tiles;
       // parts: slot 0 for an item that an earlier CTA began, slot 1 for one that a later one ends
       const int64_t part_row = ((int64_t)blockIdx.x * 2 + (s.tile0 == 0)) * P.rows;
-      if (wtid < NT / 2) {
+      if (wtid < S::kOwn) {
         float f = 0.0f;
         if (my_row < rows) {
           const float sum = st->red[0][my_row] + st->red[1][my_row] + st->red[2][my_row] + st->red[3][my_row];
@@ -984,7 +1000,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
       __syncwarp();
       tc_fence_after();
       group_sync(bar);
-      const bool bad = st->bad_value[seg & 1] == (uint32_t)seg + 1;
+      const bool bad = st->bad_value[seg & 3] == (uint32_t)seg + 1;
       const bool lost = *dead != 0;
       char* out = P.out.data + s.b * P.out.row + (int64_t)t0 * P.out.token + (int64_t)s.head * P.group * P.out.head + key * 2;
       float* part = P.part + part_row * D + key;
@@ -1008,7 +1024,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
             const float v = F8 ? ((*reinterpret_cast<const uint8_t*>(p) & 0x7F) == 0x7F ? NAN : 0.0f)
                                : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
             if (isfinite(v)) continue;
-            const uint64_t see = st->seen[wg][i];
+            const uint32_t see = st->seen[wg][i];
 #pragma unroll
             for (int n = 0; n < CK; ++n)
               if ((see >> (j * CK + n)) & 1) x[n] += v;
