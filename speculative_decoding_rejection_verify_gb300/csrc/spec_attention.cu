@@ -105,10 +105,14 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
   return __all_sync(~0u, mbar_wait(bar, parity, dead));
 }
 
+// A copy by one elected lane of a warp that goes through the code together (see tc_mma).
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
                                          uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(
+          dst),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
 }
@@ -328,7 +332,8 @@ struct Shape {
   // warps are what hides their latencies.
   static constexpr int kGroups = NT >= 64 ? 4 : 2;
   static constexpr int kSoftmaxWarps = 4 * kGroups;
-  static constexpr int kProducer = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1;
+  static constexpr int kProducer = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1;  // the producer of K and Q,
+  static constexpr int kProducerV = kIssuer + 1 + (F8 ? kConvertWarps : 0);     // and that of V
   static constexpr int kThreads = kSoftmaxWarps * 32 + (F8 ? 256 : 128);
   // Registers: the softmax warps take more than an even split of the SM's gives them, the others less.  Per
   // warpgroup of 128 threads: 4 x 128 = 512 = 2 x 176 + 2 x 80 and 6 x 80 = 480 = 4 x 88 + 2 x 64 with E4M3;
@@ -491,59 +496,78 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
     if constexpr (S::kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kFewRegs));
     Walk walk(P, start_b, start_offset, first, count);
     Segment s;
-    if (warp == kProducer) {
-      // ---- TMA: Q of every segment, K and V of every tile, page by page ----
-      const int page = 1 << P.cache.page_shift;
-      const int box = min(page, kTileSlots);                // slots of one copy
-      const int copies = kTileSlots / box;                  // copies of a tile (and half)
+    if (warp == kProducer || warp == S::kProducerV) {
+      // ---- TMA: one warp brings Q of every segment and K of every tile, another V, page by page ----
+      const auto uniform = [](int x) { return __shfl_sync(~0u, x, 0); };
+      const bool is_v = uniform(warp == S::kProducerV);
+      const CUtensorMap* map = is_v ? &P.v_map : &P.k_map;
+      const int shift = uniform(P.cache.page_shift), page = 1 << shift;
+      const int box = min(page, kTileSlots);  // slots of one copy
+      const int copies = kTileSlots / box;    // copies of a tile (and half)
       constexpr int kParts = F8 ? 1 : S::kHalves;
-      const int part = lane % kParts, copy = lane / kParts;
-      int slot = 0;
+      const uint32_t base = uniform(smem_addr(smem)), bars = uniform(smem_addr(st));
+      const auto bar_of = [&](const uint64_t* x) { return bars + (uint32_t)(reinterpret_cast<const char*>(x) - reinterpret_cast<const char*>(st)); };
+      int slot = is_v;
       uint32_t phase = 0;  // of the ring
       bool ok = true;
       int issued = 0;
       for (int seg = 0; ok && walk.next(s); ++seg) {
-        const int qb = seg % S::kQBufs;
-        ok = mbar_wait_warp(smem_addr(&st->q_empty[qb]), ((seg / S::kQBufs) & 1) ^ 1, dead);
-        if (!ok) break;
-        if (lane == 0) {
-          const uint32_t bar = smem_addr(&st->q_loaded[qb]);
-          mbar_expect(bar, P.rows * D * 2);
+        const int head = uniform(s.head), tile0 = uniform(s.tile0), tile1 = uniform(s.tile1);
+        if (!is_v) {
+          const int qb = seg % S::kQBufs;
+          ok = mbar_wait_warp(bar_of(&st->q_empty[qb]), ((seg / S::kQBufs) & 1) ^ 1, dead);
+          if (!ok) break;
+          const uint32_t bar = bar_of(&st->q_loaded[qb]);
+          if (lane == 0) mbar_expect(bar, P.rows * D * 2);
+          __syncwarp();
+#pragma unroll
           for (int h = 0; h < S::kHalves; ++h)
-            tma_load(smem_addr(q_buf + qb * S::kQ + h * NT * 128), &P.q_map, h * 64, s.head * P.group, s.row_group * P.tokens,
-                     s.b, bar);
+            tma_load(base + (uint32_t)(q_buf - smem) + qb * S::kQ + h * NT * 128, &P.q_map, h * 64, head * P.group,
+                     uniform(s.row_group) * P.tokens, uniform(s.b), bar);
         }
         const int32_t* table = P.batch.pages + (int64_t)s.b * P.batch.max_pages;
-        const auto entry = [&](int tile) {  // this lane's page of a tile; one past the pool reads as zeros
-          const int at = tile * kTileSlots + copy * box;
-          if (copy >= copies || at >= s.end) return P.cache.num_pages;
-          const int p = __ldg(table + (at >> P.cache.page_shift));
+        const auto entry = [&](int tile) {  // the page of this lane's copy of a tile; one past the pool reads as zeros
+          const int at = tile * kTileSlots + lane * box;
+          if (lane >= copies || at >= s.end) return P.cache.num_pages;
+          const int p = __ldg(table + (at >> shift));
           return p < 0 || p > P.cache.num_pages ? P.cache.num_pages : p;
         };
-        int mine_page = entry(s.tile0);
-        for (int tile = s.tile0; ok && tile < s.tile1; ++tile) {
-          const int p = mine_page;
-          if (tile + 1 < s.tile1) mine_page = entry(tile + 1);
-          const int row = (tile * kTileSlots + copy * box) & (page - 1);
-  #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            ok = ok && mbar_wait_warp(smem_addr(&st->ring_empty[slot]), phase ^ 1, dead);
-            if (!ok) break;
-            const uint32_t bar = smem_addr(&st->ring_full[slot]);
-            if (lane == 0) mbar_expect(bar, S::kRing);
-            __syncwarp();
-            if (copy < copies) {
-              const uint32_t dst = smem_addr(ring) + slot * S::kRing + (F8 ? copy * box * D : part * (kTileSlots * 128) + copy * box * 128);
-              tma_load(dst, kv ? &P.v_map : &P.k_map, part * 64, row, s.head, p, bar);
-            }
-            ++issued;
-            if (++slot == S::kSlots) slot = 0, phase ^= 1;
-          }
+        int next_page = entry(tile0);
+        for (int tile = tile0; tile < tile1; ++tile) {
+          const int my_page = next_page;
+          if (tile + 1 < tile1) next_page = entry(tile + 1);
+          ok = mbar_wait_warp(bar_of(&st->ring_empty[slot]), phase ^ 1, dead);
+          if (!ok) break;
+          const uint32_t bar = bar_of(&st->ring_full[slot]);
+          if (lane == 0) mbar_expect(bar, S::kRing);
+          __syncwarp();
+          const uint32_t dst = base + (uint32_t)(ring - smem) + slot * S::kRing;
+          const auto bring = [&](auto tag) {
+            constexpr int N = decltype(tag)::value;  // copies, of kTileSlots / N slots
+            const int row = N == 1 ? (tile * kTileSlots) & (page - 1) : 0;
+            int p[N];
+#pragma unroll
+            for (int c = 0; c < N; ++c) p[c] = __shfl_sync(~0u, my_page, c);
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+#pragma unroll
+              for (int part = 0; part < kParts; ++part)
+                tma_load(dst + c * (kTileSlots / N) * (F8 ? D : 128) + part * (kTileSlots * 128), map, part * 64, row, head, p[c], bar);
+          };
+          if (copies == 1) bring(std::integral_constant<int, 1>{});
+          else if (copies == 2) bring(std::integral_constant<int, 2>{});
+          else if (copies == 4) bring(std::integral_constant<int, 4>{});
+          else if (copies == 8) bring(std::integral_constant<int, 8>{});
+          else bring(std::integral_constant<int, 16>{});
+          ++issued;
+          slot += 2;
+          if (slot >= S::kSlots) slot -= S::kSlots, phase ^= 1;
         }
       }
       if (!ok)  // a wait ran out: see the copies in flight land before the block ends
-        for (int i = 0; i < min(issued, S::kSlots); ++i) {
-          if (--slot < 0) slot = S::kSlots - 1, phase ^= 1;
+        for (int i = 0; i < min(issued, S::kSlots / 2); ++i) {
+          slot -= 2;
+          if (slot < 0) slot += S::kSlots, phase ^= 1;
           for (int n = 0; n < (1 << 16) && !mbar_try(smem_addr(&st->ring_full[slot]), phase); ++n) {
           }
         }
