@@ -344,10 +344,13 @@ struct Shape {
   static_assert(!kSplit || kGroups * kMoreRegs + (kThreads / 128 - kGroups) * kFewRegs <= kThreads / 128 * kLaunchRegs,
                 "register split");
   static constexpr int kColumns = 3 * NT <= 64 ? 64 : 3 * NT <= 128 ? 128 : 3 * NT <= 256 ? 256 : 512;
-  static constexpr int kChunk = NT == 32 ? 16 : 8;                // columns a warpgroup takes at a time
+  static constexpr int kChunk = NT == 32 || NT == 128 ? 16 : 8;                // columns a warpgroup takes at a time
   static constexpr int kOwn = NT / kGroups;                       // columns of one warpgroup
   static constexpr int kChunks = kOwn / kChunk;
   static_assert(kOwn <= 32, "a warpgroup's columns fit a word");
+  // A tile's weights stay in registers over the vote on them; with many columns the vote is on scores that
+  // are then computed again.
+  static constexpr bool kHold = NT <= 64;
 
   struct State {
     uint64_t ring_full[8], ring_empty[8];
@@ -850,9 +853,17 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
             }
           };
           // One pass makes scores and weights with the maximum in use and adds the weights up; a vote on the
-          // largest weight then says whether they stand.
-          uint32_t p[S::kChunks][CK / 2];
+          // largest weight then says whether they stand.  (Without kHold: a vote on the scores, then the weights.)
+          uint32_t p[S::kHold ? S::kChunks : 1][CK / 2];
           uint32_t over = 0;  // two fp16 or bf16 weights
+          const auto store = [&](int j) {
+            const uint32_t* w = p[S::kHold ? j : 0];
+            char* row = p_buf + (col(j) / 64) * (kTileSlots * 128) + key * 128;
+#pragma unroll
+            for (int i = 0; i < CK / 8; ++i)
+              *reinterpret_cast<uint4*>(row + ((((col(j) % 64) + i * 8) * 2) ^ ((key & 7) * 16))) =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          };
           const auto weights = [&](int j) {
             float z[CK];
             scores(j, z);
@@ -866,18 +877,29 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
               // the weights' rounding: bf16 to go with a bf16 cache (2^-8 of each at most), fp16 with E4M3
               if constexpr (F8) {
                 const __half2 h = __floats2half2_rn(w.x, w.y), m = __hmax2(h, *reinterpret_cast<const __half2*>(&over));
-                p[j][i / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                p[S::kHold ? j : 0][i / 2] = *reinterpret_cast<const uint32_t*>(&h);
                 over = *reinterpret_cast<const uint32_t*>(&m);
               } else {
-                p[j][i / 2] = pack_bf16(w.x, w.y);
-                const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&p[j][i / 2]),
+                p[S::kHold ? j : 0][i / 2] = pack_bf16(w.x, w.y);
+                const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&p[S::kHold ? j : 0][i / 2]),
                                                  *reinterpret_cast<const __nv_bfloat162*>(&over));
                 over = *reinterpret_cast<const uint32_t*>(&m);
               }
             }
           };
           bool raise = tile == s.tile0;
-          if (!raise) {
+          if (!raise && !S::kHold) {
+            float most = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < S::kChunks; ++j)
+              if (col(j) < rows) {
+                float z[CK];
+                scores(j, z);
+#pragma unroll
+                for (int i = 0; i < CK; ++i) most = fmaxf(most, sees(j, i) ? z[i] : -INFINITY);
+              }
+            raise = group_any(bar, most > kRescale + kLift);
+          } else if (!raise) {
 #pragma unroll
             for (int j = 0; j < S::kChunks; ++j)
               if (col(j) < rows) weights(j);
@@ -890,7 +912,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
             for (int j = 0; j < S::kChunks; ++j)
               if (col(j) < rows) {
                 float x[CK];
-                if (tile > s.tile0) {  // take the weights back; those over 2^100 leave nothing of what was there before
+                if (S::kHold && tile > s.tile0) {  // take the weights back; those over 2^100 leave nothing of what was there before
                   scores(j, x);
 #pragma unroll
                   for (int i = 0; i < CK; ++i) {
@@ -937,18 +959,17 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
                 }
               tm_wait_store();
             }
+            if constexpr (S::kHold) {
 #pragma unroll
-            for (int j = 0; j < S::kChunks; ++j)
-              if (col(j) < rows) weights(j);
+              for (int j = 0; j < S::kChunks; ++j)
+                if (col(j) < rows) weights(j);
+            }
           }
 #pragma unroll
           for (int j = 0; j < S::kChunks; ++j)
             if (col(j) < rows) {
-              char* row = p_buf + (col(j) / 64) * (kTileSlots * 128) + key * 128;
-#pragma unroll
-              for (int i = 0; i < CK / 8; ++i)
-                *reinterpret_cast<uint4*>(row + ((((col(j) % 64) + i * 8) * 2) ^ ((key & 7) * 16))) =
-                    make_uint4(p[j][4 * i], p[j][4 * i + 1], p[j][4 * i + 2], p[j][4 * i + 3]);
+              if constexpr (!S::kHold) weights(j);
+              store(j);
             }
           tc_fence_before();
           if constexpr (!F8 && MASKED) {
