@@ -7,7 +7,10 @@
 
 namespace sv {
 
-constexpr int kAppendThreads = 256;
+// Threads of a token's block.  Few tokens: as many as load all of a token at once.  Many: small blocks, which start
+// and end more smoothly (4 x 2047 tokens of 32 + 2 x 8 heads, half-split: 46 us with 256, 36 with 128, 33 with 64;
+// 8 x 6 tokens: 2.8, 3.0, 3.7).
+constexpr int kAppendThreads = 256, kAppendThreadsMany = 64;
 
 struct AppendParams {
   Heads q, k, v, q_out;
@@ -48,11 +51,11 @@ __device__ __forceinline__ void store_entry(char* p, float (&x)[8], float inv_sc
 // itself).  kAhead heads are loaded before the first is used.
 template <int D, bool F8, bool INTERLEAVED>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams P) {
-  constexpr int kAhead = 4;
+  constexpr int kAhead = INTERLEAVED ? 4 : 2;
   pdl_launch_next();
   pdl_wait();
   const int paired = INTERLEAVED ? 0 : P.rot / 16;  // units that hold a vector and its partner
-  const int units = D / 8 - paired, lanes = kAppendThreads / units;
+  const int units = D / 8 - paired, lanes = blockDim.x / units;
   const int head0 = threadIdx.x / units, unit = threadIdx.x - head0 * units;
   const int b = blockIdx.x / P.batch.T, t = blockIdx.x - b * P.batch.T;
   if (head0 >= lanes) return;
@@ -286,7 +289,10 @@ spec_status_t spec_kv_append(const spec_heads_t* q, const spec_heads_t* k, const
                         : (inter ? append_kernel<128, false, true> : append_kernel<128, false, false>))
                   : (f8 ? (inter ? append_kernel<64, true, true> : append_kernel<64, true, false>)
                         : (inter ? append_kernel<64, false, true> : append_kernel<64, false, false>));
-  return launch_early(kern, dim3((unsigned)blocks), dim3(kAppendThreads), 0, st, P) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (device_sms(&dev, &sms) != cudaSuccess) return SPEC_ERR_CUDA;
+  const int threads = blocks >= 16 * sms ? kAppendThreadsMany : kAppendThreads;
+  return launch_early(kern, dim3((unsigned)blocks), dim3(threads), 0, st, P) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 spec_status_t spec_kv_keep(const spec_kv_cache_t* cache, const spec_decode_batch_t* batch, const int32_t* path,

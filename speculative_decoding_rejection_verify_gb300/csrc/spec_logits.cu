@@ -7,6 +7,8 @@
 // registers.  A thread keeps its tokens' counts in registers from position to position and adds the
 // drafts as it passes them.  Bound by reading and writing the logits once.
 
+#include <type_traits>
+
 #include "decode_common.cuh"
 
 namespace sv {
@@ -30,40 +32,13 @@ struct RuleParams {
   int B, T, V, words, stretch;
 };
 
-// VEC logits as one load and store of 2 to 16 bytes.  The loads are not read-only ones: out may be logits.
-template <int BYTES>
-struct Raw;
-template <>
-struct Raw<16> {
+// 16 bytes of logits.  The loads are not read-only ones: out may be logits.
+struct Raw {
   uint32_t w[4];
   __device__ __forceinline__ void load(const void* p) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
   }
   __device__ __forceinline__ void store(void* p) const { *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]); }
-};
-template <>
-struct Raw<8> {
-  uint32_t w[2];
-  __device__ __forceinline__ void load(const void* p) {
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
-  }
-  __device__ __forceinline__ void store(void* p) const { *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]); }
-};
-template <>
-struct Raw<4> {
-  uint32_t w[1];
-  __device__ __forceinline__ void load(const void* p) { asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p)); }
-  __device__ __forceinline__ void store(void* p) const { *reinterpret_cast<uint32_t*>(p) = w[0]; }
-};
-template <>
-struct Raw<2> {
-  uint32_t w[1];
-  __device__ __forceinline__ void load(const void* p) {
-    uint16_t h;
-    asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(h) : "l"(p));
-    w[0] = h;
-  }
-  __device__ __forceinline__ void store(void* p) const { *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0]; }
 };
 
 template <bool BF16, int VEC>
@@ -83,29 +58,35 @@ __device__ __forceinline__ void pack(uint32_t* w, const float (&x)[VEC]) {
   }
 }
 
-// A thread takes GROUPS runs of VEC tokens, kRuleThreads * VEC apart, through all positions.
-template <bool BF16, int VEC, int GROUPS>
-__global__ void __launch_bounds__(kRuleThreads) rules_kernel(const __grid_constant__ RuleParams P) {
-  constexpr int ES = BF16 ? 2 : 4;
-  extern __shared__ __align__(16) uint32_t word[];  // [stretch]
-  __shared__ int draft[SPEC_MAX_NEW];               // relative to the stretch; -1: elsewhere
-  const int b = blockIdx.y, first = blockIdx.x * P.stretch;
-  const int len = min(P.stretch, P.V - first);
+// A block's request, its stretch of the vocabulary and what the request asks for.
+struct Stretch {
+  int b, first, len, rows;
+  float rep, pre, fre, inv;
+  bool penal;
+};
+
+// Counts the request's history, bias entries and prompt over the stretch into `word`; `draft` gets the drafts
+// relative to the stretch (-1: elsewhere).
+__device__ __forceinline__ Stretch count_rules(const RuleParams& P, uint32_t* word, int* draft) {
+  Stretch s;
+  s.b = blockIdx.y, s.first = blockIdx.x * P.stretch;
+  s.len = min(P.stretch, P.V - s.first);
+  const int b = s.b, first = s.first, len = s.len;
+  const spec_logit_rules_t& R = P.r;
   pdl_launch_next();
   for (int i = threadIdx.x; i < (len + 3) / 4; i += kRuleThreads) reinterpret_cast<uint4*>(word)[i] = make_uint4(0, 0, 0, 0);
   pdl_wait();
-  const spec_logit_rules_t& R = P.r;
-  const int rows = R.t_per_row ? min(max(__ldg(R.t_per_row + b), 0), P.T) : P.T;
-  const float rep = R.repetition ? __ldg(R.repetition + b) : 1.0f;
-  const float pre = R.presence ? __ldg(R.presence + b) : 0.0f;
-  const float fre = R.frequency ? __ldg(R.frequency + b) : 0.0f;
+  s.rows = R.t_per_row ? min(max(__ldg(R.t_per_row + b), 0), P.T) : P.T;
+  s.rep = R.repetition ? __ldg(R.repetition + b) : 1.0f;
+  s.pre = R.presence ? __ldg(R.presence + b) : 0.0f;
+  s.fre = R.frequency ? __ldg(R.frequency + b) : 0.0f;
   const int held = R.history ? min(max(__ldg(R.history_len + b), 0), R.history_stride) : 0;
   const int prompt = R.history && R.prompt_len ? __ldg(R.prompt_len + b) : 0;
-  const bool penal = rep != 1.0f || pre != 0.0f || fre != 0.0f;
-
+  s.penal = s.rep != 1.0f || s.pre != 0.0f || s.fre != 0.0f;
+  s.inv = 1.0f / s.rep;
   if (threadIdx.x < SPEC_MAX_NEW) {
     int d = -1;
-    if (penal && R.draft && (int)threadIdx.x < rows - 1) d = __ldg(R.draft + (int64_t)b * (P.T - 1) + threadIdx.x);
+    if (s.penal && R.draft && (int)threadIdx.x < s.rows - 1) d = __ldg(R.draft + (int64_t)b * (P.T - 1) + threadIdx.x);
     draft[threadIdx.x] = d >= first && d - first < len ? d - first : -1;
   }
   __syncthreads();
@@ -117,7 +98,7 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(const __grid_consta
     }
     __syncthreads();
   }
-  if (penal) {
+  if (s.penal) {
     const int32_t* ids = R.history + (int64_t)b * R.history_stride;
     constexpr int kAhead = 8;  // entries a thread loads before it counts the first
     for (int i0 = threadIdx.x; i0 < held; i0 += kRuleThreads * kAhead) {
@@ -138,120 +119,242 @@ __global__ void __launch_bounds__(kRuleThreads) rules_kernel(const __grid_consta
     }
   }
   __syncthreads();
+  return s;
+}
+
+// What a token's word makes of its logit x: (seen ? x * (x > 0 ? 1 / rep : rep) : x) + off.  The reciprocal is
+// within 2^-23 of the division, and the terms of off are summed before they meet the logit.
+__device__ __forceinline__ float effect(const RuleParams& P, const Stretch& s, uint32_t w, bool& seen) {
+  const uint32_t count = w & kCountMask, e = (w & ~kPromptBit) >> kBiasShift;
+  seen = s.penal && (count > 0 || (w & kPromptBit));
+  float off = e ? __ldg(P.r.bias + (int64_t)s.b * P.r.bias_n + e - 1) : 0.0f;
+  if (count > 0) off = off - s.fre * (float)count - s.pre;
+  return off;
+}
+
+// Rows on 16-byte boundaries.  A thread takes a run of VEC tokens through all positions, with their counts' effect
+// in registers.
+template <bool BF16>
+__global__ void __launch_bounds__(kRuleThreads, BF16 ? 5 : 1) rules_kernel(const __grid_constant__ RuleParams P) {
+  constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
+  extern __shared__ __align__(16) uint32_t word[];  // [stretch]
+  __shared__ int draft[SPEC_MAX_NEW];
+  const Stretch s = count_rules(P, word, draft);
+  const int b = s.b, first = s.first, len = s.len, rows = s.rows;
 
   const int64_t row_bytes = (int64_t)P.V * ES;
   const int64_t base = ((int64_t)b * P.T * P.V + first) * ES;
   const char* in = static_cast<const char*>(P.logits) + base;
   char* out = static_cast<char*>(P.out) + base;
-  const int32_t* mask = R.mask ? R.mask + (int64_t)b * P.T * P.words + (first >> 5) : nullptr;
-  constexpr uint32_t kAll = VEC == 32 ? ~0u : (1u << VEC) - 1;
-  // What a token's word makes of its logit x: (seen ? x * (x > 0 ? 1 / rep : rep) : x) + off.  The reciprocal
-  // is within 2^-23 of the division, and the terms of off are summed before they meet the logit.
-  const float inv = 1.0f / rep;
-  const auto effect = [&](uint32_t w, bool& seen) {
-    const uint32_t count = w & kCountMask, e = (w & ~kPromptBit) >> kBiasShift;
-    seen = penal && (count > 0 || (w & kPromptBit));
-    float off = e ? __ldg(R.bias + (int64_t)b * R.bias_n + e - 1) : 0.0f;
-    if (count > 0) off = off - fre * (float)count - pre;
-    return off;
-  };
-  for (int v0 = threadIdx.x * VEC; v0 < len; v0 += kRuleThreads * VEC * GROUPS) {  // VEC divides V and the stretch
-    float off[GROUPS][VEC];
-    uint32_t seen[GROUPS];  // bit i: token i is; bit 31: some token's logit changes
+  const int32_t* mask = P.r.mask ? P.r.mask + (int64_t)b * P.T * P.words + (first >> 5) : nullptr;
+  constexpr uint32_t kAll = (1u << VEC) - 1;
+  for (int v = threadIdx.x * VEC; v < len; v += kRuleThreads * VEC) {  // VEC divides V and the stretch
+    float off[VEC];
+    uint32_t w[VEC], any = 0;
 #pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      const int v = v0 + g * kRuleThreads * VEC;
-      uint32_t w[VEC], any = 0;
+    for (int i = 0; i < VEC; ++i) {
+      w[i] = word[v + i];
+      any |= w[i];
+      off[i] = 0.0f;
+    }
+    uint32_t seen = any ? 1u << 31 : 0;  // bit i: token i is; bit 31: some token's logit changes
+    if (any) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        w[i] = v < len ? word[v + i] : 0;
-        any |= w[i];
-        off[g][i] = 0.0f;
-      }
-      seen[g] = any ? 1u << 31 : 0;
-      if (any) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          bool s;
-          off[g][i] = effect(w[i], s);
-          seen[g] |= (uint32_t)s << i;
-        }
+        bool is;
+        off[i] = effect(P, s, w[i], is);
+        seen |= (uint32_t)is << i;
       }
     }
     for (int t0 = 0; t0 < rows; t0 += kRowsAhead) {
-      uint32_t allowed[kRowsAhead][GROUPS];
-      Raw<VEC * ES> raw[kRowsAhead][GROUPS];
+      uint32_t allowed[kRowsAhead];
+      Raw raw[kRowsAhead];
 #pragma unroll
-      for (int r = 0; r < kRowsAhead; ++r)
+      for (int r = 0; r < kRowsAhead; ++r) {
+        allowed[r] = kAll;
+        if (mask && t0 + r < rows)
+          allowed[r] = ((uint32_t)__ldg(mask + (int64_t)(t0 + r) * P.words + (v >> 5)) >> (v & 31)) & kAll;
+      }
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-          const int v = v0 + g * kRuleThreads * VEC;
-          allowed[r][g] = kAll;
-          if (mask && t0 + r < rows && v < len)
-            allowed[r][g] = ((uint32_t)__ldg(mask + (int64_t)(t0 + r) * P.words + (v >> 5)) >> (v & 31)) & kAll;
-        }
+      for (int r = 0; r < kRowsAhead; ++r) {
 #pragma unroll
-      for (int r = 0; r < kRowsAhead; ++r)
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-          const int v = v0 + g * kRuleThreads * VEC;
-#pragma unroll
-          for (int i = 0; i < (VEC * ES + 3) / 4; ++i) raw[r][g].w[i] = 0;
-          // a run that the mask forbids throughout is not read
-          if (allowed[r][g] && t0 + r < rows && v < len) raw[r][g].load(in + (t0 + r) * row_bytes + v * ES);
-        }
+        for (int i = 0; i < 4; ++i) raw[r].w[i] = 0;
+        // a run that the mask forbids throughout is not read
+        if (allowed[r] && t0 + r < rows) raw[r].load(in + (t0 + r) * row_bytes + v * ES);
+      }
 #pragma unroll
       for (int r = 0; r < kRowsAhead; ++r) {
         const int t = t0 + r;
         if (t >= rows) break;
         const int d = t > 0 ? draft[t - 1] : -1;
+        if (d >= v && d < v + VEC) {  // this thread's word alone: from here on the draft counts
+          const uint32_t u = ++word[d];
+          bool is;
+          const float o = effect(P, s, u, is);
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-          const int v = v0 + g * kRuleThreads * VEC;
-          if (v >= len) continue;
-          if (d >= v && d < v + VEC) {  // this thread's word alone: from here on the draft counts
-            const uint32_t w = ++word[d];
-            bool s;
-            const float o = effect(w, s);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-              if (i == d - v) off[g][i] = o;
-            seen[g] |= 1u << 31 | 1u << (d - v);
-          }
-          if (seen[g] || allowed[r][g] != kAll) {
-            float x[VEC];
-            unpack<BF16, VEC>(raw[r][g].w, x);
-            if (seen[g]) {
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) {
-                const float f = x[i] > 0.0f ? inv : rep;
-                x[i] = fmaf(x[i], (seen[g] >> i) & 1u ? f : 1.0f, off[g][i]);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-              if (!((allowed[r][g] >> i) & 1u)) x[i] = -INFINITY;
-            pack<BF16, VEC>(raw[r][g].w, x);
-          }
-          raw[r][g].store(out + t * row_bytes + v * ES);
+          for (int i = 0; i < VEC; ++i)
+            if (i == d - v) off[i] = o;
+          seen |= 1u << 31 | 1u << (d - v);
         }
+        if (seen || allowed[r] != kAll) {
+          float x[VEC];
+          unpack<BF16, VEC>(raw[r].w, x);
+          if (seen) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              const float f = x[i] > 0.0f ? s.inv : s.rep;
+              x[i] = fmaf(x[i], (seen >> i) & 1u ? f : 1.0f, off[i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < VEC; ++i)
+            if (!((allowed[r] >> i) & 1u)) x[i] = -INFINITY;
+          pack<BF16, VEC>(raw[r].w, x);
+        }
+        raw[r].store(out + t * row_bytes + v * ES);
       }
     }
   }
 }
 
+// Rows that begin anywhere.  The runs of a row lie on its own 16-byte boundaries, so a token's run and thread
+// change from position to position: every token's effect lies in shared memory, with bitmaps of the tokens that have
+// one and that are seen.  The drafts' logits behind them are worked out beforehand and written last.  Runs that
+// reach past the stretch, and all where out lies otherwise than logits on 16 bytes, are read and written an element
+// at a time.
 template <bool BF16>
-static cudaError_t launch_rules(const RuleParams& P, int align, cudaStream_t st) {
-  // the widest vector that divides the rows and their addresses; narrow ones take several runs a thread to
-  // keep as many bytes in flight
-  constexpr int ES = BF16 ? 2 : 4;
-  void (*kern)(RuleParams) = nullptr;
-  if (align % 16 == 0) kern = rules_kernel<BF16, 16 / ES, 1>;
-  else if (align % 8 == 0) kern = rules_kernel<BF16, 8 / ES, 2>;
-  else if (align % 4 == 0) kern = rules_kernel<BF16, 4 / ES, 4>;
-  else kern = rules_kernel<BF16, 1, 4>;
-  const dim3 grid((P.V + P.stretch - 1) / P.stretch, P.B);
-  return launch_early(kern, grid, dim3(kRuleThreads), P.stretch * sizeof(uint32_t), st, P);
+__global__ void __launch_bounds__(kRuleThreads) rules_odd_kernel(const __grid_constant__ RuleParams P) {
+  constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
+  using Element = typename std::conditional<BF16, uint16_t, uint32_t>::type;
+  extern __shared__ __align__(16) uint32_t word[];  // [stretch], then the bitmaps
+  __shared__ int draft[SPEC_MAX_NEW];
+  __shared__ uint32_t draft_word[SPEC_MAX_NEW];      // the counts of the drafts
+  const int map = P.stretch / 32 + 2;                // words of a bitmap, [-1 .. stretch / 32]
+  uint32_t* marks = word + P.stretch + 1;            // tokens with an effect
+  uint32_t* seen = marks + map;                      // tokens among the prompt or the output
+  for (int i = threadIdx.x; i < 2 * map; i += kRuleThreads) marks[i - 1] = 0;
+  const Stretch s = count_rules(P, word, draft);
+  const int b = s.b, first = s.first, len = s.len, rows = s.rows;
+  if ((int)threadIdx.x < rows - 1 && draft[threadIdx.x] >= 0) draft_word[threadIdx.x] = word[draft[threadIdx.x]];
+  __syncthreads();
+  const int lane = threadIdx.x % 32;
+  for (int i = threadIdx.x - lane; i < len; i += kRuleThreads) {  // 32 neighbours a warp; a word becomes its effect
+    const int v = i + lane;
+    const uint32_t w = v < len ? word[v] : 0;
+    bool is = false;
+    float off = 0.0f;
+    if (w) off = effect(P, s, w, is);
+    if (v < len) word[v] = __float_as_uint(off);
+    const uint32_t any = __ballot_sync(~0u, w != 0), all = __ballot_sync(~0u, is);
+    if (lane == 0) marks[i / 32] = any, seen[i / 32] = all;
+  }
+  __syncthreads();
+
+  const char* in = static_cast<const char*>(P.logits) + ((int64_t)b * P.T * P.V + first) * ES;
+  char* out = static_cast<char*>(P.out) + ((int64_t)b * P.T * P.V + first) * ES;
+  const int32_t* mask = P.r.mask ? P.r.mask + (int64_t)b * P.T * P.words + (first >> 5) : nullptr;
+  const int words = (len + 31) / 32;  // of the mask, and of the bitmaps
+  const bool alike = (((uintptr_t)in ^ (uintptr_t)out) & 15) == 0;
+  constexpr uint32_t kAll = (1u << VEC) - 1;
+  const auto bits_at = [&](const uint32_t* p, int v) {  // bits v .. v + VEC - 1 of a bitmap, v > -32
+    const int at = v >> 5;
+    return __funnelshift_r(p[at], p[at + 1], v & 31) & kAll;
+  };
+  const auto shaped = [&](float x, bool is, float off) { return fmaf(x, is ? (x > 0.0f ? s.inv : s.rep) : 1.0f, off); };
+  // draft i at a position t > i counts with all drafts of its token before t
+  constexpr int kPairs = SPEC_MAX_NEW * (SPEC_MAX_NEW - 1) / 2, kPairsEach = (kPairs + kRuleThreads - 1) / kRuleThreads;
+  Element fixed[kPairsEach];
+  int64_t place[kPairsEach];  // -1: none
+#pragma unroll
+  for (int k = 0; k < kPairsEach; ++k) {
+    place[k] = -1;
+    const int pair = threadIdx.x + k * kRuleThreads;
+    if (pair >= rows * (rows - 1) / 2) continue;
+    int t = (int)((1.0f + sqrtf(1.0f + 8.0f * pair)) * 0.5f);  // t (t - 1) / 2 <= pair < t (t + 1) / 2
+    while (t * (t - 1) / 2 > pair) --t;
+    while (t * (t + 1) / 2 <= pair) ++t;
+    const int d = draft[pair - t * (t - 1) / 2];
+    if (d < 0) continue;
+    uint32_t w = 0, more = 0;
+    for (int i = 0; i < t; ++i)
+      if (draft[i] == d) w = draft_word[i], ++more;
+    const uint32_t raw[1] = {reinterpret_cast<const Element*>(in)[(int64_t)t * P.V + d]};
+    float x[1];
+    unpack<BF16, 1>(raw, x);
+    bool is;
+    const float off = effect(P, s, w + more, is);
+    x[0] = shaped(x[0], is, off);
+    if (mask && !(((uint32_t)__ldg(mask + (int64_t)t * P.words + d / 32) >> (d % 32)) & 1)) x[0] = -INFINITY;
+    uint32_t packed[1];
+    pack<BF16, 1>(packed, x);
+    fixed[k] = (Element)packed[0];
+    place[k] = (int64_t)t * P.V + d;
+  }
+  __syncthreads();  // out may be logits: they are read before any is written
+  for (int t0 = 0; t0 < rows; t0 += kRowsAhead)
+    for (int j = threadIdx.x; j * VEC < len + VEC - 1; j += kRuleThreads) {
+      uint32_t allowed[kRowsAhead];
+      Raw raw[kRowsAhead];
+      int v[kRowsAhead];
+      bool whole[kRowsAhead];
+#pragma unroll
+      for (int r = 0; r < kRowsAhead; ++r) {
+        const char* row = in + (int64_t)(t0 + r) * P.V * ES;
+        v[r] = j * VEC - (int)(((uintptr_t)row & 15) / ES);
+        whole[r] = alike && t0 + r < rows && v[r] >= 0 && v[r] + VEC <= len;
+        allowed[r] = kAll;
+        if (mask && t0 + r < rows) {
+          const int32_t* m = mask + (int64_t)(t0 + r) * P.words;
+          const int at = v[r] >> 5;
+          const uint32_t lo = at >= 0 && at < words ? (uint32_t)__ldg(m + at) : 0, hi = at + 1 < words ? (uint32_t)__ldg(m + at + 1) : 0;
+          allowed[r] = __funnelshift_r(lo, hi, v[r] & 31) & kAll;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[r].w[i] = 0;
+        if (t0 + r >= rows || !allowed[r] || v[r] >= len || v[r] + VEC <= 0) continue;
+        if (whole[r]) {
+          raw[r].load(row + v[r] * ES);
+        } else {  // (elements outside are replaced by one of this run's)
+          Element e[VEC];
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) e[i] = reinterpret_cast<const volatile Element*>(row)[min(max(v[r] + i, 0), len - 1)];
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) raw[r].w[i * ES / 4] |= (uint32_t)e[i] << (i * ES % 4 * 8);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kRowsAhead; ++r) {
+        const int t = t0 + r;
+        if (t >= rows) break;
+        char* to = out + (int64_t)t * P.V * ES;
+        const uint32_t marked = bits_at(marks, v[r]);
+        if (marked || allowed[r] != kAll) {
+          float x[VEC];
+          unpack<BF16, VEC>(raw[r].w, x);
+          if (marked) {
+            const uint32_t is = bits_at(seen, v[r]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) x[i] = shaped(x[i], (is >> i) & 1, __uint_as_float(word[min(max(v[r] + i, 0), len - 1)]));
+          }
+#pragma unroll
+          for (int i = 0; i < VEC; ++i)
+            if (!((allowed[r] >> i) & 1u)) x[i] = -INFINITY;
+          pack<BF16, VEC>(raw[r].w, x);
+        }
+        if (whole[r]) {
+          raw[r].store(to + v[r] * ES);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i)
+            if (v[r] + i >= 0 && v[r] + i < len)
+              reinterpret_cast<Element*>(to)[v[r] + i] = (Element)(raw[r].w[i * ES / 4] >> (i * ES % 4 * 8));
+        }
+      }
+    }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kPairsEach; ++k)
+    if (place[k] >= 0) reinterpret_cast<Element*>(out)[place[k]] = fixed[k];
 }
 
 }  // namespace sv
@@ -286,9 +389,11 @@ extern "C" spec_status_t spec_process_logits(const void* logits, void* out, cons
     if ((int64_t)B * ((V + s - 1) / s) >= 8 * sms) break;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // the largest power of two that divides every row's address
-  const uint64_t bits = (uint64_t)(uintptr_t)logits | (uint64_t)(uintptr_t)out | (uint64_t)((int64_t)V * es) | 16u;
-  const int align = (int)(bits & (~bits + 1));
-  const cudaError_t e = dtype == SPEC_DTYPE_BF16 ? launch_rules<true>(P, align, st) : launch_rules<false>(P, align, st);
+  const dim3 grid((V + P.stretch - 1) / P.stretch, B), block(kRuleThreads);
+  const bool even = (uintptr_t)logits % 16 == 0 && (uintptr_t)out % 16 == 0 && (int64_t)V * es % 16 == 0;
+  const bool bf16 = dtype == SPEC_DTYPE_BF16;
+  const size_t counts = P.stretch * sizeof(uint32_t), marks = 2 * (P.stretch / 32 + 2) * sizeof(uint32_t);
+  const cudaError_t e = even ? launch_early(bf16 ? rules_kernel<true> : rules_kernel<false>, grid, block, counts, st, P)
+                             : launch_early(bf16 ? rules_odd_kernel<true> : rules_odd_kernel<false>, grid, block, counts + marks, st, P);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -143,6 +143,22 @@ def test_counts_of_a_long_history_are_exact():
     check(z, r, torch.float32)
 
 
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("V", [2048, 2051])
+def test_addresses_that_are_not_aligned(dtype, V):
+    """logits and out that begin on any element, alike or not."""
+    z, r = build(2, 5, V, 21)
+    z = z.to(dtype)
+    want = call(z.cuda(), r)
+    n = z.numel()
+    for i, o in ((1, 0), (0, 1), (3, 3), (1, 2), (5, 5)):
+        src = torch.zeros(n + 16, dtype=dtype, device="cuda")[i:i + n].view(z.shape)
+        dst = torch.zeros(n + 16, dtype=dtype, device="cuda")[o:o + n].view(z.shape)
+        src.copy_(z)
+        assert torch.equal(call(src, r, out=dst), want)
+        assert torch.equal(call(src, r, out=src), want)
+
+
 def test_another_stream():
     z, r = build(4, 5, 32000, 2)
     want = call(z.cuda(), r)
