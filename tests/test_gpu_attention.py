@@ -92,6 +92,49 @@ def test_ragged_batch_with_empty_requests(dtype):
         assert (out[b, n:] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, R.F8])
+def test_row_groups_without_tokens(dtype):
+    """64 tokens of a wide group are several items; a request's few tokens leave the later ones without a row."""
+    tb = [5, 64, 0, 33]
+    d = build(4, 64, 12, 2, 64, 16, [130, 7, 50, 0], dtype, "slot", tb=tb)
+    out = call(d)
+    check(d, out)
+    for b, n in enumerate(tb):
+        assert (out[b, n:] == 0).all()
+
+
+def test_queries_shared_by_the_batch():
+    d = build(3, 2, 4, 2, 64, 16, [100, 7, 260], BF, "slot")
+    d["q"] = d["q"][:1].expand(3, -1, -1, -1)
+    import speculative_decoding_rejection_verify_gb300 as sv
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q = d["q"][:1].cuda().expand(3, -1, -1, -1)
+    out = sv.paged_attention(q, R.to_cuda(d["k"]), R.to_cuda(d["v"]), d["pages"].cuda(), i32(d["ctx"]))
+    assert out.shape == q.shape
+    check(d, out)
+
+
+@pytest.mark.parametrize("dtype", [BF, R.F8])
+@pytest.mark.parametrize("width", [1, 40, 4000])
+def test_the_page_tables_width_changes_nothing(dtype, width):
+    """A table that could hold many more pages takes the way over cut items; the result is the same."""
+    d = build(3, 5, 8, 2, 128, 16, [300, 0, 77], dtype, "slot")
+    d["pages"] = torch.cat([d["pages"], torch.full((3, width), 2 ** 30, dtype=torch.int32)], 1)
+    check(d)
+
+
+def test_values_that_are_not_finite_in_the_context():
+    """A NaN in the context's values reaches every row of its heads and no other head or element."""
+    d = build(1, 3, 4, 2, 64, 16, [200], BF, "slot", seed=8)
+    want, bound = R.attention(d["q"], d["k"], d["v"], d["pages"], d["ctx"], d["tb"], None, d["scale"])
+    p, r = R.at(d["pages"], 0, 60, 16)
+    d["v"][p, r, 1, 5] = float("nan")
+    got = call(d).cpu().double()
+    hit = torch.zeros(got.shape, dtype=torch.bool)
+    hit[0, :, 2:, 5] = True
+    assert torch.isnan(got[hit]).all() and ((got - want).abs() <= bound)[~hit].all()
+
+
 def test_many_requests_of_mixed_length():
     g = torch.Generator().manual_seed(9)
     ctx = torch.randint(0, 700, (90,), generator=g).tolist()
