@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  pdl_wait();  // nothing before this reads or writes global memory
+  pdl_wait();  // nothing before this reads or writes what another kernel may
 
   // this CTA's part of the line: a scan over the requests' lengths
   const int per_request = P.heads * P.row_groups;

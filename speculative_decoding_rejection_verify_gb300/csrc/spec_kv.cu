@@ -3,7 +3,7 @@
 // behind the context).  Both are streams of 16-byte vectors, bound by memory traffic on large calls and
 // by their launch on small ones.  Measured: 4 x 2047 tokens of 32 + 2 x 8 heads of 128, half-split, bf16: 33 us,
 // 6.2 TB/s of the bytes read and written (0.92 of a copy's 6772 GB/s); 8 x 6 tokens: 2.8 us.  64 requests' 1 to 5
-// entries in 32 layers: 7.0 us, 2.7 TB/s, bound by the chain of three dependent loads before the first entry.
+// entries in 32 layers: 5.0 us, 3.8 TB/s, bound by the chain of two dependent loads before the first entry.
 
 #include "decode_common.cuh"
 
@@ -175,8 +175,9 @@ struct KeepParams {
 };
 
 constexpr int kKeepThreads = 256;
-constexpr int kKeepColumns = 4;  // columns a thread takes together,
-constexpr int kKeepAhead = 4;    // and entries of each that it loads before it stores the first
+// Columns a thread takes together, and entries of each that it loads before it stores the first (64 requests, 32
+// layers, 0 to 4 moves: 5.0 us; 6.4 with 4 columns and 4 entries, 5.8 with 1 and 4; up to 12 moves: 15.4, 18.5, 15.6).
+constexpr int kKeepColumns = 2, kKeepAhead = 3;
 constexpr int kKeepRound = 64;   // moves whose places the block works out at a time
 
 // Block (x, y): every gridDim.x-th run of 256 columns of request y's entries.  A column is one 16-byte
@@ -189,6 +190,8 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
   pdl_launch_next();
   pdl_wait();
   const int b = blockIdx.y;
+  const int32_t* path = P.path + (int64_t)b * P.max_keep;
+  const int ahead = threadIdx.x < 32 && (int)threadIdx.x < P.max_keep ? __ldg(path + threadIdx.x) : 0;  // before n is known
   const int n = min(max(__ldg(P.n_keep + b), 0), P.max_keep);
   const int ctx = batch_context(P.batch, b);
   for (int i0 = 0; i0 < n; i0 += kKeepRound) {
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
         const int i = i1 + threadIdx.x;
         int64_t src = -1, dst = -1;
         if (i < n) {
-          const int p = __ldg(P.path + (int64_t)b * P.max_keep + i);
+          const int p = i < 32 ? ahead : __ldg(path + i);
           if (p != i && p >= 0 && p < P.batch.slots) {
             dst = slot_offset(P.batch, P.cache, b, ctx + i);
             src = slot_offset(P.batch, P.cache, b, ctx + p);
