@@ -32,7 +32,9 @@ extern "C" {
 #define SPEC_FLAG_BAD_POSITION 128 /* a position outside [0, max_positions): clamped into range     */
 
 /* Limits (SPEC_ERR_UNSUPPORTED beyond them). */
-#define SPEC_MAX_NEW 64             /* T of spec_paged_attention (a tree mask has one bit per token) */
+#define SPEC_MAX_BATCH 65535        /* B, but for spec_kv_append (B * T < 2^31)                      */
+#define SPEC_MAX_NEW 64             /* T of spec_paged_attention (a tree mask has one bit per token)
+                                       and of spec_process_logits                                    */
 #define SPEC_MAX_GROUP 128          /* q heads per kv head of spec_paged_attention                   */
 #define SPEC_MAX_PAGE 4096          /* page_size: a power of two in [8, SPEC_MAX_PAGE]               */
 #define SPEC_MAX_SLOTS (1 << 30)    /* max_pages * page_size of one request                          */

@@ -462,13 +462,14 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
     mbar_init(smem_addr(&st->o_full), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // Nothing before this reads or writes what another kernel may, nor takes TMEM that one before it may still need.
+  pdl_wait();
   if (warp == kIssuer) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&st->tmem)),
                  "r"(S::kColumns)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  pdl_wait();  // nothing before this reads or writes what another kernel may
 
   // this CTA's part of the line: a scan over the requests' lengths
   const int per_request = P.heads * P.row_groups;
@@ -1319,7 +1320,7 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
   if (s == SPEC_OK) s = check_batch(batch, cache);
   if (s != SPEC_OK) return s;
   if (q_heads < 1 || q_heads % cache->heads || !isfinite(scale)) return SPEC_ERR_INVALID_ARG;
-  if (batch->T > SPEC_MAX_NEW || batch->B > 65535 || q_heads / cache->heads > SPEC_MAX_GROUP) return SPEC_ERR_UNSUPPORTED;
+  if (batch->T > SPEC_MAX_NEW || batch->B > SPEC_MAX_BATCH || q_heads / cache->heads > SPEC_MAX_GROUP) return SPEC_ERR_UNSUPPORTED;
   if (batch->B == 0 || batch->T == 0) return SPEC_OK;
   if (!heads_ok(q) || !heads_ok(out)) return SPEC_ERR_INVALID_ARG;
   const int D = cache->head_dim, group = q_heads / cache->heads;

@@ -315,7 +315,7 @@ spec_status_t spec_kv_keep(const spec_kv_cache_t* cache, const spec_decode_batch
   P.heads = cache->heads;
   P.vecs = cache->head_dim * (cache->dtype == SPEC_DTYPE_BF16 ? 2 : 1) / 16;
   const int64_t columns = (int64_t)cache->layers * 2 * P.heads * P.vecs;
-  if (columns > 0x40000000ll || batch->B > 65535) return SPEC_ERR_UNSUPPORTED;  // column indices stay in 32 bits
+  if (columns > 0x40000000ll || batch->B > SPEC_MAX_BATCH) return SPEC_ERR_UNSUPPORTED;  // column indices stay in 32 bits
   P.columns = (int)columns;
   const int64_t run = kKeepThreads * kKeepColumns;
   const dim3 grid((unsigned)((columns + run - 1) / run), batch->B);

@@ -374,7 +374,7 @@ extern "C" spec_status_t spec_process_logits(const void* logits, void* out, cons
   const spec_logit_rules_t& r = *rules;
   if (r.history_stride < 0 || r.bias_n < 0) return SPEC_ERR_INVALID_ARG;
   if (dtype != SPEC_DTYPE_F32 && dtype != SPEC_DTYPE_BF16) return SPEC_ERR_UNSUPPORTED;
-  if (V > SPEC_MAX_V || B > 65535 || T > SPEC_MAX_NEW || r.history_stride > SPEC_MAX_HISTORY ||
+  if (V > SPEC_MAX_V || B > SPEC_MAX_BATCH || T > SPEC_MAX_NEW || r.history_stride > SPEC_MAX_HISTORY ||
       r.bias_n > SPEC_MAX_BIAS)
     return SPEC_ERR_UNSUPPORTED;
   if (r.history && !r.history_len) return SPEC_ERR_INVALID_ARG;

@@ -27,6 +27,7 @@ DTYPE_E4M3 = 2
 FLAG_BAD_SLOT = 64
 FLAG_BAD_POSITION = 128
 
+MAX_BATCH = 65535
 MAX_NEW = 64
 MAX_GROUP = 128
 MAX_PAGE = 4096

@@ -176,7 +176,7 @@ def test_header_and_binding_agree():
     header = os.path.join(INCLUDE, "spec_decode.h")
     assert set(declared_functions(header)) == set(sv.DECODE_EXPORTS)
     text = open(header).read()
-    for name, value in (("MAX_NEW", decode.MAX_NEW), ("MAX_GROUP", decode.MAX_GROUP), ("MAX_PAGE", decode.MAX_PAGE),
+    for name, value in (("MAX_BATCH", decode.MAX_BATCH), ("MAX_NEW", decode.MAX_NEW), ("MAX_GROUP", decode.MAX_GROUP), ("MAX_PAGE", decode.MAX_PAGE),
                         ("MAX_HISTORY", decode.MAX_HISTORY), ("MAX_BIAS", decode.MAX_BIAS),
                         ("FLAG_BAD_SLOT", decode.FLAG_BAD_SLOT), ("FLAG_BAD_POSITION", decode.FLAG_BAD_POSITION)):
         assert f"#define SPEC_{name} {value} " in text, name
