@@ -1293,6 +1293,8 @@ static cudaError_t launch_rows(const AttnParams& P, int dev, int ctas, cudaStrea
   if (P.rows <= 16) return launch_attention<D, F8, 16>(P, dev, ctas, st);
   if (P.rows <= 32) return launch_attention<D, F8, 32>(P, dev, ctas, st);
   if (P.rows <= 64) return launch_attention<D, F8, 64>(P, dev, ctas, st);
+  // a width of its own: 128 columns' sums spill where 96 do not (68 rows, E4M3: 118 us against 139; bf16: 114, 118)
+  if (P.rows <= 96) return launch_attention<D, F8, 96>(P, dev, ctas, st);
   return launch_attention<D, F8, 128>(P, dev, ctas, st);
 }
 
