@@ -22,10 +22,10 @@
 // an E4M3 cache four warps split Q and bring V to fp16.
 //
 // Measured (requests x tokens, kv heads x group, slots; time; of the copy bandwidth of 6772 GB/s):
-//   64 x 7, 8 x 4, 1000 to 16000, bf16   329 us  6.79 TB/s  1.00   bound by memory
-//   2 x 5, 4 x 8, 100003 to 131071, bf16  83 us  5.7  TB/s  0.84   memory, and 10 us to begin and join
-//   32 x 17 (a tree), 8 x 4, 500 to 9000, E4M3  140 us  2.3 TB/s  0.34   the softmax: 68 rows at 128 slots a step
-//   8 x 6, 8 x 4, 0 to 4001, bf16         21 us  3.1  TB/s  0.46   beginnings and ends of 64 items
+//   64 x 7, 8 x 4, 1000 to 16000, bf16   328 us  6.8 TB/s  1.00   bound by memory
+//   2 x 5, 4 x 8, 100003 to 131071, bf16  82 us  5.7 TB/s  0.85   memory, and 10 us to begin and join
+//   32 x 17 (a tree), 8 x 4, 500 to 9000, E4M3  118 us  2.7 TB/s  0.40   the softmax: 68 rows at 128 slots a step
+//   8 x 6, 8 x 4, 0 to 4001, bf16         21 us  3.1 TB/s  0.46   beginnings and ends of 64 items
 
 #include <cuda.h>
 
@@ -345,7 +345,7 @@ struct Shape {
   static constexpr int kSlots = kFit > 8 ? 8 : F8 ? kFit / 2 * 2 : kFit;  // K and V tiles in flight (E4M3: V in odd slots)
   static_assert(kSlots >= 4, "the ring holds two tiles of K and V at least");
   // Softmax warpgroups, each with every kGroups-th chunk of columns: a tile is a chain of short steps, and
-  // warps are what hides their latencies (64 rows, E4M3: 102 us with 4 warpgroups, 122 with 2; 32 rows: the same).
+  // warps are what hides their latencies (64 rows, E4M3: 93 us with 4 warpgroups, 112 with 2; 32 rows: the same).
   static constexpr int kGroups = NT >= 64 ? 4 : 2;
   static constexpr int kSoftmaxWarps = 4 * kGroups;
   static constexpr int kProducer = kSoftmaxWarps, kIssuer = kSoftmaxWarps + 1;  // the producer of K and Q,
@@ -365,7 +365,7 @@ struct Shape {
   static constexpr int kChunks = kOwn / kChunk;
   static_assert(kOwn <= 32, "a warpgroup's columns fit a word");
   // A tile's weights stay in registers over the vote on them; with many columns, which would spill, the vote
-  // is on scores that are then computed again (68 rows, bf16: 119 us against 141).
+  // is on scores that are then computed again (68 rows: 118 us against 125 in E4M3, 114 against 117 in bf16).
   static constexpr bool kHold = NT <= 64;
 
   struct State {
@@ -1346,8 +1346,8 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
 
   // the line's length at most: what the page table could hold
   const int64_t per = ((int64_t)P.batch.slots + kTileSlots - 1) / kTileSlots;
-  // E4M3 items and those of many rows take longer to begin and end (attend 32 requests of 500 to 9000 slots, 68
-  // rows: 147 us at 2 tiles, 138 at 4, 141 at 6; 24 rows in bf16, 0 to 4001 slots: 22.1 us at 1, 21.1 at 2, 21.5 at 3)
+  // E4M3 items and those of many rows take longer to begin and end (32 requests of 500 to 9000 slots, 68 rows, E4M3:
+  // 125 us at 2 tiles, 118 at 4, 119 at 6; 24 rows in bf16, 0 to 4001 slots: 22.4 us at 1, 21.0 at 2, 21.5 at 3)
   P.item_cost = cache->dtype == SPEC_DTYPE_E4M3 || P.rows > 64 ? 4 : 2;
   P.whole = per <= kWholeTiles;
   const int64_t most = (int64_t)batch->B * cache->heads * P.row_groups * ((per > 0 ? per : 1) + P.item_cost);
