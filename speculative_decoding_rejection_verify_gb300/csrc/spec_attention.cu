@@ -888,20 +888,23 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
             for (int i = 0; i < CK; i += 2) {
               if (!sees(j, i)) z[i] = -INFINITY;
               if (!sees(j, i + 1)) z[i + 1] = -INFINITY;
-              const float2 w = make_float2(exp2_approx(z[i]), exp2_approx(z[i + 1]));
-              const float2 sum = add2(make_float2(l[j][i], l[j][i + 1]), w);
-              l[j][i] = sum.x, l[j][i + 1] = sum.y;
+              float2 w = make_float2(exp2_approx(z[i]), exp2_approx(z[i + 1]));
               // the weights' rounding: bf16 to go with a bf16 cache (2^-8 of each at most), fp16 with E4M3
               if constexpr (F8) {
                 const __half2 h = __floats2half2_rn(w.x, w.y), m = __hmax2(h, *reinterpret_cast<const __half2*>(&over));
                 p[S::kHold ? j : 0][i / 2] = *reinterpret_cast<const uint32_t*>(&h);
                 over = *reinterpret_cast<const uint32_t*>(&m);
               } else {
-                p[S::kHold ? j : 0][i / 2] = pack_bf16(w.x, w.y);
-                const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&p[S::kHold ? j : 0][i / 2]),
-                                                 *reinterpret_cast<const __nv_bfloat162*>(&over));
+                const uint32_t h = pack_bf16(w.x, w.y);
+                p[S::kHold ? j : 0][i / 2] = h;
+                w = make_float2(bf16_low(h), bf16_high(h));
+                const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&h), *reinterpret_cast<const __nv_bfloat162*>(&over));
                 over = *reinterpret_cast<const uint32_t*>(&m);
               }
+              // bf16 weights are summed as they were rounded, so that a row's normalised ones sum to 1: where one slot has
+              // nearly all the weight, its rounding (2^-8 of it) leaves no error.  fp16's is below the output's rounding.
+              const float2 sum = add2(make_float2(l[j][i], l[j][i + 1]), w);
+              l[j][i] = sum.x, l[j][i + 1] = sum.y;
             }
           };
           bool raise = tile == s.tile0;
@@ -933,7 +936,8 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
                   scores(j, x);
 #pragma unroll
                   for (int i = 0; i < CK; ++i) {
-                    const float w = sees(j, i) ? exp2_approx(x[i]) : 0.0f;
+                    float w = sees(j, i) ? exp2_approx(x[i]) : 0.0f;
+                    if constexpr (!F8) w = __bfloat162float(__float2bfloat16(w));  // as it was added
                     l[j][i] = w < 0x1p100f ? l[j][i] - w : 0.0f;
                   }
                 }
