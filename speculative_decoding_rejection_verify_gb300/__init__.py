@@ -194,21 +194,27 @@ def workspace_bytes(B: int, K: int, V: int, dtype: int, top_k: int = 0) -> int:
     return n
 
 
-# Workspaces (per-call scratch) are cached per (device, stream) so repeated calls allocate nothing.
-_ws_cache: Dict[Tuple[int, int], object] = {}
+# Workspaces (per-call scratch) are cached per (device, stream), so repeated calls allocate nothing, and per host thread:
+# a call's kernels hand results on in its scratch, and another thread may enqueue a call on the same stream between them.
+class _Scratch(threading.local):
+    def __init__(self):
+        self.buffers: Dict[Tuple[int, int], object] = {}
+
+
+_scratch = _Scratch()
 
 
 def workspace(nbytes: int, device, stream):
-    """The cached scratch buffer of ``stream`` (a torch.cuda.Stream), grown to ``nbytes``.  It is
+    """The calling thread's cached scratch buffer of ``stream`` (a torch.cuda.Stream), grown to ``nbytes``.  It is
     allocated on that stream, so when a larger one replaces it the caching allocator hands the old
     memory out again only in that stream's order, after the calls that used it."""
     torch = _torch()
     key = (device.index if device.index is not None else torch.cuda.current_device(), stream.cuda_stream)
-    ws = _ws_cache.get(key)
+    ws = _scratch.buffers.get(key)
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(stream):
             ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
+        _scratch.buffers[key] = ws
     return ws
 
 

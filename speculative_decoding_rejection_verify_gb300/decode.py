@@ -248,7 +248,7 @@ def paged_attention(q, k_cache, v_cache, pages, ctx_len, t_per_row=None, mask=No
     ws = workspace_tensor
     if ws is None:
         nbytes = _attention_bytes(T, n, heads, D)
-        ws = sv._ws_cache.get((index, handle))
+        ws = sv._scratch.buffers.get((index, handle))
         if ws is None or ws.numel() < nbytes:
             ws = sv.workspace(nbytes, k_cache.device, stream if stream is not None else torch.cuda.current_stream(index))
     rc = lib.spec_paged_attention(hq, ho, n, c, b, m, D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(),
