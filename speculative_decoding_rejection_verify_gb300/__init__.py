@@ -204,11 +204,25 @@ class _Scratch(threading.local):
 _scratch = _Scratch()
 
 
+def _capturing(stream) -> bool:
+    """Whether a CUDA graph is being captured on ``stream``."""
+    torch = _torch()
+    if stream.cuda_stream == torch.cuda.current_stream().cuda_stream:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def workspace(nbytes: int, device, stream):
     """The calling thread's cached scratch buffer of ``stream`` (a torch.cuda.Stream), grown to ``nbytes``.  It is
     allocated on that stream, so when a larger one replaces it the caching allocator hands the old
-    memory out again only in that stream's order, after the calls that used it."""
+    memory out again only in that stream's order, after the calls that used it.  A graph's replays keep to no such
+    order: while ``stream`` is being captured (torch.cuda.graph) the buffer is new at every call, from the graph's own
+    memory, and is not cached."""
     torch = _torch()
+    if _capturing(stream):
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
     key = (device.index if device.index is not None else torch.cuda.current_device(), stream.cuda_stream)
     ws = _scratch.buffers.get(key)
     if ws is None or ws.numel() < nbytes:

@@ -232,7 +232,8 @@ def paged_attention(q, k_cache, v_cache, pages, ctx_len, t_per_row=None, mask=No
     """Attention of the new tokens' ``q [B, T, q_heads, head_dim]`` over the cache, their own entries included
     (spec_paged_attention, after ``kv_append``); returns ``out`` of q's shape.  ``mask [B, T]`` int64: bit i of
     ``mask[b, t]`` says whether new token t attends to new token i (None: causal); every token attends to the
-    whole context.  ``scale``: None = head_dim ** -0.5."""
+    whole context.  ``scale``: None = head_dim ** -0.5.  ``workspace_tensor``: None = the binding's own scratch, which is
+    the graph's own while one is being captured."""
     torch, lib = _load()
     c, heads, D, index = _cache(k_cache, v_cache, k_scale, v_scale, False)
     if q.dim() != 4:
@@ -249,7 +250,7 @@ def paged_attention(q, k_cache, v_cache, pages, ctx_len, t_per_row=None, mask=No
     if ws is None:
         nbytes = _attention_bytes(T, n, heads, D)
         ws = sv._scratch.buffers.get((index, handle))
-        if ws is None or ws.numel() < nbytes:
+        if ws is None or ws.numel() < nbytes or (torch.cuda.is_current_stream_capturing() if stream is None else sv._capturing(stream)):
             ws = sv.workspace(nbytes, k_cache.device, stream if stream is not None else torch.cuda.current_stream(index))
     rc = lib.spec_paged_attention(hq, ho, n, c, b, m, D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(),
                                   handle)

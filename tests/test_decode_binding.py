@@ -17,6 +17,8 @@ class FakeStream:
 def host(monkeypatch):
     """torch.cuda as the workspaces see it, on the CPU."""
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: FakeStream(0))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return torch.device("cpu", 0)
 
 
@@ -41,3 +43,41 @@ def test_two_threads_never_share_a_workspace(host):
     assert got["a"][0].data_ptr() != got["b"][0].data_ptr()
     assert sv.workspace(10, host, FakeStream(12)) is not sv.workspace(10, host, stream)
     assert sv.workspace(2000, host, stream).numel() == 2000
+
+
+def test_a_captured_call_gets_scratch_of_its_own(host, monkeypatch):
+    """While a graph is being captured the scratch is fresh at every call and not kept: a replay may come at any time, also
+    after a larger call has replaced the cached buffer, and beside another graph's."""
+    stream = FakeStream(21)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    cached = sv.workspace(1000, host, stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    first, second = sv.workspace(1000, host, stream), sv.workspace(1000, host, stream)
+    assert len({x.data_ptr() for x in (cached, first, second)}) == 3
+    assert first.numel() == second.numel() == 1000 and first.dtype == torch.uint8
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    assert sv.workspace(1000, host, stream) is cached
+    fresh = FakeStream(22)  # nothing is cached: what a capture takes is not kept either
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    one = sv.workspace(1000, host, fresh)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    assert sv.workspace(1000, host, fresh) is not one
+
+
+def test_the_capture_that_counts_is_that_of_the_calls_own_stream(monkeypatch):
+    """A call on another stream than the current one asks about its own."""
+    now, capturing = [FakeStream(1)], {2}
+
+    @contextlib.contextmanager
+    def on(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: now[-1])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[-1].cuda_stream in capturing)
+    device, plain, captured = torch.device("cpu", 0), FakeStream(1), FakeStream(2)
+    assert sv.workspace(100, device, plain) is sv.workspace(100, device, plain)
+    assert sv.workspace(100, device, captured) is not sv.workspace(100, device, captured)

@@ -35,3 +35,86 @@ def test_equal_values_come_back_as_they_are(Hq, dtype):
     out = sv.paged_attention(q.cuda(), k.to(dtype).cuda(), v.to(dtype).cuda(), torch.arange(19, dtype=torch.int32, device="cuda")[None],
                              i32([ctx]), scale=1.0)
     assert (out == 1.875).all()
+
+
+# ------------------------------------------------------------------------------------------------
+# captured calls and their scratch
+# ------------------------------------------------------------------------------------------------
+def attention_inputs(B, ctx, seed, Hq=8, H=2, D=128, page=16, T=3):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    pages = -(-(ctx + T) // page)
+    rand = lambda *shape: torch.randn(shape, generator=g, device="cuda").to(BF)  # noqa: E731
+    return [rand(B, T, Hq, D), rand(B * pages, page, H, D), rand(B * pages, page, H, D),
+            torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages), i32([ctx] * B)]
+
+
+def test_a_captured_call_without_a_workspace_keeps_its_memory():
+    """Captured behind a warm call, then a larger call on the same stream, fresh tensors, replays: the result is right
+    and nothing else changes."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    small, large = attention_inputs(2, 1500, 1), attention_inputs(2, 1500, 2, Hq=64, T=16)
+    want = sv.paged_attention(*small)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        sv.paged_attention(*small)
+    st.synchronize()
+    out = torch.zeros_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        sv.paged_attention(*small, out=out)
+    with torch.cuda.stream(st):
+        sv.paged_attention(*large)
+        fresh = [torch.full((1 << 18,), 7.0, device="cuda") for _ in range(64)]
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            st.synchronize()
+            assert torch.equal(out, want)
+    assert all((x == 7.0).all() for x in fresh)
+
+
+def test_two_graphs_of_one_stream_replay_beside_each_other():
+    import speculative_decoding_rejection_verify_gb300 as sv
+    inputs = [attention_inputs(2, 3000, seed) for seed in (1, 2)]
+    want = [sv.paged_attention(*x) for x in inputs]
+    torch.cuda.synchronize()
+    outs, graphs, streams = [torch.zeros_like(w) for w in want], [], [torch.cuda.Stream() for _ in range(2)]
+    for x, out in zip(inputs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=streams[0]):
+            for _ in range(20):
+                sv.paged_attention(*x, out=out)
+    for _ in range(5):
+        for out, graph, st in zip(outs, graphs, streams):
+            with torch.cuda.stream(st):
+                out.zero_()
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, w) for out, w in zip(outs, want))
+
+
+def test_a_captured_verify_without_a_workspace():
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator(device="cuda").manual_seed(3)
+    B, K, V = 6, 3, 5000
+    rand = lambda *shape: torch.rand(shape, generator=g, device="cuda")  # noqa: E731
+    p, q = rand(B, K + 1, V) * 4, rand(B, K, V) * 4
+    draft = torch.randint(0, V, (B, K), generator=g, device="cuda", dtype=torch.int32)
+    args = (p, q, draft, None, rand(B, K), rand(B))
+    want = sv.verify(*args)[:2]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        sv.verify(*args)
+    st.synchronize()
+    out = [torch.zeros_like(w) for w in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        sv.verify(*args, out=tuple(out))
+    with torch.cuda.stream(st):
+        sv.sample(rand(600, 40000), rand(600))  # a larger scratch on the same stream
+        fresh = [torch.full((1 << 16,), 7.0, device="cuda") for _ in range(64)]
+        graph.replay()
+        st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want)) and all((x == 7.0).all() for x in fresh)
