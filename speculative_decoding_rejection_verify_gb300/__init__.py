@@ -204,6 +204,14 @@ class _Scratch(threading.local):
 _scratch = _Scratch()
 
 
+def _launches_on(index: int) -> None:
+    """The library launches on the current device; a stream's handle alone does not say which that is (0 is every
+    device's default stream)."""
+    current = _torch().cuda.current_device()
+    if index != current:
+        raise ValueError(f"tensors on cuda:{index}, but the current device is cuda:{current}")
+
+
 def _capturing(stream) -> bool:
     """Whether a CUDA graph is being captured on ``stream``."""
     torch = _torch()
@@ -265,6 +273,7 @@ def verify(p, q, draft, k_per_row=None, u_accept=None, u_resample=None, temperat
     dev = p.device
     if dev.type != "cuda":
         raise ValueError("verify() takes CUDA tensors; use verify_host() for host arrays")
+    _launches_on(dev.index)
     dt = _dtype_code(p)
     _check(p, "p", (B, K + 1, V), p.dtype, dev)
     if q is not None:
@@ -321,6 +330,9 @@ def sample(logits, u=None, temperature: float = 1.0, top_k: int = 0, top_p: floa
         raise ValueError("logits must be [rows, V]")
     rows, V = logits.shape
     dev = logits.device
+    if dev.type != "cuda":
+        raise ValueError("sample() takes CUDA tensors")
+    _launches_on(dev.index)
     dt = _dtype_code(logits)
     _check(logits, "logits", (rows, V), logits.dtype, dev)
     if u is not None:
@@ -356,6 +368,9 @@ def verify_multi(p, q, draft, u_accept=None, u_resample=None, temperature: float
     B, N, K1, V = p.shape
     K = K1 - 1
     dev = p.device
+    if dev.type != "cuda":
+        raise ValueError("verify_multi() takes CUDA tensors")
+    _launches_on(dev.index)
     dt = _dtype_code(p)
     _check(p, "p", (B, N, K + 1, V), p.dtype, dev)
     if q is not None:
@@ -431,6 +446,8 @@ def verify_host(p, q, draft, k_per_row=None, u_accept=None, u_resample=None, tem
     u_accept, ap = host(u_accept, np.float32)
     u_resample, rp = host(u_resample, np.float32)
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    if dev.index is not None:
+        _launches_on(dev.index)
     nbytes = staging_bytes(B, K, V, dt, top_k, k_per_row is not None)
     if staging is None:
         key = dev.index if dev.index is not None else torch.cuda.current_device()

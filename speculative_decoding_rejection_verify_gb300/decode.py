@@ -137,6 +137,7 @@ def _cache(k_cache, v_cache, k_scale, v_scale, layered):
     index = k_cache.get_device()
     if index < 0:
         raise ValueError("k_cache must be a CUDA tensor")
+    sv._launches_on(index)
     if len(shape) != 4 and not (layered and len(shape) == 5):
         raise ValueError("k_cache must be [num_pages, page_size, heads, head_dim]" +
                          (", or with layers in front of it" if layered else ""))
@@ -291,6 +292,7 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
     index = logits.get_device()
     if index < 0:
         raise ValueError("logits must be a CUDA tensor")
+    sv._launches_on(index)
     dt = sv._dtype_code(logits)
     i32, f32 = torch.int32, torch.float32
     z = _fits(logits, "logits", shape, logits.dtype, index)

@@ -81,3 +81,12 @@ def test_the_capture_that_counts_is_that_of_the_calls_own_stream(monkeypatch):
     device, plain, captured = torch.device("cpu", 0), FakeStream(1), FakeStream(2)
     assert sv.workspace(100, device, plain) is sv.workspace(100, device, plain)
     assert sv.workspace(100, device, captured) is not sv.workspace(100, device, captured)
+
+
+def test_tensors_on_another_device_than_the_current_one_are_refused(monkeypatch):
+    """The library launches on the current device, so tensors of another would be reached from the wrong GPU."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    sv._launches_on(1)
+    for index in (0, 2):
+        with pytest.raises(ValueError, match=f"cuda:{index}.*cuda:1"):
+            sv._launches_on(index)

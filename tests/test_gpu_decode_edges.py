@@ -118,3 +118,32 @@ def test_a_captured_verify_without_a_workspace():
         graph.replay()
         st.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(out, want)) and all((x == 7.0).all() for x in fresh)
+
+
+# ------------------------------------------------------------------------------------------------
+# the device
+# ------------------------------------------------------------------------------------------------
+def test_calls_refuse_tensors_that_are_not_on_the_current_device(monkeypatch):
+    """With a stand-in for the current device's number nothing is launched, and every entry point says so."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    q, k, v, pages, ctx = attention_inputs(1, 40, 1)
+    p = torch.zeros((1, 2, 64), device="cuda")
+    one, key = i32([[0]]), k[:3].unsqueeze(0)
+    before = k.clone()
+    calls = [lambda: sv.paged_attention(q, k, v, pages, ctx), lambda: sv.kv_append(q, key[:, :, 0], key[:, :, 1], k, v, pages, ctx),
+             lambda: sv.kv_keep(k, v, pages, ctx, one, ctx), lambda: sv.process_logits(p),
+             lambda: sv.verify(p, None, one, temperature=0.0), lambda: sv.sample(p[0], temperature=0.0),
+             lambda: sv.verify_multi(p[None], None, one[None], temperature=0.0)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    before = k.clone()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    with pytest.raises(ValueError, match="current device"):
+        sv.verify_host(p.cpu().numpy(), None, one.cpu().numpy(), temperature=0.0, device="cuda:0")
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert torch.equal(k, before)
