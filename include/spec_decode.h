@@ -132,6 +132,8 @@ size_t spec_paged_attention_workspace_bytes(int32_t B, int32_t T, int32_t q_head
  * among them).  A page outside the pool reads as zeros; slots past the page table are dropped.
  * Scores, weights and sums are fp32; the weights are rounded (bf16 for a bf16 cache, fp16 for E4M3)
  * where they multiply V.  With an E4M3 cache a query row that holds an infinity gives NaN.
+ * Each wait inside the kernel has a limit: should one run out, the rows that its block works on come
+ * out as NaN, and the kernel ends.
  * The workspace (256-byte aligned) holds per-call scratch, needs no initialisation and must not be
  * used by two calls that may run at the same time.
  */

@@ -268,8 +268,9 @@ spec_status_t spec_verify_multi(const void* p_logits, const void* q_logits, cons
  * it leaves their summaries NaN, as a failed load would, instead of reading them, and every
  * request of a batch in sampling or greedy mode over 16-byte-aligned rows comes out with
  * SPEC_FLAG_NONFINITE, n_acc 0 and tokens -1 (top-k batches and unaligned rows are not
- * affected).  It exercises the handling of a lost streaming item without any fault.  0 restores
- * normal operation.
+ * affected).  It exercises the handling of a lost streaming item without any fault.  With bit 1 set
+ * the waits inside spec_paged_attention (spec_decode.h) give up after one try, so its rows come out as
+ * NaN, as they would if a copy or a product never ended.  0 restores normal operation.
  */
 void spec_verify_set_test_hooks(int32_t hooks);
 

@@ -183,7 +183,8 @@ def _dtype_code(t) -> int:
 
 def set_test_hooks(hooks: int) -> None:
     """spec_verify_set_test_hooks (test support: bit 0 makes the streaming pass treat every chunk
-    as lost, so a batch comes out flagged non-finite)."""
+    as lost, so a batch comes out flagged non-finite; bit 1 makes the waits inside paged_attention
+    give up at once, so its rows come out as NaN)."""
     load().spec_verify_set_test_hooks(int(hooks))
 
 

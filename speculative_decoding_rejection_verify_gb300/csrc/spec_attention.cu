@@ -36,6 +36,8 @@
 
 namespace sv {
 
+extern std::atomic<int32_t> g_test_hooks;  // spec_verify_set_test_hooks
+
 constexpr int kTileSlots = 128;       // slots per tile = rows of the matrix unit
 // Items of at most so many tiles are never cut, which saves the join (4 requests x 8 kv heads, 20 rows: 9.0 us against
 // 11.8 at 300 slots, 10.5 against 12.0 at 600, 12.5 against 12.6 at 1000; one request x 2 heads: 7.2 / 8.6, 8.5 / 8.5, 10.3 / 9.1).
@@ -58,6 +60,7 @@ struct AttnParams {
   int rows;                    // group * tokens
   int item_cost;               // an item's beginning and end, in tiles
   int whole;                   // items are not cut: the CTA that one begins in takes all of it
+  int wait_tries;              // the limit of every wait
   float scale_log2;            // scale * log2(e)
   float* part;                 // [CTA][2][rows][D] unnormalised O
   float2* part_ml;             // [CTA][2][rows] (m in log2 units, l)
@@ -103,20 +106,30 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {  // d
   return done != 0;
 }
 
-// Waits for the phase with a limit; a wait that runs out marks the block dead, which ends every other
+// Waits for the phase, `limit` tries at most; a wait that runs out marks the block dead, which ends every other
 // wait in it soon after.  Nothing here waits on another block.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+struct Patience {
+  volatile int* dead;
+  int limit;
+};
+constexpr int kWaitTries = 1 << 22;
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Patience& w) {
   if (mbar_try(bar, parity)) return true;
-  for (int i = 0; i < (1 << 22); ++i) {
+  for (int i = 0; i < w.limit; ++i) {
     if (mbar_try(bar, parity)) return true;
-    if ((i & 255) == 0 && *dead) return false;
+    if ((i & 255) == 0 && *w.dead) return false;
   }
-  *dead = 1;
+  *w.dead = 1;
   return false;
 }
 // the same for a whole warp that goes on together
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* dead) {
-  return __all_sync(~0u, mbar_wait(bar, parity, dead));
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, const Patience& w) {
+  return __all_sync(~0u, mbar_wait(bar, parity, w));
+}
+// Behind a wait that ran out: sees what is in flight come to its end before the block goes.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < (1 << 16) && !mbar_try(bar, parity); ++i) {
+  }
 }
 
 // A copy by one elected lane of a warp that goes through the code together (see tc_mma).
@@ -373,8 +386,10 @@ struct Shape {
     uint64_t q_loaded[2], q_full[2], q_empty[2], mult_full[2];
     uint64_t v16_full[2], v16_empty[2];
     uint64_t s_full[2], s_empty[2], p_full, o_full;
+    uint64_t products_done;          // behind a wait that ran out
     uint32_t tmem;
     int dead;
+    int copies[2], queries;          // tiles of K and V, and Qs, whose copies were issued
     int start_b, start_offset, total;
     uint32_t bad_value[4];           // segment + 1 whose new tokens hold a value that is not finite, by segment % 4
     int warp_sum[24];
@@ -460,6 +475,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
     }
     mbar_init(smem_addr(&st->p_full), kSoftmaxWarps);
     mbar_init(smem_addr(&st->o_full), 1);
+    mbar_init(smem_addr(&st->products_done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // Nothing before this reads or writes what another kernel may, nor takes TMEM that one before it may still need.
@@ -509,7 +525,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
   }
   __syncthreads();
   const uint32_t tmem = st->tmem;
-  volatile int* dead = &st->dead;
+  const Patience dead = {&st->dead, P.wait_tries};
   const int start_b = count > 0 ? st->start_b : 0, start_offset = count > 0 ? st->start_offset : 0;
 
   if (warp >= kSoftmaxWarps) {
@@ -530,7 +546,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
       int slot = is_v;
       uint32_t phase = 0;  // of the ring
       bool ok = true;
-      int issued = 0;
+      int issued = 0, queries = 0;
       for (int seg = 0; ok && walk.next(s); ++seg) {
         const int head = uniform(s.head), tile0 = uniform(s.tile0), tile1 = uniform(s.tile1);
         if (!is_v) {
@@ -544,6 +560,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
           for (int h = 0; h < S::kHalves; ++h)
             tma_load(base + (uint32_t)(q_buf - smem) + qb * S::kQ + h * NT * 128, &P.q_map, h * 64, head * P.group,
                      uniform(s.row_group) * P.tokens, uniform(s.b), bar);
+          ++queries;
         }
         const int32_t* table = P.batch.pages + (int64_t)s.b * P.batch.max_pages;
         const auto entry = [&](int tile) {  // the page of this lane's copy of a tile; one past the pool reads as zeros
@@ -584,13 +601,10 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
           if (slot >= S::kSlots) slot -= S::kSlots, phase ^= 1;
         }
       }
-      if (!ok)  // a wait ran out: see the copies in flight land before the block ends
-        for (int i = 0; i < min(issued, S::kSlots / 2); ++i) {
-          slot -= 2;
-          if (slot < 0) slot += S::kSlots, phase ^= 1;
-          for (int n = 0; n < (1 << 16) && !mbar_try(smem_addr(&st->ring_full[slot]), phase); ++n) {
-          }
-        }
+      if (lane == 0) {
+        st->copies[is_v] = issued;
+        if (!is_v) st->queries = queries;
+      }
     } else if (warp == kIssuer) {
       // ---- matrix products: weighted values of a tile or scores of the next, as either is ready ----
       const auto uniform = [](uint32_t x) { return __shfl_sync(~0u, x, 0); };
@@ -670,13 +684,11 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
         }
         if (moved) {
           idle = 0;
-        } else if (++idle > (1 << 24) || ((idle & 255) == 0 && uniform(*dead))) {
-          *dead = 1;
+        } else if (++idle > 4 * P.wait_tries || ((idle & 255) == 0 && uniform(*dead.dead))) {
+          *dead.dead = 1;
           break;
         }
       }
-      if (uniform(*dead) && s_it > 0)  // a wait ran out: let the products in flight end before TMEM is freed
-        for (int n = 0; n < (1 << 16); ++n) __nanosleep(20);
       __syncwarp();
     } else if (F8 && warp > kIssuer && warp <= kIssuer + kConvertWarps) {
       // ---- E4M3 caches: Q split for the product with K as it is; V to fp16 (exact) for that with P ----
@@ -1067,7 +1079,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
       tc_fence_after();
       group_sync(bar);
       const bool bad = st->bad_value[seg & 3] == (uint32_t)seg + 1;
-      const bool lost = *dead != 0;
+      const bool lost = *dead.dead != 0;
       char* out = P.out.data + s.b * P.out.row + (int64_t)t0 * P.out.token + (int64_t)s.head * P.group * P.out.head + key * 2;
       float* part = P.part + part_row * D + key;
       const int rows_all = min(P.rows, (P.batch.T - t0) * P.group);
@@ -1128,9 +1140,33 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
 
   tc_fence_before();
   __syncthreads();
+  const bool lost = *dead.dead != 0;  // a wait ran out: products and copies may be in flight that nobody saw end
   if (warp == kIssuer) {
     tc_fence_after();
+    if (lost) {
+      tc_commit(smem_addr(&st->products_done));  // arrives behind every product of this warp
+      mbar_drain(smem_addr(&st->products_done), 0);
+      __syncwarp();
+    }
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kColumns));
+  }
+  if (lost && warp == kProducer) {
+    // Tile i of K is copy 2 i of the ring, of V copy 2 i + 1; copy n goes to slot n % kSlots.  A slot is filled again only
+    // when its last filling was used, so the last copy of each slot is the only one that may be in flight.
+    for (int slot = 0; slot < S::kSlots; ++slot) {
+      int last = -1;
+      for (int kv = 0; kv < 2; ++kv) {
+        const int issued = st->copies[kv];
+        for (int i = issued - 1; i >= max(issued - S::kSlots, 0); --i)
+          if ((2 * i + kv) % S::kSlots == slot) {
+            last = max(last, 2 * i + kv);
+            break;
+          }
+      }
+      if (last >= 0) mbar_drain(smem_addr(&st->ring_full[slot]), (last / S::kSlots) & 1);
+    }
+    for (int i = max(st->queries - S::kQBufs, 0); i < st->queries; ++i)
+      mbar_drain(smem_addr(&st->q_loaded[i % S::kQBufs]), (i / S::kQBufs) & 1);
   }
 }
 
@@ -1354,6 +1390,7 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
   // 125 us at 2 tiles, 118 at 4, 119 at 6; 24 rows in bf16, 0 to 4001 slots: 22.4 us at 1, 21.0 at 2, 21.5 at 3)
   P.item_cost = cache->dtype == SPEC_DTYPE_E4M3 || P.rows > 64 ? 4 : 2;
   P.whole = per <= kWholeTiles;
+  P.wait_tries = g_test_hooks.load(std::memory_order_relaxed) & 2 ? 0 : kWaitTries;
   const int64_t most = (int64_t)batch->B * cache->heads * P.row_groups * ((per > 0 ? per : 1) + P.item_cost);
   if (most > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
 

@@ -13,6 +13,14 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
+def attention_inputs(B, ctx, seed, Hq=8, H=2, D=128, page=16, T=3):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    pages = -(-(ctx + T) // page)
+    rand = lambda *shape: torch.randn(shape, generator=g, device="cuda").to(BF)  # noqa: E731
+    return [rand(B, T, Hq, D), rand(B * pages, page, H, D), rand(B * pages, page, H, D),
+            torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages), i32([ctx] * B)]
+
+
 # ------------------------------------------------------------------------------------------------
 # paged_attention
 # ------------------------------------------------------------------------------------------------
@@ -37,17 +45,31 @@ def test_equal_values_come_back_as_they_are(Hq, dtype):
     assert (out == 1.875).all()
 
 
+@pytest.mark.parametrize("T,Hq", [(1, 4), (4, 16), (17, 8), (16, 16), (64, 8)])
+@pytest.mark.parametrize("ctx,width", [(300, 0), (1500, 0), (300, 4000)])
+@pytest.mark.parametrize("dtype", [BF, R.F8])
+def test_a_wait_that_runs_out_ends_the_call_with_nan_rows(T, Hq, ctx, width, dtype):
+    """Every wait inside the kernel gives up after one try, with copies in flight: the call ends, all rows say so, and
+    the next call is exact."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    q, k, v, pages, n = attention_inputs(3, ctx, 5, Hq=Hq, T=T)
+    k, v = k.to(dtype), v.to(dtype)
+    if width:
+        pages = torch.cat([pages, i32([[0] * width] * 3)], 1).contiguous()
+    want = sv.paged_attention(q, k, v, pages, n)
+    sv.set_test_hooks(2)
+    try:
+        lost = sv.paged_attention(q, k, v, pages, n)
+        torch.cuda.synchronize()
+    finally:
+        sv.set_test_hooks(0)
+    assert torch.isfinite(want).all() and torch.isnan(lost).all()
+    assert torch.equal(sv.paged_attention(q, k, v, pages, n), want)
+
+
 # ------------------------------------------------------------------------------------------------
 # captured calls and their scratch
 # ------------------------------------------------------------------------------------------------
-def attention_inputs(B, ctx, seed, Hq=8, H=2, D=128, page=16, T=3):
-    g = torch.Generator(device="cuda").manual_seed(seed)
-    pages = -(-(ctx + T) // page)
-    rand = lambda *shape: torch.randn(shape, generator=g, device="cuda").to(BF)  # noqa: E731
-    return [rand(B, T, Hq, D), rand(B * pages, page, H, D), rand(B * pages, page, H, D),
-            torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages), i32([ctx] * B)]
-
-
 def test_a_captured_call_without_a_workspace_keeps_its_memory():
     """Captured behind a warm call, then a larger call on the same stream, fresh tensors, replays: the result is right
     and nothing else changes."""
