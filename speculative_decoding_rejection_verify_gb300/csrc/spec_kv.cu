@@ -34,13 +34,27 @@ __device__ __forceinline__ int64_t slot_offset(const Batch& b, const Cache& c, i
   return page * c.page + (slot & ((1 << c.page_shift) - 1)) * c.slot;
 }
 
-// 8 elements of a key or value into the cache.  E4M3: times the scale's reciprocal, which is within 2^-23 of
-// the quotient, 2^-19 of the rounding to 4 significant bits.
+// x / s for E4M3's rounding: the product with the reciprocal is up to 1.5 units in the last place off, which puts a
+// quotient that lies halfway between two codes on either side; corrected by its residual x - q s (P. Markstein, IBM Journal
+// of Research and Development 34, 1990) it is the quotient.  For s within 2^+-80 the residual is exact for all quotients
+// that are neither under half of the smallest code nor over the largest.  (4 x 2047 tokens, interleaved: 22.5 us without
+// the correction, 23.0 with it, 24.9 with divisions.)
+__device__ __forceinline__ float quotient(float x, float s, float inverse) {
+  const float q = x * inverse;
+  return fabsf(q) < 512.0f ? fmaf(fmaf(-q, s, x), inverse, q) : q;  // beyond 448, infinite or NaN: q says it
+}
+constexpr float kLeastScale = 0x1p-80f, kMostScale = 0x1p80f;
+// A power of two that brings another scale to [1, 2), or a subnormal one as near as it reaches; 0 and NaN stay.
+__device__ __forceinline__ float scale_power(float s) {
+  return __int_as_float(max((254 - ((__float_as_int(s) >> 23) & 255)) << 23, 1 << 22));
+}
+
+// 8 elements of a key or value into the cache.
 template <bool F8>
-__device__ __forceinline__ void store_entry(char* p, float (&x)[8], float inv_scale) {
+__device__ __forceinline__ void store_entry(char* p, float (&x)[8], float scale, float inverse) {
   if constexpr (F8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= inv_scale;
+    for (int i = 0; i < 8; ++i) x[i] = quotient(x[i], scale, inverse);
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_e4m3(x[0], x[1], x[2], x[3]), pack_e4m3(x[4], x[5], x[6], x[7]));
   } else {
     *reinterpret_cast<uint4*>(p) = pack8(x);
@@ -153,10 +167,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         constexpr int ES = F8 ? 1 : 2;
         const int hh = h < k_end ? h - P.q_heads : h - k_end;
         const float* scales = h < k_end ? P.cache.k_scale : P.cache.v_scale;
-        const float inv = F8 && scales ? 1.0f / __ldg(scales + hh) : 1.0f;
+        float scale = F8 && scales ? __ldg(scales + hh) : 1.0f;
+        if (F8 && !(fabsf(scale) >= kLeastScale && fabsf(scale) <= kMostScale)) {
+          const float power = scale_power(scale);
+          scale *= power;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            x[n] *= power;
+            if (pair) y[n] *= power;
+          }
+        }
+        const float inverse = 1.0f / scale;
         char* e = (h < k_end ? P.cache.k : P.cache.v) + at + hh * P.cache.head;
-        store_entry<F8>(e + lo * ES, x, inv);
-        if (pair) store_entry<F8>(e + (lo + far) * ES, y, inv);
+        store_entry<F8>(e + lo * ES, x, scale, inverse);
+        if (pair) store_entry<F8>(e + (lo + far) * ES, y, scale, inverse);
       }
     }
   }

@@ -68,6 +68,33 @@ def test_a_wait_that_runs_out_ends_the_call_with_nan_rows(T, Hq, ctx, width, dty
 
 
 # ------------------------------------------------------------------------------------------------
+# kv_append
+# ------------------------------------------------------------------------------------------------
+def test_entries_are_the_quotients_codes():
+    """An E4M3 entry is x / scale in fp32, rounded once: the code of the exact quotient where that lies halfway between two
+    codes (odd multiples of 5 bits times a scale of few bits), 0 / scale = 0 however small the scale is."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    D, page = 64, 16
+    scales = [3.0, 5.0, 7.0, 0.0390625, 1.75, 0.1, 0.4375, 7 * 2.0 ** -120, 3 * 2.0 ** -149, 2.0 ** -140, 7 * 2.0 ** 120, 2.0 ** 127]
+    H = len(scales)
+    ties = torch.tensor([17.0, 19, 21, 23, 25, 27, 29, 31])
+    x = torch.zeros((1, 1, H, D))
+    for h, s in enumerate(scales):
+        x[0, 0, h, :8] = ties * s
+        x[0, 0, h, 8:16] = -ties * s / 16
+        x[0, 0, h, 16:48] = torch.randn(32, generator=torch.Generator().manual_seed(h)) * s * 30
+        x[0, 0, h, 48:56] = torch.tensor([1e38, -1e38, float("inf"), -float("inf"), 1e-38, 1.0, -3.0, 2.0 ** -130])
+    x = x.to(BF)
+    scale = torch.tensor(scales)
+    want = (x[0, 0].float() / scale[:, None]).clamp(-448, 448).to(R.F8).float()
+    k = torch.zeros((1, page, H, D), device="cuda").to(R.F8)
+    v = torch.zeros((1, page, H, D), device="cuda").to(R.F8)
+    sv.kv_append(None, x.cuda(), x.cuda(), k, v, i32([[0]]), i32([3]), k_scale=scale.cuda(), v_scale=scale.cuda())
+    for c in (k, v):
+        assert torch.equal(c[0, 3].float().cpu(), want)
+
+
+# ------------------------------------------------------------------------------------------------
 # captured calls and their scratch
 # ------------------------------------------------------------------------------------------------
 def test_a_captured_call_without_a_workspace_keeps_its_memory():
