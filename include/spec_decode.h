@@ -160,7 +160,7 @@ spec_status_t spec_kv_keep(const spec_kv_cache_t* cache, const spec_decode_batch
  *       [0, V) are skipped, lengths are clamped into [0, history_stride];
  *   draft [B, T-1] int32: at position t the drafts before t count as output too;
  *   t_per_row [B] int32: rows past T_b are neither read nor written;
- *   repetition, presence, frequency [B] float (repetition > 0);
+ *   repetition, presence, frequency [B] float (repetition in [2^-126, 2^126]);
  *   bias_ids [B, bias_n] int32, bias [B, bias_n] float: added to the logit of the id (an id
  *       outside [0, V) is skipped; of two entries with one id the later holds);
  *   mask [B, T, ceil(V / 32)] int32: token v is allowed where bit v % 32 of word v / 32 is set.
@@ -181,8 +181,8 @@ typedef struct {
 } spec_logit_rules_t;
 
 /*
- * out[b, t, v] from logits[b, t, v] ([B, T, V] of dtype; out may be logits itself), in fp32 and
- * rounded once; c = times v is among the output tokens and the drafts before t:
+ * out[b, t, v] from logits[b, t, v] ([B, T, V] of dtype; out may be logits itself), each step in fp32 (a
+ * logit or quotient outside 2^+-60 is divided to within 2 units in the last place); c = times v is among the output tokens and the drafts before t:
  *   z > 0 ? z / repetition : z * repetition   where v is in the prompt or c > 0;
  *   z - frequency * c - presence * (c > 0);
  *   z + bias;   -inf where the mask forbids v (whatever the logit was).

@@ -129,11 +129,24 @@ __device__ __forceinline__ Stretch count_rules(const RuleParams& P, uint32_t* wo
   return s;
 }
 
-// What a token's word makes of its logit x: (seen ? x * (x > 0 ? 1 / rep : rep) : x) + off.  The reciprocal is
-// within 2^-23 of the division, and the terms of off are summed before they meet the logit.
+// A repeated token's logit: x / rep or x * rep.  The quotient is the product with the reciprocal, twice corrected by its
+// residual (P. Markstein, IBM Journal of Research and Development 34, 1990): the first leaves it within a unit in the
+// last place, so the second rounds it correctly.  Where the residual may not be exact the product stands, within 2 units.
+// (64 x 7 x 128256 in bf16: 53.3 us without the corrections, 54.4 with them, 56.7 with divisions.)
+__device__ __forceinline__ float repeated(float x, const Stretch& s) {
+  float q = x * s.inv;
+  if (fabsf(x) > 0x1p-60f && fabsf(q) < 0x1p60f) {
+    q = fmaf(fmaf(-q, s.rep, x), s.inv, q);
+    q = fmaf(fmaf(-q, s.rep, x), s.inv, q);
+  }
+  return x > 0.0f ? q : x * s.rep;
+}
+
+// What a token's word makes of its logit: (seen ? repeated(x) : x) + off.  The terms of off are summed before they meet
+// the logit.
 __device__ __forceinline__ float effect(const RuleParams& P, const Stretch& s, uint32_t w, bool& seen) {
   const uint32_t count = w & kCountMask, e = (w & ~kPromptBit) >> kBiasShift;
-  seen = s.penal && (count > 0 || (w & kPromptBit));
+  seen = s.rep != 1.0f && (count > 0 || (w & kPromptBit));
   float off = e ? __ldg(P.r.bias + (int64_t)s.b * P.r.bias_n + e - 1) : 0.0f;
   if (count > 0) off = off - s.fre * (float)count - s.pre;
   return off;
@@ -209,8 +222,8 @@ __global__ void __launch_bounds__(kRuleThreads, 5) rules_kernel(const __grid_con
           if (seen) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-              const float f = x[i] > 0.0f ? s.inv : s.rep;
-              x[i] = fmaf(x[i], (seen >> i) & 1u ? f : 1.0f, off[i]);
+              if ((seen >> i) & 1u) x[i] = repeated(x[i], s);
+              x[i] += off[i];
             }
           }
 #pragma unroll
@@ -228,9 +241,9 @@ __global__ void __launch_bounds__(kRuleThreads, 5) rules_kernel(const __grid_con
 // change from position to position: every token's effect lies in shared memory, with bitmaps of the tokens that have
 // one and that are seen.  The drafts' logits behind them are worked out beforehand and written last.  Runs that
 // reach past the stretch, and all where out lies otherwise than logits on 16 bytes, are read and written an element
-// at a time.
+// at a time.  (Four blocks an SM, not the three that its registers would leave: 64 x 7 x 128257 in bf16: 115 us against 133.)
 template <bool BF16>
-__global__ void __launch_bounds__(kRuleThreads) rules_odd_kernel(const __grid_constant__ RuleParams P) {
+__global__ void __launch_bounds__(kRuleThreads, 4) rules_odd_kernel(const __grid_constant__ RuleParams P) {
   constexpr int ES = BF16 ? 2 : 4, VEC = 16 / ES;
   using Element = typename std::conditional<BF16, uint16_t, uint32_t>::type;
   extern __shared__ __align__(16) uint32_t word[];  // [stretch], then the bitmaps
@@ -267,7 +280,7 @@ __global__ void __launch_bounds__(kRuleThreads) rules_odd_kernel(const __grid_co
     const int at = v >> 5;
     return __funnelshift_r(p[at], p[at + 1], v & 31) & kAll;
   };
-  const auto shaped = [&](float x, bool is, float off) { return fmaf(x, is ? (x > 0.0f ? s.inv : s.rep) : 1.0f, off); };
+  const auto shaped = [&](float x, bool is, float off) { return (is ? repeated(x, s) : x) + off; };
   // draft i at a position t > i counts with all drafts of its token before t
   constexpr int kPairs = SPEC_MAX_NEW * (SPEC_MAX_NEW - 1) / 2, kPairsEach = (kPairs + kRuleThreads - 1) / kRuleThreads;
   Element fixed[kPairsEach];

@@ -95,6 +95,25 @@ def test_entries_are_the_quotients_codes():
 
 
 # ------------------------------------------------------------------------------------------------
+# process_logits
+# ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("V", [2048, 2051])
+def test_repeated_tokens_logits_are_quotients(V):
+    """z / repetition is the quotient rounded to fp32, wherever the row begins."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(5)
+    B, T = 6, 3
+    z = torch.randn((B, T, V), generator=g) * 10
+    z[:, :, :200] = z[:, :, :200].abs() * torch.exp(torch.randn(200, generator=g) * 10)
+    rep = torch.tensor([1.1, 1.0 / 3, 1.9999999, 1.3, 7.0, 0.7])
+    ids = torch.arange(V, dtype=torch.int32).expand(B, V).contiguous()
+    n = torch.full((B,), V, dtype=torch.int32)
+    got = sv.process_logits(z.cuda(), history=ids.cuda(), history_len=n.cuda(), prompt_len=n.cuda(), repetition=rep.cuda()).cpu()
+    r = rep[:, None, None]
+    assert torch.equal(got, torch.where(z > 0, z / r, z * r))
+
+
+# ------------------------------------------------------------------------------------------------
 # captured calls and their scratch
 # ------------------------------------------------------------------------------------------------
 def test_a_captured_call_without_a_workspace_keeps_its_memory():
