@@ -92,16 +92,18 @@ _pack_rules = struct.Struct("11Pii").pack
 # with it only when something is.
 _torch = None
 _raw_stream = None
+_current_device = None
 
 
 def _load():
     """(torch, the library), and this module's shortcuts to them."""
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device
     lib = sv.load()
     if _torch is None:
         import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _torch = torch
     return _torch, lib
 
@@ -137,7 +139,8 @@ def _cache(k_cache, v_cache, k_scale, v_scale, layered):
     index = k_cache.get_device()
     if index < 0:
         raise ValueError("k_cache must be a CUDA tensor")
-    sv._launches_on(index)
+    if index != _current_device():
+        sv._launches_on(index)
     if len(shape) != 4 and not (layered and len(shape) == 5):
         raise ValueError("k_cache must be [num_pages, page_size, heads, head_dim]" +
                          (", or with layers in front of it" if layered else ""))
@@ -292,7 +295,8 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
     index = logits.get_device()
     if index < 0:
         raise ValueError("logits must be a CUDA tensor")
-    sv._launches_on(index)
+    if index != _current_device():
+        sv._launches_on(index)
     dt = sv._dtype_code(logits)
     i32, f32 = torch.int32, torch.float32
     z = _fits(logits, "logits", shape, logits.dtype, index)

@@ -207,6 +207,7 @@ def test_calls_refuse_tensors_that_are_not_on_the_current_device(monkeypatch):
     torch.cuda.synchronize()
     before = k.clone()
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(sv.decode, "_current_device", lambda: 1)
     for call in calls:
         with pytest.raises(ValueError, match="current device"):
             call()
