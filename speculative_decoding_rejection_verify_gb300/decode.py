@@ -183,11 +183,8 @@ def _like(x, stream):
 
 @functools.lru_cache(maxsize=None)
 def _attention_bytes(T: int, q_heads: int, heads: int, D: int) -> int:
-    """The workspace does not depend on the number of requests."""
-    n = sv.load().spec_paged_attention_workspace_bytes(1, T, q_heads, heads, D)
-    if n == 0:
-        raise sv.SpecVerifyError(1, "spec_paged_attention_workspace_bytes")
-    return n
+    """The workspace does not depend on the number of requests.  0: the call itself says what is wrong."""
+    return sv.load().spec_paged_attention_workspace_bytes(1, T, q_heads, heads, D)
 
 
 def kv_append(q, k, v, k_cache, v_cache, pages, ctx_len, cos=None, sin=None, t_per_row=None, positions=None,
@@ -256,7 +253,7 @@ def paged_attention(q, k_cache, v_cache, pages, ctx_len, t_per_row=None, mask=No
         ws = sv._scratch.buffers.get((index, handle))
         if ws is None or ws.numel() < nbytes or (torch.cuda.is_current_stream_capturing() if stream is None else sv._capturing(stream)):
             ws = sv.workspace(nbytes, k_cache.device, stream if stream is not None else torch.cuda.current_stream(index))
-    rc = lib.spec_paged_attention(hq, ho, n, c, b, m, D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(),
+    rc = lib.spec_paged_attention(hq, ho, n, c, b, m, max(D, 1) ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(),
                                   handle)
     if rc != sv.SPEC_OK:
         raise sv.SpecVerifyError(rc, "spec_paged_attention")

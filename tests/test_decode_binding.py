@@ -90,3 +90,11 @@ def test_tensors_on_another_device_than_the_current_one_are_refused(monkeypatch)
     for index in (0, 2):
         with pytest.raises(ValueError, match=f"cuda:{index}.*cuda:1"):
             sv._launches_on(index)
+
+
+def test_sizes_that_have_no_workspace_are_left_to_the_call():
+    """Zero bytes, not an error of the binding's own: the library tells sizes beyond a limit from impossible ones."""
+    sv._build.build()
+    for T, q_heads, heads, D in ((65, 4, 2, 64), (2, 4, 2, 96), (2, 129, 1, 64), (2, 3, 2, 64)):
+        assert sv.decode._attention_bytes(T, q_heads, heads, D) == 0
+    assert sv.decode._attention_bytes(2, 4, 2, 64) > 0

@@ -216,3 +216,23 @@ def test_calls_refuse_tensors_that_are_not_on_the_current_device(monkeypatch):
     monkeypatch.undo()
     torch.cuda.synchronize()
     assert torch.equal(k, before)
+
+
+# ------------------------------------------------------------------------------------------------
+# refusals
+# ------------------------------------------------------------------------------------------------
+def test_sizes_beyond_the_limits_are_unsupported():
+    """The binding raises what the library says of the sizes: 2 beyond a limit, 1 where they cannot be."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+
+    def code(T=2, Hq=4, H=2, D=64):
+        c = torch.zeros((3, 16, H, D), dtype=BF, device="cuda")
+        q = torch.zeros((1, T, Hq, D), dtype=BF, device="cuda")
+        with pytest.raises(sv.SpecVerifyError) as e:
+            sv.paged_attention(q, c, c, i32([[0, 1, 2]]), i32([3]))
+        return e.value.code
+
+    assert code(T=65) == 2
+    assert code(D=96) == 2
+    assert code(Hq=129, H=1) == 2
+    assert code(Hq=3) == 1
