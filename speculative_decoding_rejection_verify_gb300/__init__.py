@@ -241,6 +241,17 @@ def workspace(nbytes: int, device, stream):
     return ws
 
 
+def _given_workspace(t, device, name: str = "workspace_tensor"):
+    """A caller's workspace: the library may write to every byte of it."""
+    if t.dtype != _torch().uint8:
+        raise TypeError(f"{name}: dtype {t.dtype} != torch.uint8")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t
+
+
 def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -310,7 +321,7 @@ def verify(p, q, draft, k_per_row=None, u_accept=None, u_resample=None, temperat
         sp = sp if sp is not None else StatsStruct()
         sp.pass1_done = pass1_event.cuda_event
     nbytes = workspace_bytes(B, K, V, dt, top_k)
-    ws = workspace_tensor if workspace_tensor is not None else workspace(nbytes, dev, st)
+    ws = workspace(nbytes, dev, st) if workspace_tensor is None else _given_workspace(workspace_tensor, dev)
     smp = _sampling(temperature, draft_temperature, top_k, top_p)
     rc = lib.spec_verify_ex(_ptr(p), _ptr(q), _ptr(draft), _ptr(k_per_row), _ptr(u_accept), _ptr(u_resample),
                             ctypes.byref(smp), tokens.data_ptr(), nacc.data_ptr(),
@@ -347,7 +358,7 @@ def sample(logits, u=None, temperature: float = 1.0, top_k: int = 0, top_p: floa
     nbytes = lib.spec_sample_workspace_bytes(rows, V, dt, int(top_k))
     if nbytes == 0:
         raise SpecVerifyError(1, "spec_sample_workspace_bytes")
-    ws = workspace_tensor if workspace_tensor is not None else workspace(nbytes, dev, st)
+    ws = workspace(nbytes, dev, st) if workspace_tensor is None else _given_workspace(workspace_tensor, dev)
     smp = SamplingStruct(float(temperature), float(temperature), int(top_k), float(top_p))
     rc = lib.spec_sample(_ptr(logits), _ptr(u), ctypes.byref(smp), tokens.data_ptr(),
                          None if pr is None else pr.data_ptr(), rows, V, dt, ws.data_ptr(), ws.numel(),
@@ -391,7 +402,7 @@ def verify_multi(p, q, draft, u_accept=None, u_resample=None, temperature: float
     nbytes = lib.spec_verify_multi_workspace_bytes(B, N, K, V, dt)
     if nbytes == 0:
         raise SpecVerifyError(1, "spec_verify_multi_workspace_bytes")
-    ws = workspace_tensor if workspace_tensor is not None else workspace(nbytes, dev, st)
+    ws = workspace(nbytes, dev, st) if workspace_tensor is None else _given_workspace(workspace_tensor, dev)
     smp = _sampling(temperature, draft_temperature, 0, 1.0)
     rc = lib.spec_verify_multi(_ptr(p), _ptr(q), _ptr(draft), _ptr(u_accept), _ptr(u_resample), ctypes.byref(smp),
                                tokens.data_ptr(), nacc.data_ptr(), _ptr(chain), _ptr(flags), B, N, K, V, dt,
@@ -456,6 +467,8 @@ def verify_host(p, q, draft, k_per_row=None, u_accept=None, u_resample=None, tem
         if staging is None or staging.numel() < nbytes:
             staging = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
             _stage_cache[key] = staging
+    else:
+        _given_workspace(staging, torch.device("cuda", dev.index if dev.index is not None else torch.cuda.current_device()), "staging")
     if out is None:
         tokens = np.empty((B, K + 1), np.int32)
         nacc = np.empty(B, np.int32)

@@ -253,6 +253,8 @@ def paged_attention(q, k_cache, v_cache, pages, ctx_len, t_per_row=None, mask=No
         ws = sv._scratch.buffers.get((index, handle))
         if ws is None or ws.numel() < nbytes or (torch.cuda.is_current_stream_capturing() if stream is None else sv._capturing(stream)):
             ws = sv.workspace(nbytes, k_cache.device, stream if stream is not None else torch.cuda.current_stream(index))
+    else:
+        sv._given_workspace(ws, k_cache.device)
     rc = lib.spec_paged_attention(hq, ho, n, c, b, m, max(D, 1) ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(),
                                   handle)
     if rc != sv.SPEC_OK:

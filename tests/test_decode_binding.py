@@ -98,3 +98,16 @@ def test_sizes_that_have_no_workspace_are_left_to_the_call():
     for T, q_heads, heads, D in ((65, 4, 2, 64), (2, 4, 2, 96), (2, 129, 1, 64), (2, 3, 2, 64)):
         assert sv.decode._attention_bytes(T, q_heads, heads, D) == 0
     assert sv.decode._attention_bytes(2, 4, 2, 64) > 0
+
+
+def test_a_callers_workspace_is_checked():
+    """Bytes on the device of the call, without gaps: the library writes numel() of them behind the address."""
+    device = torch.device("cpu", 0)
+    good = torch.zeros(512, dtype=torch.uint8)
+    assert sv._given_workspace(good, good.device) is good
+    with pytest.raises(TypeError, match="uint8"):
+        sv._given_workspace(good.view(torch.float32), good.device)
+    with pytest.raises(ValueError, match="expected cuda:0"):
+        sv._given_workspace(good, torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="contiguous"):
+        sv._given_workspace(good[::2], good.device)

@@ -236,3 +236,20 @@ def test_sizes_beyond_the_limits_are_unsupported():
     assert code(D=96) == 2
     assert code(Hq=129, H=1) == 2
     assert code(Hq=3) == 1
+
+
+def test_a_workspace_on_the_host_is_refused():
+    import speculative_decoding_rejection_verify_gb300 as sv
+    ws = torch.zeros(64 << 20, dtype=torch.uint8)
+    p, draft = torch.zeros((1, 2, 64), device="cuda"), i32([[0]])
+    for call in (lambda w: sv.paged_attention(*attention_inputs(1, 20, 1), workspace_tensor=w),
+                 lambda w: sv.verify(p, None, draft, temperature=0.0, workspace_tensor=w),
+                 lambda w: sv.sample(p[0], temperature=0.0, workspace_tensor=w),
+                 lambda w: sv.verify_multi(p[None], None, draft[None], temperature=0.0, workspace_tensor=w)):
+        with pytest.raises(ValueError):
+            call(ws)
+        with pytest.raises(TypeError):
+            call(ws.cuda().view(torch.int32))
+        call(ws.cuda())
+    with pytest.raises(ValueError):
+        sv.verify_host(p.cpu().numpy(), None, draft.cpu().numpy(), temperature=0.0, staging=ws)
