@@ -221,6 +221,8 @@ def kv_append(q, k, v, k_cache, v_cache, pages, ctx_len, cos=None, sin=None, t_p
         r = _pack_rotary(_fits(cos, "cos", table, torch.float32, index), _fits(sin, "sin", table, torch.float32, index),
                          _maybe(positions, "positions", (B, T), torch.int32, index), 2 * table[1], table[0],
                          1 if interleaved else 0)
+    elif sin is not None:
+        raise ValueError("sin without cos: both are [max_positions, rot_dim / 2]")
     f = _maybe(flags, "flags", (B,), torch.int32, index)
     rc = lib.spec_kv_append(hq, hk, hv, ho, n, c, b, r, f, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != sv.SPEC_OK:
@@ -315,6 +317,8 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
         nb = bias_ids.shape[1]
         ids = _fits(bias_ids, "bias_ids", (B, nb), i32, index)
         bias_at = _fits(bias, "bias", (B, nb), f32, index)
+    elif bias is not None:
+        raise ValueError("bias needs the bias_ids [B, n] that it is for")
     row = (B,)
     r = _pack_rules(hist, _maybe(history_len, "history_len", row, i32, index),
                     _maybe(prompt_len, "prompt_len", row, i32, index),

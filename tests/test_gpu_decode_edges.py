@@ -253,3 +253,15 @@ def test_a_workspace_on_the_host_is_refused():
         call(ws.cuda())
     with pytest.raises(ValueError):
         sv.verify_host(p.cpu().numpy(), None, draft.cpu().numpy(), temperature=0.0, staging=ws)
+
+
+def test_halves_of_a_pair_are_refused():
+    """bias without its ids and sin without cos were left out of the result without a word."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    z = torch.zeros((2, 1, 64), device="cuda")
+    with pytest.raises(ValueError, match="bias"):
+        sv.process_logits(z, bias=torch.ones((2, 64), device="cuda"))
+    q, k, v, pages, ctx = attention_inputs(1, 40, 1)
+    x = torch.zeros((1, 3, 2, 128), dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="sin"):
+        sv.kv_append(q, x, x, k, v, pages, ctx, sin=torch.zeros((64, 32), device="cuda"))
