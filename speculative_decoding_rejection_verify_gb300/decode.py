@@ -322,7 +322,7 @@ def process_logits(logits, history=None, history_len=None, prompt_len=None, draf
     row = (B,)
     r = _pack_rules(hist, _maybe(history_len, "history_len", row, i32, index),
                     _maybe(prompt_len, "prompt_len", row, i32, index),
-                    _maybe(draft, "draft", (B, T - 1), i32, index), _maybe(t_per_row, "t_per_row", row, i32, index),
+                    _maybe(draft, "draft", (B, max(T - 1, 0)), i32, index), _maybe(t_per_row, "t_per_row", row, i32, index),
                     _maybe(repetition, "repetition", row, f32, index), _maybe(presence, "presence", row, f32, index),
                     _maybe(frequency, "frequency", row, f32, index), ids, bias_at,
                     _maybe(mask, "mask", (B, T, (V + 31) // 32), i32, index), stride, nb)

@@ -265,3 +265,9 @@ def test_halves_of_a_pair_are_refused():
     x = torch.zeros((1, 3, 2, 128), dtype=BF, device="cuda")
     with pytest.raises(ValueError, match="sin"):
         sv.kv_append(q, x, x, k, v, pages, ctx, sin=torch.zeros((64, 32), device="cuda"))
+
+
+def test_no_position_at_all_with_drafts():
+    import speculative_decoding_rejection_verify_gb300 as sv
+    z = torch.zeros((2, 0, 64), device="cuda")
+    assert sv.process_logits(z, draft=torch.zeros((2, 0), dtype=torch.int32, device="cuda")).shape == z.shape
