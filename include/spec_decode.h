@@ -28,7 +28,8 @@ extern "C" {
 #endif
 
 /* Flag bits that spec_kv_append ORs into out_flags (beside SPEC_FLAG_BAD_K for t_per_row). */
-#define SPEC_FLAG_BAD_SLOT 64      /* a new token's slot or page lies outside the table or the pool */
+#define SPEC_FLAG_BAD_SLOT 64      /* a new token's slot or page lies outside the table or the pool,
+                                      or ctx_len is negative                                        */
 #define SPEC_FLAG_BAD_POSITION 128 /* a position outside [0, max_positions): clamped into range     */
 
 /* Limits (SPEC_ERR_UNSUPPORTED beyond them). */

@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   // cos and sin of the unit: 8 pairs half-split, 4 pairs interleaved
   float co[8], si[8];
   if (P.rot > 0) {
-    int pos = P.positions ? __ldg(P.positions + (int64_t)b * P.batch.T + t) : ctx + t;
+    // (of the context as it is given, which the table may not hold)
+    int pos = P.positions ? __ldg(P.positions + (int64_t)b * P.batch.T + t) : (int)min((int64_t)max(held, 0) + t, (int64_t)INT32_MAX);
     if (pos < 0 || pos >= P.max_positions) {
       flag |= SPEC_FLAG_BAD_POSITION;
       pos = min(max(pos, 0), P.max_positions - 1);

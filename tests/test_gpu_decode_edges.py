@@ -271,3 +271,22 @@ def test_no_position_at_all_with_drafts():
     import speculative_decoding_rejection_verify_gb300 as sv
     z = torch.zeros((2, 0, 64), device="cuda")
     assert sv.process_logits(z, draft=torch.zeros((2, 0), dtype=torch.int32, device="cuda")).shape == z.shape
+
+
+def test_queries_turn_by_their_position_also_without_a_slot():
+    """A context longer than the page table: the entries have no slot (flagged), the queries still are at ctx_len + t."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    q, k, v, pages, _ = attention_inputs(2, 40, 1)
+    x = torch.zeros((2, 3, 2, 128), dtype=BF, device="cuda")
+    angle = torch.arange(400, device="cuda").double()[:, None] * 10000.0 ** (-torch.arange(64, device="cuda").double() / 64)
+    cos, sin = angle.cos().float(), angle.sin().float()
+    flags, ctx = i32([0, 0]), i32([300, 46])  # the table holds 48 slots
+    before = k.clone()
+    out = sv.kv_append(q, x, x, k, v, pages, ctx, cos, sin, flags=flags)
+    want = sv.kv_append(q, x, x, k.clone(), v.clone(), pages, i32([0, 0]), cos, sin, positions=i32([[300, 301, 302], [46, 47, 48]]))
+    assert torch.equal(out, want) and flags.tolist() == [64, 64]
+    changed = (k != before).flatten(1).any(1).nonzero().flatten().tolist()
+    assert changed == [int(pages[1, 2])]
+    flags.zero_()
+    sv.kv_append(q, x, x, k, v, pages, i32([2 ** 31 - 1, 0]), cos, sin, flags=flags)  # no position that large
+    assert flags.tolist() == [64 | 128, 0]
