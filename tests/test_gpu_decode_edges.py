@@ -94,9 +94,104 @@ def test_entries_are_the_quotients_codes():
         assert torch.equal(c[0, 3].float().cpu(), want)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [BF, R.F8])
+@pytest.mark.parametrize("D,rot,Hq,H", [(128, 128, 8, 2), (128, 48, 5, 1), (64, 64, 7, 7), (64, 32, 2, 1), (128, 0, 3, 3)])
+def test_append_of_thousands_of_tokens(D, rot, Hq, H, dtype, interleaved):
+    """From 16 tokens per SM on a token has 64 threads: 48 rotated elements leave some of them without a unit, and a token's
+    heads take several rounds."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    B, page, ctx, tb = 2, 32, [7, 100], [1700, 1733]
+    T = max(tb)
+    assert B * T >= 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator().manual_seed(D + rot)
+    max_pages = -(-(max(ctx) + T) // page)
+    k, v = R.pool(B * max_pages, page, H, D, dtype, "head", g)
+    pages = R.tables(B, max_pages, B * max_pages, g)
+    x = (torch.randn((B, T, Hq + 2 * H, D), generator=g) * 2).to(BF)
+    f = 10000.0 ** (-torch.arange(0, max(rot, 2), 2).double() / max(rot, 1))
+    a = torch.arange(max(ctx) + T).double()[:, None] * f
+    cos, sin = (a.cos().float(), a.sin().float()) if rot else (None, None)
+    scales = [torch.rand(H, generator=g) * 0.1 + 0.02 for _ in range(2)] if dtype == R.F8 else [None, None]
+    dev, kc, vc = x.cuda(), R.to_cuda(k), R.to_cuda(v)
+    out = sv.kv_append(dev[:, :, :Hq], dev[:, :, Hq:Hq + H], dev[:, :, Hq + H:], kc, vc, pages.cuda(), i32(ctx),
+                       None if cos is None else cos.cuda(), None if sin is None else sin.cuda(), i32(tb), interleaved=interleaved,
+                       k_scale=R.to_cuda(scales[0]), v_scale=R.to_cuda(scales[1])).cpu().double()
+    for b in range(B):
+        n = tb[b]
+        slot = ctx[b] + torch.arange(n)
+        y, err = x[b, :n].double(), torch.zeros((n, Hq + 2 * H, D), dtype=torch.float64)
+        if rot:
+            one, two = (slice(0, rot, 2), slice(1, rot, 2)) if interleaved else (slice(0, rot // 2), slice(rot // 2, rot))
+            c, s = cos[slot].double()[:, None], sin[slot].double()[:, None]
+            p, q = y[:, :Hq + H, one].clone(), y[:, :Hq + H, two].clone()
+            y[:, :Hq + H, one], y[:, :Hq + H, two] = p * c - q * s, q * c + p * s
+            err[:, :Hq + H, one] = err[:, :Hq + H, two] = 2.0 ** -22 * (p.abs() + q.abs())
+        assert ((out[b, :n] - y[:, :Hq]).abs() <= R.U_BF16 * y[:, :Hq].abs() + err[:, :Hq]).all() and (out[b, n:] == 0).all()
+        at = pages[b].long()[slot // page], slot % page
+        for got, scale, h0 in ((kc, scales[0], Hq), (vc, scales[1], Hq + H)):
+            raw = got.cpu()
+            entry = raw.view(torch.uint8)[at].view(R.F8).double() if dtype == R.F8 else raw[at].double()
+            want, e = y[:, h0:h0 + H], err[:, h0:h0 + H]
+            if dtype == R.F8:
+                want, e = (want / scale.double()[:, None]).clamp(-448, 448), e / scale.double()[:, None]
+                assert ((entry - want).abs() <= (want.abs() * R.U_E4M3 + e) * (1 + 2.0 ** -20) + 2.0 ** -10).all()
+            else:
+                assert ((entry - want).abs() <= R.U_BF16 * want.abs() + e).all()
+
+
+# ------------------------------------------------------------------------------------------------
+# kv_keep
+# ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF, R.F8])
+@pytest.mark.parametrize("layers", [1, 3])
+def test_keep_of_many_entries(layers, dtype):
+    """More kept entries than a warp's lanes (32) and than a round's moves (64), with moves that begin, end and stand
+    still on both sides of these."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(6)
+    most, page, H, D = 150, 16, 2, 64
+    paths = [[i + 1 for i in range(most)], [i if i < 31 else i + 2 for i in range(most)], [i if i < 64 else 2 * i - 63 for i in range(most)],
+             [2 * i for i in range(most)], [i if i % 3 == 0 and i < 60 else i + (1 if i < 61 else 7) for i in range(most)],
+             [i + 40 for i in range(most)]]
+    paths[4] = sorted(set(paths[4]))
+    paths[4] += [paths[4][-1] + 1 + i for i in range(most - len(paths[4]))]
+    keep = [150, 97, 150, 65, 128, 64]
+    for p in paths:
+        assert len(p) == most and all(b > a for a, b in zip(p, p[1:]))
+    ctx = [0, 5, 16, 31, 100, 2]
+    B = len(paths)
+    max_pages = -(-(max(ctx) + max(max(p) for p in paths) + 1) // page)
+    k, v = R.pool(B * max_pages, page, H, D, dtype, "slot", g, layers=layers)
+    pages = R.tables(B, max_pages, B * max_pages, g)
+    dev = [R.to_cuda(c) for c in (k, v)]
+    sv.kv_keep(*dev, pages.cuda(), i32(ctx), i32(paths), i32(keep))
+    for got, c in zip(dev, (k, v)):
+        s = c.view(torch.uint8) if dtype == R.F8 else c
+        w = s.clone()
+        for b in range(B):
+            for i in range(keep[b]):
+                to, fr = R.at(pages, b, ctx[b] + i, page), R.at(pages, b, ctx[b] + paths[b][i], page)
+                w[:, to[0], to[1]] = s[:, fr[0], fr[1]]
+        raw = got.cpu()
+        assert torch.equal(raw.view(torch.uint8) if dtype == R.F8 else raw, w)
+
+
 # ------------------------------------------------------------------------------------------------
 # process_logits
 # ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("B,V", [(610, 9001), (420, 9001), (420, 9008), (610, 9008)])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_longer_stretches_of_the_vocabulary(B, V, dtype):
+    """Batches that take 4096 and 8192 tokens a block, with rows on 16-byte boundaries and on any."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    want = 8192 if B == 610 else 4096
+    assert next(s for s in (8192, 4096, 2048) if B * -(-V // s) >= 8 * sms) == want
+    from test_gpu_logits import build, check
+    z, r = build(B, 2, V, V + B, bias=20)
+    check(z, r, dtype, in_place=V % 2 == 1)
+
+
 @pytest.mark.parametrize("V", [2048, 2051])
 def test_repeated_tokens_logits_are_quotients(V):
     """z / repetition is the quotient rounded to fp32, wherever the row begins."""
