@@ -131,8 +131,10 @@ size_t spec_paged_attention_workspace_bytes(int32_t B, int32_t T, int32_t q_head
  *   q, out [B, T, q_heads, head_dim] bf16.  Rows past T_b, and rows that attend to nothing, are 0.
  * Slots that a row does not attend to have no part in it, whatever they hold (NaN and infinities
  * among them).  A page outside the pool reads as zeros; slots past the page table are dropped.
- * Scores, weights and sums are fp32; the weights are rounded (bf16 for a bf16 cache, fp16 for E4M3)
- * where they multiply V.  With an E4M3 cache a query row that holds an infinity gives NaN.
+ * Scores, weights and sums are fp32; the weights are rounded where they multiply V (bf16 for a bf16 cache, whose
+ * row's sum is that of the rounded ones; fp16 for E4M3).  Over an E4M3 cache a query row enters the scores as two E4M3 numbers
+ * an element: exactly where the element reaches 2^-9 of the row's largest, within 2^-17 of that largest elsewhere; a row
+ * that holds an infinity gives NaN.
  * Each wait inside the kernel has a limit: should one run out, the rows that its block works on come
  * out as NaN, and the kernel ends.
  * The workspace (256-byte aligned) holds per-call scratch, needs no initialisation and must not be

@@ -45,6 +45,34 @@ def test_equal_values_come_back_as_they_are(Hq, dtype):
     assert (out == 1.875).all()
 
 
+@pytest.mark.parametrize("Hq,D", [(4, 128), (64, 64)])
+def test_a_query_with_one_large_element_over_e4m3(Hq, D):
+    """Queries enter an E4M3 cache's scores as two E4M3 numbers: exactly where an element reaches 2^-9 of its row's largest, and
+    to 2^-17 of that largest elsewhere.  Here the largest meets zeros, so the scores are all made of the others."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(9)
+    T, ctx, page, scale = 2, 250, 16, D ** -0.5
+    q = torch.randn((1, T, Hq, D), generator=g)
+    q[..., 0] = 700.0
+    q[:, 1] *= 1e-3
+    q = q.to(BF)
+    k, v = R.pool(16, page, 1, D, R.F8, "slot", g)
+    k.view(torch.uint8)[..., 0] = 0
+    pages = torch.arange(16, dtype=torch.int32)[None]
+    got = sv.paged_attention(q.cuda(), k.cuda(), v.cuda(), pages.cuda(), i32([ctx])).cpu().double()
+    want, bound = R.attention(q, k, v, pages, [ctx], [T], None, scale)
+    size, _ = R.attention(q, k, v.float().abs().to(R.F8), pages, [ctx], [T], None, scale)
+    # a score is off by 2^-17 of the row's largest times the sum of a key's elements, a normalised weight by twice that
+    off = 2.0 ** -17 * q.double().abs().amax(-1, keepdim=True) * k.double().abs().sum(-1).max() * scale
+    assert ((got - want).abs() <= bound + (torch.exp(2 * off) - 1) * size).all()
+    # elements within 2^-9 of the largest: no further error
+    q[..., 0] = 300.0
+    q[..., 1:] = (q[..., 1:].float().sign() * (0.6 + torch.rand(q[..., 1:].shape, generator=g) * 0.4)).to(BF)
+    got = sv.paged_attention(q.cuda(), k.cuda(), v.cuda(), pages.cuda(), i32([ctx])).cpu().double()
+    want, bound = R.attention(q, k, v, pages, [ctx], [T], None, scale)
+    assert ((got - want).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("T,Hq", [(1, 4), (4, 16), (17, 8), (16, 16), (64, 8)])
 @pytest.mark.parametrize("ctx,width", [(300, 0), (1500, 0), (300, 4000)])
 @pytest.mark.parametrize("dtype", [BF, R.F8])
