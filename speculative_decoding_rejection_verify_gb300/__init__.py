@@ -200,6 +200,7 @@ def workspace_bytes(B: int, K: int, V: int, dtype: int, top_k: int = 0) -> int:
 class _Scratch(threading.local):
     def __init__(self):
         self.buffers: Dict[Tuple[int, int], object] = {}
+        self.staging: Dict[int, object] = {}  # verify_host's, per device
 
 
 _scratch = _Scratch()
@@ -412,14 +413,22 @@ def verify_multi(p, q, draft, u_accept=None, u_resample=None, temperature: float
     return tokens, nacc, chain, flags
 
 
-_stage_cache: Dict[int, object] = {}
-
-
 def staging_bytes(B: int, K: int, V: int, dtype: int, top_k: int, ragged: bool) -> int:
     n = load().spec_verify_host_staging_bytes(B, K, V, dtype, top_k, int(ragged))
     if n == 0:
         raise SpecVerifyError(1, "spec_verify_host_staging_bytes")
     return n
+
+
+def _staging(nbytes: int, device):
+    """The calling thread's staging buffer of a device.  verify_host blocks its thread, not others."""
+    torch = _torch()
+    key = device.index if device.index is not None else torch.cuda.current_device()
+    staging = _scratch.staging.get(key)
+    if staging is None or staging.numel() < nbytes:
+        staging = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        _scratch.staging[key] = staging
+    return staging
 
 
 def verify_host(p, q, draft, k_per_row=None, u_accept=None, u_resample=None, temperature: float = 1.0,
@@ -462,11 +471,7 @@ def verify_host(p, q, draft, k_per_row=None, u_accept=None, u_resample=None, tem
         _launches_on(dev.index)
     nbytes = staging_bytes(B, K, V, dt, top_k, k_per_row is not None)
     if staging is None:
-        key = dev.index if dev.index is not None else torch.cuda.current_device()
-        staging = _stage_cache.get(key)
-        if staging is None or staging.numel() < nbytes:
-            staging = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-            _stage_cache[key] = staging
+        staging = _staging(nbytes, dev)
     else:
         _given_workspace(staging, torch.device("cuda", dev.index if dev.index is not None else torch.cuda.current_device()), "staging")
     if out is None:

@@ -111,3 +111,23 @@ def test_a_callers_workspace_is_checked():
         sv._given_workspace(good, torch.device("cuda", 0))
     with pytest.raises(ValueError, match="contiguous"):
         sv._given_workspace(good[::2], good.device)
+
+
+def test_two_threads_never_share_a_staging_buffer(host, monkeypatch):
+    """verify_host blocks its own thread only: another one's call may copy its inputs in meanwhile."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    got, both = {}, threading.Barrier(2)
+
+    def work(name):
+        first = sv._staging(1000, host)
+        both.wait(20)
+        got[name] = (first, sv._staging(500, host))
+        both.wait(20)
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in "ab"]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(20)
+    assert all(first is again for first, again in got.values())
+    assert got["a"][0].data_ptr() != got["b"][0].data_ptr()
