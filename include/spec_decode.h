@@ -36,7 +36,9 @@ extern "C" {
 #define SPEC_MAX_BATCH 65535        /* B, but for spec_kv_append (B * T < 2^31)                      */
 #define SPEC_MAX_NEW 64             /* T of spec_paged_attention (a tree mask has one bit per token)
                                        and of spec_process_logits                                    */
-#define SPEC_MAX_GROUP 128          /* q heads per kv head of spec_paged_attention                   */
+#define SPEC_MAX_GROUP 128          /* q heads per kv head of spec_paged_attention; its requests x kv
+                                       heads x row groups (of at most 128 rows) x (page table's slots /
+                                       128 + 4) stay under 2^31                                      */
 #define SPEC_MAX_PAGE 4096          /* page_size: a power of two in [8, SPEC_MAX_PAGE]               */
 #define SPEC_MAX_SLOTS (1 << 30)    /* max_pages * page_size of one request                          */
 #define SPEC_MAX_HISTORY 1048448    /* history entries of spec_process_logits                        */

@@ -22,9 +22,9 @@
 // an E4M3 cache four warps split Q and bring V to fp16.
 //
 // Measured (requests x tokens, kv heads x group, slots; time; of the copy bandwidth of 6772 GB/s):
-//   64 x 7, 8 x 4, 1000 to 16000, bf16   328 us  6.8 TB/s  1.00   bound by memory
-//   2 x 5, 4 x 8, 100003 to 131071, bf16  82 us  5.7 TB/s  0.85   memory, and 10 us to begin and join
-//   32 x 17 (a tree), 8 x 4, 500 to 9000, E4M3  118 us  2.7 TB/s  0.40   the softmax: 68 rows at 128 slots a step
+//   64 x 7, 8 x 4, 1000 to 16000, bf16   330 us  6.8 TB/s  1.00   bound by memory
+//   2 x 5, 4 x 8, 100003 to 131071, bf16  83 us  5.7 TB/s  0.84   memory, and 10 us to begin and join
+//   32 x 17 (a tree), 8 x 4, 500 to 9000, E4M3  120 us  2.7 TB/s  0.39   the softmax: 68 rows at 128 slots a step
 //   8 x 6, 8 x 4, 0 to 4001, bf16         21 us  3.1 TB/s  0.46   beginnings and ends of 64 items
 
 #include <cuda.h>
@@ -39,7 +39,8 @@ namespace sv {
 extern std::atomic<int32_t> g_test_hooks;  // spec_verify_set_test_hooks
 
 constexpr int kTileSlots = 128;       // slots per tile = rows of the matrix unit
-// Items of at most so many tiles are never cut, which saves the join (4 requests x 8 kv heads, 20 rows: 9.0 us against
+// Where the page table could hold no item of more tiles, none is cut, which saves the join (the host knows the table's
+// width, not the lengths, so short requests under a wide table are cut; 4 requests x 8 kv heads, 20 rows: 9.0 us against
 // 11.8 at 300 slots, 10.5 against 12.0 at 600, 12.5 against 12.6 at 1000; one request x 2 heads: 7.2 / 8.6, 8.5 / 8.5, 10.3 / 9.1).
 constexpr int kWholeTiles = 6;
 constexpr int kMaxParts = 160;        // CTAs of the stream at most (one per SM), for the workspace's size

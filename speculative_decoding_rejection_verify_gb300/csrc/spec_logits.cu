@@ -199,7 +199,9 @@ __global__ void __launch_bounds__(kRuleThreads, 5) rules_kernel(const __grid_con
       for (int r = 0; r < kRowsAhead; ++r) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) raw[r].w[i] = 0;
-        // a run that the mask forbids throughout is not read
+        // a run that the mask forbids throughout is not read: the load then waits for the mask, but a mask that allows
+        // tokens in 1 of its words in 100 leaves most memory sectors unread (64 x 7 x 128256 in bf16, such masks: 46.8 us
+        // against 51.1; 1 token in 16 for half of the requests, 15 for the others: 53.9 against 51.8)
         if (allowed[r] && t0 + r < rows) raw[r].load(in + (t0 + r) * row_bytes + v * ES);
       }
 #pragma unroll
