@@ -19,7 +19,7 @@ own = False
 F8 = torch.float8_e4m3fn
 F8_MAX = 448.0
 ROPE_BASE = 10000.0
-LEAST, MOST = -32, 32  # a page's scale is a power of two in 2^LEAST .. 2^MOST
+LEAST, MOST = -24, 24  # a page's scale is a power of two in 2^LEAST .. 2^MOST
 
 
 # ------------------------------------------------------------------------------------------------
