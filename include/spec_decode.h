@@ -9,6 +9,11 @@
  *   on the logits    spec_process_logits  penalties for repeated tokens, biases and grammar masks at
  *                                         every drafted position (then spec_verify / spec_verify_multi);
  *   after verifying  spec_kv_keep         moves the accepted branch's cache entries up behind the context.
+ * Where the cache is to stay small, an E4M3 one may have a scale per page and head that follows what goes into it
+ * (spec_kv_page_scales_t: the _ex forms below), and entries that attention does not look at may go:
+ *   after attention  spec_kv_weigh        adds up the weight that the new tokens give every entry;
+ *   now and then     spec_kv_select       picks the entries of each head that stay within a budget;
+ *                    spec_kv_move         brings them together at the front.
  *
  * Conventions are those of spec_verify.h: caller-owned device memory, no allocation, no
  * synchronisation, work enqueued on `stream`, host-checkable errors as status codes.  Problems in
@@ -76,6 +81,33 @@ typedef struct {
 } spec_kv_cache_t;
 
 /*
+ * A scale per page and head of an E4M3 cache: an entry of layer l, page p and head h stands for its code times
+ * k[l * layer_stride + p * heads + h] (v likewise).  A scale counts where it lies in [2^-24, 2^24]; spec_kv_append_ex,
+ * spec_kv_keep_ex and spec_kv_move set it:
+ *   need(a) = the smallest power of two s in that range with a <= 448 s, a the largest finite magnitude that goes in.
+ * An E4M3 code has 4 significant bits whatever its scale, so a power of two loses none of them, and where a page's scale
+ * grows the codes that stay are codes again, exactly but for those that become subnormal.  Pages of two requests that
+ * share them must not be written to.
+ */
+typedef struct {
+  float* k;
+  float* v;
+  int64_t layer_stride;
+} spec_kv_page_scales_t;
+
+/*
+ * What is known about every entry of a cache: the attention weight that it has gathered and the position of its token,
+ * element (l, page, h, row) at [l * layer_stride + (page * heads + h) * page_size + row].  Either may be NULL where an
+ * operator says so.  The sizes are the cache's.
+ */
+typedef struct {
+  float* weight;
+  int32_t* position;
+  int64_t layer_stride;
+  int32_t layers, num_pages, page_size, heads;
+} spec_kv_record_t;
+
+/*
  * The batch of a step.
  *   pages      [B, max_pages] int32: the page of every page_size slots of a request.  Entries past
  *              those that hold its slots are not read;
@@ -120,6 +152,17 @@ spec_status_t spec_kv_append(const spec_heads_t* q, const spec_heads_t* k, const
                              const spec_decode_batch_t* batch, const spec_rotary_t* rotary,
                              int32_t* out_flags, void* stream);
 
+/*
+ * spec_kv_append into an E4M3 cache with page scales (layer 0 of `scales`; cache->k_scale and v_scale are NULL).  A page's
+ * new scale is need(the new tokens' keys in it, rotated in 32 bits), values likewise; where the page also holds tokens from before
+ * (slots < ctx_len[b]) and has a scale that counts, it is not less than that one, and if it is more, those tokens' codes
+ * become round(code * old / new).  The new codes are round(x / scale), infinities cut to +-448.  scales == NULL is spec_kv_append.
+ */
+spec_status_t spec_kv_append_ex(const spec_heads_t* q, const spec_heads_t* k, const spec_heads_t* v,
+                                const spec_heads_t* q_out, int32_t q_heads, const spec_kv_cache_t* cache,
+                                const spec_kv_page_scales_t* scales, const spec_decode_batch_t* batch,
+                                const spec_rotary_t* rotary, int32_t* out_flags, void* stream);
+
 /* Bytes of device workspace spec_paged_attention needs for these sizes (0 for invalid ones). */
 size_t spec_paged_attention_workspace_bytes(int32_t B, int32_t T, int32_t q_heads, int32_t heads,
                                             int32_t head_dim);
@@ -148,6 +191,18 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
                                    size_t workspace_bytes, void* stream);
 
 /*
+ * spec_paged_attention with two things more, each of which may be NULL:
+ *   scales   page scales of an E4M3 cache (layer 0; cache->k_scale and v_scale are NULL).  A row that attends to a slot
+ *            whose page's scale does not count comes out as NaN.  A page outside the pool has scale 1;
+ *   lse      [B, T, q_heads] float: log sum_s exp(scale * q . K_s) of every row, -inf for rows past T_b and rows that
+ *            attend to nothing.  Over a bf16 cache the sum is that of the rounded weights: within 2^-8 of the logarithm.
+ */
+spec_status_t spec_paged_attention_ex(const spec_heads_t* q, const spec_heads_t* out, int32_t q_heads,
+                                      const spec_kv_cache_t* cache, const spec_kv_page_scales_t* scales,
+                                      const spec_decode_batch_t* batch, const int64_t* mask, float scale, float* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Move the accepted branch of a verified tree up behind the context, in every layer, K and V:
  *   slot ctx_len[b] + i  <-  slot ctx_len[b] + path[b, i]   for i < n_keep[b].
  *   path [B, max_keep] int32: the kept new tokens' indices, strictly increasing from >= 0;
@@ -157,6 +212,59 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
  */
 spec_status_t spec_kv_keep(const spec_kv_cache_t* cache, const spec_decode_batch_t* batch,
                            const int32_t* path, const int32_t* n_keep, int32_t max_keep, void* stream);
+
+/*
+ * spec_kv_keep with two things more, each of which may be NULL:
+ *   scales   page scales of an E4M3 cache.  A page that entries move into takes the scale max(its own, need(their
+ *            values)); where it grows, the codes of its other slots < ctx_len[b] + n_keep[b] become round(code * old / new)
+ *            (what lies behind them is left as it is).  max_keep <= SPEC_MAX_NEW;
+ *   record   weights and positions that move with the entries.
+ */
+spec_status_t spec_kv_keep_ex(const spec_kv_cache_t* cache, const spec_kv_page_scales_t* scales,
+                              const spec_kv_record_t* record, const spec_decode_batch_t* batch, const int32_t* path,
+                              const int32_t* n_keep, int32_t max_keep, void* stream);
+
+/*
+ * Add up the attention weight that the new tokens of a step give every entry of layer 0 of the cache:
+ *   weight[s, h] = (s < ctx_len[b] ? weight[s, h] : 0) + sum over the rows (t, i), i a q head of h's group, that attend to s
+ *                  of exp(scale * q[b, t, i] . K_s - lse[b, t, i])
+ * for the context's slots and the T_b new tokens', whose positions are recorded too (record->position may be NULL).  Who
+ * attends to what, q, cache (v is not used), scales, batch and mask are as for spec_paged_attention_ex, and lse is what it
+ * gave; a row whose lse is +inf or -inf has no part (a caller may set it, for rows of rejected drafts).
+ * positions [B, T] int32 or NULL: ctx_len[b] + t.  Slots whose page lies outside the table or the pool are left out.
+ * Two requests must not share a page.  Scores, weights and sums are fp32.
+ */
+spec_status_t spec_kv_weigh(const spec_heads_t* q, int32_t q_heads, const spec_kv_cache_t* cache,
+                            const spec_kv_page_scales_t* scales, const spec_decode_batch_t* batch, const int64_t* mask,
+                            float scale, const float* lse, const spec_kv_record_t* record, const int32_t* positions,
+                            void* stream);
+
+/*
+ * Pick, for every layer, request and head, the m = min(ctx_len[b], budget[b]) entries of its context that stay:
+ * those of the largest weight, where the lowest slot wins a tie.  Entries at a position < first, or, where recent > 0, at one
+ * >= seen[b] - recent, count as of infinite weight, NaN as of -infinity, and those in pages outside the pool too.
+ *   target [layers, B, heads, max_moves] int32: the slots < m that do not stay, in ascending order;
+ *   source, likewise: the slots >= m that do, in ascending order.  There are as many of each: moves [layers, B, heads],
+ *   at most half of the page table's slots, and max_moves is that half at least.  Elements past them are not written;
+ *   new_len [B]: m;  budget [B] int32 (a negative one counts as 0);  seen [B] int32: tokens so far, NULL: ctx_len.
+ *   record->position may be NULL where first and recent are 0.  batch->T and t_per_row are not used.
+ */
+spec_status_t spec_kv_select(const spec_kv_record_t* record, const spec_decode_batch_t* batch, const int32_t* budget,
+                             const int32_t* seen, int32_t first, int32_t recent, int32_t* source, int32_t* target,
+                             int32_t max_moves, int32_t* moves, int32_t* new_len, void* stream);
+
+/*
+ * Move entries of every layer and head within their request, keys, values and what `record` holds:
+ *   slot target[l, b, h, i]  <-  slot source[l, b, h, i]   for i < moves[l, b, h] (clamped into [0, max_moves]).
+ * The lists are spec_kv_select's, or others in ascending order with every target < batch->ctx_len[b] <= every source: ctx_len is
+ * the context that the moves leave (new_len).  scales (or NULL): as for spec_kv_keep_ex; the codes that a growing scale
+ * changes are those of the page's other slots < ctx_len[b].  Entries keep their positions' rotation, so the next tokens need their
+ * positions given.  Moves whose slots or pages lie outside the table or the pool, or on the wrong side of ctx_len[b], are left out.
+ * record may be NULL.  batch->T and t_per_row are not used.  Two requests must not share a page.
+ */
+spec_status_t spec_kv_move(const spec_kv_cache_t* cache, const spec_kv_page_scales_t* scales,
+                           const spec_kv_record_t* record, const spec_decode_batch_t* batch, const int32_t* source,
+                           const int32_t* target, const int32_t* moves, int32_t max_moves, void* stream);
 
 /*
  * What shapes a batch's logits; every pointer is device memory and NULL leaves its part out.

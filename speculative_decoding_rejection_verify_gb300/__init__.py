@@ -16,7 +16,8 @@ The C ABI is declared in ``include/spec_verify.h``; the names here mirror it:
 * ``workspace_bytes(B, K, V, dtype, top_k)``;
 * ``kv_append``, ``paged_attention``, ``kv_keep``, ``process_logits``: the operators of a decode step around
   the verify step (``decode.py``, ``include/spec_decode.h``, ``csrc/spec_kv.cu``, ``csrc/spec_attention.cu``,
-  ``csrc/spec_logits.cu``);
+  ``csrc/spec_pages.cu``, ``csrc/spec_logits.cu``), and ``kv_weigh``, ``kv_select``, ``kv_move``, which keep its cache
+  within a budget (``csrc/spec_evict.cu``, ``csrc/spec_pages.cu``);
 * ``Controller(...)``: the host-side draft-length controller of ``include/spec_control.h``
   (2kiu.com/news/5895634 §4.4 and §7), fed with each batch's ``num_accepted``.
 
@@ -556,5 +557,5 @@ def _host_i32(a) -> np.ndarray:
 
 
 from . import decode  # noqa: E402  (its functions use what is defined above)
-from .decode import (DECODE_EXPORTS, DTYPE_E4M3, FLAG_BAD_POSITION, FLAG_BAD_SLOT, kv_append, kv_keep,  # noqa: E402,F401
-                     paged_attention, process_logits)
+from .decode import (DECODE_EXPORTS, DTYPE_E4M3, FLAG_BAD_POSITION, FLAG_BAD_SLOT, kv_append, kv_keep, kv_move,  # noqa: E402,F401
+                     kv_select, kv_weigh, paged_attention, process_logits)

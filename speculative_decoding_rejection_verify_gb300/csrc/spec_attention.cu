@@ -48,12 +48,18 @@ constexpr int kMaxRows = 128;         // query rows of one item
 constexpr float kRescale = 8.0f;      // rescale when a score passes the maximum in use by 2^8
 constexpr float kNone = 3e38f;        // shift of a row without a maximum yet: any score asks for one
 constexpr int kConvertWarps = 4;      // E4M3 caches: E4M3 -> fp16
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// fp16 weights are lifted to a largest of 2^7 (2^15 before a rescale), so they reach down to 2^-31 of it
+constexpr float kLift16 = 7.0f;
+
+// What the cache holds: E4M3 with a scale per head, or per page and head.
+enum { kBf16 = 0, kE4m3 = 1, kE4m3Pages = 2 };
 
 struct AttnParams {
   CUtensorMap q_map, k_map, v_map;
   Heads out;
   Cache cache;                 // for the rare reads of single entries, and the scales
+  PageScales scales;
   Batch batch;
   const int64_t* mask;
   int heads, group;
@@ -63,6 +69,7 @@ struct AttnParams {
   int whole;                   // items are not cut: the CTA that one begins in takes all of it
   int wait_tries;              // the limit of every wait
   float scale_log2;            // scale * log2(e)
+  float* lse;                  // [B, T, q heads] or null
   float* part;                 // [CTA][2][rows][D] unnormalised O
   float2* part_ml;             // [CTA][2][rows] (m in log2 units, l)
   int4* cut;                   // [CTA] (b, head * row_groups + row group, item's end, total) on the line of an
@@ -260,6 +267,22 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return r;
+}
+
+// A row's log of its sum of exponentials: `sum` is of weights 2^(score - top + lift), scores in log2 units.
+__device__ __forceinline__ float row_lse(float top, float lift, float sum) {
+  return sum == 0.0f ? -INFINITY : (top - lift + log2f(sum)) * kLn2;
+}
+__device__ __forceinline__ int64_t lse_place(int b, int T, int t, int heads, int head, int group, int g) {
+  return (((int64_t)b * T + t) * heads + head) * group + g;
+}
+
 // Shared-memory matrix descriptors: 128-byte swizzle (or 64-byte: E4M3 rows of 64), strides in bytes.  Along
 // a swizzled row lies the reduction (Q and K) or the free dimension (V^T and P^T, "transposed" in the
 // instruction).
@@ -407,20 +430,6 @@ struct Shape {
   static_assert(kBytes <= 232448, "shared memory");
 };
 
-// Four E4M3 codes as fp16 pairs, exactly.
-__device__ __forceinline__ void e4m3_to_half(uint32_t x, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(x));
-}
-__device__ __forceinline__ float4 unpack_e4m3(uint32_t x) {
-  uint32_t lo, hi;
-  e4m3_to_half(x, lo, hi);
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
-
 // Over the 32 lanes, `op` of every one of N values: lane l ends with that of value l % N.
 template <int N, typename Op>
 __device__ __forceinline__ float fold_lanes(float (&x)[N], int lane, Op op) {
@@ -442,8 +451,9 @@ __device__ __forceinline__ float fold_lanes(float (&x)[N], int lane, Op op) {
 // ------------------------------------------------------------------------------------------------
 // the stream over the cache
 // ------------------------------------------------------------------------------------------------
-template <int D, bool F8, int NT>
-__global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams P) {
+template <int D, int KIND, int NT>
+__global__ void __launch_bounds__(Shape<D, KIND != kBf16, NT>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams P) {
+  constexpr bool F8 = KIND != kBf16, PAGES = KIND == kE4m3Pages;
   using S = Shape<D, F8, NT>;
   extern __shared__ char raw_smem[];
   char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
@@ -708,7 +718,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
         // which are off by 2^-17 of it at most (q's own rounding to bf16 is 2^-8 of each element).  The
         // scale goes into the row's factor.  The split overwrites the row: no other row's lines.
         constexpr int kLanes = D / 16;  // threads per row, 16 elements each
-        const float c = P.scale_log2 * (P.cache.k_scale ? __ldg(P.cache.k_scale + s.head) : 1.0f);
+        const float c = P.scale_log2 * (!PAGES && P.cache.k_scale ? __ldg(P.cache.k_scale + s.head) : 1.0f);
         char* q = q_buf + qb * S::kQ;
         const int i = tid % kLanes;
 #pragma unroll 1
@@ -819,8 +829,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
     }
     // this lane's column and its token, for the ballots
     const int rule_row = lane < S::kOwn ? row_of(lane) : kMaxRows, rule_token = rule_row / P.group;
-    // fp16 weights are lifted to a largest of 2^7 (2^15 before a rescale), so they reach down to 2^-31 of it
-    constexpr float kLift = F8 ? 7.0f : 0.0f;
+    constexpr float kLift = F8 ? kLift16 : 0.0f;
     float l[S::kChunks][CK];
     uint32_t it = 0;
     int v_slot = 1;
@@ -833,7 +842,7 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
       const int rows = min(max((s.tokens - t0) * P.group, 0), P.rows);  // valid ones come first
       const float c = P.scale_log2;
       const float* mult = st->mult[seg & 1];
-      const float v_scale = F8 && P.cache.v_scale ? __ldg(P.cache.v_scale + s.head) : 1.0f;
+      const float v_scale = F8 && !PAGES && P.cache.v_scale ? __ldg(P.cache.v_scale + s.head) : 1.0f;
       group_sync(bar);  // the last segment's row states are read
       if (wtid < S::kOwn) {
         st->top[my_row] = -INFINITY;
@@ -856,9 +865,38 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
 #pragma unroll
         for (int i = 0; i < CK; ++i) l[j][i] = 0.0f;
 
+      // Page scales: a key's is a factor of its scores.  A value's goes into the weight, as an addend of the exponent, so
+      // that the largest product of weight and scale is what a row's maximum follows and fp16 reaches down from; the sum of the weights
+      // themselves takes it out again.  Read a tile ahead, the page two.
+      int ahead_page = P.cache.num_pages;
+      float ahead_k = 1.0f, ahead_v = 1.0f;
+      const auto page_of = [&](int tile) {
+        const int at = tile * kTileSlots + key;
+        if (at >= s.end) return P.cache.num_pages;
+        const int p = __ldg(P.batch.pages + (int64_t)s.b * P.batch.max_pages + (at >> P.cache.page_shift));
+        return p < 0 ? P.cache.num_pages : p;
+      };
+      const auto scales_of_page = [&](int p) {  // of a page outside the pool, which reads as zeros, 1
+        const bool in = p < P.cache.num_pages;
+        const int64_t at = (int64_t)p * P.heads + s.head;
+        ahead_k = in ? P.scales.k[at] : 1.0f, ahead_v = in ? P.scales.v[at] : 1.0f;
+      };
+      if constexpr (PAGES) {
+        scales_of_page(page_of(s.tile0));
+        if (s.tile0 + 1 < s.tile1) ahead_page = page_of(s.tile0 + 1);
+      }
+
       for (int tile = s.tile0; tile < s.tile1; ++tile, ++it) {
         const int sb = it & 1;
         const uint32_t s_col = lanes + sb * NT;
+        // (one that does not count makes the slot's scores NaN)
+        const float k_factor = scale_counts(ahead_k) ? ahead_k : NAN;
+        const bool v_counts = scale_counts(ahead_v);
+        const float v_log2 = v_counts ? log2f(ahead_v) : NAN, v_inverse = v_counts ? 1.0f / ahead_v : 1.0f;
+        if constexpr (PAGES) {
+          scales_of_page(ahead_page);
+          ahead_page = tile + 2 < s.tile1 ? page_of(tile + 2) : P.cache.num_pages;
+        }
         mbar_wait(smem_addr(&st->s_full[sb]), (it >> 1) & 1, dead);
         __syncwarp();
         tc_fence_after();
@@ -877,8 +915,13 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
             for (int i = 0; i < CK; i += 4) {
               const float4 m = *reinterpret_cast<const float4*>(&st->shift[col(j) + i]);
               const float4 f = F8 ? *reinterpret_cast<const float4*>(&mult[col(j) + i]) : make_float4(c, c, c, c);
-              const float2 a = fma2(make_float2(z[i], z[i + 1]), make_float2(f.x, f.y), make_float2(m.x, m.y));
-              const float2 b = fma2(make_float2(z[i + 2], z[i + 3]), make_float2(f.z, f.w), make_float2(m.z, m.w));
+              float2 z0 = make_float2(z[i], z[i + 1]), z1 = make_float2(z[i + 2], z[i + 3]), m0 = make_float2(m.x, m.y), m1 = make_float2(m.z, m.w);
+              if constexpr (PAGES) {
+                z0 = mul2(z0, make_float2(k_factor, k_factor)), z1 = mul2(z1, make_float2(k_factor, k_factor));
+                m0 = add2(m0, make_float2(v_log2, v_log2)), m1 = add2(m1, make_float2(v_log2, v_log2));
+              }
+              const float2 a = fma2(z0, make_float2(f.x, f.y), m0);
+              const float2 b = fma2(z1, make_float2(f.z, f.w), m1);
               z[i] = a.x, z[i + 1] = a.y, z[i + 2] = b.x, z[i + 3] = b.y;
             }
           };
@@ -916,7 +959,8 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
               }
               // bf16 weights are summed as they were rounded, so that a row's normalised ones sum to 1: where one slot has
               // nearly all the weight, its rounding (2^-8 of it) leaves no error.  fp16's is below the output's rounding.
-              const float2 sum = add2(make_float2(l[j][i], l[j][i + 1]), w);
+              const float2 old = make_float2(l[j][i], l[j][i + 1]);
+              const float2 sum = PAGES ? fma2(w, make_float2(v_inverse, v_inverse), old) : add2(old, w);
               l[j][i] = sum.x, l[j][i + 1] = sum.y;
             }
           };
@@ -945,18 +989,21 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
             for (int j = 0; j < S::kChunks; ++j)
               if (col(j) < rows) {
                 float x[CK];
-                if (S::kHold && tile > s.tile0) {  // take the weights back; those over 2^100 leave nothing of what was there before
+                if (S::kHold && tile > s.tile0) {  // take the weights back; those over 2^100 (2^90) leave nothing of what was there before
                   scores(j, x);
 #pragma unroll
                   for (int i = 0; i < CK; ++i) {
                     float w = sees(j, i) ? exp2_approx(x[i]) : 0.0f;
                     if constexpr (!F8) w = __bfloat162float(__float2bfloat16(w));  // as it was added
-                    l[j][i] = w < 0x1p100f ? l[j][i] - w : 0.0f;
+                    l[j][i] = w < (PAGES ? 0x1p90f : 0x1p100f) ? (PAGES ? fmaf(-w, v_inverse, l[j][i]) : l[j][i] - w) : 0.0f;
                   }
                 }
                 tm_load<CK>(s_col + col(j), x);
 #pragma unroll
-                for (int i = 0; i < CK; ++i) x[i] = sees(j, i) ? x[i] * (F8 ? mult[col(j) + i] : c) : -INFINITY;
+                for (int i = 0; i < CK; ++i) {
+                  const float z = PAGES ? fmaf(x[i] * k_factor, mult[col(j) + i], v_log2) : x[i] * (F8 ? mult[col(j) + i] : c);
+                  x[i] = sees(j, i) ? z : -INFINITY;
+                }
                 const float m = fold_lanes<CK>(x, lane, [](float a, float b) { return fmaxf(a, b); });
                 if (lane < CK) st->red[quad][col(j) + lane] = m;
               }
@@ -1066,12 +1113,14 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
       const bool whole = s.tile0 == 0 && s.tile1 == s.tiles;
       // parts: slot 0 for an item that an earlier CTA began, slot 1 for one that a later one ends
       const int64_t part_row = ((int64_t)blockIdx.x * 2 + (s.tile0 == 0)) * P.rows;
+      float lse = -INFINITY;
       if (wtid < S::kOwn) {
         float f = 0.0f;
         if (my_row < rows) {
           const float sum = st->red[0][my_row] + st->red[1][my_row] + st->red[2][my_row] + st->red[3][my_row];
           f = sum == 0.0f ? 0.0f : v_scale / sum;
           if (!whole) P.part_ml[part_row + my_row] = make_float2(st->top[my_row], sum);
+          else if (P.lse) lse = row_lse(st->top[my_row], kLift, sum);
         }
         st->factor[my_row] = f;
       }
@@ -1084,6 +1133,8 @@ __global__ void __launch_bounds__(Shape<D, F8, NT>::kThreads, 1) attn_kernel(con
       char* out = P.out.data + s.b * P.out.row + (int64_t)t0 * P.out.token + (int64_t)s.head * P.group * P.out.head + key * 2;
       float* part = P.part + part_row * D + key;
       const int rows_all = min(P.rows, (P.batch.T - t0) * P.group);
+      if (P.lse && whole && wtid < S::kOwn && my_row < rows_all)
+        P.lse[lse_place(s.b, P.batch.T, t0 + my_row / P.group, P.heads, s.head, P.group, my_row % P.group)] = lost ? NAN : lse;
 #pragma unroll
       for (int j = 0; j < S::kChunks; ++j) {
         const int n0 = col(j);
@@ -1183,7 +1234,9 @@ struct JoinParams {
   const float* part;
   const float2* part_ml;
   const int4* cut;
-  int group, tokens, row_groups, rows, ctas;
+  float* lse;
+  float lift;
+  int heads, group, tokens, row_groups, rows, ctas;
 };
 
 // Block (x, y): the item that begins in CTA x and ends in a later one, rows 8 y .. 8 y + 7, a warp each.
@@ -1204,14 +1257,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
                                                         (int64_t)(head * P.group + n % P.group) * P.out.head);
   constexpr int E = D / 32;
   float o[E] = {};
-  float sum = 0.0f;
+  float sum = 0.0f, top = -INFINITY;
   if (t < batch_tokens(P.batch, b)) {
     // the last CTA of the item: the one whose part of the line holds tile end - 1
     int c1 = (int)(((int64_t)end * ctas - 1) / total);
     while (c1 + 1 < ctas && line_cut(total, c1 + 1, ctas) < end) ++c1;
     while (line_cut(total, c1, ctas) >= end) --c1;
     const auto row_of = [&](int c) { return ((int64_t)c * 2 + (c == c0)) * P.rows + n; };
-    float top = -INFINITY;
     for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, P.part_ml[row_of(c)].x);
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
@@ -1244,6 +1296,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
       }
     }
   }
+  if (P.lse && lane == 0) P.lse[lse_place(b, P.batch.T, t, P.heads, head, P.group, n % P.group)] = row_lse(top, P.lift, sum);
   const float v = P.v_scale ? __ldg(P.v_scale + head) : 1.0f;
   const float inv = sum == 0.0f ? 0.0f : v / sum;
 #pragma unroll
@@ -1305,10 +1358,11 @@ static bool encode(CUtensorMap* map, CUtensorMapDataType type, int es, void* dat
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool F8, int NT>
+template <int D, int KIND, int NT>
 static cudaError_t launch_attention(const AttnParams& P, int dev, int ctas, cudaStream_t st) {
+  constexpr bool F8 = KIND != kBf16;
   using S = Shape<D, F8, NT>;
-  auto kern = attn_kernel<D, F8, NT>;
+  auto kern = attn_kernel<D, KIND, NT>;
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory is set
   cudaError_t e = cudaSuccess;
   if (!((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
@@ -1324,19 +1378,19 @@ static cudaError_t launch_attention(const AttnParams& P, int dev, int ctas, cuda
   }
   e = launch_early(kern, dim3(ctas), dim3(S::kThreads), S::kBytes, st, P);
   if (e != cudaSuccess || ctas == 1 || P.whole) return e;
-  const JoinParams J = {P.out, P.batch, F8 ? P.cache.v_scale : nullptr, P.part, P.part_ml, P.cut, P.group, P.tokens,
-                        P.row_groups, P.rows, ctas};
+  const JoinParams J = {P.out, P.batch, F8 ? P.cache.v_scale : nullptr, P.part, P.part_ml, P.cut, P.lse, F8 ? kLift16 : 0.0f,
+                        P.heads, P.group, P.tokens, P.row_groups, P.rows, ctas};
   return launch_early(join_kernel<D>, dim3(ctas, (P.rows + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0, st, J);
 }
 
-template <int D, bool F8>
+template <int D, int KIND>
 static cudaError_t launch_rows(const AttnParams& P, int dev, int ctas, cudaStream_t st) {
-  if (P.rows <= 16) return launch_attention<D, F8, 16>(P, dev, ctas, st);
-  if (P.rows <= 32) return launch_attention<D, F8, 32>(P, dev, ctas, st);
-  if (P.rows <= 64) return launch_attention<D, F8, 64>(P, dev, ctas, st);
+  if (P.rows <= 16) return launch_attention<D, KIND, 16>(P, dev, ctas, st);
+  if (P.rows <= 32) return launch_attention<D, KIND, 32>(P, dev, ctas, st);
+  if (P.rows <= 64) return launch_attention<D, KIND, 64>(P, dev, ctas, st);
   // a width of its own: 128 columns' sums spill where 96 do not (68 rows, E4M3: 118 us against 139; bf16: 114, 118)
-  if (P.rows <= 96) return launch_attention<D, F8, 96>(P, dev, ctas, st);
-  return launch_attention<D, F8, 128>(P, dev, ctas, st);
+  if (P.rows <= 96) return launch_attention<D, KIND, 96>(P, dev, ctas, st);
+  return launch_attention<D, KIND, 128>(P, dev, ctas, st);
 }
 
 }  // namespace sv
@@ -1355,11 +1409,12 @@ size_t spec_paged_attention_workspace_bytes(int32_t B, int32_t T, int32_t q_head
   return attn_layout(tokens * (q_heads / heads), head_dim).bytes;
 }
 
-spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* out, int32_t q_heads,
-                                   const spec_kv_cache_t* cache, const spec_decode_batch_t* batch,
-                                   const int64_t* mask, float scale, void* workspace, size_t workspace_bytes,
-                                   void* stream) {
+spec_status_t spec_paged_attention_ex(const spec_heads_t* q, const spec_heads_t* out, int32_t q_heads,
+                                      const spec_kv_cache_t* cache, const spec_kv_page_scales_t* scales,
+                                      const spec_decode_batch_t* batch, const int64_t* mask, float scale, float* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
   spec_status_t s = check_cache(cache, true);
+  if (s == SPEC_OK) s = check_scales(scales, cache);
   if (s == SPEC_OK) s = check_batch(batch, cache);
   if (s != SPEC_OK) return s;
   if (q_heads < 1 || q_heads % cache->heads || !isfinite(scale)) return SPEC_ERR_INVALID_ARG;
@@ -1373,8 +1428,10 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
   AttnParams P = {};
   P.out = heads_of(out);
   P.cache = cache_of(cache);
+  P.scales = scales_of(scales);
   P.batch = batch_of(batch, cache);
   P.mask = mask;
+  P.lse = lse;
   P.heads = cache->heads, P.group = group;
   row_groups(batch->T, group, &P.tokens, &P.row_groups);
   P.rows = group * P.tokens;
@@ -1413,9 +1470,19 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
   int ctas = sms < kMaxParts ? sms : kMaxParts;
   if (most < ctas) ctas = (int)most;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  e = D == 128 ? (f8 ? launch_rows<128, true>(P, dev, ctas, st) : launch_rows<128, false>(P, dev, ctas, st))
-               : (f8 ? launch_rows<64, true>(P, dev, ctas, st) : launch_rows<64, false>(P, dev, ctas, st));
+  const int kind = scales ? kE4m3Pages : f8 ? kE4m3 : kBf16;
+  e = D == 128 ? (kind == kBf16 ? launch_rows<128, kBf16>(P, dev, ctas, st)
+                  : kind == kE4m3 ? launch_rows<128, kE4m3>(P, dev, ctas, st) : launch_rows<128, kE4m3Pages>(P, dev, ctas, st))
+               : (kind == kBf16 ? launch_rows<64, kBf16>(P, dev, ctas, st)
+                  : kind == kE4m3 ? launch_rows<64, kE4m3>(P, dev, ctas, st) : launch_rows<64, kE4m3Pages>(P, dev, ctas, st));
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* out, int32_t q_heads,
+                                   const spec_kv_cache_t* cache, const spec_decode_batch_t* batch,
+                                   const int64_t* mask, float scale, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  return spec_paged_attention_ex(q, out, q_heads, cache, nullptr, batch, mask, scale, nullptr, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -26,23 +26,6 @@ struct AppendParams {
   int rot, max_positions;  // rot = rot_dim
 };
 
-// Where new token t of a request goes in the cache: its byte offset within a head, or -1.
-__device__ __forceinline__ int64_t slot_offset(const Batch& b, const Cache& c, int row, int slot) {
-  if (slot < 0 || slot >= b.slots) return -1;
-  const int page = __ldg(b.pages + (int64_t)row * b.max_pages + (slot >> c.page_shift));
-  if (page < 0 || page >= c.num_pages) return -1;
-  return page * c.page + (slot & ((1 << c.page_shift) - 1)) * c.slot;
-}
-
-// x / s for E4M3's rounding: the product with the reciprocal is up to 1.5 units in the last place off, which puts a
-// quotient that lies halfway between two codes on either side; corrected by its residual x - q s (P. Markstein, IBM Journal
-// of Research and Development 34, 1990) it is the quotient.  For s within 2^+-80 the residual is exact for all quotients
-// that are neither under half of the smallest code nor over the largest.  (4 x 2047 tokens, interleaved: 22.5 us without
-// the correction, 23.0 with it, 24.9 with divisions.)
-__device__ __forceinline__ float quotient(float x, float s, float inverse) {
-  const float q = x * inverse;
-  return fabsf(q) < 512.0f ? fmaf(fmaf(-q, s, x), inverse, q) : q;  // beyond 448, infinite or NaN: q says it
-}
 constexpr float kLeastScale = 0x1p-80f, kMostScale = 0x1p80f;
 // A power of two that brings another scale to [1, 2), or a subnormal one as near as it reaches; 0 and NaN stay.
 __device__ __forceinline__ float scale_power(float s) {
@@ -188,6 +171,150 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------------------------------------
+// spec_kv_append_ex: a page's scale follows what goes into it
+// ------------------------------------------------------------------------------------------------
+constexpr int kPageThreads = 128;
+constexpr int kPageHeld = 4;  // tokens a thread holds between the two passes
+
+struct PageAppendParams {
+  Heads k, v;
+  Cache cache;
+  PageScales scales;
+  Batch batch;
+  const float* cos_table;
+  const float* sin_table;
+  const int32_t* positions;
+  int heads, touched;  // touched: pages that T tokens can lie in
+  int rot, max_positions;
+};
+
+// One block per (request, page that gets tokens, head, k or v): the largest magnitude of what goes in, then the page's
+// scale, then the codes.  A thread owns one unit of the head dimension as in append_kernel, for every lanes-th token; the
+// products of a rotation are rounded one by one, so the magnitude does not depend on how they are fused.
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kPageThreads) page_append_kernel(const __grid_constant__ PageAppendParams P) {
+  __shared__ float most_of[kPageThreads / 32];
+  pdl_launch_next();
+  pdl_wait();
+  int index = blockIdx.x;
+  const bool is_v = index & 1;
+  index >>= 1;
+  const int head = index % P.heads;
+  index /= P.heads;
+  const int nth = index % P.touched, b = index / P.touched;
+
+  const int page_size = 1 << P.cache.page_shift;
+  const int held = __ldg(P.batch.ctx_len + b);
+  const int tb = batch_tokens(P.batch, b), ctx = min(max(held, 0), P.batch.slots);
+  const int ordinal = (ctx >> P.cache.page_shift) + nth;
+  if (ordinal >= P.batch.max_pages) return;
+  const int from = ordinal << P.cache.page_shift;  // the page's first slot
+  const int t0 = max(from - ctx, 0), t1 = (int)min((int64_t)tb, (int64_t)from + page_size - ctx);
+  if (t0 >= t1) return;
+  const int page = __ldg(P.batch.pages + (int64_t)b * P.batch.max_pages + ordinal);
+  if (page < 0 || page >= P.cache.num_pages) return;
+
+  const int rot = is_v ? 0 : P.rot;
+  const int paired = INTERLEAVED ? 0 : rot / 16, units = D / 8 - paired, lanes = kPageThreads / units;
+  const int lane0 = threadIdx.x / units, unit = threadIdx.x - lane0 * units;
+  const bool works = lane0 < lanes, pair = unit < paired;
+  const int lo = pair || INTERLEAVED ? unit * 8 : rot + (unit - paired) * 8, far = rot / 2;
+  const bool turns = pair || (INTERLEAVED && lo < rot);
+  const Heads& in = is_v ? P.v : P.k;
+  const char* src = in.data + b * in.row + head * in.head;
+
+  uint4 w0[kPageHeld], w1[kPageHeld];
+  const auto load = [&](int t, uint4& a, uint4& c) {
+    const char* p = src + t * in.token;
+    a = *reinterpret_cast<const uint4*>(p + lo * 2);
+    if (pair) c = *reinterpret_cast<const uint4*>(p + (lo + far) * 2);
+  };
+  const auto turned = [&](int t, const uint4& a, const uint4& c, float (&x)[8], float (&y)[8]) {
+    unpack8(a, x);
+    if (pair) unpack8(c, y);
+    if (!turns) return;
+    int pos = P.positions ? __ldg(P.positions + (int64_t)b * P.batch.T + t) : (int)min((int64_t)max(held, 0) + t, (int64_t)INT32_MAX);
+    pos = min(max(pos, 0), P.max_positions - 1);
+    const int64_t base = (int64_t)pos * (rot / 2) + (INTERLEAVED ? lo / 2 : lo);
+#pragma unroll
+    for (int i = 0; i < (INTERLEAVED ? 4 : 8); i += 4) {
+      const float4 c4 = __ldg(reinterpret_cast<const float4*>(P.cos_table + base + i));
+      const float4 s4 = __ldg(reinterpret_cast<const float4*>(P.sin_table + base + i));
+      const float co[4] = {c4.x, c4.y, c4.z, c4.w}, si[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float& first = INTERLEAVED ? x[2 * e] : x[i + e];
+        float& second = INTERLEAVED ? x[2 * e + 1] : y[i + e];
+        const float u = first, v = second;
+        first = __fsub_rn(__fmul_rn(u, co[e]), __fmul_rn(v, si[e]));
+        second = __fadd_rn(__fmul_rn(v, co[e]), __fmul_rn(u, si[e]));
+      }
+    }
+  };
+
+  float most = 0.0f;  // of the finite magnitudes
+  const auto look = [&](int t, const uint4& a, const uint4& c) {
+    float x[8], y[8];
+    turned(t, a, c, x, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (fabsf(x[e]) < INFINITY) most = fmaxf(most, fabsf(x[e]));
+      if (pair && fabsf(y[e]) < INFINITY) most = fmaxf(most, fabsf(y[e]));
+    }
+  };
+  if (works) {
+#pragma unroll
+    for (int i = 0; i < kPageHeld; ++i)
+      if (t0 + lane0 + i * lanes < t1) load(t0 + lane0 + i * lanes, w0[i], w1[i]);
+#pragma unroll
+    for (int i = 0; i < kPageHeld; ++i)
+      if (t0 + lane0 + i * lanes < t1) look(t0 + lane0 + i * lanes, w0[i], w1[i]);
+    for (int t = t0 + lane0 + kPageHeld * lanes; t < t1; t += lanes) {
+      uint4 a, c;
+      load(t, a, c);
+      look(t, a, c);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
+  if ((threadIdx.x & 31) == 0) most_of[threadIdx.x >> 5] = most;
+  float* place = (is_v ? P.scales.v : P.scales.k) + (int64_t)page * P.heads + head;
+  const int before = nth == 0 ? ctx - from : 0;  // rows of the page that hold tokens already
+  const float old = before > 0 ? *place : 0.0f;
+  __syncthreads();  // every thread has read the old scale
+#pragma unroll
+  for (int w = 0; w < kPageThreads / 32; ++w) most = fmaxf(most, most_of[w]);
+  const bool counts = before > 0 && scale_counts(old);
+  const float need = scale_need(most), scale = counts ? fmaxf(old, need) : need, inverse = 1.0f / scale;
+  if (threadIdx.x == 0) *place = scale;
+
+  char* out = (is_v ? P.cache.v : P.cache.k) + page * P.cache.page + head * P.cache.head;
+  if (counts && need > old) {  // the rows before: their codes at the new scale, a power of two
+    const float ratio = old * inverse;
+    for (int u = threadIdx.x; u < before * (D / 16); u += kPageThreads) {
+      uint4* p = reinterpret_cast<uint4*>(out + (u / (D / 16)) * P.cache.slot + (u % (D / 16)) * 16);
+      *p = rescaled(*p, ratio);
+    }
+  }
+  if (!works) return;
+  const auto store = [&](int t, const uint4& a, const uint4& c) {
+    float x[8], y[8];
+    turned(t, a, c, x, y);
+    char* p = out + (int64_t)(ctx + t - from) * P.cache.slot;
+    store_entry<true>(p + lo, x, scale, inverse);
+    if (pair) store_entry<true>(p + lo + far, y, scale, inverse);
+  };
+#pragma unroll
+  for (int i = 0; i < kPageHeld; ++i)
+    if (t0 + lane0 + i * lanes < t1) store(t0 + lane0 + i * lanes, w0[i], w1[i]);
+  for (int t = t0 + lane0 + kPageHeld * lanes; t < t1; t += lanes) {
+    uint4 a, c;
+    load(t, a, c);
+    store(t, a, c);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
 // spec_kv_keep
 // ------------------------------------------------------------------------------------------------
 struct KeepParams {
@@ -281,11 +408,12 @@ using namespace sv;
 
 extern "C" {
 
-spec_status_t spec_kv_append(const spec_heads_t* q, const spec_heads_t* k, const spec_heads_t* v,
-                             const spec_heads_t* q_out, int32_t q_heads, const spec_kv_cache_t* cache,
-                             const spec_decode_batch_t* batch, const spec_rotary_t* rotary, int32_t* out_flags,
-                             void* stream) {
+spec_status_t spec_kv_append_ex(const spec_heads_t* q, const spec_heads_t* k, const spec_heads_t* v,
+                                const spec_heads_t* q_out, int32_t q_heads, const spec_kv_cache_t* cache,
+                                const spec_kv_page_scales_t* scales, const spec_decode_batch_t* batch,
+                                const spec_rotary_t* rotary, int32_t* out_flags, void* stream) {
   spec_status_t s = check_cache(cache, true);
+  if (s == SPEC_OK) s = check_scales(scales, cache);
   if (s == SPEC_OK) s = check_batch(batch, cache);
   if (s != SPEC_OK) return s;
   if (q_heads < 0 || (q_heads == 0) != (q == nullptr) || (q_heads == 0) != (q_out == nullptr))
@@ -308,9 +436,12 @@ spec_status_t spec_kv_append(const spec_heads_t* q, const spec_heads_t* k, const
     P.positions = rotary->positions, P.max_positions = rotary->max_positions;
   }
   P.flags = out_flags;
-  P.q_heads = q_heads, P.heads = cache->heads;
+  P.q_heads = q_heads, P.heads = scales ? 0 : cache->heads;  // with page scales: the queries and flags alone
   const bool inter = rot > 0 && rotary->interleaved != 0;
   const int64_t blocks = (int64_t)batch->B * batch->T;
+  const int64_t touched = ((int64_t)batch->T + cache->page_size - 2) / cache->page_size + 1;
+  const int64_t page_blocks = batch->B * touched * cache->heads * 2;
+  if (scales && page_blocks > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
   if (blocks > 0x7fffffffll || q_heads > 65535) return SPEC_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f8 = cache->dtype == SPEC_DTYPE_E4M3;
@@ -322,7 +453,21 @@ spec_status_t spec_kv_append(const spec_heads_t* q, const spec_heads_t* k, const
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != cudaSuccess) return SPEC_ERR_CUDA;
   const int threads = blocks >= 16 * sms ? kAppendThreadsMany : kAppendThreads;
-  return launch_early(kern, dim3((unsigned)blocks), dim3(threads), 0, st, P) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  if (!scales || q_heads > 0 || out_flags)
+    if (launch_early(kern, dim3((unsigned)blocks), dim3(threads), 0, st, P) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (!scales) return SPEC_OK;
+  const PageAppendParams A = {P.k, P.v, P.cache, scales_of(scales), P.batch, P.cos_table, P.sin_table, P.positions,
+                              cache->heads, (int)touched, rot, P.max_positions};
+  auto pages = cache->head_dim == 128 ? (inter ? page_append_kernel<128, true> : page_append_kernel<128, false>)
+                                      : (inter ? page_append_kernel<64, true> : page_append_kernel<64, false>);
+  return launch_early(pages, dim3((unsigned)page_blocks), dim3(kPageThreads), 0, st, A) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+spec_status_t spec_kv_append(const spec_heads_t* q, const spec_heads_t* k, const spec_heads_t* v,
+                             const spec_heads_t* q_out, int32_t q_heads, const spec_kv_cache_t* cache,
+                             const spec_decode_batch_t* batch, const spec_rotary_t* rotary, int32_t* out_flags,
+                             void* stream) {
+  return spec_kv_append_ex(q, k, v, q_out, q_heads, cache, nullptr, batch, rotary, out_flags, stream);
 }
 
 spec_status_t spec_kv_keep(const spec_kv_cache_t* cache, const spec_decode_batch_t* batch, const int32_t* path,

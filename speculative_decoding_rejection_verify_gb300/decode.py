@@ -8,6 +8,14 @@ One round of speculative decoding with a target model:
   position; then ``verify`` or ``verify_multi``;
 * after a tree of drafts ``kv_keep`` moves the accepted branch's entries up behind the context.
 
+Two ways to keep a long context small:
+
+* a float8_e4m3fn cache with a scale per page and head instead of one per head: pass ``k_scale`` and ``v_scale`` as
+  ``[num_pages, heads]`` to every one of these calls; ``kv_append``, ``kv_keep`` and ``kv_move`` set them;
+* eviction: ``kv_weigh`` adds up the weight that attention gives every entry (``paged_attention`` leaves the rows' sums in ``lse``),
+  ``kv_select`` picks the entries of every head that stay within a budget, ``kv_move`` brings them together.  Weights
+  (float32) and positions (int32) of the entries are tensors ``[num_pages, heads, page_size]``.
+
 The cache is a pair of tensors ``[num_pages, page_size, heads, head_dim]`` (bfloat16, or float8_e4m3fn
 with a scale per head); any memory order with ``head_dim`` innermost does, so a pool laid out
 ``[num_pages, heads, page_size, head_dim]`` is passed as its ``transpose(1, 2)``.  ``pages [B, max_pages]``
@@ -35,8 +43,9 @@ MAX_SLOTS = 1 << 30
 MAX_HISTORY = 1048448
 MAX_BIAS = 2046
 
-DECODE_EXPORTS = ("spec_kv_append", "spec_paged_attention_workspace_bytes", "spec_paged_attention", "spec_kv_keep",
-                  "spec_process_logits")
+DECODE_EXPORTS = ("spec_kv_append", "spec_kv_append_ex", "spec_paged_attention_workspace_bytes", "spec_paged_attention",
+                  "spec_paged_attention_ex", "spec_kv_keep", "spec_kv_keep_ex", "spec_kv_weigh", "spec_kv_select",
+                  "spec_kv_move", "spec_process_logits")
 
 _P, _I, _L, _F, _Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 
@@ -49,6 +58,15 @@ class CacheStruct(ctypes.Structure):
     _fields_ = [("k", _P), ("v", _P), ("layer_stride", _L), ("page_stride", _L), ("slot_stride", _L),
                 ("head_stride", _L), ("layers", _I), ("num_pages", _I), ("page_size", _I), ("heads", _I),
                 ("head_dim", _I), ("dtype", _I), ("k_scale", _P), ("v_scale", _P)]
+
+
+class PageScalesStruct(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("layer_stride", _L)]
+
+
+class RecordStruct(ctypes.Structure):
+    _fields_ = [("weight", _P), ("position", _P), ("layer_stride", _L), ("layers", _I), ("num_pages", _I),
+                ("page_size", _I), ("heads", _I)]
 
 
 class BatchStruct(ctypes.Structure):
@@ -76,6 +94,18 @@ def declare(lib) -> None:
     lib.spec_paged_attention.restype = _I
     lib.spec_kv_keep.argtypes = [_P, _P, _P, _P, _I, _P]
     lib.spec_kv_keep.restype = _I
+    lib.spec_kv_append_ex.argtypes = [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P]
+    lib.spec_kv_append_ex.restype = _I
+    lib.spec_paged_attention_ex.argtypes = [_P, _P, _I, _P, _P, _P, _P, _F, _P, _P, _Z, _P]
+    lib.spec_paged_attention_ex.restype = _I
+    lib.spec_kv_keep_ex.argtypes = [_P, _P, _P, _P, _P, _P, _I, _P]
+    lib.spec_kv_keep_ex.restype = _I
+    lib.spec_kv_weigh.argtypes = [_P, _I, _P, _P, _P, _P, _F, _P, _P, _P, _P]
+    lib.spec_kv_weigh.restype = _I
+    lib.spec_kv_select.argtypes = [_P, _P, _P, _P, _I, _I, _P, _P, _I, _P, _P, _P]
+    lib.spec_kv_select.restype = _I
+    lib.spec_kv_move.argtypes = [_P, _P, _P, _P, _P, _P, _P, _I, _P]
+    lib.spec_kv_move.restype = _I
     lib.spec_process_logits.argtypes = [_P, _P, _P, _I, _I, _I, _I, _P]
     lib.spec_process_logits.restype = _I
 
@@ -83,6 +113,8 @@ def declare(lib) -> None:
 # The structs as bytes, field by field as in the classes above (NULL is 0).
 _pack_heads = struct.Struct("Pqqq").pack
 _pack_cache = struct.Struct("PPqqqqiiiiiiPP").pack
+_pack_scales = struct.Struct("PPq").pack
+_pack_record = struct.Struct("PPqiiii").pack
 _pack_batch = struct.Struct("PPPiiixxxx").pack
 _pack_rotary = struct.Struct("PPPiiixxxx").pack
 _pack_rules = struct.Struct("11Pii").pack
@@ -158,10 +190,31 @@ def _cache(k_cache, v_cache, k_scale, v_scale, layered):
         raise TypeError(f"k_cache must be bfloat16 or float8_e4m3fn, got {dtype}")
     layers, layer = (1, 0) if len(shape) == 4 else (shape[0], st[0])
     num_pages, page, heads, D = shape[-4:]
-    ks = 0 if k_scale is None else _fits(k_scale, "k_scale", (heads,), _torch.float32, index)
-    vs = 0 if v_scale is None else _fits(v_scale, "v_scale", (heads,), _torch.float32, index)
+    scales, ks, vs = None, 0, 0
+    if (k_scale is not None and k_scale.dim() > 1) or (v_scale is not None and v_scale.dim() > 1):
+        scales = _page_scales(k_scale, v_scale, shape[:-3] + (heads,), index)
+    else:
+        ks, vs = _maybe(k_scale, "k_scale", (heads,), _torch.float32, index), _maybe(v_scale, "v_scale", (heads,), _torch.float32, index)
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), layer, st[-4], st[-3], st[-2], layers, num_pages, page,
-                       heads, D, dt, ks, vs), heads, D, index
+                       heads, D, dt, ks, vs), heads, D, index, scales
+
+
+def _page_scales(k_scale, v_scale, shape, index):
+    """Scales per page and head, [num_pages, heads] (with the cache's layers in front)."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale must both have a scale per page, or neither")
+    k, v = (_fits(x, name, shape, _torch.float32, index) for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")))
+    return _pack_scales(k, v, shape[-2] * shape[-1] if len(shape) == 3 else 0)
+
+
+def _record(weight, position, shape, index):
+    """The struct of weights and positions [num_pages, heads, page_size] (with layers in front), either of which may be None."""
+    if weight is None and position is None:
+        return None
+    w, p = _maybe(weight, "weight", shape, _torch.float32, index), _maybe(position, "position", shape, _torch.int32, index)
+    num_pages, heads, page = shape[-3:]
+    return _pack_record(w, p, num_pages * heads * page if len(shape) == 4 else 0, 1 if len(shape) == 3 else shape[0], num_pages,
+                        page, heads)
 
 
 def _batch(pages, ctx_len, t_per_row, B, T, index):
@@ -191,11 +244,12 @@ def kv_append(q, k, v, k_cache, v_cache, pages, ctx_len, cos=None, sin=None, t_p
               interleaved: bool = False, k_scale=None, v_scale=None, out=None, flags=None, stream=None):
     """Rotate the new tokens' ``q [B, T, q_heads, head_dim]`` and ``k [B, T, heads, head_dim]`` and put k and
     ``v`` into the cache at slots ``ctx_len[b] + t`` (spec_kv_append); returns the rotated q (``out``, which may
-    be q itself).  ``q`` may be None.  ``cos``/``sin [max_positions, rot_dim / 2]``: None = no rotation;
+    be q itself).  ``k_scale``/``v_scale [heads]``, or ``[num_pages, heads]``: set by what goes into each page
+    (spec_kv_append_ex).  ``q`` may be None.  ``cos``/``sin [max_positions, rot_dim / 2]``: None = no rotation;
     ``positions [B, T]``: None = ``ctx_len[b] + t``.  ``t_per_row [B]``: each request's valid tokens (the
     others' rotated q is 0).  ``flags [B]`` int32, cleared by the caller: FLAG_* bits are ORed into it."""
     torch, lib = _load()
-    c, heads, D, index = _cache(k_cache, v_cache, k_scale, v_scale, False)
+    c, heads, D, index, scales = _cache(k_cache, v_cache, k_scale, v_scale, False)
     if k.dim() != 4:
         raise ValueError("k must be [B, T, heads, head_dim]")
     B, T = k.shape[:2]
@@ -224,21 +278,26 @@ def kv_append(q, k, v, k_cache, v_cache, pages, ctx_len, cos=None, sin=None, t_p
     elif sin is not None:
         raise ValueError("sin without cos: both are [max_positions, rot_dim / 2]")
     f = _maybe(flags, "flags", (B,), torch.int32, index)
-    rc = lib.spec_kv_append(hq, hk, hv, ho, n, c, b, r, f, _raw_stream(index) if stream is None else stream.cuda_stream)
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if scales is None:
+        rc = lib.spec_kv_append(hq, hk, hv, ho, n, c, b, r, f, handle)
+    else:
+        rc = lib.spec_kv_append_ex(hq, hk, hv, ho, n, c, scales, b, r, f, handle)
     if rc != sv.SPEC_OK:
         raise sv.SpecVerifyError(rc, "spec_kv_append")
     return out
 
 
 def paged_attention(q, k_cache, v_cache, pages, ctx_len, t_per_row=None, mask=None, scale: Optional[float] = None,
-                    k_scale=None, v_scale=None, out=None, workspace_tensor=None, stream=None):
+                    k_scale=None, v_scale=None, out=None, workspace_tensor=None, stream=None, lse=None):
     """Attention of the new tokens' ``q [B, T, q_heads, head_dim]`` over the cache, their own entries included
     (spec_paged_attention, after ``kv_append``); returns ``out`` of q's shape.  ``mask [B, T]`` int64: bit i of
     ``mask[b, t]`` says whether new token t attends to new token i (None: causal); every token attends to the
-    whole context.  ``scale``: None = head_dim ** -0.5.  ``workspace_tensor``: None = the binding's own scratch, which is
+    whole context.  ``scale``: None = head_dim ** -0.5.  ``k_scale``/``v_scale [heads]``, or ``[num_pages, heads]``.
+    ``lse [B, T, q_heads]`` float32: takes the log of every row's sum of exponentials (spec_paged_attention_ex).  ``workspace_tensor``: None = the binding's own scratch, which is
     the graph's own while one is being captured."""
     torch, lib = _load()
-    c, heads, D, index = _cache(k_cache, v_cache, k_scale, v_scale, False)
+    c, heads, D, index, scales = _cache(k_cache, v_cache, k_scale, v_scale, False)
     if q.dim() != 4:
         raise ValueError("q must be [B, T, q_heads, head_dim]")
     B, T, n, _ = shape = q.shape
@@ -257,28 +316,132 @@ def paged_attention(q, k_cache, v_cache, pages, ctx_len, t_per_row=None, mask=No
             ws = sv.workspace(nbytes, k_cache.device, stream if stream is not None else torch.cuda.current_stream(index))
     else:
         sv._given_workspace(ws, k_cache.device)
-    rc = lib.spec_paged_attention(hq, ho, n, c, b, m, max(D, 1) ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel(),
-                                  handle)
+    scale = max(D, 1) ** -0.5 if scale is None else scale
+    if scales is None and lse is None:
+        rc = lib.spec_paged_attention(hq, ho, n, c, b, m, scale, ws.data_ptr(), ws.numel(), handle)
+    else:
+        rc = lib.spec_paged_attention_ex(hq, ho, n, c, scales, b, m, scale, _maybe(lse, "lse", (B, T, n), torch.float32, index),
+                                         ws.data_ptr(), ws.numel(), handle)
     if rc != sv.SPEC_OK:
         raise sv.SpecVerifyError(rc, "spec_paged_attention")
     return out
 
 
-def kv_keep(k_cache, v_cache, pages, ctx_len, path, n_keep, stream=None) -> None:
+def kv_keep(k_cache, v_cache, pages, ctx_len, path, n_keep, stream=None, k_scale=None, v_scale=None, weight=None,
+            position=None) -> None:
     """Move the accepted branch's entries up behind the context (spec_kv_keep): in every layer slot
     ``ctx_len[b] + i`` takes slot ``ctx_len[b] + path[b, i]`` for ``i < n_keep[b]``.  The cache may have a leading
-    layer dimension; ``path [B, max_keep]`` holds strictly increasing indices of new tokens."""
+    layer dimension; ``path [B, max_keep]`` holds strictly increasing indices of new tokens.  With page scales
+    ``k_scale``/``v_scale [num_pages, heads]`` (layers in front as the cache has them) an entry takes its new page's, which grows where it has
+    to; ``weight`` and ``position`` move with the entries (spec_kv_keep_ex)."""
     torch, lib = _load()
-    c, _, _, index = _cache(k_cache, v_cache, None, None, True)
+    c, heads, _, index, scales = _cache(k_cache, v_cache, k_scale, v_scale, True)
+    if scales is None and (k_scale is not None or v_scale is not None):
+        raise ValueError("k_scale and v_scale of kv_keep are scales per page: a scale per head moves with nothing")
     if path.dim() != 2:
         raise ValueError("path must be [B, max_keep]")
     B, most = path.shape
     b = _batch(pages, ctx_len, None, B, 0, index)
-    rc = lib.spec_kv_keep(c, b, _fits(path, "path", (B, most), torch.int32, index),
-                          _fits(n_keep, "n_keep", (B,), torch.int32, index), most,
-                          _raw_stream(index) if stream is None else stream.cuda_stream)
+    r = _record(weight, position, _record_shape(k_cache), index)
+    p, n = _fits(path, "path", (B, most), torch.int32, index), _fits(n_keep, "n_keep", (B,), torch.int32, index)
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if scales is None and r is None:
+        rc = lib.spec_kv_keep(c, b, p, n, most, handle)
+    else:
+        rc = lib.spec_kv_keep_ex(c, scales, r, b, p, n, most, handle)
     if rc != sv.SPEC_OK:
         raise sv.SpecVerifyError(rc, "spec_kv_keep")
+
+
+def _record_shape(k_cache):
+    s = k_cache.shape
+    return s[:-3] + (s[-2], s[-3])
+
+
+def kv_weigh(q, k_cache, pages, ctx_len, lse, weight, position=None, t_per_row=None, mask=None, positions=None,
+             scale: Optional[float] = None, k_scale=None, stream=None) -> None:
+    """Add up what the new tokens' attention gives every entry (spec_kv_weigh): ``weight [num_pages, heads, page_size]``
+    float32 gains the weights that the rows of ``q`` (with the ``lse`` that ``paged_attention`` left, and its arguments) give the
+    context's entries, and takes those that they give one another; ``position`` (int32, of weight's shape) takes the new tokens'
+    ``positions [B, T]`` (None: ``ctx_len[b] + t``).  A row whose ``lse`` is infinite has no part."""
+    torch, lib = _load()
+    paged = k_scale is not None and k_scale.dim() > 1
+    c, heads, D, index, scales = _cache(k_cache, k_cache, k_scale, k_scale if paged else None, False)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, q_heads, head_dim]")
+    if weight is None:
+        raise ValueError("weight must be [num_pages, heads, page_size]")
+    B, T, n, _ = q.shape
+    b = _batch(pages, ctx_len, t_per_row, B, T, index)
+    rc = lib.spec_kv_weigh(_heads(q, "q", (B, T, n, D), index), n, c, scales, b, _maybe(mask, "mask", (B, T), torch.int64, index),
+                           max(D, 1) ** -0.5 if scale is None else scale, _fits(lse, "lse", (B, T, n), torch.float32, index),
+                           _record(weight, position, _record_shape(k_cache), index),
+                           _maybe(positions, "positions", (B, T), torch.int32, index),
+                           _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc != sv.SPEC_OK:
+        raise sv.SpecVerifyError(rc, "spec_kv_weigh")
+
+
+def kv_select(weight, position, pages, ctx_len, budget, seen=None, first: int = 0, recent: int = 0, out=None, stream=None):
+    """Pick the ``min(ctx_len[b], budget[b])`` entries of largest weight that stay, of every head by itself (spec_kv_select):
+    ``weight`` and ``position [num_pages, heads, page_size]``, or with layers in front.  Entries at positions ``< first`` or
+    ``>= seen[b] - recent`` (``seen [B]``: tokens so far, None: ``ctx_len``) go before all others; ``position`` may be None without
+    them.  Returns ``(source, target, moves, new_len)`` for ``kv_move``: lists ``[(layers,) B, heads, slots // 2]`` of which
+    the first ``moves [(layers,) B, heads]`` count, and the context's new lengths ``[B]`` (``out``: such tensors to write to)."""
+    torch, lib = _load()
+    if weight.dim() not in (3, 4):
+        raise ValueError("weight must be [num_pages, heads, page_size], or with layers in front of it")
+    index = weight.get_device()
+    if index < 0:
+        raise ValueError("weight must be a CUDA tensor")
+    if index != _current_device():
+        sv._launches_on(index)
+    shape = weight.shape
+    r = _record(weight, position, shape, index)
+    if pages.dim() != 2:
+        raise ValueError("pages must be [B, max_pages]")
+    B, max_pages = pages.shape
+    b = _batch(pages, ctx_len, None, B, 0, index)
+    lists = shape[:-3] + (B, shape[-2])
+    most = max_pages * shape[-1] // 2
+    if out is None:
+        new = lambda size: torch.empty(size, dtype=torch.int32, device=weight.device)  # noqa: E731
+        if stream is None:
+            out = new(lists + (most,)), new(lists + (most,)), new(lists), new((B,))
+        else:
+            with torch.cuda.stream(stream):
+                out = new(lists + (most,)), new(lists + (most,)), new(lists), new((B,))
+    source, target, moves, new_len = out
+    most = source.shape[-1] if source.dim() else 0
+    i32 = torch.int32
+    rc = lib.spec_kv_select(r, b, _fits(budget, "budget", (B,), i32, index), _maybe(seen, "seen", (B,), i32, index), first, recent,
+                            _fits(source, "source", lists + (most,), i32, index), _fits(target, "target", lists + (most,), i32, index),
+                            most, _fits(moves, "moves", lists, i32, index), _fits(new_len, "new_len", (B,), i32, index),
+                            _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc != sv.SPEC_OK:
+        raise sv.SpecVerifyError(rc, "spec_kv_select")
+    return source, target, moves, new_len
+
+
+def kv_move(k_cache, v_cache, pages, new_len, source, target, moves, k_scale=None, v_scale=None, weight=None, position=None,
+            stream=None) -> None:
+    """Move the entries that ``kv_select`` picked to the front (spec_kv_move): in every layer and head slot
+    ``target[..., i]`` takes slot ``source[..., i]`` for ``i < moves``, keys, values, page scales, ``weight`` and ``position``.
+    The context has ``new_len`` entries from then on; they keep their rotation, so the next tokens' positions have to be given."""
+    torch, lib = _load()
+    c, heads, _, index, scales = _cache(k_cache, v_cache, k_scale, v_scale, True)
+    if scales is None and (k_scale is not None or v_scale is not None):
+        raise ValueError("k_scale and v_scale of kv_move are scales per page: a scale per head moves with nothing")
+    if pages.dim() != 2 or source.dim() < 1:
+        raise ValueError("pages must be [B, max_pages], and source [B, heads, n]")
+    B, most = pages.shape[0], source.shape[-1]
+    b = _batch(pages, new_len, None, B, 0, index)
+    lists, i32 = k_cache.shape[:-4] + (B, heads), torch.int32
+    rc = lib.spec_kv_move(c, scales, _record(weight, position, _record_shape(k_cache), index), b,
+                          _fits(source, "source", lists + (most,), i32, index), _fits(target, "target", lists + (most,), i32, index),
+                          _fits(moves, "moves", lists, i32, index), most, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc != sv.SPEC_OK:
+        raise sv.SpecVerifyError(rc, "spec_kv_move")
 
 
 def process_logits(logits, history=None, history_len=None, prompt_len=None, draft=None, t_per_row=None,
