@@ -11,10 +11,11 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "spec_verify.cu")
 SRC_CTRL = os.path.join(PKG, "csrc", "spec_control.cpp")
-SRC_DECODE = [os.path.join(PKG, "csrc", f) for f in ("spec_kv.cu", "spec_attention.cu", "spec_pages.cu", "spec_evict.cu", "spec_logits.cu")]
+SRC_DECODE = [os.path.join(PKG, "csrc", f) for f in ("spec_kv.cu", "spec_attention.cu", "spec_pages.cu", "spec_weigh.cu", "spec_select.cu", "spec_logits.cu")]
 HDR = os.path.join(ROOT, "include", "spec_verify.h")
 HDR_CTRL = os.path.join(ROOT, "include", "spec_control.h")
-HDR_DECODE = [os.path.join(ROOT, "include", "spec_decode.h"), os.path.join(PKG, "csrc", "decode_common.cuh")]
+HDR_DECODE = [os.path.join(ROOT, "include", "spec_decode.h"), os.path.join(PKG, "csrc", "decode_common.cuh"),
+              os.path.join(PKG, "csrc", "tile_stream.cuh")]
 LIB = os.path.join(PKG, "libspecverify.so")
 
 NVCC_FLAGS = [

@@ -109,6 +109,9 @@ __device__ __forceinline__ float quotient(float x, float s, float inverse) {
   return fabsf(q) < 512.0f ? fmaf(fmaf(-q, s, x), inverse, q) : q;  // beyond 448, infinite or NaN: q says it
 }
 
+// The same, with -0 kept.
+__device__ __forceinline__ float signed_quotient(float x, float s, float inverse) { return x == 0.0f ? x : quotient(x, s, inverse); }
+
 // Page scales (spec_kv_page_scales_t): [layers][num_pages, heads].
 struct PageScales {
   float* k;

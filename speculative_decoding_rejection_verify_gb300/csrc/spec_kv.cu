@@ -301,8 +301,14 @@ __global__ void __launch_bounds__(kPageThreads) page_append_kernel(const __grid_
     float x[8], y[8];
     turned(t, a, c, x, y);
     char* p = out + (int64_t)(ctx + t - from) * P.cache.slot;
-    store_entry<true>(p + lo, x, scale, inverse);
-    if (pair) store_entry<true>(p + lo + far, y, scale, inverse);
+    const auto put = [&](char* at, const float (&z)[8]) {
+      float c[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = signed_quotient(z[e], scale, inverse);
+      *reinterpret_cast<uint2*>(at) = make_uint2(pack_e4m3(c[0], c[1], c[2], c[3]), pack_e4m3(c[4], c[5], c[6], c[7]));
+    };
+    put(p + lo, x);
+    if (pair) put(p + lo + far, y);
   };
 #pragma unroll
   for (int i = 0; i < kPageHeld; ++i)

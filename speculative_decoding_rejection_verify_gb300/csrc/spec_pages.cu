@@ -8,80 +8,185 @@
 
 namespace sv {
 
-// What a warp needs of one page that entries move into.
-struct Target {
-  char* rows;       // row 0 of the page, of one head
-  int64_t slot;     // bytes from row to row
-  float* scale;
-  int end;          // rows from here on hold nothing that stays
-};
-
 // The values of 16 codes at scale `from`, as codes at scale `to`.
 __device__ __forceinline__ uint4 recoded(uint4 w, float from, float to, float inverse) {
   uint32_t* x = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float4 f = unpack_e4m3(x[i]);
-    x[i] = pack_e4m3(quotient(f.x * from, to, inverse), quotient(f.y * from, to, inverse), quotient(f.z * from, to, inverse),
-                     quotient(f.w * from, to, inverse));
+    x[i] = pack_e4m3(signed_quotient(f.x * from, to, inverse), signed_quotient(f.y * from, to, inverse),
+                     signed_quotient(f.z * from, to, inverse), signed_quotient(f.w * from, to, inverse));
   }
   return w;
 }
 
-// A warp's moves into one page: entries 0 .. n - 1, of which fetch(i, vec, scale) gives 16 codes (vector vec) and their
-// scale, and row(i) the page's row, or -1 for a move that is left out.  `taken` [page_size / 32] marks the rows.
-template <int D, typename Fetch, typename Row>
-__device__ void put_entries(const Target& to, int n, uint32_t* taken, int page_size, Fetch fetch, Row row) {
+// One lane's move of a warp's 32: where its entry lies and goes, as byte offsets from row 0 of page 0 of the head.  Moves
+// into one page are neighbours, lanes lo .. hi; a lane whose move is left out still belongs to its page.
+struct Move {
+  bool is;
+  int64_t src, dst;
+  int from, to;   // pages; to < 0: the page is outside the pool
+  int lo, hi;
+};
+
+// A warp's view of one head of a cache with page scales.
+struct Side {
+  char* base;       // row 0 of page 0
+  float* scales;    // of page 0
+  int heads;        // from page to page
+  int64_t slot, page;
+  int page_size;
+};
+
+// The entries' codes: lane l has vector l % (D / 16) of entries j * 32 / (D / 16) + l / (D / 16).
+template <int D>
+__device__ __forceinline__ void load_entries(const Side& c, const Move& m, uint4 (&w)[D / 16]) {
   constexpr int kVecs = D / 16, kAtOnce = 32 / kVecs;
-  const int lane = threadIdx.x & 31, vec = lane % kVecs, mine = lane / kVecs;
-  float most = 0.0f;  // of the finite magnitudes
-  for (int i0 = 0; i0 < n; i0 += kAtOnce) {
-    const int i = i0 + mine;
-    if (i >= n || row(i) < 0) continue;
-    float scale;
-    const uint4 w = fetch(i, vec, scale);
-    const uint32_t* x = reinterpret_cast<const uint32_t*>(&w);
-    uint32_t top = 0;  // a larger code without its sign is a larger magnitude; 0x7F is NaN
+  const int lane = threadIdx.x & 31;
+  const uint32_t all = __ballot_sync(~0u, m.is);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t size = x[j] & 0x7F7F7F7Fu;
+  for (int j = 0; j < kVecs; ++j) {
+    const int e = j * kAtOnce + lane / kVecs;
+    const int64_t at = __shfl_sync(~0u, m.src, e);
+    w[j] = (all >> e) & 1 ? *reinterpret_cast<const uint4*>(c.base + at + lane % kVecs * 16) : make_uint4(0, 0, 0, 0);
+  }
+}
+// The largest code of this lane's entry, without its sign: a larger one is a larger magnitude.  0x7F, NaN, does not count.
+template <int D>
+__device__ __forceinline__ uint32_t largest_code(const uint4 (&w)[D / 16]) {
+  constexpr int kVecs = D / 16, kAtOnce = 32 / kVecs;
+  const int lane = threadIdx.x & 31;
+  uint32_t mine = 0;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const uint32_t* x = reinterpret_cast<const uint32_t*>(&w[j]);
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t size = x[k] & 0x7F7F7F7Fu;
       top = __vmaxu4(top, size & ~__vcmpeq4(size, 0x7F7F7F7Fu));
     }
-    top = max(max(top & 0xFF, (top >> 8) & 0xFF), max((top >> 16) & 0xFF, top >> 24));
-    const float size = unpack_e4m3(top).x * fabsf(scale);
-    if (size < INFINITY) most = fmaxf(most, size);
+#pragma unroll
+    for (int d = 1; d < kVecs; d *= 2) top = __vmaxu4(top, __shfl_xor_sync(~0u, top, d));
+    const uint32_t of_entry = __shfl_sync(~0u, top, lane % kAtOnce * kVecs);
+    if (lane / kAtOnce == j) mine = of_entry;
+  }
+  return max(max(mine & 0xFF, (mine >> 8) & 0xFF), max((mine >> 16) & 0xFF, mine >> 24));
+}
+__device__ __forceinline__ float magnitude(uint32_t code, float scale) {  // a finite one, or 0
+  const float x = unpack_e4m3(code).x * fabsf(scale);
+  return x < INFINITY ? x : 0.0f;
+}
+template <int D>
+__device__ __forceinline__ void store_entries(const Side& c, const Move& m, const uint4 (&w)[D / 16], float from, float to) {
+  constexpr int kVecs = D / 16, kAtOnce = 32 / kVecs;
+  const int lane = threadIdx.x & 31;
+  const uint32_t all = __ballot_sync(~0u, m.is);
+  const float inverse = 1.0f / to;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int e = j * kAtOnce + lane / kVecs;
+    const int64_t at = __shfl_sync(~0u, m.dst, e);
+    const float f = __shfl_sync(~0u, from, e), t = __shfl_sync(~0u, to, e), i = __shfl_sync(~0u, inverse, e);
+    if ((all >> e) & 1) *reinterpret_cast<uint4*>(c.base + at + lane % kVecs * 16) = f == t ? w[j] : recoded(w[j], f, t, i);
+  }
+}
+// The page's scale with `most` in it, and what its codes have to be multiplied by.
+struct NewScale {
+  float scale, ratio;  // ratio 1: the codes stay
+};
+__device__ __forceinline__ NewScale new_scale(float old, float most) {
+  const bool counts = scale_counts(old);
+  const float need = scale_need(most), scale = counts ? fmaxf(old, need) : need;
+  return {scale, counts && need > old ? old / need : 1.0f};
+}
+// A warp rescales the rows < end of a page but for those marked in `taken`.
+template <int D>
+__device__ __forceinline__ void rescale_page(const Side& c, int page, int end, const uint32_t* taken, float ratio) {
+  constexpr int kVecs = D / 16, kAtOnce = 32 / kVecs;
+  const int lane = threadIdx.x & 31;
+  for (int r = lane / kVecs; r < end; r += kAtOnce) {
+    if ((taken[r >> 5] >> (r & 31)) & 1) continue;
+    uint4* p = reinterpret_cast<uint4*>(c.base + page * c.page + r * c.slot + lane % kVecs * 16);
+    *p = rescaled(*p, ratio);
+  }
+}
+__device__ __forceinline__ void clear_taken(uint32_t* taken, int page_size) {
+  for (int i = threadIdx.x & 31; i < (page_size + 31) / 32; i += 32) taken[i] = 0;
+  __syncwarp();
+}
+
+// A warp's moves, whole pages' of them, at most 32: every entry is in registers before the first is written.  row: the
+// target's row in its page; end: the rows of that page that hold what stays.
+template <int D>
+__device__ void move_batch(const Side& c, const Move& m, int row, int end, uint32_t* taken) {
+  const int lane = threadIdx.x & 31;
+  uint4 w[D / 16];
+  load_entries<D>(c, m, w);
+  const float from = m.is ? c.scales[(int64_t)m.from * c.heads] : 1.0f, old = m.to >= 0 ? c.scales[(int64_t)m.to * c.heads] : 1.0f;
+  float most = magnitude(largest_code<D>(w), m.is ? from : 0.0f);
+  bool any = m.is;  // of the lane's page
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const float x = __shfl_up_sync(~0u, most, d);
+    const bool a = __shfl_up_sync(~0u, any, d);
+    if (lane - d >= m.lo) most = fmaxf(most, x), any |= a;
+  }
+  most = __shfl_sync(~0u, most, m.hi), any = __shfl_sync(~0u, any, m.hi);
+  const NewScale s = new_scale(old, most);
+  uint32_t grown = __ballot_sync(~0u, any && lane == m.lo && s.ratio != 1.0f);
+  while (grown) {
+    const int leader = __ffs(grown) - 1;
+    grown &= grown - 1;
+    clear_taken(taken, c.page_size);
+    const int hi = __shfl_sync(~0u, m.hi, leader);
+    if (lane >= leader && lane <= hi && m.is) atomicOr(&taken[row >> 5], 1u << (row & 31));
+    __syncwarp();
+    rescale_page<D>(c, __shfl_sync(~0u, m.to, leader), __shfl_sync(~0u, end, leader), taken, __shfl_sync(~0u, s.ratio, leader));
+    __syncwarp();
+  }
+  store_entries<D>(c, m, w, from, s.scale);
+  __syncwarp();  // an entry may come from a page that others go to: its old scale was needed until here
+  if (any && lane == m.lo) c.scales[(int64_t)m.to * c.heads] = s.scale;
+  __syncwarp();
+}
+
+// A warp's n moves into one page: info(i) is lane's move i (is = false behind the last), row(move) its row.
+template <int D, typename Info, typename Row>
+__device__ void move_page(const Side& c, int n, int to, int end, uint32_t* taken, Info info, Row row) {
+  const int lane = threadIdx.x & 31;
+  float most = 0.0f;
+  bool any = false;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const Move m = info(i0 + lane);
+    uint4 w[D / 16];
+    load_entries<D>(c, m, w);
+    const uint32_t top = largest_code<D>(w);
+    if (m.is) most = fmaxf(most, magnitude(top, c.scales[(int64_t)m.from * c.heads])), any = true;
   }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
-  const float old = *to.scale;
-  const bool counts = scale_counts(old);
-  const float need = scale_need(most), scale = counts ? fmaxf(old, need) : need, inverse = 1.0f / scale;
-
-  if (counts && need > old) {
-    for (int i = lane; i < page_size / 32 + 1; i += 32) taken[i] = 0;
-    __syncwarp();
-    for (int i = lane; i < n; i += 32) {
-      const int r = row(i);
-      if (r >= 0) atomicOr(&taken[r >> 5], 1u << (r & 31));
+  if (!__any_sync(~0u, any)) return;
+  float* place = c.scales + (int64_t)to * c.heads;
+  const NewScale s = new_scale(*place, most);
+  if (s.ratio != 1.0f) {
+    clear_taken(taken, c.page_size);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const Move m = info(i0 + lane);
+      if (m.is) atomicOr(&taken[row(m) >> 5], 1u << (row(m) & 31));
     }
     __syncwarp();
-    const float ratio = old * inverse;
-    for (int r0 = 0; r0 < to.end; r0 += kAtOnce) {
-      const int r = r0 + mine;
-      if (r >= to.end || ((taken[r >> 5] >> (r & 31)) & 1)) continue;
-      uint4* p = reinterpret_cast<uint4*>(to.rows + r * to.slot + vec * 16);
-      *p = rescaled(*p, ratio);
-    }
+    rescale_page<D>(c, to, end, taken, s.ratio);
   }
-  for (int i0 = 0; i0 < n; i0 += kAtOnce) {
-    const int i = i0 + mine, r = i < n ? row(i) : -1;
-    if (r < 0) continue;
-    float from;
-    const uint4 w = fetch(i, vec, from);
-    *reinterpret_cast<uint4*>(to.rows + r * to.slot + vec * 16) = from == scale ? w : recoded(w, from, scale, inverse);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const Move m = info(i0 + lane);
+    uint4 w[D / 16];
+    load_entries<D>(c, m, w);
+    store_entries<D>(c, m, w, m.is ? c.scales[(int64_t)m.from * c.heads] : 1.0f, s.scale);
   }
   __syncwarp();  // an entry may come from the same page: its old scale was needed until here
-  if (lane == 0) *to.scale = scale;
+  if (lane == 0) *place = s.scale;
+  __syncwarp();
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -94,77 +199,106 @@ struct PageKeepParams {
   const int32_t* path;
   const int32_t* n_keep;
   int max_keep, heads;
-  int64_t lists;  // layers * B * heads * 2
+  int lists;  // layers * heads * 2
 };
 
-constexpr int kPageKeepWarps = 4;
+constexpr int kPageKeepWarps = 8;
 
-// A warp per (layer, request, head, k or v).  The moved entries and their scales come into shared memory before the first
-// one is written: a path's targets may be its later sources, and a page's scale may change.
-template <int D>
+// Where the moves of a request's path go, of all its layers and heads.
+struct PathMoves {
+  int64_t src[SPEC_MAX_NEW], dst[SPEC_MAX_NEW];
+  int from[SPEC_MAX_NEW], to[SPEC_MAX_NEW];  // from < 0: left out
+};
+
+// A block's warps take the (layer, head, k or v) of one request.  Nothing is written before everything is read, since a path's
+// targets may be its later sources: up to 32 entries wait in registers; more (BIG) are copied to shared memory first, which takes
+// the place of the cache as their source.
+template <int D, bool BIG>
 __global__ void __launch_bounds__(kPageKeepWarps * 32) page_keep_kernel(const __grid_constant__ PageKeepParams P) {
-  __shared__ uint4 entries[kPageKeepWarps][SPEC_MAX_NEW * (D / 16)];
-  __shared__ float scales[kPageKeepWarps][SPEC_MAX_NEW];
-  __shared__ int targets[kPageKeepWarps][SPEC_MAX_NEW];                // slots, -1: left out
-  __shared__ uint32_t taken[kPageKeepWarps][SPEC_MAX_PAGE / 32 + 1];
+  __shared__ PathMoves path;
+  __shared__ uint32_t taken_of[kPageKeepWarps][SPEC_MAX_PAGE / 32];
+  __shared__ float scales_of[kPageKeepWarps][BIG ? SPEC_MAX_NEW : 1];
+  extern __shared__ uint4 copies[];  // BIG: [warps][SPEC_MAX_NEW][D / 16]
   pdl_launch_next();
   pdl_wait();
   constexpr int kVecs = D / 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t list = (int64_t)blockIdx.x * kPageKeepWarps + warp;
-  if (list >= P.lists) return;
-  const bool is_v = list & 1;
-  list >>= 1;
-  const int head = list % P.heads;
-  list /= P.heads;
-  const int b = list % P.batch.B, layer = list / P.batch.B;
-
-  const int n = min(max(__ldg(P.n_keep + b), 0), P.max_keep);
-  const int ctx = batch_context(P.batch, b), page_size = 1 << P.cache.page_shift;
-  char* base = (is_v ? P.cache.v : P.cache.k) + layer * P.cache.layer + head * P.cache.head;
-  float* scale = (is_v ? P.scales.v : P.scales.k) + layer * P.scales.layer + head;
-  const int32_t* table = P.batch.pages + (int64_t)b * P.batch.max_pages;
-  bool any = false;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int i = i0 + lane;
-    int64_t src = -1, dst = -1;
+  const int b = blockIdx.y, shift = P.cache.page_shift, page_size = 1 << shift;
+  const int n = min(max(__ldg(P.n_keep + b), 0), P.max_keep), ctx = batch_context(P.batch, b);
+  if (threadIdx.x < SPEC_MAX_NEW) {
+    const int i = threadIdx.x;
+    int from = -1, to = -1;
+    int64_t src = 0, dst = 0;
     if (i < n) {
       const int p = __ldg(P.path + (int64_t)b * P.max_keep + i);
-      if (p != i && p >= 0 && p < P.batch.slots) {
-        dst = slot_offset(P.batch, P.cache, b, ctx + i);
-        src = slot_offset(P.batch, P.cache, b, ctx + p);
+      const int64_t t = slot_offset(P.batch, P.cache, b, ctx + i);
+      if (t >= 0) to = __ldg(P.batch.pages + (int64_t)b * P.batch.max_pages + ((ctx + i) >> shift)), dst = t;
+      if (t >= 0 && p != i && p >= 0 && p < P.batch.slots) {
+        const int64_t s = slot_offset(P.batch, P.cache, b, ctx + p);
+        if (s >= 0) from = __ldg(P.batch.pages + (int64_t)b * P.batch.max_pages + ((ctx + p) >> shift)), src = s;
       }
-      targets[warp][i] = src >= 0 && dst >= 0 ? ctx + i : -1;
-      if (src >= 0 && dst >= 0) scales[warp][i] = scale[(int64_t)__ldg(table + ((ctx + p) >> P.cache.page_shift)) * P.heads];
     }
-    const uint32_t moves = __ballot_sync(~0u, src >= 0 && dst >= 0);
-    any |= moves != 0;
-    for (int u = lane; u < 32 * kVecs; u += 32) {
-      const int64_t from = __shfl_sync(~0u, src, u / kVecs);  // the same u / kVecs for lanes of one entry
-      if ((moves >> (u / kVecs)) & 1) entries[warp][i0 * kVecs + u] = *reinterpret_cast<const uint4*>(base + from + (u % kVecs) * 16);
-    }
+    path.src[i] = src, path.dst[i] = dst, path.from[i] = from, path.to[i] = to;
   }
-  __syncwarp();
-  if (!any) return;
+  const bool any = __syncthreads_or(threadIdx.x < n && path.from[threadIdx.x] >= 0);
+  const int list = blockIdx.x * kPageKeepWarps + warp;
+  if (!any || list >= P.lists) return;
+  const bool is_v = list & 1;
+  const int head = (list >> 1) % P.heads, layer = (list >> 1) / P.heads;
+  const Side c = {(is_v ? P.cache.v : P.cache.k) + layer * P.cache.layer + head * P.cache.head,
+                  (is_v ? P.scales.v : P.scales.k) + layer * P.scales.layer + head, P.heads, P.cache.slot, P.cache.page, page_size};
   const int end = (int)min((int64_t)ctx + n, (int64_t)P.batch.slots);
-  for (int i = 0; i < n;) {  // a page at a time
-    const int ordinal = (ctx + i) >> P.cache.page_shift, first = i;
-    bool moves = false;
-    for (; i < n && (ctx + i) >> P.cache.page_shift == ordinal; ++i) moves |= targets[warp][i] >= 0;
-    if (!moves) continue;
-    const int page = __ldg(table + ordinal);  // in the pool: a move into it is not left out
-    const Target to = {base + page * P.cache.page, P.cache.slot, scale + (int64_t)page * P.heads,
-                       min(end - (ordinal << P.cache.page_shift), page_size)};
-    put_entries<D>(
-        to, i - first, taken[warp], page_size,
-        [&](int k, int vec, float& s) {
-          s = scales[warp][first + k];
-          return entries[warp][(first + k) * kVecs + vec];
-        },
-        [&](int k) {
-          const int t = targets[warp][first + k];
-          return t < 0 ? -1 : t & (page_size - 1);
-        });
+  const auto rows_of = [&](int ordinal) { return min(end - (ordinal << shift), page_size); };
+  if constexpr (!BIG) {
+    const int ordinal = (ctx + lane) >> shift;
+    Move m = {lane < n && path.from[lane] >= 0, path.src[lane], path.dst[lane], path.from[lane], lane < n ? path.to[lane] : -1,
+              lane, lane};
+    if (lane < n) m.lo = max((ordinal << shift) - ctx, 0), m.hi = min(((ordinal + 1) << shift) - ctx, n) - 1;
+    move_batch<D>(c, m, (ctx + lane) & (page_size - 1), rows_of(ordinal), taken_of[warp]);
+  } else {
+    uint4* mine = copies + warp * SPEC_MAX_NEW * kVecs;
+    for (int u = lane; u < n * kVecs; u += 32)
+      if (path.from[u / kVecs] >= 0) mine[u] = *reinterpret_cast<const uint4*>(c.base + path.src[u / kVecs] + u % kVecs * 16);
+    for (int i = lane; i < n; i += 32)
+      if (path.from[i] >= 0) scales_of[warp][i] = c.scales[(int64_t)path.from[i] * P.heads];
+    __syncwarp();
+    for (int i = 0; i < n;) {  // a page at a time
+      const int ordinal = (ctx + i) >> shift, first = i, to = path.to[i];
+      float most = 0.0f;
+      bool moves = false;
+      for (; i < n && (ctx + i) >> shift == ordinal; ++i) {
+        if (path.from[i] < 0) continue;
+        moves = true;
+        uint32_t top = 0;
+        if (lane < kVecs * 4) {
+          const uint32_t size = reinterpret_cast<const uint32_t*>(mine + i * kVecs)[lane] & 0x7F7F7F7Fu;
+          top = size & ~__vcmpeq4(size, 0x7F7F7F7Fu);
+        }
+        top = max(max(top & 0xFF, (top >> 8) & 0xFF), max((top >> 16) & 0xFF, top >> 24));
+        most = fmaxf(most, magnitude(__reduce_max_sync(~0u, top), scales_of[warp][i]));
+      }
+      if (!moves) continue;
+      float* place = c.scales + (int64_t)to * P.heads;
+      const NewScale s = new_scale(*place, most);
+      if (s.ratio != 1.0f) {
+        clear_taken(taken_of[warp], page_size);
+        for (int k = first + lane; k < i; k += 32) {
+          const int row = (ctx + k) & (page_size - 1);
+          if (path.from[k] >= 0) atomicOr(&taken_of[warp][row >> 5], 1u << (row & 31));
+        }
+        __syncwarp();
+        rescale_page<D>(c, to, rows_of(ordinal), taken_of[warp], s.ratio);
+      }
+      for (int u = first * kVecs + lane; u < i * kVecs; u += 32) {
+        const int k = u / kVecs;
+        if (path.from[k] < 0) continue;
+        const float from = scales_of[warp][k];
+        *reinterpret_cast<uint4*>(c.base + path.dst[k] + u % kVecs * 16) = from == s.scale ? mine[u] : recoded(mine[u], from, s.scale, 1.0f / s.scale);
+      }
+      __syncwarp();
+      if (lane == 0) *place = s.scale;
+      __syncwarp();
+    }
   }
 }
 
@@ -264,12 +398,15 @@ __device__ __forceinline__ void move_record(const MoveParams& P, const MoveList&
   if (P.record.position) P.record.position[dst] = P.record.position[src];
 }
 
-// Entries as they are.  A warp takes 32 moves: each lane works out one, then the warp copies their vectors.
+// Entries as they are.  A warp takes 32 moves: each lane works out one, then the warp copies their vectors, kAhead of
+// keys and of values in flight.
 __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const __grid_constant__ MoveParams P) {
+  constexpr int kAhead = 4;
   pdl_launch_next();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int mask = (1 << P.cache.page_shift) - 1;
+  const int at_once = 32 / P.vecs, vec = lane % P.vecs;  // entries that the warp takes in one go, 2 to 8
   for (int list = blockIdx.y; list < P.lists; list += gridDim.y) {
     const MoveList m(P, list);
     for (int i0 = (blockIdx.x * kMoveWarps + (threadIdx.x >> 5)) * 32; i0 < m.n; i0 += gridDim.x * kMoveWarps * 32) {
@@ -278,25 +415,36 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const __grid_cons
       const uint32_t all = __ballot_sync(~0u, is);
       const int64_t src = from * P.cache.page + (s & mask) * P.cache.slot, dst = to * P.cache.page + (t & mask) * P.cache.slot;
       if (is) move_record(P, m, s, t, from, to);
-      const int64_t base = m.layer * P.cache.layer + m.head * P.cache.head;
-      for (int u = lane; u < 32 * P.vecs; u += 32) {
-        const int64_t a = __shfl_sync(~0u, src, u / P.vecs), d = __shfl_sync(~0u, dst, u / P.vecs);
-        if (!((all >> (u / P.vecs)) & 1)) continue;
-        const int64_t at = base + (u % P.vecs) * 16;
-        const uint4 k = *reinterpret_cast<const uint4*>(P.cache.k + at + a), v = *reinterpret_cast<const uint4*>(P.cache.v + at + a);
-        *reinterpret_cast<uint4*>(P.cache.k + at + d) = k;
-        *reinterpret_cast<uint4*>(P.cache.v + at + d) = v;
+      const int64_t base = m.layer * P.cache.layer + m.head * P.cache.head + vec * 16;
+      for (int e0 = lane / P.vecs; e0 < 32; e0 += at_once * kAhead) {
+        uint4 k[kAhead], v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int e = e0 + j * at_once;
+          const int64_t a = base + __shfl_sync(~0u, src, e & 31);
+          if (e < 32 && ((all >> e) & 1))
+            k[j] = *reinterpret_cast<const uint4*>(P.cache.k + a), v[j] = *reinterpret_cast<const uint4*>(P.cache.v + a);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int e = e0 + j * at_once;
+          const int64_t d = base + __shfl_sync(~0u, dst, e & 31);
+          if (e < 32 && ((all >> e) & 1))
+            *reinterpret_cast<uint4*>(P.cache.k + d) = k[j], *reinterpret_cast<uint4*>(P.cache.v + d) = v[j];
+        }
       }
     }
   }
 }
 
-// Entries of a cache with page scales.  A warp takes the pages whose first move lies among its 32 moves (targets are in
-// ascending order), and all moves into them.  The page that the context ends in holds sources of other pages' moves, whose
-// scale is still needed: its own moves wait for a launch of their own.
+constexpr int kMoveStretch = 32;  // moves among which a warp's pages begin
+
+// Entries of a cache with page scales.  A warp takes the pages whose first move lies in its stretch of the list (targets
+// are in ascending order), as many at a time as have 32 moves together; a page with more goes by itself.  The page that the
+// context ends in holds sources of other pages' moves, whose scale is still needed: its own moves wait for a launch of their own.
 template <int D>
 __global__ void __launch_bounds__(kMoveWarps * 32) page_move_kernel(const __grid_constant__ MoveParams P) {
-  __shared__ uint32_t taken_of[kMoveWarps][SPEC_MAX_PAGE / 32 + 1];
+  __shared__ uint32_t taken_of[kMoveWarps][SPEC_MAX_PAGE / 32];
   pdl_launch_next();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -305,62 +453,82 @@ __global__ void __launch_bounds__(kMoveWarps * 32) page_move_kernel(const __grid
     const MoveList m(P, list);
     const bool is_v = blockIdx.y & 1;
     const int last = m.end & mask ? m.end >> shift : -1;  // the page that the context ends in
-    if (P.last && last < 0) continue;
-    int first = 0, stop = m.n;  // the first moves of the pages that this launch takes
-    // the first move into the last page
-    if (last >= 0) {
+    if (m.n == 0 || (P.last && last < 0)) continue;
+    int begin = 0, stop = m.n;  // the moves that this launch takes
+    if (last >= 0) {            // the first move into the last page
       int lo = 0, hi = m.n;
       while (lo < hi) {
-        const int mid = (lo + hi) / 2;
+        const int mid = lo + (hi - lo) / 2;
         if (m.target[mid] >> shift < last) lo = mid + 1;
         else hi = mid;
       }
-      if (P.last) first = lo;
+      if (P.last) begin = lo;
       else stop = lo;
     }
-    char* base = (is_v ? P.cache.v : P.cache.k) + m.layer * P.cache.layer + m.head * P.cache.head;
-    float* scales = (is_v ? P.scales.v : P.scales.k) + m.layer * P.scales.layer + m.head;
-    for (int i0 = first + (blockIdx.x * kMoveWarps + warp) * 32; i0 < stop; i0 += gridDim.x * kMoveWarps * 32) {
-      const int i = i0 + lane;
-      const int page = i < stop ? m.target[i] >> shift : -2;
-      int before = __shfl_up_sync(~0u, page, 1);
-      if (lane == 0) before = i0 > first ? m.target[i0 - 1] >> shift : -2;
-      uint32_t starts = __ballot_sync(~0u, i < stop && page != before);
-      while (starts) {
-        const int begin = __ffs(starts) - 1;
-        starts &= starts - 1;
-        const int ordinal = __shfl_sync(~0u, page, begin);
-        // its moves: up to the next start, or on beyond these 32
-        int n = (starts ? __ffs(starts) - 1 : min(32, stop - i0)) - begin;
-        if (!starts)
-          for (int j = i0 + begin + n; j < stop; j += 32) {
-            const bool same = j + lane < stop && m.target[j + lane] >> shift == ordinal;
-            const uint32_t all = __ballot_sync(~0u, same);
-            n += all == ~0u ? 32 : __ffs(~all) - 1;
-            if (all != ~0u) break;
+    const Side c = {(is_v ? P.cache.v : P.cache.k) + m.layer * P.cache.layer + m.head * P.cache.head,
+                    (is_v ? P.scales.v : P.scales.k) + m.layer * P.scales.layer + m.head, P.heads, P.cache.slot, P.cache.page, page_size};
+    const auto info = [&](int i) {
+      Move x = {false, 0, 0, 0, -1, lane, lane};
+      if (i >= stop) return x;
+      int s, t;
+      x.is = m.pages(P, i, s, t, x.from, x.to);
+      if (x.is) x.src = x.from * P.cache.page + (s & mask) * P.cache.slot, x.dst = x.to * P.cache.page + (t & mask) * P.cache.slot;
+      return x;
+    };
+    const auto record = [&](int i) {
+      int s, t, from, to;
+      if (!is_v && m.pages(P, i, s, t, from, to)) move_record(P, m, s, t, from, to);
+    };
+    for (int i0 = begin + (blockIdx.x * kMoveWarps + warp) * kMoveStretch; i0 < stop; i0 += gridDim.x * kMoveWarps * kMoveStretch) {
+      const int bound = min(i0 + kMoveStretch, stop);
+      int before = i0 > begin ? m.target[i0 - 1] >> shift : -1 << 30;  // the page of the move before
+      bool looking = true;  // for the first page that begins here
+      for (int i = i0; i < bound;) {
+        const int page = i + lane < stop ? m.target[i + lane] >> shift : 1 << 30, next = i + 32 < stop ? m.target[i + 32] >> shift : 1 << 30;
+        int previous = __shfl_up_sync(~0u, page, 1);
+        if (lane == 0) previous = before;
+        const uint32_t starts = __ballot_sync(~0u, page != previous);
+        if (looking && !(starts & 1)) {  // the stretch begins within a page that is another warp's
+          const int skip = starts ? __ffs(starts) - 1 : 32;
+          before = __shfl_sync(~0u, page, skip - 1);
+          i += skip;
+          continue;
+        }
+        looking = false;
+        // pages that begin before `bound` and end within these 32 moves
+        const int valid = min(32, stop - i);
+        const uint32_t behind = bound - i < 32 ? starts & (~0u << (bound - i)) : 0;
+        int n = behind ? __ffs(behind) - 1 : valid;
+        if (n == 32 && next == __shfl_sync(~0u, page, 31)) n = 31 - __clz(starts);  // the last one goes on
+        if (n > 0) {
+          Move x = info(lane < n ? i + lane : stop);
+          const uint32_t mine = starts & (lane == 31 ? ~0u : (2u << lane) - 1), after = lane == 31 ? 0u : starts & (~0u << (lane + 1));
+          if (lane < n) {
+            x.lo = 31 - __clz(mine | 1), x.hi = min(after ? __ffs(after) - 2 : 31, n - 1);
+            if (page >= 0 && page << shift < m.end) x.to = m.page_of(P, page << shift);  // also where this move is left out
+            record(i + lane);
           }
-        const int at = i0 + begin;
-        if (ordinal < 0 || ordinal << shift >= m.end) continue;
-        const int into = m.page_of(P, ordinal << shift);
-        if (into < 0) continue;
-        const Target to = {base + into * P.cache.page, P.cache.slot, scales + (int64_t)into * P.heads,
-                           min(m.end - (ordinal << shift), page_size)};
-        put_entries<D>(
-            to, n, taken_of[warp], page_size,
-            [&](int k, int vec, float& scale) {
-              const int s = m.source[at + k], p = m.page_of(P, s);
-              scale = scales[(int64_t)p * P.heads];
-              return *reinterpret_cast<const uint4*>(base + p * P.cache.page + (s & mask) * P.cache.slot + vec * 16);
-            },
-            [&](int k) {
-              int s, t, from, page;
-              return m.pages(P, at + k, s, t, from, page) ? t & mask : -1;
-            });
-        if (!is_v)
-          for (int k = lane; k < n; k += 32) {
-            int s, t, from, page;
-            if (m.pages(P, at + k, s, t, from, page)) move_record(P, m, s, t, from, page);
+          move_batch<D>(c, x, lane < n ? m.target[i + lane] & mask : 0, lane < n ? min(m.end - (page << shift), page_size) : 0,
+                        taken_of[warp]);
+        } else {  // a page of more than 32 moves
+          const int ordinal = __shfl_sync(~0u, page, 0);
+          for (n = 32; i + n < stop;) {
+            const uint32_t same = __ballot_sync(~0u, i + n + lane < stop && m.target[i + n + lane] >> shift == ordinal);
+            n += same == ~0u ? 32 : __ffs(~same) - 1;
+            if (same != ~0u) break;
           }
+          if (ordinal >= 0 && ordinal << shift < m.end) {
+            const int into = m.page_of(P, ordinal << shift);
+            if (into >= 0)
+              move_page<D>(
+                  c, n, into, min(m.end - (ordinal << shift), page_size), taken_of[warp],
+                  [&](int k) { return info(k < n ? i + k : stop); },
+                  [&](const Move& x) { return (int)((x.dst - into * P.cache.page) / P.cache.slot); });
+            for (int k = lane; k < n; k += 32) record(i + k);
+          }
+        }
+        before = __shfl_sync(~0u, page, min(n, 32) - 1);
+        i += n;
       }
     }
   }
@@ -383,7 +551,7 @@ spec_status_t spec_kv_keep_ex(const spec_kv_cache_t* cache, const spec_kv_page_s
   if (max_keep < 0) return SPEC_ERR_INVALID_ARG;
   if (scales && max_keep > SPEC_MAX_NEW) return SPEC_ERR_UNSUPPORTED;
   const int64_t lists = (int64_t)cache->layers * batch->B * cache->heads;
-  if (lists > 0x3fffffffll || batch->B > SPEC_MAX_BATCH) return SPEC_ERR_UNSUPPORTED;
+  if ((int64_t)cache->layers * cache->heads > 0x3fffffffll || lists > 0x3fffffffll || batch->B > SPEC_MAX_BATCH) return SPEC_ERR_UNSUPPORTED;
   if (batch->B == 0 || max_keep == 0) return SPEC_OK;
   if (!path || !n_keep) return SPEC_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -391,10 +559,23 @@ spec_status_t spec_kv_keep_ex(const spec_kv_cache_t* cache, const spec_kv_page_s
     s = spec_kv_keep(cache, batch, path, n_keep, max_keep, stream);
     if (s != SPEC_OK) return s;
   } else {
-    const PageKeepParams P = {cache_of(cache), scales_of(scales), batch_of(batch, cache), path, n_keep, max_keep, cache->heads, lists * 2};
-    const dim3 grid((unsigned)((lists * 2 + kPageKeepWarps - 1) / kPageKeepWarps));
-    auto kern = cache->head_dim == 128 ? page_keep_kernel<128> : page_keep_kernel<64>;
-    if (launch_early(kern, grid, dim3(kPageKeepWarps * 32), 0, st, P) != cudaSuccess) return SPEC_ERR_CUDA;
+    const int D = cache->head_dim, sides = cache->layers * cache->heads * 2;
+    const PageKeepParams P = {cache_of(cache), scales_of(scales), batch_of(batch, cache), path, n_keep, max_keep, cache->heads, sides};
+    const dim3 grid((unsigned)((sides + kPageKeepWarps - 1) / kPageKeepWarps), batch->B), block(kPageKeepWarps * 32);
+    const bool big = max_keep > 32;
+    const size_t smem = big ? (size_t)kPageKeepWarps * SPEC_MAX_NEW * D : 0;
+    auto kern = big ? (D == 128 ? page_keep_kernel<128, true> : page_keep_kernel<64, true>)
+                    : (D == 128 ? page_keep_kernel<128, false> : page_keep_kernel<64, false>);
+    if (big && D == 128) {  // 64 KB
+      int dev = 0, sms = 0;
+      if (device_sms(&dev, &sms) != cudaSuccess) return SPEC_ERR_CUDA;
+      static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory is set
+      if (!((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SPEC_ERR_CUDA;
+        ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+      }
+    }
+    if (launch_early(kern, grid, block, smem, st, P) != cudaSuccess) return SPEC_ERR_CUDA;
   }
   if (record && (record->weight || record->position)) {
     const RecordKeepParams R = {cache_of(cache), record_of(record), batch_of(batch, cache), path, n_keep, max_keep, cache->heads, lists};
@@ -429,7 +610,7 @@ spec_status_t spec_kv_move(const spec_kv_cache_t* cache, const spec_kv_page_scal
   const unsigned y = (unsigned)(rows < 65534 ? rows : 65534);
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != cudaSuccess) return SPEC_ERR_CUDA;
-  int64_t x = (8 * sms + y - 1) / y;
+  int64_t x = (32 * (int64_t)sms + y - 1) / y;
   if (x > most) x = most;
   if (!scales) return launch_early(move_kernel, dim3((unsigned)x, y), block, 0, st, P) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
   auto kern = cache->head_dim == 128 ? page_move_kernel<128> : page_move_kernel<64>;
