@@ -127,8 +127,28 @@ __device__ __forceinline__ float scale_need(float most) {
   return __int_as_float((min(max(power, -24), 24) + 127) << 23);
 }
 
-// 16 codes at another scale: each times `ratio` and rounded.
+// 16 codes at another scale: each times `ratio`, a power of two in 2^-24 .. 2^15, and rounded.  In fp16 a code and its
+// product are exact down to 2^-14, and what is below 2^-10 is 0 whatever its last bits.
+__device__ __forceinline__ uint4 rescaled_half(uint4 w, float ratio) {
+  const __half2 r = __float2half2_rn(ratio);
+  uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t lo, hi;
+    e4m3_to_half(x[i], lo, hi);
+    const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&lo), r), b = __hmul2(*reinterpret_cast<const __half2*>(&hi), r);
+    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\tmov.b32 %0, {a, b};\n\t}"
+        : "=r"(x[i])
+        : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
+  }
+  return w;
+}
+__device__ __forceinline__ bool half_ratio(float ratio) {  // whether rescaled_half does it
+  return (__float_as_int(ratio) & 0x7FFFFF) == 0 && ratio >= 0x1p-24f && ratio <= 0x1p15f;
+}
+// The same for any ratio.
 __device__ __forceinline__ uint4 rescaled(uint4 w, float ratio) {
+  if (half_ratio(ratio)) return rescaled_half(w, ratio);
   uint32_t* x = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -77,8 +77,9 @@ __device__ __forceinline__ int64_t lse_place(int b, int T, int t, int heads, int
 // ------------------------------------------------------------------------------------------------
 // shared memory
 // ------------------------------------------------------------------------------------------------
-template <int D, bool F8, int NT>
+template <int D, int KIND, int NT>
 struct Shape {
+  static constexpr bool F8 = KIND != kBf16;
   static constexpr int kHalves = D / 64;                          // 128-byte columns of a 16-bit row
   static constexpr int kTile16 = kTileSlots * D * 2;              // a K or V tile in 16 bits
   static constexpr int kRing = kTileSlots * D * (F8 ? 1 : 2);     // a ring slot: a tile as the cache holds it
@@ -161,9 +162,9 @@ __device__ __forceinline__ float fold_lanes(float (&x)[N], int lane, Op op) {
 // the stream over the cache
 // ------------------------------------------------------------------------------------------------
 template <int D, int KIND, int NT>
-__global__ void __launch_bounds__(Shape<D, KIND != kBf16, NT>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams P) {
   constexpr bool F8 = KIND != kBf16, PAGES = KIND == kE4m3Pages;
-  using S = Shape<D, F8, NT>;
+  using S = Shape<D, KIND, NT>;
   extern __shared__ char raw_smem[];
   char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
   char* q_buf = smem;                                     // [kQBufs][halves][NT][128 B]
@@ -961,7 +962,7 @@ static AttnLayout attn_layout(int rows, int D) {
 template <int D, int KIND, int NT>
 static cudaError_t launch_attention(const AttnParams& P, int dev, int ctas, cudaStream_t st) {
   constexpr bool F8 = KIND != kBf16;
-  using S = Shape<D, F8, NT>;
+  using S = Shape<D, KIND, NT>;
   auto kern = attn_kernel<D, KIND, NT>;
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory is set
   cudaError_t e = cudaSuccess;

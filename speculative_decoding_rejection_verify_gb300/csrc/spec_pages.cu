@@ -8,10 +8,12 @@
 
 namespace sv {
 
-// The values of 16 codes at scale `from`, as codes at scale `to`.
-__device__ __forceinline__ uint4 recoded(uint4 w, float from, float to, float inverse) {
+// The values of 16 codes at scale `from`, as codes at scale `to` (by way of fp16 where both are powers of two).
+__device__ __forceinline__ uint4 recoded(uint4 w, float from, float to) {
+  const float inverse = 1.0f / to, ratio = from * inverse;
+  if (((__float_as_int(from) | __float_as_int(to)) & 0x7FFFFF) == 0 && half_ratio(ratio)) return rescaled_half(w, ratio);
   uint32_t* x = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < 4; ++i) {
     const float4 f = unpack_e4m3(x[i]);
     x[i] = pack_e4m3(signed_quotient(f.x * from, to, inverse), signed_quotient(f.y * from, to, inverse),
@@ -38,57 +40,74 @@ struct Side {
   int page_size;
 };
 
-// The entries' codes: lane l has vector l % (D / 16) of entries j * 32 / (D / 16) + l / (D / 16).
+// The entries' codes: lane l has vector l % (D / 16) of entries j * 32 / (D / 16) + l / (D / 16).  n: the moves are lanes 0 .. n - 1.
 template <int D>
-__device__ __forceinline__ void load_entries(const Side& c, const Move& m, uint4 (&w)[D / 16]) {
+__device__ __forceinline__ void load_entries(const Side& c, const Move& m, int n, uint4 (&w)[D / 16]) {
   constexpr int kVecs = D / 16, kAtOnce = 32 / kVecs;
   const int lane = threadIdx.x & 31;
   const uint32_t all = __ballot_sync(~0u, m.is);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
+    w[j] = make_uint4(0, 0, 0, 0);
+    if (j * kAtOnce >= n) continue;
     const int e = j * kAtOnce + lane / kVecs;
     const int64_t at = __shfl_sync(~0u, m.src, e);
-    w[j] = (all >> e) & 1 ? *reinterpret_cast<const uint4*>(c.base + at + lane % kVecs * 16) : make_uint4(0, 0, 0, 0);
+    if ((all >> e) & 1) w[j] = *reinterpret_cast<const uint4*>(c.base + at + lane % kVecs * 16);
   }
 }
-// The largest code of this lane's entry, without its sign: a larger one is a larger magnitude.  0x7F, NaN, does not count.
+// Bytes 1 and 3 of the largest codes among a vector's, without their signs: a larger one is a larger magnitude.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t largest_of(const uint4& w) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) top = max_u16x2(top, max_u16x2(x[k] & 0x7F007F00u, (x[k] << 8) & 0x7F007F00u));
+  return top;
+}
+__device__ __forceinline__ uint4 without_nan(uint4 w) {
+  uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] &= ~__vcmpeq4(x[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  return w;
+}
+// The largest code of this lane's entry that is not NaN (0x7F), without its sign.
 template <int D>
-__device__ __forceinline__ uint32_t largest_code(const uint4 (&w)[D / 16]) {
+__device__ __forceinline__ uint32_t largest_code(const uint4 (&w)[D / 16], int n) {
   constexpr int kVecs = D / 16, kAtOnce = 32 / kVecs;
   const int lane = threadIdx.x & 31;
   uint32_t mine = 0;
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
-    const uint32_t* x = reinterpret_cast<const uint32_t*>(&w[j]);
-    uint32_t top = 0;
+    if (j * kAtOnce >= n) continue;
+    uint32_t top = largest_of(w[j]);
+    if (__any_sync(~0u, top >= 0x7F000000u || (top & 0xFFFF) >= 0x7F00u)) top = largest_of(without_nan(w[j]));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t size = x[k] & 0x7F7F7F7Fu;
-      top = __vmaxu4(top, size & ~__vcmpeq4(size, 0x7F7F7F7Fu));
-    }
-#pragma unroll
-    for (int d = 1; d < kVecs; d *= 2) top = __vmaxu4(top, __shfl_xor_sync(~0u, top, d));
+    for (int d = 1; d < kVecs; d *= 2) top = max_u16x2(top, __shfl_xor_sync(~0u, top, d));
     const uint32_t of_entry = __shfl_sync(~0u, top, lane % kAtOnce * kVecs);
     if (lane / kAtOnce == j) mine = of_entry;
   }
-  return max(max(mine & 0xFF, (mine >> 8) & 0xFF), max((mine >> 16) & 0xFF, mine >> 24));
+  return max(mine >> 24, (mine >> 8) & 0xFF);
 }
 __device__ __forceinline__ float magnitude(uint32_t code, float scale) {  // a finite one, or 0
   const float x = unpack_e4m3(code).x * fabsf(scale);
   return x < INFINITY ? x : 0.0f;
 }
 template <int D>
-__device__ __forceinline__ void store_entries(const Side& c, const Move& m, const uint4 (&w)[D / 16], float from, float to) {
+__device__ __forceinline__ void store_entries(const Side& c, const Move& m, int n, const uint4 (&w)[D / 16], float from, float to) {
   constexpr int kVecs = D / 16, kAtOnce = 32 / kVecs;
   const int lane = threadIdx.x & 31;
   const uint32_t all = __ballot_sync(~0u, m.is);
-  const float inverse = 1.0f / to;
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
+    if (j * kAtOnce >= n) continue;
     const int e = j * kAtOnce + lane / kVecs;
     const int64_t at = __shfl_sync(~0u, m.dst, e);
-    const float f = __shfl_sync(~0u, from, e), t = __shfl_sync(~0u, to, e), i = __shfl_sync(~0u, inverse, e);
-    if ((all >> e) & 1) *reinterpret_cast<uint4*>(c.base + at + lane % kVecs * 16) = f == t ? w[j] : recoded(w[j], f, t, i);
+    const float f = __shfl_sync(~0u, from, e), t = __shfl_sync(~0u, to, e);
+    if ((all >> e) & 1) *reinterpret_cast<uint4*>(c.base + at + lane % kVecs * 16) = f == t ? w[j] : recoded(w[j], f, t);
   }
 }
 // The page's scale with `most` in it, and what its codes have to be multiplied by.
@@ -116,15 +135,15 @@ __device__ __forceinline__ void clear_taken(uint32_t* taken, int page_size) {
   __syncwarp();
 }
 
-// A warp's moves, whole pages' of them, at most 32: every entry is in registers before the first is written.  row: the
+// A warp's n moves, whole pages' of them, at most 32: every entry is in registers before the first is written.  row: the
 // target's row in its page; end: the rows of that page that hold what stays.
 template <int D>
-__device__ void move_batch(const Side& c, const Move& m, int row, int end, uint32_t* taken) {
+__device__ __forceinline__ void move_batch(const Side& c, const Move& m, int n, int row, int end, uint32_t* taken) {
   const int lane = threadIdx.x & 31;
   uint4 w[D / 16];
-  load_entries<D>(c, m, w);
+  load_entries<D>(c, m, n, w);
   const float from = m.is ? c.scales[(int64_t)m.from * c.heads] : 1.0f, old = m.to >= 0 ? c.scales[(int64_t)m.to * c.heads] : 1.0f;
-  float most = magnitude(largest_code<D>(w), m.is ? from : 0.0f);
+  float most = magnitude(largest_code<D>(w, n), m.is ? from : 0.0f);
   bool any = m.is;  // of the lane's page
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
@@ -145,7 +164,7 @@ __device__ void move_batch(const Side& c, const Move& m, int row, int end, uint3
     rescale_page<D>(c, __shfl_sync(~0u, m.to, leader), __shfl_sync(~0u, end, leader), taken, __shfl_sync(~0u, s.ratio, leader));
     __syncwarp();
   }
-  store_entries<D>(c, m, w, from, s.scale);
+  store_entries<D>(c, m, n, w, from, s.scale);
   __syncwarp();  // an entry may come from a page that others go to: its old scale was needed until here
   if (any && lane == m.lo) c.scales[(int64_t)m.to * c.heads] = s.scale;
   __syncwarp();
@@ -153,15 +172,15 @@ __device__ void move_batch(const Side& c, const Move& m, int row, int end, uint3
 
 // A warp's n moves into one page: info(i) is lane's move i (is = false behind the last), row(move) its row.
 template <int D, typename Info, typename Row>
-__device__ void move_page(const Side& c, int n, int to, int end, uint32_t* taken, Info info, Row row) {
+__device__ __noinline__ void move_page(const Side& c, int n, int to, int end, uint32_t* taken, Info info, Row row) {
   const int lane = threadIdx.x & 31;
   float most = 0.0f;
   bool any = false;
   for (int i0 = 0; i0 < n; i0 += 32) {
     const Move m = info(i0 + lane);
     uint4 w[D / 16];
-    load_entries<D>(c, m, w);
-    const uint32_t top = largest_code<D>(w);
+    load_entries<D>(c, m, n - i0, w);
+    const uint32_t top = largest_code<D>(w, n - i0);
     if (m.is) most = fmaxf(most, magnitude(top, c.scales[(int64_t)m.from * c.heads])), any = true;
   }
 #pragma unroll
@@ -181,8 +200,8 @@ __device__ void move_page(const Side& c, int n, int to, int end, uint32_t* taken
   for (int i0 = 0; i0 < n; i0 += 32) {
     const Move m = info(i0 + lane);
     uint4 w[D / 16];
-    load_entries<D>(c, m, w);
-    store_entries<D>(c, m, w, m.is ? c.scales[(int64_t)m.from * c.heads] : 1.0f, s.scale);
+    load_entries<D>(c, m, n - i0, w);
+    store_entries<D>(c, m, n - i0, w, m.is ? c.scales[(int64_t)m.from * c.heads] : 1.0f, s.scale);
   }
   __syncwarp();  // an entry may come from the same page: its old scale was needed until here
   if (lane == 0) *place = s.scale;
@@ -241,8 +260,8 @@ __global__ void __launch_bounds__(kPageKeepWarps * 32) page_keep_kernel(const __
     path.src[i] = src, path.dst[i] = dst, path.from[i] = from, path.to[i] = to;
   }
   const bool any = __syncthreads_or(threadIdx.x < n && path.from[threadIdx.x] >= 0);
-  const int list = blockIdx.x * kPageKeepWarps + warp;
-  if (!any || list >= P.lists) return;
+  if (!any) return;
+  for (int list = blockIdx.x * kPageKeepWarps + warp; list < P.lists; list += gridDim.x * kPageKeepWarps) {
   const bool is_v = list & 1;
   const int head = (list >> 1) % P.heads, layer = (list >> 1) / P.heads;
   const Side c = {(is_v ? P.cache.v : P.cache.k) + layer * P.cache.layer + head * P.cache.head,
@@ -254,7 +273,7 @@ __global__ void __launch_bounds__(kPageKeepWarps * 32) page_keep_kernel(const __
     Move m = {lane < n && path.from[lane] >= 0, path.src[lane], path.dst[lane], path.from[lane], lane < n ? path.to[lane] : -1,
               lane, lane};
     if (lane < n) m.lo = max((ordinal << shift) - ctx, 0), m.hi = min(((ordinal + 1) << shift) - ctx, n) - 1;
-    move_batch<D>(c, m, (ctx + lane) & (page_size - 1), rows_of(ordinal), taken_of[warp]);
+    move_batch<D>(c, m, n, (ctx + lane) & (page_size - 1), rows_of(ordinal), taken_of[warp]);
   } else {
     uint4* mine = copies + warp * SPEC_MAX_NEW * kVecs;
     for (int u = lane; u < n * kVecs; u += 32)
@@ -293,12 +312,13 @@ __global__ void __launch_bounds__(kPageKeepWarps * 32) page_keep_kernel(const __
         const int k = u / kVecs;
         if (path.from[k] < 0) continue;
         const float from = scales_of[warp][k];
-        *reinterpret_cast<uint4*>(c.base + path.dst[k] + u % kVecs * 16) = from == s.scale ? mine[u] : recoded(mine[u], from, s.scale, 1.0f / s.scale);
+        *reinterpret_cast<uint4*>(c.base + path.dst[k] + u % kVecs * 16) = from == s.scale ? mine[u] : recoded(mine[u], from, s.scale);
       }
       __syncwarp();
       if (lane == 0) *place = s.scale;
       __syncwarp();
     }
+  }
   }
 }
 
@@ -455,15 +475,15 @@ __global__ void __launch_bounds__(kMoveWarps * 32) page_move_kernel(const __grid
     const int last = m.end & mask ? m.end >> shift : -1;  // the page that the context ends in
     if (m.n == 0 || (P.last && last < 0)) continue;
     int begin = 0, stop = m.n;  // the moves that this launch takes
-    if (last >= 0) {            // the first move into the last page
-      int lo = 0, hi = m.n;
-      while (lo < hi) {
-        const int mid = lo + (hi - lo) / 2;
-        if (m.target[mid] >> shift < last) lo = mid + 1;
-        else hi = mid;
+    if (last >= 0) {            // the first move into the last page, among as many as the page has slots before the end
+      int first = m.n;
+      for (int i = m.n - 1 - lane; first > m.n - (m.end & mask); i -= 32) {
+        const uint32_t in = __ballot_sync(~0u, i >= 0 && m.target[max(i, 0)] >> shift >= last);
+        first -= in == ~0u ? 32 : __ffs(~in) - 1;
+        if (in != ~0u) break;
       }
-      if (P.last) begin = lo;
-      else stop = lo;
+      if (P.last) begin = first;
+      else stop = first;
     }
     const Side c = {(is_v ? P.cache.v : P.cache.k) + m.layer * P.cache.layer + m.head * P.cache.head,
                     (is_v ? P.scales.v : P.scales.k) + m.layer * P.scales.layer + m.head, P.heads, P.cache.slot, P.cache.page, page_size};
@@ -508,7 +528,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) page_move_kernel(const __grid
             if (page >= 0 && page << shift < m.end) x.to = m.page_of(P, page << shift);  // also where this move is left out
             record(i + lane);
           }
-          move_batch<D>(c, x, lane < n ? m.target[i + lane] & mask : 0, lane < n ? min(m.end - (page << shift), page_size) : 0,
+          move_batch<D>(c, x, n, lane < n ? m.target[i + lane] & mask : 0, lane < n ? min(m.end - (page << shift), page_size) : 0,
                         taken_of[warp]);
         } else {  // a page of more than 32 moves
           const int ordinal = __shfl_sync(~0u, page, 0);
@@ -561,7 +581,8 @@ spec_status_t spec_kv_keep_ex(const spec_kv_cache_t* cache, const spec_kv_page_s
   } else {
     const int D = cache->head_dim, sides = cache->layers * cache->heads * 2;
     const PageKeepParams P = {cache_of(cache), scales_of(scales), batch_of(batch, cache), path, n_keep, max_keep, cache->heads, sides};
-    const dim3 grid((unsigned)((sides + kPageKeepWarps - 1) / kPageKeepWarps), batch->B), block(kPageKeepWarps * 32);
+    const int64_t most = (sides + kPageKeepWarps - 1) / kPageKeepWarps, rounds = (most * batch->B + 1023) / 1024;
+    const dim3 grid((unsigned)((most + rounds - 1) / rounds), batch->B), block(kPageKeepWarps * 32);
     const bool big = max_keep > 32;
     const size_t smem = big ? (size_t)kPageKeepWarps * SPEC_MAX_NEW * D : 0;
     auto kern = big ? (D == 128 ? page_keep_kernel<128, true> : page_keep_kernel<64, true>)

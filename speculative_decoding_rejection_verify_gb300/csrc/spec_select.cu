@@ -33,6 +33,7 @@ struct SelectParams {
 constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
+constexpr uint32_t kNoKey = 0x007FFFFFu;  // of -infinity
 
 struct SelectState {
   int bins[kBins];
@@ -64,20 +65,20 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
   const int mask = (1 << P.page_shift) - 1;
   const int64_t base = layer * P.record.layer;
   // A larger key is a larger weight; +0 and -0 are one.
-  const auto key_of = [&](int slot) -> uint32_t {
-    const int page = __ldg(table + (slot >> P.page_shift));
-    float w = -INFINITY;
-    if (page >= 0 && page < P.num_pages) {
-      const int64_t at = base + (((int64_t)page * P.heads + head) << P.page_shift) + (slot & mask);
-      w = P.record.weight[at] + 0.0f;
-      if (w != w) w = -INFINITY;
-      if (P.record.position) {
-        const int position = P.record.position[at];
-        if (position < P.first || position >= recent) w = INFINITY;
-      }
-    }
+  const auto key = [&](float w, int position) -> uint32_t {
+    w += 0.0f;
+    if (w != w) w = -INFINITY;
+    if (P.record.position && (position < P.first || position >= recent)) w = INFINITY;
     const uint32_t bits = __float_as_uint(w);
     return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
+  };
+  const auto place_of = [&](int slot) -> int64_t {  // -1: in a page outside the pool
+    const int page = __ldg(table + (slot >> P.page_shift));
+    return page < 0 || page >= P.num_pages ? -1 : base + (((int64_t)page * P.heads + head) << P.page_shift) + (slot & mask);
+  };
+  const auto key_of = [&](int slot) {
+    const int64_t at = place_of(slot);
+    return at < 0 ? kNoKey : key(P.record.weight[at], P.record.position ? P.record.position[at] : 0);
   };
   // this block's slots, whole words of 32 of them, and this warp's
   const int words = (ctx + 31) / 32, share = (words + blocks - 1) / blocks;
@@ -87,18 +88,29 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
 
   for (int i = threadIdx.x; i < kBins; i += kSelectThreads) st.bins[i] = 0;
   __syncthreads();
-  // the keys, with the first digit's histogram
-  constexpr int kAhead = 4;
+  // the keys, with the first digit's histogram: kAhead in flight a thread
+  constexpr int kAhead = 8;
   for (int i0 = threadIdx.x; i0 < n; i0 += kSelectThreads * kAhead) {
-    uint32_t key[kAhead];
+    float weight[kAhead];
+    int position[kAhead];
+    uint32_t in = 0;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) key[k] = i0 + k * kSelectThreads < n ? key_of(slot0 + i0 + k * kSelectThreads) : 0;
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * kSelectThreads;
+      weight[k] = -INFINITY, position[k] = P.first;
+      const int64_t at = i < n ? place_of(slot0 + i) : -1;
+      if (at >= 0) {
+        weight[k] = P.record.weight[at], in |= 1u << k;
+        if (P.record.position) position[k] = P.record.position[at];
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       const int i = i0 + k * kSelectThreads;
       if (i >= n) break;
-      if (i < P.held) keys[i] = key[k];
-      atomicAdd(&st.bins[key[k] >> 21], 1);
+      const uint32_t x = (in >> k) & 1 ? key(weight[k], position[k]) : kNoKey;
+      if (i < P.held) keys[i] = x;
+      atomicAdd(&st.bins[x >> 21], 1);
     }
   }
   uint32_t prefix = 0;
@@ -224,11 +236,11 @@ extern "C" spec_status_t spec_kv_select(const spec_kv_record_t* record, const sp
 
   constexpr int kMostHeld = 24576;  // 96 KB: two blocks an SM
   int blocks = 1;
-  while (blocks < kMaxCluster && slots > 4096 * blocks) blocks *= 2;
-  const int64_t stretch = ((slots + 31) / 32 + blocks - 1) / blocks * 32;
-  P.held = (int)(stretch < kMostHeld ? stretch : kMostHeld);
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != cudaSuccess) return SPEC_ERR_CUDA;
+  while (blocks < kMaxCluster && slots > 4096 * blocks && (lists * blocks < 4 * sms || slots > (int64_t)kMostHeld * blocks)) blocks *= 2;
+  const int64_t stretch = ((slots + 31) / 32 + blocks - 1) / blocks * 32;
+  P.held = (int)(stretch < kMostHeld ? stretch : kMostHeld);
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory is set
   if (!((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
     if (cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld * 4) != cudaSuccess) return SPEC_ERR_CUDA;

@@ -44,9 +44,8 @@ struct WeighShape {
   static constexpr int kFit = (kBudget - 2 * kQ) / kRing;
   static constexpr int kSlots = kFit > 12 ? 12 : kFit;  // keys' tiles in flight
   static_assert(kSlots >= 3, "the ring holds three tiles at least");
-  static constexpr int kBuffers = NT <= 64 ? 4 : 2;     // of scores
-  static constexpr int kColumns = NT * kBuffers < 32 ? 32 : NT * kBuffers;
-  static constexpr int kGroups = 2;                     // warpgroups that add up, each every other tile
+  static constexpr int kGroups = 4;                     // warpgroups that add up, each every kGroups-th tile of an item,
+  static constexpr int kColumns = NT * kGroups;         // with a buffer of scores of its own
   static constexpr int kAddWarps = 4 * kGroups, kProducer = kAddWarps, kIssuer = kAddWarps + 1;
   static constexpr int kPrepare = kIssuer + 1, kPrepareWarps = 2;
   static constexpr int kThreads = (kAddWarps + 2 + kPrepareWarps) * 32;
@@ -63,9 +62,9 @@ struct WeighShape {
     int copies, queries;                          // tiles and Qs whose copies were issued
     int start_b, start_offset;
     int warp_sum[kThreads / 32];
-    int plain[2];                                 // every row of the pass has a finite sum
+    int plain[2][kPrepareWarps];                  // every row that a warp looked at has a finite sum
     alignas(16) float shift[2][NT];               // -lse in log2 units; -inf: the row has no part
-    alignas(16) float mult[2][NT];                // a score's factor to log2 units
+    alignas(16) float mult[2][F8 ? NT : 4];       // E4M3: a score's factor to log2 units
     uint64_t rule[2][SPEC_MAX_NEW];               // which new tokens the pass's tokens attend to
     int token[NT];                                // of a row, within the pass
   };
@@ -99,7 +98,7 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
       mbar_init(smem_addr(&st->rows_full[i]), S::kPrepareWarps);
       mbar_init(smem_addr(&st->rows_empty[i]), S::kAddWarps);
     }
-    for (int i = 0; i < S::kBuffers; ++i) {
+    for (int i = 0; i < S::kGroups; ++i) {
       mbar_init(smem_addr(&st->s_full[i]), 1);
       mbar_init(smem_addr(&st->s_empty[i]), 4);
     }
@@ -122,6 +121,8 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
   Segment s;
   // Every role goes through the same passes: of each segment, as many as its tokens need.
   const auto passes_of = [&](const Segment& s) { return (s.tokens + P.tokens - 1) / P.tokens; };
+  // The warpgroup that has a tile: the same in every pass, another for another head, as short items have but one.
+  const auto owner = [](const Segment& s, int tile) { return (tile + s.head + s.b) & (S::kGroups - 1); };
 
   if (warp == S::kProducer) {
     // ---- TMA: Q of every pass and K of every tile, page by page ----
@@ -198,16 +199,18 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
     const uint64_t q_desc = matrix_desc(base, 16, 1024);
     const uint64_t k_desc = F8 ? matrix_desc<D>(base + 2 * S::kQ, 16, 8 * D) : matrix_desc(base + 2 * S::kQ, 16, 1024);
     const auto ahead = [](int bytes) { return (uint64_t)(bytes >> 4); };
-    int slot = 0, nth = 0, buffer = 0;
-    uint32_t phase = 0, s_phase = 0;
+    int slot = 0, nth = 0;
+    uint32_t phase = 0, s_phase = 0;  // s_phase: a bit for each buffer
     bool ok = true;
     while (ok && uniform(walk.next(s))) {
-      const int tiles = uniform(s.tile1 - s.tile0), passes = uniform(passes_of(s));
+      const int tiles = uniform(s.tile1 - s.tile0), passes = uniform(passes_of(s)), first = uniform(owner(s, s.tile0));
       for (int pass = 0; ok && pass < passes; ++pass, ++nth) {
         const int qb = nth & 1;
         ok = mbar_wait_warp(bar_of(F8 ? &st->q_full[qb] : &st->q_loaded[qb]), (nth >> 1) & 1, dead);
         for (int tile = 0; ok && tile < tiles; ++tile) {
-          ok = mbar_wait_warp(bar_of(&st->ring_full[slot]), phase, dead) && mbar_wait_warp(bar_of(&st->s_empty[buffer]), s_phase ^ 1, dead);
+          const int buffer = (first + tile) & (S::kGroups - 1);
+          ok = mbar_wait_warp(bar_of(&st->ring_full[slot]), phase, dead) &&
+               mbar_wait_warp(bar_of(&st->s_empty[buffer]), ((s_phase >> buffer) & 1) ^ 1, dead);
           if (!ok) break;
           tc_fence_after();
           const uint64_t a = k_desc + ahead(slot * S::kRing), b = q_desc + ahead(qb * S::kQ);
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
           tc_commit(bar_of(&st->s_full[buffer]));
           tc_commit(bar_of(&st->ring_empty[slot]));
           if (++slot == S::kSlots) slot = 0, phase ^= 1;
-          if (++buffer == S::kBuffers) buffer = 0, s_phase ^= 1;
+          s_phase ^= 1u << buffer;
         }
         if (ok) tc_commit(bar_of(&st->q_empty[qb]));
       }
@@ -242,24 +245,24 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
         const int qb = nth & 1, t0 = pass * P.tokens, rows = min(s.tokens - t0, P.tokens) * P.group;
         ok = mbar_wait_warp(smem_addr(&st->rows_empty[qb]), ((nth >> 1) & 1) ^ 1, dead);
         if (!ok) break;
-        if (tid == 0) st->plain[qb] = 1;
-        asm volatile("bar.sync 1, %0;" ::"n"(kCount) : "memory");
-        const float c = P.scale_log2 * (F8 && !PAGES && P.cache.k_scale ? __ldg(P.cache.k_scale + s.head) : 1.0f);
+        bool finite = true;
         for (int r = tid; r < NT; r += kCount) {
           float x = -INFINITY;
           if (r < rows) {
             const int t = t0 + r / P.group, g = r % P.group;
             x = -P.lse[(((int64_t)s.b * P.batch.T + t) * P.heads + s.head) * P.group + g] * kLog2e;
-            if (fabsf(x) == INFINITY) x = -INFINITY, st->plain[qb] = 0;
+            if (fabsf(x) == INFINITY) x = -INFINITY, finite = false;
           }
           st->shift[qb][r] = x;
-          if (!F8) st->mult[qb][r] = c;
         }
+        finite = __all_sync(~0u, finite);
+        if (lane == 0) st->plain[qb][warp - S::kPrepare] = finite;
         for (int t = tid; t < min(P.tokens, s.tokens - t0); t += kCount)
           st->rule[qb][t] = P.mask ? (uint64_t)__ldg(P.mask + (int64_t)s.b * P.batch.T + t0 + t) : t0 + t >= 63 ? ~0ull : (2ull << (t0 + t)) - 1;
         if constexpr (F8) {
           ok = mbar_wait_warp(smem_addr(&st->q_loaded[qb]), (nth >> 1) & 1, dead);
           if (!ok) break;
+          const float c = P.scale_log2 * (!PAGES && P.cache.k_scale ? __ldg(P.cache.k_scale + s.head) : 1.0f);
           split_queries<D, NT, kCount>(q_buf + qb * S::kQ, tid, c, st->mult[qb]);
           fence_async_shared();
         }
@@ -271,13 +274,14 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
       }
     }
   } else {
-    // ---- the sums: a thread per slot, each warpgroup the tiles of its parity ----
+    // ---- the sums: a thread per slot, each warpgroup every kGroups-th tile ----
     const int wg = warp >> 2, key = threadIdx.x & 127;
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     constexpr int CK = S::kChunk;
+    const float c = P.scale_log2;
     const int page_mask = (1 << P.cache.page_shift) - 1;
-    int nth = 0, buffer = 0;
-    uint32_t s_phase = 0;
+    int nth = 0;
+    uint32_t parity = 0;  // of this warpgroup's buffer
     bool ok = true;
     while (walk.next(s)) {
       const int passes = passes_of(s);
@@ -292,10 +296,10 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
         const int qb = nth & 1, t0 = pass * P.tokens, rows = min(s.tokens - t0, P.tokens) * P.group;
         ok = ok && mbar_wait(smem_addr(&st->rows_full[qb]), (nth >> 1) & 1, dead);
         __syncwarp();
-        const bool plain = __shfl_sync(~0u, st->plain[qb], 0);
+        const bool plain = __shfl_sync(~0u, st->plain[qb][0] && st->plain[qb][1], 0);
         // what a slot has and its page's scale come a tile (of this warpgroup) ahead, its page two
-        const int mine = s.tile0 + ((s.tile0 & 1) != wg);
-        int page = page_of(mine), next_page = page_of(mine + 2);
+        const int mine = s.tile0 + ((wg - owner(s, s.tile0)) & (S::kGroups - 1));
+        int page = page_of(mine), next_page = page_of(mine + S::kGroups);
         float* place = nullptr;
         float had = 0.0f, scale = 1.0f;
         const auto look = [&](int tile) {
@@ -308,42 +312,45 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
           if constexpr (PAGES) scale = P.scales.k[at];
         };
         look(mine);
-        for (int tile = s.tile0; tile < s.tile1; ++tile) {
-          const int sb = buffer;
-          const uint32_t parity = s_phase;
-          if (++buffer == S::kBuffers) buffer = 0, s_phase ^= 1;
-          if ((tile & 1) != wg) continue;
+        for (int tile = mine; tile < s.tile1; tile += S::kGroups) {
           const int slot = tile * kTileSlots + key;
           float* const to = place;
           const float before = had, factor = PAGES && !scale_counts(scale) ? NAN : scale;
           const int at_page = page;
           page = next_page;
-          look(tile + 2);
-          next_page = page_of(tile + 4);
+          look(tile + S::kGroups);
+          next_page = page_of(tile + 2 * S::kGroups);
 
-          ok = ok && mbar_wait(smem_addr(&st->s_full[sb]), parity, dead);
+          ok = ok && mbar_wait(smem_addr(&st->s_full[wg]), parity, dead);
+          parity ^= 1;
           __syncwarp();
           tc_fence_after();
           float2 sum = make_float2(0.0f, 0.0f);
+          // columns four at a time, so that those past the rows cost nothing
           const auto add = [&](int c0, auto tag) {
             constexpr bool CHECKED = decltype(tag)::value;
             float z[CK];
+            __syncwarp();
             if constexpr (CK == 32) {
-              tm_load<16>(lanes + sb * NT + c0, reinterpret_cast<float(&)[16]>(z[0]));
-              tm_load<16>(lanes + sb * NT + c0 + 16, reinterpret_cast<float(&)[16]>(z[CK - 16]));
+              tm_load<16>(lanes + wg * NT + c0, reinterpret_cast<float(&)[16]>(z[0]));
+              tm_load<16>(lanes + wg * NT + c0 + 16, reinterpret_cast<float(&)[16]>(z[CK - 16]));
             } else {
-              tm_load<CK>(lanes + sb * NT + c0, z);
+              tm_load<CK>(lanes + wg * NT + c0, z);
             }
 #pragma unroll
             for (int i = 0; i < CK; i += 4) {
+              if (c0 + i >= rows) break;
               const float4 m = *reinterpret_cast<const float4*>(&st->shift[qb][c0 + i]);
-              const float4 f = *reinterpret_cast<const float4*>(&st->mult[qb][c0 + i]);
+              const float4 f = F8 ? *reinterpret_cast<const float4*>(&st->mult[qb][c0 + i]) : make_float4(c, c, c, c);
               float2 z0 = make_float2(z[i], z[i + 1]), z1 = make_float2(z[i + 2], z[i + 3]);
               if constexpr (PAGES) z0 = mul2(z0, make_float2(factor, factor)), z1 = mul2(z1, make_float2(factor, factor));
               const float2 a = fma2(z0, make_float2(f.x, f.y), make_float2(m.x, m.y));
               const float2 b = fma2(z1, make_float2(f.z, f.w), make_float2(m.z, m.w));
               float2 w0 = make_float2(exp2_approx(a.x), exp2_approx(a.y)), w1 = make_float2(exp2_approx(b.x), exp2_approx(b.y));
-              if constexpr (CHECKED) {  // rows without a part may hold anything
+              if (!CHECKED && c0 + i + 4 > rows) {  // columns past the rows may hold anything
+                w0.y = c0 + i + 1 < rows ? w0.y : 0.0f, w1.x = c0 + i + 2 < rows ? w1.x : 0.0f, w1.y = 0.0f;
+              }
+              if constexpr (CHECKED) {  // so may rows without a part
                 const int fresh = slot - s.ctx;
                 const auto has = [&](float shift, int c) {
                   return shift > -INFINITY && (fresh < 0 || ((st->rule[qb][st->token[c]] >> (fresh & 63)) & 1));
@@ -355,13 +362,13 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
             }
           };
           const bool checked = !plain || (tile + 1) * kTileSlots > s.ctx;
-          for (int c0 = 0; c0 < rows; c0 += CK) {
-            if (checked || c0 + CK > rows) add(c0, std::true_type{});
-            else add(c0, std::false_type{});
-          }
+          if (checked)
+            for (int c0 = 0; c0 < rows; c0 += CK) add(c0, std::true_type{});
+          else
+            for (int c0 = 0; c0 < rows; c0 += CK) add(c0, std::false_type{});
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&st->s_empty[sb]));
+          if (lane == 0) mbar_arrive(smem_addr(&st->s_empty[wg]));
           if (to) {
             *to = ok ? before + (sum.x + sum.y) : NAN;
             if (pass == 0 && slot >= s.ctx && P.record.position) {

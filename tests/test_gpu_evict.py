@@ -144,6 +144,13 @@ def test_weigh_a_wide_table_and_pages_outside(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("tb", [None, [1 + i % 3 for i in range(60)]])
+def test_weigh_many_short_items(kind, tb):
+    """Several items of one or two tiles a block, of which each warpgroup has some and passes the others by."""
+    check(build(kind, 60, 3, 16, 8, 64, 16, [(37 * i) % 300 for i in range(60)], tb=tb))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_weigh_many_rows_sums_to_the_rows(kind):
     """Every row's weights sum to 1, so a step adds as much as it has rows (2^-12: 2^-24 a weight and the bound of the scores)."""
     import speculative_decoding_rejection_verify_gb300 as sv
