@@ -129,8 +129,7 @@ __device__ __forceinline__ float scale_need(float most) {
 
 // 16 codes at another scale: each times `ratio`, a power of two in 2^-24 .. 2^15, and rounded.  In fp16 a code and its
 // product are exact down to 2^-14, and what is below 2^-10 is 0 whatever its last bits.
-__device__ __forceinline__ uint4 rescaled_half(uint4 w, float ratio) {
-  const __half2 r = __float2half2_rn(ratio);
+__device__ __forceinline__ uint4 rescaled_half(uint4 w, __half2 r) {
   uint32_t* x = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -148,7 +147,7 @@ __device__ __forceinline__ bool half_ratio(float ratio) {  // whether rescaled_h
 }
 // The same for any ratio.
 __device__ __forceinline__ uint4 rescaled(uint4 w, float ratio) {
-  if (half_ratio(ratio)) return rescaled_half(w, ratio);
+  if (half_ratio(ratio)) return rescaled_half(w, __float2half2_rn(ratio));
   uint32_t* x = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

@@ -114,12 +114,15 @@ struct Shape {
   // A tile's weights stay in registers over the vote on them; with many columns, which would spill, the vote
   // is on scores that are then computed again (68 rows: 118 us against 125 in E4M3, 114 against 117 in bf16).
   static constexpr bool kHold = NT <= 64;
+  static constexpr int kAheadScales = KIND == kE4m3Pages ? 8 : 1, kPageScales = KIND == kE4m3Pages ? kTileSlots / 8 : 1;
+  static_assert(KIND != kE4m3Pages || kSlots / 2 + 3 < kAheadScales, "a tile's scales stay until it is weighed");
 
   struct State {
     uint64_t ring_full[8], ring_empty[8];
     uint64_t q_loaded[2], q_full[2], q_empty[2], mult_full[2];
     uint64_t v16_full[2], v16_empty[2];
     uint64_t s_full[2], s_empty[2], p_full, o_full;
+    uint64_t scales_full[kAheadScales];
     uint64_t products_done;          // behind a wait that ran out
     uint32_t tmem;
     int dead;
@@ -133,6 +136,9 @@ struct Shape {
     float red[4][NT];
     alignas(16) float mult[2][NT];   // E4M3: a score's factor to log2 units, by the segment's parity
     alignas(16) int64_t place[NT];   // the row's offset in the item's output
+    // Page scales: of every page of a tile, (a key's, the logarithm of a value's, its inverse).  K's producer writes them; it
+    // is kSlots / 2 tiles ahead of the products at most, and those two ahead of the softmax.
+    alignas(16) float4 scales[kAheadScales][kPageScales];
     uint32_t seen[kGroups][SPEC_MAX_NEW];  // which columns of each warpgroup attend to a new token
   };
   static constexpr int kState = kFixed + kSlots * kRing;
@@ -196,6 +202,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
     }
     mbar_init(smem_addr(&st->p_full), kSoftmaxWarps);
     mbar_init(smem_addr(&st->o_full), 1);
+    for (int i = 0; i < S::kAheadScales; ++i) mbar_init(smem_addr(&st->scales_full[i]), 1);
     mbar_init(smem_addr(&st->products_done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -255,13 +262,36 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
           const int p = __ldg(table + (at >> shift));
           return p < 0 || p > P.cache.num_pages ? P.cache.num_pages : p;
         };
-        int next_page = entry(tile0);
+        // page scales, a tile ahead of their copies, and so the page another
+        const bool scaled = PAGES && !is_v;
+        const auto scales_of = [&](int page) {  // of a page outside the pool, which reads as zeros, 1
+          const int64_t at = (int64_t)page * P.heads + head;
+          return scaled && page < P.cache.num_pages ? make_float2(P.scales.k[at], P.scales.v[at]) : make_float2(1.0f, 1.0f);
+        };
+        int next_page = entry(tile0), far_page = scaled && tile0 + 1 < tile1 ? entry(tile0 + 1) : P.cache.num_pages;
+        float2 next_scales = scales_of(next_page);
         for (int tile = tile0; tile < tile1; ++tile) {
           const int my_page = next_page;
-          if (tile + 1 < tile1) next_page = entry(tile + 1);
+          const float2 my_scales = next_scales;
+          if (scaled) {
+            next_page = far_page;
+            next_scales = scales_of(next_page);
+            far_page = tile + 2 < tile1 ? entry(tile + 2) : P.cache.num_pages;
+          } else if (tile + 1 < tile1) {
+            next_page = entry(tile + 1);
+          }
           ok = mbar_wait_warp(bar_of(&st->ring_empty[slot]), phase ^ 1, dead);
           if (!ok) break;
           const uint32_t bar = bar_of(&st->ring_full[slot]);
+          if (scaled) {  // (one that does not count makes the slots' scores NaN)
+            const bool counts = scale_counts(my_scales.y);
+            const int at = issued & (S::kAheadScales - 1);
+            if (lane < copies)
+              st->scales[at][lane % S::kPageScales] = make_float4(scale_counts(my_scales.x) ? my_scales.x : NAN, counts ? log2f(my_scales.y) : NAN,
+                                                                  counts ? 1.0f / my_scales.y : 1.0f, 0.0f);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_of(&st->scales_full[at]));
+          }
           if (lane == 0) mbar_expect(bar, S::kRing);
           __syncwarp();
           const uint32_t dst = base + (uint32_t)(ring - smem) + slot * S::kRing;
@@ -389,7 +419,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
         ok = ok && mbar_wait_warp(smem_addr(&st->v16_empty[it & 1]), ((it >> 1) & 1) ^ 1, dead);
         if (!ok) break;
         const float c = P.scale_log2 * (!PAGES && P.cache.k_scale ? __ldg(P.cache.k_scale + s.head) : 1.0f);
-        split_queries<D, NT, kConvertWarps * 32>(q_buf + qb * S::kQ, tid, c, st->mult[seg & 1]);
+        split_queries<D, NT, kConvertWarps * 32>(q_buf + qb * S::kQ, tid, NT, c, st->mult[seg & 1]);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) {
@@ -504,39 +534,19 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
 #pragma unroll
         for (int i = 0; i < CK; ++i) l[j][i] = 0.0f;
 
-      // Page scales: a key's is a factor of its scores.  A value's goes into the weight, as an addend of the exponent, so
-      // that the largest product of weight and scale is what a row's maximum follows and fp16 reaches down from; the sum of the weights
-      // themselves takes it out again.  Read a tile ahead, the page two.
-      int ahead_page = P.cache.num_pages;
-      float ahead_k = 1.0f, ahead_v = 1.0f;
-      const auto page_of = [&](int tile) {
-        const int at = tile * kTileSlots + key;
-        if (at >= s.end) return P.cache.num_pages;
-        const int p = __ldg(P.batch.pages + (int64_t)s.b * P.batch.max_pages + (at >> P.cache.page_shift));
-        return p < 0 ? P.cache.num_pages : p;
-      };
-      const auto scales_of_page = [&](int p) {  // of a page outside the pool, which reads as zeros, 1
-        const bool in = p < P.cache.num_pages;
-        const int64_t at = (int64_t)p * P.heads + s.head;
-        ahead_k = in ? P.scales.k[at] : 1.0f, ahead_v = in ? P.scales.v[at] : 1.0f;
-      };
-      if constexpr (PAGES) {
-        scales_of_page(page_of(s.tile0));
-        if (s.tile0 + 1 < s.tile1) ahead_page = page_of(s.tile0 + 1);
-      }
-
       for (int tile = s.tile0; tile < s.tile1; ++tile, ++it) {
         const int sb = it & 1;
         const uint32_t s_col = lanes + sb * NT;
-        // (one that does not count makes the slot's scores NaN)
-        const float k_factor = scale_counts(ahead_k) ? ahead_k : NAN;
-        const bool v_counts = scale_counts(ahead_v);
-        const float v_log2 = v_counts ? log2f(ahead_v) : NAN, v_inverse = v_counts ? 1.0f / ahead_v : 1.0f;
-        if constexpr (PAGES) {
-          scales_of_page(ahead_page);
-          ahead_page = tile + 2 < s.tile1 ? page_of(tile + 2) : P.cache.num_pages;
-        }
         mbar_wait(smem_addr(&st->s_full[sb]), (it >> 1) & 1, dead);
+        // Page scales: a key's is a factor of its scores.  A value's goes into the weight, as an addend of the exponent, so
+        // that the largest product of weight and scale is what a row's maximum follows and fp16 reaches down from; the sum of
+        // the weights themselves takes it out again.
+        float k_factor = 1.0f, v_log2 = 0.0f, v_inverse = 1.0f;
+        if constexpr (PAGES) {
+          mbar_wait(smem_addr(&st->scales_full[it & (S::kAheadScales - 1)]), (it / S::kAheadScales) & 1, dead);
+          const float4 x = st->scales[it & (S::kAheadScales - 1)][key >> min(P.cache.page_shift, 7)];
+          k_factor = x.x, v_log2 = x.y, v_inverse = x.z;
+        }
         __syncwarp();
         tc_fence_after();
 

@@ -49,14 +49,12 @@ __device__ __forceinline__ void store_entry(char* p, float (&x)[8], float scale,
 // sin are loaded once a thread and an element's partner is always in the same thread (q_out may be q
 // itself).  kAhead heads are loaded before the first is used.
 template <int D, bool F8, bool INTERLEAVED>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams P) {
+__device__ __forceinline__ void append_token(const AppendParams& P, int block) {
   constexpr int kAhead = INTERLEAVED ? 4 : 2;
-  pdl_launch_next();
-  pdl_wait();
   const int paired = INTERLEAVED ? 0 : P.rot / 16;  // units that hold a vector and its partner
   const int units = D / 8 - paired, lanes = blockDim.x / units;
   const int head0 = threadIdx.x / units, unit = threadIdx.x - head0 * units;
-  const int b = blockIdx.x / P.batch.T, t = blockIdx.x - b * P.batch.T;
+  const int b = block / P.batch.T, t = block - b * P.batch.T;
   if (head0 >= lanes) return;
 
   const bool pair = unit < paired;
@@ -170,10 +168,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   }
 }
 
+template <int D, bool F8, bool INTERLEAVED>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams P) {
+  pdl_launch_next();
+  pdl_wait();
+  append_token<D, F8, INTERLEAVED>(P, blockIdx.x);
+}
+
 // ------------------------------------------------------------------------------------------------
 // spec_kv_append_ex: a page's scale follows what goes into it
 // ------------------------------------------------------------------------------------------------
-constexpr int kPageThreads = 128;
+// Threads of a page's block, by the tokens that it can get (4 x 2047 tokens, pages of 8: 38 us with 64, 46 with 128; of 32: 30, 31, and
+// 49 with 256; of 256: 106, 58, 43).
+constexpr int kPageThreadsMost = 256;
+static int page_threads(int tokens) { return tokens <= 32 ? 64 : tokens <= 128 ? 128 : 256; }
 constexpr int kPageHeld = 4;  // tokens a thread holds between the two passes
 
 struct PageAppendParams {
@@ -188,15 +196,12 @@ struct PageAppendParams {
   int rot, max_positions;
 };
 
-// One block per (request, page that gets tokens, head, k or v): the largest magnitude of what goes in, then the page's
+// One block per (request, page that gets tokens, head, k or v), `index`: the largest magnitude of what goes in, then the page's
 // scale, then the codes.  A thread owns one unit of the head dimension as in append_kernel, for every lanes-th token; the
 // products of a rotation are rounded one by one, so the magnitude does not depend on how they are fused.
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kPageThreads) page_append_kernel(const __grid_constant__ PageAppendParams P) {
-  __shared__ float most_of[kPageThreads / 32];
-  pdl_launch_next();
-  pdl_wait();
-  int index = blockIdx.x;
+__device__ __forceinline__ void append_page(const PageAppendParams& P, int index) {
+  __shared__ float most_of[kPageThreadsMost / 32];
   const bool is_v = index & 1;
   index >>= 1;
   const int head = index % P.heads;
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(kPageThreads) page_append_kernel(const __grid_
   if (page < 0 || page >= P.cache.num_pages) return;
 
   const int rot = is_v ? 0 : P.rot;
-  const int paired = INTERLEAVED ? 0 : rot / 16, units = D / 8 - paired, lanes = kPageThreads / units;
+  const int paired = INTERLEAVED ? 0 : rot / 16, units = D / 8 - paired, lanes = blockDim.x / units;
   const int lane0 = threadIdx.x / units, unit = threadIdx.x - lane0 * units;
   const bool works = lane0 < lanes, pair = unit < paired;
   const int lo = pair || INTERLEAVED ? unit * 8 : rot + (unit - paired) * 8, far = rot / 2;
@@ -282,8 +287,7 @@ __global__ void __launch_bounds__(kPageThreads) page_append_kernel(const __grid_
   const int before = nth == 0 ? ctx - from : 0;  // rows of the page that hold tokens already
   const float old = before > 0 ? *place : 0.0f;
   __syncthreads();  // every thread has read the old scale
-#pragma unroll
-  for (int w = 0; w < kPageThreads / 32; ++w) most = fmaxf(most, most_of[w]);
+  for (int w = 0; w < blockDim.x / 32; ++w) most = fmaxf(most, most_of[w]);
   const bool counts = before > 0 && scale_counts(old);
   const float need = scale_need(most), scale = counts ? fmaxf(old, need) : need, inverse = 1.0f / scale;
   if (threadIdx.x == 0) *place = scale;
@@ -291,7 +295,7 @@ __global__ void __launch_bounds__(kPageThreads) page_append_kernel(const __grid_
   char* out = (is_v ? P.cache.v : P.cache.k) + page * P.cache.page + head * P.cache.head;
   if (counts && need > old) {  // the rows before: their codes at the new scale, a power of two
     const float ratio = old * inverse;
-    for (int u = threadIdx.x; u < before * (D / 16); u += kPageThreads) {
+    for (int u = threadIdx.x; u < before * (D / 16); u += blockDim.x) {
       uint4* p = reinterpret_cast<uint4*>(out + (u / (D / 16)) * P.cache.slot + (u % (D / 16)) * 16);
       *p = rescaled(*p, ratio);
     }
@@ -318,6 +322,22 @@ __global__ void __launch_bounds__(kPageThreads) page_append_kernel(const __grid_
     load(t, a, c);
     store(t, a, c);
   }
+}
+
+struct PageStepParams {
+  AppendParams queries;  // heads = 0: the queries and the flags
+  PageAppendParams pages;
+  int page_blocks;
+};
+
+// The pages' blocks, then the tokens' that rotate the queries: in one launch they run beside one another (4 x 2047 tokens of 32 +
+// 2 x 8 heads, pages of 32: 30 us, 31 in two; 8 x 6 tokens: a launch less).
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kPageThreadsMost) page_append_kernel(const __grid_constant__ PageStepParams P) {
+  pdl_launch_next();
+  pdl_wait();
+  if (blockIdx.x < P.page_blocks) append_page<D, INTERLEAVED>(P.pages, blockIdx.x);
+  else append_token<D, true, INTERLEAVED>(P.queries, blockIdx.x - P.page_blocks);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -447,7 +467,7 @@ spec_status_t spec_kv_append_ex(const spec_heads_t* q, const spec_heads_t* k, co
   const int64_t blocks = (int64_t)batch->B * batch->T;
   const int64_t touched = ((int64_t)batch->T + cache->page_size - 2) / cache->page_size + 1;
   const int64_t page_blocks = batch->B * touched * cache->heads * 2;
-  if (scales && page_blocks > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
+  if (scales && page_blocks + blocks > 0x7fffffffll) return SPEC_ERR_UNSUPPORTED;
   if (blocks > 0x7fffffffll || q_heads > 65535) return SPEC_ERR_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f8 = cache->dtype == SPEC_DTYPE_E4M3;
@@ -456,17 +476,20 @@ spec_status_t spec_kv_append_ex(const spec_heads_t* q, const spec_heads_t* k, co
                         : (inter ? append_kernel<128, false, true> : append_kernel<128, false, false>))
                   : (f8 ? (inter ? append_kernel<64, true, true> : append_kernel<64, true, false>)
                         : (inter ? append_kernel<64, false, true> : append_kernel<64, false, false>));
+  if (scales) {
+    const bool tokens = q_heads > 0 || out_flags;
+    const PageStepParams A = {P, {P.k, P.v, P.cache, scales_of(scales), P.batch, P.cos_table, P.sin_table, P.positions, cache->heads,
+                              (int)touched, rot, P.max_positions}, (int)page_blocks};
+    auto pages = cache->head_dim == 128 ? (inter ? page_append_kernel<128, true> : page_append_kernel<128, false>)
+                                        : (inter ? page_append_kernel<64, true> : page_append_kernel<64, false>);
+    const dim3 grid((unsigned)(page_blocks + (tokens ? blocks : 0)));
+    const int threads = page_threads(batch->T < cache->page_size ? batch->T : cache->page_size);
+    return launch_early(pages, grid, dim3(threads), 0, st, A) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  }
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != cudaSuccess) return SPEC_ERR_CUDA;
   const int threads = blocks >= 16 * sms ? kAppendThreadsMany : kAppendThreads;
-  if (!scales || q_heads > 0 || out_flags)
-    if (launch_early(kern, dim3((unsigned)blocks), dim3(threads), 0, st, P) != cudaSuccess) return SPEC_ERR_CUDA;
-  if (!scales) return SPEC_OK;
-  const PageAppendParams A = {P.k, P.v, P.cache, scales_of(scales), P.batch, P.cos_table, P.sin_table, P.positions,
-                              cache->heads, (int)touched, rot, P.max_positions};
-  auto pages = cache->head_dim == 128 ? (inter ? page_append_kernel<128, true> : page_append_kernel<128, false>)
-                                      : (inter ? page_append_kernel<64, true> : page_append_kernel<64, false>);
-  return launch_early(pages, dim3((unsigned)page_blocks), dim3(kPageThreads), 0, st, A) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return launch_early(kern, dim3((unsigned)blocks), dim3(threads), 0, st, P) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 spec_status_t spec_kv_append(const spec_heads_t* q, const spec_heads_t* k, const spec_heads_t* v,

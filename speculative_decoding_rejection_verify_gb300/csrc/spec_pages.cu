@@ -11,7 +11,7 @@ namespace sv {
 // The values of 16 codes at scale `from`, as codes at scale `to` (by way of fp16 where both are powers of two).
 __device__ __forceinline__ uint4 recoded(uint4 w, float from, float to) {
   const float inverse = 1.0f / to, ratio = from * inverse;
-  if (((__float_as_int(from) | __float_as_int(to)) & 0x7FFFFF) == 0 && half_ratio(ratio)) return rescaled_half(w, ratio);
+  if (((__float_as_int(from) | __float_as_int(to)) & 0x7FFFFF) == 0 && half_ratio(ratio)) return rescaled_half(w, __float2half2_rn(ratio));
   uint32_t* x = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {
@@ -31,7 +31,7 @@ struct Move {
   int lo, hi;
 };
 
-// A warp's view of one head of a cache with page scales.
+// A warp's view of the keys or values of one head of a cache with page scales.
 struct Side {
   char* base;       // row 0 of page 0
   float* scales;    // of page 0
@@ -40,19 +40,30 @@ struct Side {
   int page_size;
 };
 
+// What a warp's lanes tell one another.
+struct Exchange {
+  int64_t src[32], dst[32];
+  float2 scales[32];                    // an entry's, old and new
+  uint32_t ratio[32];                   // the old over the new, twice in fp16; 0: fp16 does not do it
+  uint32_t taken[SPEC_MAX_PAGE / 32];   // rows of a page that entries move into
+};
+
+__device__ __forceinline__ void tell_places(Exchange& x, const Move& m) {
+  const int lane = threadIdx.x & 31;
+  x.src[lane] = m.is ? m.src : -1, x.dst[lane] = m.dst;
+  __syncwarp();
+}
 // The entries' codes: lane l has vector l % (D / 16) of entries j * 32 / (D / 16) + l / (D / 16).  n: the moves are lanes 0 .. n - 1.
 template <int D>
-__device__ __forceinline__ void load_entries(const Side& c, const Move& m, int n, uint4 (&w)[D / 16]) {
+__device__ __forceinline__ void load_entries(const char* base, const Exchange& x, int n, uint4 (&w)[D / 16]) {
   constexpr int kVecs = D / 16, kAtOnce = 32 / kVecs;
   const int lane = threadIdx.x & 31;
-  const uint32_t all = __ballot_sync(~0u, m.is);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     w[j] = make_uint4(0, 0, 0, 0);
     if (j * kAtOnce >= n) continue;
-    const int e = j * kAtOnce + lane / kVecs;
-    const int64_t at = __shfl_sync(~0u, m.src, e);
-    if ((all >> e) & 1) w[j] = *reinterpret_cast<const uint4*>(c.base + at + lane % kVecs * 16);
+    const int64_t at = x.src[j * kAtOnce + lane / kVecs];
+    if (at >= 0) w[j] = *reinterpret_cast<const uint4*>(base + at + lane % kVecs * 16);
   }
 }
 // Bytes 1 and 3 of the largest codes among a vector's, without their signs: a larger one is a larger magnitude.
@@ -79,35 +90,56 @@ template <int D>
 __device__ __forceinline__ uint32_t largest_code(const uint4 (&w)[D / 16], int n) {
   constexpr int kVecs = D / 16, kAtOnce = 32 / kVecs;
   const int lane = threadIdx.x & 31;
-  uint32_t mine = 0;
+  uint32_t top[kVecs], all = 0;
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
-    if (j * kAtOnce >= n) continue;
-    uint32_t top = largest_of(w[j]);
-    if (__any_sync(~0u, top >= 0x7F000000u || (top & 0xFFFF) >= 0x7F00u)) top = largest_of(without_nan(w[j]));
-#pragma unroll
-    for (int d = 1; d < kVecs; d *= 2) top = max_u16x2(top, __shfl_xor_sync(~0u, top, d));
-    const uint32_t of_entry = __shfl_sync(~0u, top, lane % kAtOnce * kVecs);
-    if (lane / kAtOnce == j) mine = of_entry;
+    top[j] = j * kAtOnce < n ? largest_of(w[j]) : 0;
+    all = max_u16x2(all, top[j]);
   }
+  if (__any_sync(~0u, all >= 0x7F000000u || (all & 0xFFFF) >= 0x7F00u)) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) top[j] = largest_of(without_nan(w[j]));
+  }
+  // over the lanes of an entry, each of which ends with the entry of its own number
+#pragma unroll
+  for (int d = kVecs / 2; d > 0; d /= 2) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int k = 0; k < d; ++k) {
+      const uint32_t keep = up ? top[k + d] : top[k], send = up ? top[k] : top[k + d];
+      top[k] = max_u16x2(keep, __shfl_xor_sync(~0u, send, d));
+    }
+  }
+  const uint32_t mine = __shfl_sync(~0u, top[0], lane % kAtOnce * kVecs + lane / kAtOnce);
   return max(mine >> 24, (mine >> 8) & 0xFF);
 }
 __device__ __forceinline__ float magnitude(uint32_t code, float scale) {  // a finite one, or 0
   const float x = unpack_e4m3(code).x * fabsf(scale);
   return x < INFINITY ? x : 0.0f;
 }
+__device__ __forceinline__ void tell_scales(Exchange& x, float from, float to) {
+  const int lane = threadIdx.x & 31;
+  const float ratio = from * (1.0f / to);
+  const __half2 r = __float2half2_rn(ratio);
+  const bool half = ((__float_as_int(from) | __float_as_int(to)) & 0x7FFFFF) == 0 && half_ratio(ratio);
+  x.scales[lane] = make_float2(from, to);
+  x.ratio[lane] = from == to ? 0x3C003C00u : half ? *reinterpret_cast<const uint32_t*>(&r) : 0;
+  __syncwarp();
+}
 template <int D>
-__device__ __forceinline__ void store_entries(const Side& c, const Move& m, int n, const uint4 (&w)[D / 16], float from, float to) {
+__device__ __forceinline__ void store_entries(char* base, const Exchange& x, int n, const uint4 (&w)[D / 16]) {
   constexpr int kVecs = D / 16, kAtOnce = 32 / kVecs;
   const int lane = threadIdx.x & 31;
-  const uint32_t all = __ballot_sync(~0u, m.is);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     if (j * kAtOnce >= n) continue;
     const int e = j * kAtOnce + lane / kVecs;
-    const int64_t at = __shfl_sync(~0u, m.dst, e);
-    const float f = __shfl_sync(~0u, from, e), t = __shfl_sync(~0u, to, e);
-    if ((all >> e) & 1) *reinterpret_cast<uint4*>(c.base + at + lane % kVecs * 16) = f == t ? w[j] : recoded(w[j], f, t);
+    if (x.src[e] < 0) continue;
+    const uint32_t ratio = x.ratio[e];
+    uint4 y = w[j];
+    if (ratio == 0) y = recoded(y, x.scales[e].x, x.scales[e].y);
+    else if (ratio != 0x3C003C00u) y = rescaled_half(y, *reinterpret_cast<const __half2*>(&ratio));
+    *reinterpret_cast<uint4*>(base + x.dst[e] + lane % kVecs * 16) = y;
   }
 }
 // The page's scale with `most` in it, and what its codes have to be multiplied by.
@@ -119,16 +151,21 @@ __device__ __forceinline__ NewScale new_scale(float old, float most) {
   const float need = scale_need(most), scale = counts ? fmaxf(old, need) : need;
   return {scale, counts && need > old ? old / need : 1.0f};
 }
+// Whether a page of scale `old` holds whatever a page of scale `from` does: a power of two that is not less.
+__device__ __forceinline__ bool holds(float old, float from) {
+  return scale_counts(old) && (__float_as_int(old) & 0x7FFFFF) == 0 && from >= 0.0f && from <= old;
+}
 // A warp rescales the rows < end of a page but for those marked in `taken`.
 template <int D>
-__device__ __forceinline__ void rescale_page(const Side& c, int page, int end, const uint32_t* taken, float ratio) {
+__device__ __noinline__ void rescale_page(char* page, int64_t slot, int end, const uint32_t* taken, float ratio) {
   constexpr int kVecs = D / 16, kAtOnce = 32 / kVecs;
   const int lane = threadIdx.x & 31;
   for (int r = lane / kVecs; r < end; r += kAtOnce) {
     if ((taken[r >> 5] >> (r & 31)) & 1) continue;
-    uint4* p = reinterpret_cast<uint4*>(c.base + page * c.page + r * c.slot + lane % kVecs * 16);
+    uint4* p = reinterpret_cast<uint4*>(page + r * slot + lane % kVecs * 16);
     *p = rescaled(*p, ratio);
   }
+  __syncwarp();
 }
 __device__ __forceinline__ void clear_taken(uint32_t* taken, int page_size) {
   for (int i = threadIdx.x & 31; i < (page_size + 31) / 32; i += 32) taken[i] = 0;
@@ -138,73 +175,89 @@ __device__ __forceinline__ void clear_taken(uint32_t* taken, int page_size) {
 // A warp's n moves, whole pages' of them, at most 32: every entry is in registers before the first is written.  row: the
 // target's row in its page; end: the rows of that page that hold what stays.
 template <int D>
-__device__ __forceinline__ void move_batch(const Side& c, const Move& m, int n, int row, int end, uint32_t* taken) {
+__device__ __forceinline__ void move_batch(const Side& c, const Move& m, int n, int row, int end, Exchange& x) {
   const int lane = threadIdx.x & 31;
+  tell_places(x, m);
   uint4 w[D / 16];
-  load_entries<D>(c, m, n, w);
-  const float from = m.is ? c.scales[(int64_t)m.from * c.heads] : 1.0f, old = m.to >= 0 ? c.scales[(int64_t)m.to * c.heads] : 1.0f;
-  float most = magnitude(largest_code<D>(w, n), m.is ? from : 0.0f);
-  bool any = m.is;  // of the lane's page
+  load_entries<D>(c.base, x, n, w);
+  const float from = m.is ? c.scales[(int64_t)m.from * c.heads] : 0.0f, old = m.to >= 0 ? c.scales[(int64_t)m.to * c.heads] : 1.0f;
+  const uint32_t page_lanes = (m.hi == 31 ? ~0u : (2u << m.hi) - 1) & (~0u << m.lo);
+  const bool any = __ballot_sync(~0u, m.is) & page_lanes;  // of the lane's page
+  float scale = old;
+  if (__any_sync(~0u, m.is && !holds(old, from))) {
+    float most = magnitude(largest_code<D>(w, n), from);
 #pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const float x = __shfl_up_sync(~0u, most, d);
-    const bool a = __shfl_up_sync(~0u, any, d);
-    if (lane - d >= m.lo) most = fmaxf(most, x), any |= a;
+    for (int d = 1; d < 32; d *= 2) {
+      const float y = __shfl_up_sync(~0u, most, d);
+      if (lane - d >= m.lo) most = fmaxf(most, y);
+    }
+    const NewScale s = new_scale(old, __shfl_sync(~0u, most, m.hi));
+    scale = s.scale;
+    uint32_t grown = __ballot_sync(~0u, any && lane == m.lo && s.ratio != 1.0f);
+    while (grown) {
+      const int leader = __ffs(grown) - 1;
+      grown &= grown - 1;
+      clear_taken(x.taken, c.page_size);
+      if (m.is && m.lo == leader) atomicOr(&x.taken[row >> 5], 1u << (row & 31));
+      __syncwarp();
+      rescale_page<D>(c.base + __shfl_sync(~0u, m.to, leader) * c.page, c.slot, __shfl_sync(~0u, end, leader), x.taken,
+                      __shfl_sync(~0u, s.ratio, leader));
+    }
   }
-  most = __shfl_sync(~0u, most, m.hi), any = __shfl_sync(~0u, any, m.hi);
-  const NewScale s = new_scale(old, most);
-  uint32_t grown = __ballot_sync(~0u, any && lane == m.lo && s.ratio != 1.0f);
-  while (grown) {
-    const int leader = __ffs(grown) - 1;
-    grown &= grown - 1;
-    clear_taken(taken, c.page_size);
-    const int hi = __shfl_sync(~0u, m.hi, leader);
-    if (lane >= leader && lane <= hi && m.is) atomicOr(&taken[row >> 5], 1u << (row & 31));
-    __syncwarp();
-    rescale_page<D>(c, __shfl_sync(~0u, m.to, leader), __shfl_sync(~0u, end, leader), taken, __shfl_sync(~0u, s.ratio, leader));
-    __syncwarp();
-  }
-  store_entries<D>(c, m, n, w, from, s.scale);
-  __syncwarp();  // an entry may come from a page that others go to: its old scale was needed until here
-  if (any && lane == m.lo) c.scales[(int64_t)m.to * c.heads] = s.scale;
+  tell_scales(x, from, scale);
+  store_entries<D>(c.base, x, n, w);
+  // an entry may come from a page that others go to: its old scale was needed until here, and is in registers
+  if (any && lane == m.lo && scale != old) c.scales[(int64_t)m.to * c.heads] = scale;
   __syncwarp();
 }
 
 // A warp's n moves into one page: info(i) is lane's move i (is = false behind the last), row(move) its row.
 template <int D, typename Info, typename Row>
-__device__ __noinline__ void move_page(const Side& c, int n, int to, int end, uint32_t* taken, Info info, Row row) {
+__device__ __noinline__ void move_page(const Side& c, int n, int to, int end, Exchange& x, Info info, Row row) {
   const int lane = threadIdx.x & 31;
+  float* place = c.scales + (int64_t)to * c.heads;
+  const float old = *place;
   float most = 0.0f;
-  bool any = false;
+  bool any = false, look = false;
   for (int i0 = 0; i0 < n; i0 += 32) {
     const Move m = info(i0 + lane);
+    const float from = m.is ? c.scales[(int64_t)m.from * c.heads] : 0.0f;
+    any |= m.is;
+    if (!__any_sync(~0u, m.is && !holds(old, from))) continue;
+    look = true;
+    tell_places(x, m);
     uint4 w[D / 16];
-    load_entries<D>(c, m, n - i0, w);
-    const uint32_t top = largest_code<D>(w, n - i0);
-    if (m.is) most = fmaxf(most, magnitude(top, c.scales[(int64_t)m.from * c.heads])), any = true;
+    load_entries<D>(c.base, x, n - i0, w);
+    most = fmaxf(most, magnitude(largest_code<D>(w, n - i0), from));
+    __syncwarp();
   }
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
   if (!__any_sync(~0u, any)) return;
-  float* place = c.scales + (int64_t)to * c.heads;
-  const NewScale s = new_scale(*place, most);
+  NewScale s = {old, 1.0f};
+  if (look) {
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
+    s = new_scale(old, most);
+  }
   if (s.ratio != 1.0f) {
-    clear_taken(taken, c.page_size);
+    clear_taken(x.taken, c.page_size);
     for (int i0 = 0; i0 < n; i0 += 32) {
       const Move m = info(i0 + lane);
-      if (m.is) atomicOr(&taken[row(m) >> 5], 1u << (row(m) & 31));
+      if (m.is) atomicOr(&x.taken[row(m) >> 5], 1u << (row(m) & 31));
     }
     __syncwarp();
-    rescale_page<D>(c, to, end, taken, s.ratio);
+    rescale_page<D>(c.base + to * c.page, c.slot, end, x.taken, s.ratio);
   }
   for (int i0 = 0; i0 < n; i0 += 32) {
     const Move m = info(i0 + lane);
+    tell_places(x, m);
     uint4 w[D / 16];
-    load_entries<D>(c, m, n - i0, w);
-    store_entries<D>(c, m, n - i0, w, m.is ? c.scales[(int64_t)m.from * c.heads] : 1.0f, s.scale);
+    load_entries<D>(c.base, x, n - i0, w);
+    tell_scales(x, m.is ? c.scales[(int64_t)m.from * c.heads] : 1.0f, s.scale);
+    store_entries<D>(c.base, x, n - i0, w);
+    __syncwarp();
   }
-  __syncwarp();  // an entry may come from the same page: its old scale was needed until here
-  if (lane == 0) *place = s.scale;
+  // an entry may come from the same page: its old scale was needed until here
+  if (lane == 0 && s.scale != old) *place = s.scale;
   __syncwarp();
 }
 
@@ -221,7 +274,7 @@ struct PageKeepParams {
   int lists;  // layers * heads * 2
 };
 
-constexpr int kPageKeepWarps = 8;
+constexpr int kPageKeepWarps = 4;
 
 // Where the moves of a request's path go, of all its layers and heads.
 struct PathMoves {
@@ -233,9 +286,9 @@ struct PathMoves {
 // targets may be its later sources: up to 32 entries wait in registers; more (BIG) are copied to shared memory first, which takes
 // the place of the cache as their source.
 template <int D, bool BIG>
-__global__ void __launch_bounds__(kPageKeepWarps * 32) page_keep_kernel(const __grid_constant__ PageKeepParams P) {
+__global__ void __launch_bounds__(kPageKeepWarps * 32, 6) page_keep_kernel(const __grid_constant__ PageKeepParams P) {
   __shared__ PathMoves path;
-  __shared__ uint32_t taken_of[kPageKeepWarps][SPEC_MAX_PAGE / 32];
+  __shared__ Exchange exchange[kPageKeepWarps];
   __shared__ float scales_of[kPageKeepWarps][BIG ? SPEC_MAX_NEW : 1];
   extern __shared__ uint4 copies[];  // BIG: [warps][SPEC_MAX_NEW][D / 16]
   pdl_launch_next();
@@ -261,64 +314,60 @@ __global__ void __launch_bounds__(kPageKeepWarps * 32) page_keep_kernel(const __
   }
   const bool any = __syncthreads_or(threadIdx.x < n && path.from[threadIdx.x] >= 0);
   if (!any) return;
-  for (int list = blockIdx.x * kPageKeepWarps + warp; list < P.lists; list += gridDim.x * kPageKeepWarps) {
-  const bool is_v = list & 1;
-  const int head = (list >> 1) % P.heads, layer = (list >> 1) / P.heads;
-  const Side c = {(is_v ? P.cache.v : P.cache.k) + layer * P.cache.layer + head * P.cache.head,
-                  (is_v ? P.scales.v : P.scales.k) + layer * P.scales.layer + head, P.heads, P.cache.slot, P.cache.page, page_size};
   const int end = (int)min((int64_t)ctx + n, (int64_t)P.batch.slots);
   const auto rows_of = [&](int ordinal) { return min(end - (ordinal << shift), page_size); };
-  if constexpr (!BIG) {
-    const int ordinal = (ctx + lane) >> shift;
-    Move m = {lane < n && path.from[lane] >= 0, path.src[lane], path.dst[lane], path.from[lane], lane < n ? path.to[lane] : -1,
-              lane, lane};
-    if (lane < n) m.lo = max((ordinal << shift) - ctx, 0), m.hi = min(((ordinal + 1) << shift) - ctx, n) - 1;
-    move_batch<D>(c, m, n, (ctx + lane) & (page_size - 1), rows_of(ordinal), taken_of[warp]);
-  } else {
-    uint4* mine = copies + warp * SPEC_MAX_NEW * kVecs;
-    for (int u = lane; u < n * kVecs; u += 32)
-      if (path.from[u / kVecs] >= 0) mine[u] = *reinterpret_cast<const uint4*>(c.base + path.src[u / kVecs] + u % kVecs * 16);
-    for (int i = lane; i < n; i += 32)
-      if (path.from[i] >= 0) scales_of[warp][i] = c.scales[(int64_t)path.from[i] * P.heads];
-    __syncwarp();
-    for (int i = 0; i < n;) {  // a page at a time
-      const int ordinal = (ctx + i) >> shift, first = i, to = path.to[i];
-      float most = 0.0f;
-      bool moves = false;
-      for (; i < n && (ctx + i) >> shift == ordinal; ++i) {
-        if (path.from[i] < 0) continue;
-        moves = true;
-        uint32_t top = 0;
-        if (lane < kVecs * 4) {
-          const uint32_t size = reinterpret_cast<const uint32_t*>(mine + i * kVecs)[lane] & 0x7F7F7F7Fu;
-          top = size & ~__vcmpeq4(size, 0x7F7F7F7Fu);
+  Exchange& x = exchange[warp];
+  for (int list = blockIdx.x * kPageKeepWarps + warp; list < P.lists; list += gridDim.x * kPageKeepWarps) {
+    const bool is_v = list & 1;
+    const int head = (list >> 1) % P.heads, layer = (list >> 1) / P.heads;
+    const Side c = {(is_v ? P.cache.v : P.cache.k) + layer * P.cache.layer + head * P.cache.head,
+                    (is_v ? P.scales.v : P.scales.k) + layer * P.scales.layer + head, P.heads, P.cache.slot, P.cache.page, page_size};
+    if constexpr (!BIG) {
+      const int ordinal = (ctx + lane) >> shift;
+      Move m = {lane < n && path.from[lane] >= 0, path.src[lane], path.dst[lane], path.from[lane], lane < n ? path.to[lane] : -1, lane, lane};
+      if (lane < n) m.lo = max((ordinal << shift) - ctx, 0), m.hi = min(((ordinal + 1) << shift) - ctx, n) - 1;
+      move_batch<D>(c, m, n, (ctx + lane) & (page_size - 1), rows_of(ordinal), x);
+    } else {
+      uint4* mine = copies + warp * SPEC_MAX_NEW * kVecs;
+      for (int u = lane; u < n * kVecs; u += 32)
+        if (path.from[u / kVecs] >= 0) mine[u] = *reinterpret_cast<const uint4*>(c.base + path.src[u / kVecs] + u % kVecs * 16);
+      for (int i = lane; i < n; i += 32)
+        if (path.from[i] >= 0) scales_of[warp][i] = c.scales[(int64_t)path.from[i] * P.heads];
+      __syncwarp();
+      for (int i = 0; i < n;) {  // a page at a time
+        const int ordinal = (ctx + i) >> shift, first = i, to = path.to[i];
+        float most = 0.0f;
+        bool moves = false;
+        for (; i < n && (ctx + i) >> shift == ordinal; ++i) {
+          if (path.from[i] < 0) continue;
+          moves = true;
+          uint32_t top = lane < kVecs ? largest_of(without_nan(mine[i * kVecs + lane])) : 0;
+          top = max(top >> 24, (top >> 8) & 0xFF);
+          most = fmaxf(most, magnitude(__reduce_max_sync(~0u, top), scales_of[warp][i]));
         }
-        top = max(max(top & 0xFF, (top >> 8) & 0xFF), max((top >> 16) & 0xFF, top >> 24));
-        most = fmaxf(most, magnitude(__reduce_max_sync(~0u, top), scales_of[warp][i]));
-      }
-      if (!moves) continue;
-      float* place = c.scales + (int64_t)to * P.heads;
-      const NewScale s = new_scale(*place, most);
-      if (s.ratio != 1.0f) {
-        clear_taken(taken_of[warp], page_size);
-        for (int k = first + lane; k < i; k += 32) {
-          const int row = (ctx + k) & (page_size - 1);
-          if (path.from[k] >= 0) atomicOr(&taken_of[warp][row >> 5], 1u << (row & 31));
+        if (!moves) continue;
+        float* place = c.scales + (int64_t)to * P.heads;
+        const NewScale s = new_scale(*place, most);
+        if (s.ratio != 1.0f) {
+          clear_taken(x.taken, page_size);
+          for (int k = first + lane; k < i; k += 32) {
+            const int row = (ctx + k) & (page_size - 1);
+            if (path.from[k] >= 0) atomicOr(&x.taken[row >> 5], 1u << (row & 31));
+          }
+          __syncwarp();
+          rescale_page<D>(c.base + to * c.page, c.slot, rows_of(ordinal), x.taken, s.ratio);
+        }
+        for (int u = first * kVecs + lane; u < i * kVecs; u += 32) {
+          const int k = u / kVecs;
+          if (path.from[k] < 0) continue;
+          const float from = scales_of[warp][k];
+          *reinterpret_cast<uint4*>(c.base + path.dst[k] + u % kVecs * 16) = from == s.scale ? mine[u] : recoded(mine[u], from, s.scale);
         }
         __syncwarp();
-        rescale_page<D>(c, to, rows_of(ordinal), taken_of[warp], s.ratio);
+        if (lane == 0) *place = s.scale;
+        __syncwarp();
       }
-      for (int u = first * kVecs + lane; u < i * kVecs; u += 32) {
-        const int k = u / kVecs;
-        if (path.from[k] < 0) continue;
-        const float from = scales_of[warp][k];
-        *reinterpret_cast<uint4*>(c.base + path.dst[k] + u % kVecs * 16) = from == s.scale ? mine[u] : recoded(mine[u], from, s.scale);
-      }
-      __syncwarp();
-      if (lane == 0) *place = s.scale;
-      __syncwarp();
     }
-  }
   }
 }
 
@@ -457,21 +506,25 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const __grid_cons
   }
 }
 
-constexpr int kMoveStretch = 32;  // moves among which a warp's pages begin
+// Moves among which a warp's pages begin: more for large pages, of which it then has whole ones (32 requests, half of 8000 to
+// 16000 entries, pages of 32: 150 us with 32, 154 with 128; of 64: 253, 271; of 256: 347, 266).
+constexpr int kMoveStretch = 32, kMoveStretchLong = 128, kLongPage = 128;
 
 // Entries of a cache with page scales.  A warp takes the pages whose first move lies in its stretch of the list (targets
 // are in ascending order), as many at a time as have 32 moves together; a page with more goes by itself.  The page that the
 // context ends in holds sources of other pages' moves, whose scale is still needed: its own moves wait for a launch of their own.
 template <int D>
-__global__ void __launch_bounds__(kMoveWarps * 32) page_move_kernel(const __grid_constant__ MoveParams P) {
-  __shared__ uint32_t taken_of[kMoveWarps][SPEC_MAX_PAGE / 32];
+__global__ void __launch_bounds__(kMoveWarps * 32, 6) page_move_kernel(const __grid_constant__ MoveParams P) {
+  __shared__ Exchange exchange[kMoveWarps];
   pdl_launch_next();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int shift = P.cache.page_shift, page_size = 1 << shift, mask = page_size - 1;
+  const int stretch = page_size >= kLongPage ? kMoveStretchLong : kMoveStretch;
+  Exchange& x = exchange[warp];
+  const bool is_v = blockIdx.y & 1;
   for (int list = blockIdx.y >> 1; list < P.lists; list += gridDim.y >> 1) {
     const MoveList m(P, list);
-    const bool is_v = blockIdx.y & 1;
     const int last = m.end & mask ? m.end >> shift : -1;  // the page that the context ends in
     if (m.n == 0 || (P.last && last < 0)) continue;
     int begin = 0, stop = m.n;  // the moves that this launch takes
@@ -488,19 +541,15 @@ __global__ void __launch_bounds__(kMoveWarps * 32) page_move_kernel(const __grid
     const Side c = {(is_v ? P.cache.v : P.cache.k) + m.layer * P.cache.layer + m.head * P.cache.head,
                     (is_v ? P.scales.v : P.scales.k) + m.layer * P.scales.layer + m.head, P.heads, P.cache.slot, P.cache.page, page_size};
     const auto info = [&](int i) {
-      Move x = {false, 0, 0, 0, -1, lane, lane};
-      if (i >= stop) return x;
+      Move y = {false, 0, 0, 0, -1, lane, lane};
+      if (i >= stop) return y;
       int s, t;
-      x.is = m.pages(P, i, s, t, x.from, x.to);
-      if (x.is) x.src = x.from * P.cache.page + (s & mask) * P.cache.slot, x.dst = x.to * P.cache.page + (t & mask) * P.cache.slot;
-      return x;
+      y.is = m.pages(P, i, s, t, y.from, y.to);
+      if (y.is) y.src = y.from * P.cache.page + (s & mask) * P.cache.slot, y.dst = y.to * P.cache.page + (t & mask) * P.cache.slot;
+      return y;
     };
-    const auto record = [&](int i) {
-      int s, t, from, to;
-      if (!is_v && m.pages(P, i, s, t, from, to)) move_record(P, m, s, t, from, to);
-    };
-    for (int i0 = begin + (blockIdx.x * kMoveWarps + warp) * kMoveStretch; i0 < stop; i0 += gridDim.x * kMoveWarps * kMoveStretch) {
-      const int bound = min(i0 + kMoveStretch, stop);
+    for (int i0 = begin + (blockIdx.x * kMoveWarps + warp) * stretch; i0 < stop; i0 += gridDim.x * kMoveWarps * stretch) {
+      const int bound = min(i0 + stretch, stop);
       int before = i0 > begin ? m.target[i0 - 1] >> shift : -1 << 30;  // the page of the move before
       bool looking = true;  // for the first page that begins here
       for (int i = i0; i < bound;) {
@@ -521,15 +570,19 @@ __global__ void __launch_bounds__(kMoveWarps * 32) page_move_kernel(const __grid
         int n = behind ? __ffs(behind) - 1 : valid;
         if (n == 32 && next == __shfl_sync(~0u, page, 31)) n = 31 - __clz(starts);  // the last one goes on
         if (n > 0) {
-          Move x = info(lane < n ? i + lane : stop);
-          const uint32_t mine = starts & (lane == 31 ? ~0u : (2u << lane) - 1), after = lane == 31 ? 0u : starts & (~0u << (lane + 1));
+          Move y = {false, 0, 0, 0, -1, lane, lane};
+          int s = 0, t = 0;
           if (lane < n) {
-            x.lo = 31 - __clz(mine | 1), x.hi = min(after ? __ffs(after) - 2 : 31, n - 1);
-            if (page >= 0 && page << shift < m.end) x.to = m.page_of(P, page << shift);  // also where this move is left out
-            record(i + lane);
+            const uint32_t mine = starts & (lane == 31 ? ~0u : (2u << lane) - 1), after = lane == 31 ? 0u : starts & (~0u << (lane + 1));
+            y.is = m.pages(P, i + lane, s, t, y.from, y.to);
+            y.lo = 31 - __clz(mine | 1), y.hi = min(after ? __ffs(after) - 2 : 31, n - 1);
+            if (page >= 0 && page << shift < m.end) y.to = m.page_of(P, page << shift);  // also where this move is left out
+            if (y.is) {
+              y.src = y.from * P.cache.page + (s & mask) * P.cache.slot, y.dst = y.to * P.cache.page + (t & mask) * P.cache.slot;
+              if (!is_v) move_record(P, m, s, t, y.from, y.to);
+            }
           }
-          move_batch<D>(c, x, n, lane < n ? m.target[i + lane] & mask : 0, lane < n ? min(m.end - (page << shift), page_size) : 0,
-                        taken_of[warp]);
+          move_batch<D>(c, y, n, t & mask, lane < n ? min(m.end - (page << shift), page_size) : 0, x);
         } else {  // a page of more than 32 moves
           const int ordinal = __shfl_sync(~0u, page, 0);
           for (n = 32; i + n < stop;) {
@@ -541,10 +594,13 @@ __global__ void __launch_bounds__(kMoveWarps * 32) page_move_kernel(const __grid
             const int into = m.page_of(P, ordinal << shift);
             if (into >= 0)
               move_page<D>(
-                  c, n, into, min(m.end - (ordinal << shift), page_size), taken_of[warp],
+                  c, n, into, min(m.end - (ordinal << shift), page_size), x,
                   [&](int k) { return info(k < n ? i + k : stop); },
-                  [&](const Move& x) { return (int)((x.dst - into * P.cache.page) / P.cache.slot); });
-            for (int k = lane; k < n; k += 32) record(i + k);
+                  [&](const Move& y) { return (int)((y.dst - into * P.cache.page) / P.cache.slot); });
+            for (int k = lane; k < n && !is_v; k += 32) {
+              int s, t, from, to;
+              if (m.pages(P, i + k, s, t, from, to)) move_record(P, m, s, t, from, to);
+            }
           }
         }
         before = __shfl_sync(~0u, page, min(n, 32) - 1);
@@ -579,23 +635,14 @@ spec_status_t spec_kv_keep_ex(const spec_kv_cache_t* cache, const spec_kv_page_s
     s = spec_kv_keep(cache, batch, path, n_keep, max_keep, stream);
     if (s != SPEC_OK) return s;
   } else {
-    const int D = cache->head_dim, sides = cache->layers * cache->heads * 2;
-    const PageKeepParams P = {cache_of(cache), scales_of(scales), batch_of(batch, cache), path, n_keep, max_keep, cache->heads, sides};
-    const int64_t most = (sides + kPageKeepWarps - 1) / kPageKeepWarps, rounds = (most * batch->B + 1023) / 1024;
+    const int D = cache->head_dim, lists_each = cache->layers * cache->heads * 2;
+    const PageKeepParams P = {cache_of(cache), scales_of(scales), batch_of(batch, cache), path, n_keep, max_keep, cache->heads, lists_each};
+    const int64_t most = (lists_each + kPageKeepWarps - 1) / kPageKeepWarps, rounds = (most * batch->B + 2047) / 2048;
     const dim3 grid((unsigned)((most + rounds - 1) / rounds), batch->B), block(kPageKeepWarps * 32);
     const bool big = max_keep > 32;
     const size_t smem = big ? (size_t)kPageKeepWarps * SPEC_MAX_NEW * D : 0;
     auto kern = big ? (D == 128 ? page_keep_kernel<128, true> : page_keep_kernel<64, true>)
                     : (D == 128 ? page_keep_kernel<128, false> : page_keep_kernel<64, false>);
-    if (big && D == 128) {  // 64 KB
-      int dev = 0, sms = 0;
-      if (device_sms(&dev, &sms) != cudaSuccess) return SPEC_ERR_CUDA;
-      static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory is set
-      if (!((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SPEC_ERR_CUDA;
-        ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-      }
-    }
     if (launch_early(kern, grid, block, smem, st, P) != cudaSuccess) return SPEC_ERR_CUDA;
   }
   if (record && (record->weight || record->position)) {
@@ -626,8 +673,8 @@ spec_status_t spec_kv_move(const spec_kv_cache_t* cache, const spec_kv_page_scal
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 block(kMoveWarps * 32);
   // blocks for the lists, and more for each where there are few; a list's moves go round its blocks
-  const int sides = scales ? 2 : 1;
-  const int64_t rows = lists * sides, most = ((int64_t)max_moves + kMoveWarps * 32 - 1) / (kMoveWarps * 32);
+  const int64_t most = ((int64_t)max_moves + kMoveWarps * 32 - 1) / (kMoveWarps * 32);
+  const int64_t rows = lists * (scales ? 2 : 1);
   const unsigned y = (unsigned)(rows < 65534 ? rows : 65534);
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != cudaSuccess) return SPEC_ERR_CUDA;

@@ -32,19 +32,21 @@ struct SelectParams {
 
 constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kRun = 128;  // slots that a warp takes at a time
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kNoKey = 0x007FFFFFu;  // of -infinity
 
 struct SelectState {
-  int bins[kBins];
+  alignas(16) int bins[kBins];
   int warp_sum[kSelectWarps];
-  int digit, above;
-  int counts[4];                    // of the block: larger, equal; and of those the ones below m
+  int digit, above, whole;
+  alignas(16) int counts[4];                    // of the block: larger, equal; and of those the ones below m
   int warp_counts[2][kSelectWarps];
+  alignas(16) uint32_t turned[kSelectWarps][kRun];  // keys of a warp's run that the block does not hold
 };
 
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ SelectParams P) {
-  extern __shared__ uint32_t keys[];  // [held]
+__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_constant__ SelectParams P) {
+  extern __shared__ __align__(16) uint32_t keys[];  // [held]
   __shared__ SelectState st;
   pdl_launch_next();
   pdl_wait();
@@ -66,51 +68,56 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
   const int64_t base = layer * P.record.layer;
   // A larger key is a larger weight; +0 and -0 are one.
   const auto key = [&](float w, int position) -> uint32_t {
-    w += 0.0f;
-    if (w != w) w = -INFINITY;
-    if (P.record.position && (position < P.first || position >= recent)) w = INFINITY;
-    const uint32_t bits = __float_as_uint(w);
-    return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
+    w = w != w ? -INFINITY : w + 0.0f;
+    if (position < P.first || position >= recent) w = INFINITY;
+    const int bits = __float_as_int(w);
+    return bits ^ ((bits >> 31) | 0x80000000);
   };
-  const auto place_of = [&](int slot) -> int64_t {  // -1: in a page outside the pool
+  // The keys of four slots that lie in one page, of which the last may be behind the context.
+  const auto keys_of = [&](int slot) -> uint4 {
     const int page = __ldg(table + (slot >> P.page_shift));
-    return page < 0 || page >= P.num_pages ? -1 : base + (((int64_t)page * P.heads + head) << P.page_shift) + (slot & mask);
+    if (page < 0 || page >= P.num_pages) return make_uint4(kNoKey, kNoKey, kNoKey, kNoKey);
+    const int64_t at = base + (((int64_t)page * P.heads + head) << P.page_shift) + (slot & mask);
+    const float4 w = *reinterpret_cast<const float4*>(P.record.weight + at);
+    int4 p = make_int4(P.first, P.first, P.first, P.first);
+    if (P.record.position) p = *reinterpret_cast<const int4*>(P.record.position + at);
+    return make_uint4(key(w.x, p.x), key(w.y, p.y), key(w.z, p.z), key(w.w, p.w));
   };
-  const auto key_of = [&](int slot) {
-    const int64_t at = place_of(slot);
-    return at < 0 ? kNoKey : key(P.record.weight[at], P.record.position ? P.record.position[at] : 0);
+  // this block's slots, whole runs of 128 of them
+  const int runs = (ctx + kRun - 1) / kRun, share = (runs + blocks - 1) / blocks;
+  const int run0 = min(rank * share, runs), run1 = min(run0 + share, runs);
+  const int slot0 = run0 * kRun, n = max(min(run1 * kRun, ctx) - slot0, 0);
+  // four keys from i on, 0 (less than any) behind the last one
+  const auto keys_at = [&](int i) -> uint4 {
+    if (i < P.held) return *reinterpret_cast<const uint4*>(&keys[i]);
+    uint4 x = keys_of(slot0 + i);
+    if (i + 3 >= n) x.y = i + 1 < n ? x.y : 0, x.z = i + 2 < n ? x.z : 0, x.w = 0;
+    return x;
   };
-  // this block's slots, whole words of 32 of them, and this warp's
-  const int words = (ctx + 31) / 32, share = (words + blocks - 1) / blocks;
-  const int word0 = min(rank * share, words), word1 = min(word0 + share, words);
-  const int slot0 = word0 * 32, n = min(word1 * 32, ctx) - slot0;
-  const auto key_at = [&](int i) { return i < P.held ? keys[i] : key_of(slot0 + i); };
 
   for (int i = threadIdx.x; i < kBins; i += kSelectThreads) st.bins[i] = 0;
   __syncthreads();
-  // the keys, with the first digit's histogram: kAhead in flight a thread
-  constexpr int kAhead = 8;
-  for (int i0 = threadIdx.x; i0 < n; i0 += kSelectThreads * kAhead) {
-    float weight[kAhead];
-    int position[kAhead];
-    uint32_t in = 0;
+  // the keys, with the first digit's histogram: kAhead loads in flight a thread
+  constexpr int kAhead = 4;
+  const int whole = (run1 - run0) * kRun;  // up to a run's end: 0 behind the last key
+  for (int i0 = threadIdx.x * 4; i0 < whole; i0 += kSelectThreads * 4 * kAhead) {
+    uint4 x[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int i = i0 + k * kSelectThreads;
-      weight[k] = -INFINITY, position[k] = P.first;
-      const int64_t at = i < n ? place_of(slot0 + i) : -1;
-      if (at >= 0) {
-        weight[k] = P.record.weight[at], in |= 1u << k;
-        if (P.record.position) position[k] = P.record.position[at];
-      }
+      const int i = i0 + k * kSelectThreads * 4;
+      x[k] = make_uint4(0, 0, 0, 0);
+      if (i < n) x[k] = keys_of(slot0 + i);
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int i = i0 + k * kSelectThreads;
-      if (i >= n) break;
-      const uint32_t x = (in >> k) & 1 ? key(weight[k], position[k]) : kNoKey;
-      if (i < P.held) keys[i] = x;
-      atomicAdd(&st.bins[x >> 21], 1);
+      const int i = i0 + k * kSelectThreads * 4;
+      if (i >= whole) break;
+      if (i + 3 >= n) x[k].y = i + 1 < n ? x[k].y : 0, x[k].z = i + 2 < n ? x[k].z : 0, x[k].w = 0;
+      if (i < P.held) *reinterpret_cast<uint4*>(&keys[i]) = x[k];
+      if (x[k].x) atomicAdd(&st.bins[x[k].x >> 21], 1);
+      if (x[k].y) atomicAdd(&st.bins[x[k].y >> 21], 1);
+      if (x[k].z) atomicAdd(&st.bins[x[k].z >> 21], 1);
+      if (x[k].w) atomicAdd(&st.bins[x[k].w >> 21], 1);
     }
   }
   uint32_t prefix = 0;
@@ -121,20 +128,25 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     if (digit > 0) {
       for (int i = threadIdx.x; i < kBins; i += kSelectThreads) st.bins[i] = 0;
       __syncthreads();
-      const int above = digit == 1 ? 21 : 10;  // bits that have to agree
-      for (int i = threadIdx.x; i < n; i += kSelectThreads) {
-        const uint32_t key = key_at(i);
-        if (key >> above == prefix >> above) atomicAdd(&st.bins[(key >> shift) & (digit == 1 ? 2047 : 1023)], 1);
+      const uint32_t above = digit == 1 ? 0xFFE00000u : 0xFFFFFC00u;  // bits that have to agree
+      const auto count = [&](uint32_t key) {
+        if (((key ^ prefix) & above) == 0) atomicAdd(&st.bins[(key >> shift) & (digit == 1 ? 2047 : 1023)], 1);
+      };
+      for (int i = threadIdx.x * 4; i < n; i += kSelectThreads * 4) {
+        const uint4 x = keys_at(i);
+        count(x.x), count(x.y), count(x.z), count(x.w);
       }
     }
     cluster.sync();
     // this thread's four bins, from the top, over all blocks
     const int top = kBins - 4 - threadIdx.x * 4;
-    int4 sum = make_int4(0, 0, 0, 0);
-    for (int r = 0; r < blocks; ++r) {
-      const int4 x = *reinterpret_cast<const int4*>(cluster.map_shared_rank(&st.bins[top], r));
-      sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
-    }
+    int4 sum = make_int4(0, 0, 0, 0), of_block[kMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)  // all in flight
+      if (r < blocks) of_block[r] = *reinterpret_cast<const int4*>(cluster.map_shared_rank(&st.bins[top], r));
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r)
+      if (r < blocks) sum.x += of_block[r].x, sum.y += of_block[r].y, sum.z += of_block[r].z, sum.w += of_block[r].w;
     const int mine = sum.x + sum.y + sum.z + sum.w;
     int before = mine;
 #pragma unroll
@@ -145,33 +157,59 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     if (lane == 31) st.warp_sum[warp] = before;
     before -= mine;
     cluster.sync();  // every block has read the bins
-#pragma unroll
-    for (int w = 0; w < kSelectWarps; ++w)
-      if (w < warp) before += st.warp_sum[w];
+    before += __reduce_add_sync(~0u, lane < warp ? st.warp_sum[lane] : 0);
     if (before < left && before + mine >= left) {  // one thread's
       int bin = top + 3;
       const int four[4] = {sum.w, sum.z, sum.y, sum.x};
 #pragma unroll
       for (int k = 0; k < 3; ++k)
         if (bin == top + 3 - k && before + four[k] < left) before += four[k], --bin;
-      st.digit = bin, st.above = before;
+      const int in_bin = bin == top + 3 ? sum.w : bin == top + 2 ? sum.z : bin == top + 1 ? sum.y : sum.x;
+      st.digit = bin, st.above = before, st.whole = before + in_bin == left;
     }
     __syncthreads();
     prefix |= (uint32_t)st.digit << shift;
     left -= st.above;
+    if (st.whole) {  // all of the bin's keys stay, and the lower digits do not matter
+      prefix -= 1, left = 0;
+      break;
+    }
   }
-  // `left` of the keys equal to prefix stay, the lowest slots first.  Counts: of each warp's stretch, of the block, of the cluster
-  const int mine_words = (word1 - word0 + kSelectWarps - 1) / kSelectWarps;
-  const int first_word = min(word0 + warp * mine_words, word1), last_word = min(first_word + mine_words, word1);
-  int larger = 0, equal = 0, larger_below = 0, equal_below = 0;
+  // `left` of the keys equal to prefix stay, the lowest slots first.  A warp takes runs of 128 slots, a word of 32 at a time:
+  // what stays is a word of bits, and its counts are the warp's, of the block, of the cluster.
+  const int mine_runs = (run1 - run0 + kSelectWarps - 1) / kSelectWarps;
+  const int first_run = min(run0 + warp * mine_runs, run1), last_run = min(first_run + mine_runs, run1);
+  const auto run_keys = [&](int r, uint32_t (&x)[4]) {  // lane l has slots r * 128 + l, + 32, ...
+    const int i = r * kRun - slot0;
+    if (i < P.held) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = keys[i + j * 32 + lane];
+    } else {  // turned from four slots a lane
+      const uint4 y = i + lane * 4 < n ? keys_at(i + lane * 4) : make_uint4(0, 0, 0, 0);
+      __syncwarp();
+      *reinterpret_cast<uint4*>(&st.turned[warp][lane * 4]) = y;
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = st.turned[warp][j * 32 + lane];
+    }
+  };
+  int larger = 0, equal = 0, larger_below = 0, equal_below = 0;  // this lane's, then the warp's
   if (threadIdx.x < 4) st.counts[threadIdx.x] = 0;
-  for (int w = first_word; w < last_word; ++w) {
-    const int slot = w * 32 + lane;
-    const uint32_t key = slot < ctx ? key_at(slot - slot0) : 0;
-    const uint32_t gt = __ballot_sync(~0u, slot < ctx && key > prefix), eq = __ballot_sync(~0u, slot < ctx && key == prefix);
-    const uint32_t below = m - w * 32 >= 32 ? ~0u : m <= w * 32 ? 0u : (1u << (m - w * 32)) - 1;
-    larger += __popc(gt), equal += __popc(eq), larger_below += __popc(gt & below), equal_below += __popc(eq & below);
+  for (int r = first_run; r < last_run; ++r) {
+    uint32_t x[4];
+    run_keys(r, x);
+    if (r * kRun <= m && m < r * kRun + kRun) {  // m lies in it
+      larger_below = larger, equal_below = equal;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (r * kRun + j * 32 + lane < m) larger_below += x[j] > prefix, equal_below += x[j] == prefix;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) larger += x[j] > prefix, equal += x[j] == prefix;
   }
+  if (last_run * kRun <= m) larger_below = larger, equal_below = equal;
+  larger = __reduce_add_sync(~0u, larger), equal = __reduce_add_sync(~0u, equal);
+  larger_below = __reduce_add_sync(~0u, larger_below), equal_below = __reduce_add_sync(~0u, equal_below);
   __syncthreads();
   if (lane == 0) {
     st.warp_counts[0][warp] = larger, st.warp_counts[1][warp] = equal;
@@ -180,28 +218,45 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
   }
   cluster.sync();
   int G = 0, E = 0, G_below = 0, E_below = 0;
-  for (int r = 0; r < blocks; ++r) {
-    const int* c = cluster.map_shared_rank(st.counts, r);
-    if (r < rank) G += c[0], E += c[1];
-    G_below += c[2], E_below += c[3];
-  }
-  cluster.sync();  // no block leaves while its counts are read
-  for (int w = 0; w < warp; ++w) G += st.warp_counts[0][w], E += st.warp_counts[1][w];
+  int4 of_block[kMaxCluster];
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < blocks) of_block[r] = *reinterpret_cast<const int4*>(cluster.map_shared_rank(st.counts, r));
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r)
+    if (r < blocks) {
+      if (r < rank) G += of_block[r].x, E += of_block[r].y;
+      G_below += of_block[r].z, E_below += of_block[r].w;
+    }
+  G += __reduce_add_sync(~0u, lane < warp ? st.warp_counts[0][lane] : 0), E += __reduce_add_sync(~0u, lane < warp ? st.warp_counts[1][lane] : 0);
   const int below_m = G_below + min(E_below, left);  // what stays below m
   if (tells) P.moves[list] = min(m - below_m, P.max_moves);
   int32_t* source = P.source + (int64_t)list * P.max_moves;
   int32_t* target = P.target + (int64_t)list * P.max_moves;
-  for (int w = first_word; w < last_word; ++w) {
-    const int slot = w * 32 + lane;
-    const uint32_t key = slot < ctx ? key_at(slot - slot0) : 0;
-    const bool is_eq = slot < ctx && key == prefix;
-    const uint32_t gt = __ballot_sync(~0u, slot < ctx && key > prefix), eq = __ballot_sync(~0u, is_eq), lower = (1u << lane) - 1;
-    const int e = E + __popc(eq & lower), k = G + __popc(gt & lower) + min(e, left);
-    const bool stays = ((gt >> lane) & 1) || (is_eq && e < left);
-    if (slot < m && !stays && slot - k < P.max_moves) target[slot - k] = slot;
-    if (slot >= m && stays && k - below_m < P.max_moves) source[k - below_m] = slot;
-    G += __popc(gt), E += __popc(eq);
+  const uint32_t lower = (1u << lane) - 1;
+  for (int r = first_run; r < last_run; ++r) {
+    uint32_t x[4];
+    run_keys(r, x);
+    const bool below = r * kRun + kRun <= m, above = r * kRun >= m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int slot = r * kRun + j * 32 + lane, before = G + min(E, left);  // `before` stay of the slots before these 32
+      uint32_t stays = __ballot_sync(~0u, x[j] > prefix);
+      const uint32_t eq = __ballot_sync(~0u, x[j] == prefix);
+      if (eq) {  // few words have any
+        G += __popc(stays);
+        stays |= __ballot_sync(~0u, ((eq >> lane) & 1) && E + __popc(eq & lower) < left);
+        E += __popc(eq);
+      }
+      const bool mine = (stays >> lane) & 1;
+      const int k = __popc(stays & lower);
+      if (!eq) G += __shfl_sync(~0u, k + mine, 31);  // (a count of bits takes longer)
+      const int t = slot - before - k, c = before - below_m + k;
+      if (!mine && (below || (!above && slot < m)) && t < P.max_moves) target[t] = slot;
+      if (mine && (above || (!below && slot >= m)) && c < P.max_moves) source[c] = slot;
+    }
   }
+  cluster.sync();  // no block leaves while its counts are read
 }
 
 }  // namespace sv
@@ -218,7 +273,8 @@ extern "C" spec_status_t spec_kv_select(const spec_kv_record_t* record, const sp
   sizes.page_size = record->page_size;
   s = check_batch(batch, &sizes);
   if (s != SPEC_OK) return s;
-  if (first < 0 || recent < 0 || max_moves < 0 || !record->weight || ((first > 0 || recent > 0) && !record->position))
+  if (first < 0 || recent < 0 || max_moves < 0 || !record->weight || ((uintptr_t)record->weight & 15u) || ((uintptr_t)record->position & 15u) || record->layer_stride % 4 ||
+      ((first > 0 || recent > 0) && !record->position))
     return SPEC_ERR_INVALID_ARG;
   const int64_t lists = (int64_t)record->layers * batch->B * record->heads;
   if (lists > 0x0fffffffll || batch->B > SPEC_MAX_BATCH) return SPEC_ERR_UNSUPPORTED;
@@ -238,8 +294,8 @@ extern "C" spec_status_t spec_kv_select(const spec_kv_record_t* record, const sp
   int blocks = 1;
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != cudaSuccess) return SPEC_ERR_CUDA;
-  while (blocks < kMaxCluster && slots > 4096 * blocks && (lists * blocks < 4 * sms || slots > (int64_t)kMostHeld * blocks)) blocks *= 2;
-  const int64_t stretch = ((slots + 31) / 32 + blocks - 1) / blocks * 32;
+  while (blocks < kMaxCluster && ((slots > 4096 * blocks && lists * blocks * 2 <= sms) || slots > (int64_t)kMostHeld * blocks)) blocks *= 2;
+  const int64_t stretch = ((slots + kRun - 1) / kRun + blocks - 1) / blocks * kRun;
   P.held = (int)(stretch < kMostHeld ? stretch : kMostHeld);
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory is set
   if (!((ready.load(std::memory_order_relaxed) >> dev) & 1)) {

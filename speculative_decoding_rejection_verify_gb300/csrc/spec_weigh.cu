@@ -46,10 +46,15 @@ struct WeighShape {
   static_assert(kSlots >= 3, "the ring holds three tiles at least");
   static constexpr int kGroups = 4;                     // warpgroups that add up, each every kGroups-th tile of an item,
   static constexpr int kColumns = NT * kGroups;         // with a buffer of scores of its own
-  static constexpr int kAddWarps = 4 * kGroups, kProducer = kAddWarps, kIssuer = kAddWarps + 1;
-  static constexpr int kPrepare = kIssuer + 1, kPrepareWarps = 2;
-  static constexpr int kThreads = (kAddWarps + 2 + kPrepareWarps) * 32;
-  static constexpr int kChunk = NT < 32 ? 16 : 32;
+  static constexpr int kAddWarps = 4 * kGroups;
+  static constexpr int kProducer = kAddWarps, kProducers = 2;  // each every other tile
+  static constexpr int kIssuer = kProducer + kProducers;
+  static constexpr int kPrepare = kIssuer + 1, kPrepareWarps = F8 && NT > 32 ? 4 : 1;
+  // 20 warps or 24, the last one idle: more rows take longer to split (128 rows, 4 requests' worth of 20 tiles an SM: 68 us with
+  // one warp, 57 with four), fewer leave registers for twice as many scores at a time (28 rows: 104 us against 110).
+  static constexpr int kThreads = kPrepareWarps == 4 ? 768 : 640;
+  static_assert(kThreads % 128 == 0, "whole warpgroups");
+  static constexpr int kChunk = kPrepareWarps == 4 || NT < 32 ? 16 : 32;  // scores a thread has in registers
 
   struct State {
     uint64_t ring_full[12], ring_empty[12];
@@ -59,14 +64,13 @@ struct WeighShape {
     uint64_t products_done;                       // behind a wait that ran out
     uint32_t tmem;
     int dead;
-    int copies, queries;                          // tiles and Qs whose copies were issued
+    int copies[kProducers], queries;              // tiles and Qs whose copies were issued, up to the last one
     int start_b, start_offset;
     int warp_sum[kThreads / 32];
-    int plain[2][kPrepareWarps];                  // every row that a warp looked at has a finite sum
     alignas(16) float shift[2][NT];               // -lse in log2 units; -inf: the row has no part
     alignas(16) float mult[2][F8 ? NT : 4];       // E4M3: a score's factor to log2 units
     uint64_t rule[2][SPEC_MAX_NEW];               // which new tokens the pass's tokens attend to
-    int token[NT];                                // of a row, within the pass
+    uint32_t active[2][(NT + 31) / 32];           // rows that have a part
   };
   static constexpr int kState = 2 * kQ + kSlots * kRing;
   static constexpr int kBytes = kState + (int)sizeof(State) + 1024;
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
 
   pdl_launch_next();
   if (threadIdx.x == 0) {
-    st->dead = 0;
+    st->dead = st->queries = 0;
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(smem_addr(&st->ring_full[i]), 1);
       mbar_init(smem_addr(&st->ring_empty[i]), 1);
@@ -105,7 +109,6 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
     mbar_init(smem_addr(&st->products_done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = threadIdx.x; i < NT; i += S::kThreads) st->token[i] = i / P.group;
   // Nothing before this reads or writes what another kernel may, nor takes TMEM that one before it may still need.
   pdl_wait();
   if (warp == S::kIssuer) {
@@ -124,8 +127,9 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
   // The warpgroup that has a tile: the same in every pass, another for another head, as short items have but one.
   const auto owner = [](const Segment& s, int tile) { return (tile + s.head + s.b) & (S::kGroups - 1); };
 
-  if (warp == S::kProducer) {
-    // ---- TMA: Q of every pass and K of every tile, page by page ----
+  if (warp >= S::kProducer && warp < S::kIssuer) {
+    // ---- TMA: K of every tile, page by page, by two warps in turn (copies of 8 or 16 slots take one longer than they take
+    // the memory: 64 x 7 tokens, E4M3, pages of 16: 155 us with one, 122 with two) ----
     const auto uniform = [](int x) { return __shfl_sync(~0u, x, 0); };
     const int shift = uniform(P.cache.page_shift), page = 1 << shift;
     const int box = min(page, kTileSlots);  // slots of one copy
@@ -133,7 +137,8 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
     constexpr int kParts = F8 ? 1 : S::kHalves;
     const uint32_t base = uniform(smem_addr(smem)), bars = uniform(smem_addr(st));
     const auto bar_of = [&](const uint64_t* x) { return bars + (uint32_t)(reinterpret_cast<const char*>(x) - reinterpret_cast<const char*>(st)); };
-    int slot = 0, issued = 0, queries = 0;
+    const int me = uniform(warp - S::kProducer);
+    int slot = 0, nth = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
     while (ok && walk.next(s)) {
@@ -146,26 +151,22 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
         return p < 0 || p > P.cache.num_pages ? P.cache.num_pages : p;
       };
       for (int pass = 0; ok && pass < passes; ++pass) {
-        const int qb = queries & 1;
-        ok = mbar_wait_warp(bar_of(&st->q_empty[qb]), ((queries >> 1) & 1) ^ 1, dead);
-        if (!ok) break;
-        const uint32_t bar = bar_of(&st->q_loaded[qb]);
-        if (lane == 0) mbar_expect(bar, P.rows * D * 2);
-        __syncwarp();
-#pragma unroll
-        for (int h = 0; h < S::kHalves; ++h)
-          tma_load(base + qb * S::kQ + h * NT * 128, &P.q_map, h * 64, head * P.group, pass * P.tokens, uniform(s.b), bar);
-        ++queries;
-        int next_page = entry(tile0);
+        const int mine = tile0 + ((nth ^ me) & 1);
+        int next_page = mine < tile1 ? entry(mine) : P.cache.num_pages;
         for (int tile = tile0; tile < tile1; ++tile) {
+          const bool other = (nth++ ^ me) & 1;
+          const int at_slot = slot;
+          const uint32_t at_phase = phase;
+          if (++slot == S::kSlots) slot = 0, phase ^= 1;
+          if (other) continue;
           const int my_page = next_page;
-          if (tile + 1 < tile1) next_page = entry(tile + 1);
-          ok = mbar_wait_warp(bar_of(&st->ring_empty[slot]), phase ^ 1, dead);
+          if (tile + 2 < tile1) next_page = entry(tile + 2);
+          ok = mbar_wait_warp(bar_of(&st->ring_empty[at_slot]), at_phase ^ 1, dead);
           if (!ok) break;
-          const uint32_t bar = bar_of(&st->ring_full[slot]);
+          const uint32_t bar = bar_of(&st->ring_full[at_slot]);
           if (lane == 0) mbar_expect(bar, S::kRing);
           __syncwarp();
-          const uint32_t dst = base + 2 * S::kQ + slot * S::kRing;
+          const uint32_t dst = base + 2 * S::kQ + at_slot * S::kRing;
           const auto bring = [&](auto tag) {
             constexpr int N = decltype(tag)::value;  // copies, of kTileSlots / N slots
             const int row = N == 1 ? (tile * kTileSlots) & (page - 1) : 0;
@@ -183,12 +184,11 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
           else if (copies == 4) bring(std::integral_constant<int, 4>{});
           else if (copies == 8) bring(std::integral_constant<int, 8>{});
           else bring(std::integral_constant<int, 16>{});
-          ++issued;
-          if (++slot == S::kSlots) slot = 0, phase ^= 1;
+          issued = nth;
         }
       }
     }
-    if (lane == 0) st->copies = issued, st->queries = queries;
+    if (lane == 0) st->copies[me] = issued;
   } else if (warp == S::kIssuer) {
     // ---- scores: a tile as soon as it is there and a buffer is free ----
     const auto uniform = [](uint32_t x) { return __shfl_sync(~0u, x, 0); };
@@ -233,9 +233,14 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (warp >= S::kPrepare + S::kPrepareWarps) {
+    // (so that the block has whole warpgroups)
   } else if (warp >= S::kPrepare) {
-    // ---- what each pass knows of its rows: sums, factors, rules; over E4M3 keys, Q split ----
-    const int tid = threadIdx.x - S::kPrepare * 32;
+    // ---- what each pass knows of its rows, up to two passes ahead: Q (over E4M3 keys split), sums, factors, rules ----
+    const auto uniform = [](int x) { return __shfl_sync(~0u, x, 0); };
+    const uint32_t base = uniform(smem_addr(smem)), bars = uniform(smem_addr(st));
+    const auto bar_of = [&](const uint64_t* x) { return bars + (uint32_t)(reinterpret_cast<const char*>(x) - reinterpret_cast<const char*>(st)); };
+    const int tid = threadIdx.x - S::kPrepare * 32, me = uniform(tid / 32);
     constexpr int kCount = S::kPrepareWarps * 32;
     int nth = 0;
     bool ok = true;
@@ -243,27 +248,37 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
       const int passes = passes_of(s);
       for (int pass = 0; ok && pass < passes; ++pass, ++nth) {
         const int qb = nth & 1, t0 = pass * P.tokens, rows = min(s.tokens - t0, P.tokens) * P.group;
+        if (me == 0) {
+          ok = mbar_wait_warp(bar_of(&st->q_empty[qb]), ((nth >> 1) & 1) ^ 1, dead);
+          if (!ok) break;
+          const uint32_t bar = bar_of(&st->q_loaded[qb]);
+          if (lane == 0) mbar_expect(bar, P.rows * D * 2), st->queries = nth + 1;
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < S::kHalves; ++h)
+            tma_load(base + qb * S::kQ + h * NT * 128, &P.q_map, h * 64, uniform(s.head) * P.group, uniform(t0), uniform(s.b), bar);
+        }
         ok = mbar_wait_warp(smem_addr(&st->rows_empty[qb]), ((nth >> 1) & 1) ^ 1, dead);
         if (!ok) break;
-        bool finite = true;
-        for (int r = tid; r < NT; r += kCount) {
+        for (int r0 = me * 32; r0 < NT; r0 += kCount) {
+          const int r = r0 + lane;
           float x = -INFINITY;
           if (r < rows) {
             const int t = t0 + r / P.group, g = r % P.group;
             x = -P.lse[(((int64_t)s.b * P.batch.T + t) * P.heads + s.head) * P.group + g] * kLog2e;
-            if (fabsf(x) == INFINITY) x = -INFINITY, finite = false;
+            if (fabsf(x) == INFINITY) x = -INFINITY;
           }
-          st->shift[qb][r] = x;
+          if (r < NT) st->shift[qb][r] = x;
+          const uint32_t word = __ballot_sync(~0u, r < rows && !(x == -INFINITY));
+          if (lane == 0) st->active[qb][r0 / 32] = word;
         }
-        finite = __all_sync(~0u, finite);
-        if (lane == 0) st->plain[qb][warp - S::kPrepare] = finite;
         for (int t = tid; t < min(P.tokens, s.tokens - t0); t += kCount)
           st->rule[qb][t] = P.mask ? (uint64_t)__ldg(P.mask + (int64_t)s.b * P.batch.T + t0 + t) : t0 + t >= 63 ? ~0ull : (2ull << (t0 + t)) - 1;
         if constexpr (F8) {
           ok = mbar_wait_warp(smem_addr(&st->q_loaded[qb]), (nth >> 1) & 1, dead);
           if (!ok) break;
           const float c = P.scale_log2 * (!PAGES && P.cache.k_scale ? __ldg(P.cache.k_scale + s.head) : 1.0f);
-          split_queries<D, NT, kCount>(q_buf + qb * S::kQ, tid, c, st->mult[qb]);
+          split_queries<D, NT, kCount>(q_buf + qb * S::kQ, tid, (rows + 15) & ~15, c, st->mult[qb]);
           fence_async_shared();
         }
         __syncwarp();
@@ -296,7 +311,11 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
         const int qb = nth & 1, t0 = pass * P.tokens, rows = min(s.tokens - t0, P.tokens) * P.group;
         ok = ok && mbar_wait(smem_addr(&st->rows_full[qb]), (nth >> 1) & 1, dead);
         __syncwarp();
-        const bool plain = __shfl_sync(~0u, st->plain[qb][0] && st->plain[qb][1], 0);
+        bool plain = true;  // every row has a part
+#pragma unroll
+        for (int r0 = 0; r0 < NT; r0 += 32)
+          if (r0 < rows) plain = plain && st->active[qb][r0 / 32] == (rows - r0 >= 32 ? ~0u : (1u << (rows - r0)) - 1);
+        plain = __all_sync(~0u, plain);
         // what a slot has and its page's scale come a tile (of this warpgroup) ahead, its page two
         const int mine = s.tile0 + ((wg - owner(s, s.tile0)) & (S::kGroups - 1));
         int page = page_of(mine), next_page = page_of(mine + S::kGroups);
@@ -330,12 +349,27 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
           const auto add = [&](int c0, auto tag) {
             constexpr bool CHECKED = decltype(tag)::value;
             float z[CK];
-            __syncwarp();
+            uint32_t see = ~0u;  // columns, from c0 on, that have a part in this slot
+            if constexpr (CHECKED) {
+              see = st->active[qb][c0 / 32] >> (c0 & 31);
+              const int fresh = slot - s.ctx;
+              if (fresh >= 0 && fresh < 64)
+                for (int t = c0 / P.group; t * P.group < min(rows, c0 + CK); ++t)
+                  if (!((st->rule[qb][t] >> fresh) & 1)) {
+                    const int from = max(t * P.group - c0, 0), to = min((t + 1) * P.group - c0, CK);
+                    see &= ~((to == 32 ? ~0u : (1u << to) - 1) & (~0u << from));
+                  }
+              __syncwarp();
+            }
             if constexpr (CK == 32) {
               tm_load<16>(lanes + wg * NT + c0, reinterpret_cast<float(&)[16]>(z[0]));
               tm_load<16>(lanes + wg * NT + c0 + 16, reinterpret_cast<float(&)[16]>(z[CK - 16]));
             } else {
               tm_load<CK>(lanes + wg * NT + c0, z);
+            }
+            if (c0 + CK >= rows) {  // the last scores are in registers: the buffer is the next tile's
+              tc_fence_before();
+              if (lane == 0) mbar_arrive(smem_addr(&st->s_empty[wg]));
             }
 #pragma unroll
             for (int i = 0; i < CK; i += 4) {
@@ -351,12 +385,8 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
                 w0.y = c0 + i + 1 < rows ? w0.y : 0.0f, w1.x = c0 + i + 2 < rows ? w1.x : 0.0f, w1.y = 0.0f;
               }
               if constexpr (CHECKED) {  // so may rows without a part
-                const int fresh = slot - s.ctx;
-                const auto has = [&](float shift, int c) {
-                  return shift > -INFINITY && (fresh < 0 || ((st->rule[qb][st->token[c]] >> (fresh & 63)) & 1));
-                };
-                w0.x = has(m.x, c0 + i) ? w0.x : 0.0f, w0.y = has(m.y, c0 + i + 1) ? w0.y : 0.0f;
-                w1.x = has(m.z, c0 + i + 2) ? w1.x : 0.0f, w1.y = has(m.w, c0 + i + 3) ? w1.y : 0.0f;
+                w0.x = (see >> i) & 1 ? w0.x : 0.0f, w0.y = (see >> (i + 1)) & 1 ? w0.y : 0.0f;
+                w1.x = (see >> (i + 2)) & 1 ? w1.x : 0.0f, w1.y = (see >> (i + 3)) & 1 ? w1.y : 0.0f;
               }
               sum = add2(sum, add2(w0, w1));
             }
@@ -366,9 +396,6 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
             for (int c0 = 0; c0 < rows; c0 += CK) add(c0, std::true_type{});
           else
             for (int c0 = 0; c0 < rows; c0 += CK) add(c0, std::false_type{});
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&st->s_empty[wg]));
           if (to) {
             *to = ok ? before + (sum.x + sum.y) : NAN;
             if (pass == 0 && slot >= s.ctx && P.record.position) {
@@ -396,9 +423,10 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kColumns));
   }
   if (lost && warp == S::kProducer) {
-    // a slot is filled again only when its last filling was used: the last copies of each are the ones that may be in flight
-    for (int i = max(st->copies - S::kSlots, 0); i < st->copies; ++i)
-      mbar_drain(smem_addr(&st->ring_full[i % S::kSlots]), (i / S::kSlots) & 1);
+    // a slot is filled again only when its last filling was used: the last copy of each is the one that may be in flight
+    const int copies = max(st->copies[0], st->copies[1]);
+    for (int i = max(copies - S::kSlots - 1, 0); i < copies; ++i)
+      if (i < st->copies[i & 1]) mbar_drain(smem_addr(&st->ring_full[i % S::kSlots]), (i / S::kSlots) & 1);
     for (int i = max(st->queries - 2, 0); i < st->queries; ++i) mbar_drain(smem_addr(&st->q_loaded[i & 1]), (i >> 1) & 1);
   }
 }
@@ -463,7 +491,7 @@ extern "C" spec_status_t spec_kv_weigh(const spec_heads_t* q, int32_t q_heads, c
   P.rows = P.group * P.tokens;
   P.row_groups = 1;
   P.scale_log2 = scale * kLog2e;
-  P.item_cost = 1;
+  P.item_cost = cache->dtype == SPEC_DTYPE_E4M3 ? 4 : 1;
   P.wait_tries = g_test_hooks.load(std::memory_order_relaxed) & 2 ? 0 : kWaitTries;
   const int64_t per = ((int64_t)P.batch.slots + kTileSlots - 1) / kTileSlots;
   const int64_t most = (int64_t)batch->B * cache->heads * ((per > 0 ? per : 1) + P.item_cost);

@@ -230,13 +230,13 @@ __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lead, ui
 // Over an E4M3 cache the queries are E4M3 too: a row is scaled by a power of two to a largest element in [128, 256), and
 // its 8-bit significands split into E4M3's 4 bits and a remainder of 4: exact but for elements under 2^-9 of the largest,
 // which are off by 2^-17 of it at most (q's own rounding to bf16 is 2^-8 of each element).  The scale goes into the row's
-// factor, beside `c`.  The split overwrites the row (a TMA-loaded [halves][NT][128 bytes]): no other row's lines.
+// factor, beside `c`.  rows: a multiple of 16.  The split overwrites the row (a TMA-loaded [halves][NT][128 bytes]): no other row's lines.
 template <int D, int NT, int THREADS>
-__device__ __forceinline__ void split_queries(char* q, int tid, float c, float* mult) {
+__device__ __forceinline__ void split_queries(char* q, int tid, int rows, float c, float* mult) {
   constexpr int kLanes = D / 16;  // threads per row, 16 elements each
   const int i = tid % kLanes;
 #pragma unroll 1
-  for (int row = tid / kLanes; row < NT; row += THREADS / kLanes) {
+  for (int row = tid / kLanes; row < rows; row += THREADS / kLanes) {
     const int sw = row & 7;
     const char* src = q + (i * 16 / 64) * (NT * 128) + row * 128;
     const int v0 = (i * 16 % 64) / 8;
