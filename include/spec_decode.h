@@ -232,7 +232,8 @@ spec_status_t spec_kv_keep_ex(const spec_kv_cache_t* cache, const spec_kv_page_s
  * attends to what, q, cache (v is not used), scales, batch and mask are as for spec_paged_attention_ex, and lse is what it
  * gave; a row whose lse is +inf or -inf has no part (a caller may set it, for rows of rejected drafts).
  * positions [B, T] int32 or NULL: ctx_len[b] + t.  Slots whose page lies outside the table or the pool are left out.
- * Two requests must not share a page.  Scores, weights and sums are fp32.
+ * Two requests must not share a page.  Scores, weights and sums are fp32.  Each wait inside the kernel has a limit, as for
+ * spec_paged_attention: should one run out, weights that its block works on come out as NaN.
  */
 spec_status_t spec_kv_weigh(const spec_heads_t* q, int32_t q_heads, const spec_kv_cache_t* cache,
                             const spec_kv_page_scales_t* scales, const spec_decode_batch_t* batch, const int64_t* mask,

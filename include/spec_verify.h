@@ -269,8 +269,8 @@ spec_status_t spec_verify_multi(const void* p_logits, const void* q_logits, cons
  * request of a batch in sampling or greedy mode over 16-byte-aligned rows comes out with
  * SPEC_FLAG_NONFINITE, n_acc 0 and tokens -1 (top-k batches and unaligned rows are not
  * affected).  It exercises the handling of a lost streaming item without any fault.  With bit 1 set
- * the waits inside spec_paged_attention (spec_decode.h) give up after one try, so its rows come out as
- * NaN, as they would if a copy or a product never ended.  0 restores normal operation.
+ * the waits inside spec_paged_attention and spec_kv_weigh (spec_decode.h) give up after one try, so rows and
+ * weights come out as NaN, as they would if a copy or a product never ended.  0 restores normal operation.
  */
 void spec_verify_set_test_hooks(int32_t hooks);
 

@@ -114,15 +114,16 @@ struct Shape {
   // A tile's weights stay in registers over the vote on them; with many columns, which would spill, the vote
   // is on scores that are then computed again (68 rows: 118 us against 125 in E4M3, 114 against 117 in bf16).
   static constexpr bool kHold = NT <= 64;
+  static constexpr int kScales = kProducerV + 1;  // of page scales, which other caches leave idle
   static constexpr int kAheadScales = KIND == kE4m3Pages ? 8 : 1, kPageScales = KIND == kE4m3Pages ? kTileSlots / 8 : 1;
-  static_assert(KIND != kE4m3Pages || kSlots / 2 + 3 < kAheadScales, "a tile's scales stay until it is weighed");
+  static_assert(KIND != kE4m3Pages || kScales < kThreads / 32, "a warp for the scales");
 
   struct State {
     uint64_t ring_full[8], ring_empty[8];
     uint64_t q_loaded[2], q_full[2], q_empty[2], mult_full[2];
     uint64_t v16_full[2], v16_empty[2];
     uint64_t s_full[2], s_empty[2], p_full, o_full;
-    uint64_t scales_full[kAheadScales];
+    uint64_t scales_full[kAheadScales], scales_empty[kAheadScales];
     uint64_t products_done;          // behind a wait that ran out
     uint32_t tmem;
     int dead;
@@ -136,8 +137,7 @@ struct Shape {
     float red[4][NT];
     alignas(16) float mult[2][NT];   // E4M3: a score's factor to log2 units, by the segment's parity
     alignas(16) int64_t place[NT];   // the row's offset in the item's output
-    // Page scales: of every page of a tile, (a key's, the logarithm of a value's, its inverse).  K's producer writes them; it
-    // is kSlots / 2 tiles ahead of the products at most, and those two ahead of the softmax.
+    // Page scales: of every page of a tile, (a key's, the logarithm of a value's, its inverse)
     alignas(16) float4 scales[kAheadScales][kPageScales];
     uint32_t seen[kGroups][SPEC_MAX_NEW];  // which columns of each warpgroup attend to a new token
   };
@@ -202,7 +202,10 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
     }
     mbar_init(smem_addr(&st->p_full), kSoftmaxWarps);
     mbar_init(smem_addr(&st->o_full), 1);
-    for (int i = 0; i < S::kAheadScales; ++i) mbar_init(smem_addr(&st->scales_full[i]), 1);
+    for (int i = 0; i < S::kAheadScales; ++i) {
+      mbar_init(smem_addr(&st->scales_full[i]), 1);
+      mbar_init(smem_addr(&st->scales_empty[i]), kSoftmaxWarps);
+    }
     mbar_init(smem_addr(&st->products_done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -262,36 +265,13 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
           const int p = __ldg(table + (at >> shift));
           return p < 0 || p > P.cache.num_pages ? P.cache.num_pages : p;
         };
-        // page scales, a tile ahead of their copies, and so the page another
-        const bool scaled = PAGES && !is_v;
-        const auto scales_of = [&](int page) {  // of a page outside the pool, which reads as zeros, 1
-          const int64_t at = (int64_t)page * P.heads + head;
-          return scaled && page < P.cache.num_pages ? make_float2(P.scales.k[at], P.scales.v[at]) : make_float2(1.0f, 1.0f);
-        };
-        int next_page = entry(tile0), far_page = scaled && tile0 + 1 < tile1 ? entry(tile0 + 1) : P.cache.num_pages;
-        float2 next_scales = scales_of(next_page);
+        int next_page = entry(tile0);
         for (int tile = tile0; tile < tile1; ++tile) {
           const int my_page = next_page;
-          const float2 my_scales = next_scales;
-          if (scaled) {
-            next_page = far_page;
-            next_scales = scales_of(next_page);
-            far_page = tile + 2 < tile1 ? entry(tile + 2) : P.cache.num_pages;
-          } else if (tile + 1 < tile1) {
-            next_page = entry(tile + 1);
-          }
+          if (tile + 1 < tile1) next_page = entry(tile + 1);
           ok = mbar_wait_warp(bar_of(&st->ring_empty[slot]), phase ^ 1, dead);
           if (!ok) break;
           const uint32_t bar = bar_of(&st->ring_full[slot]);
-          if (scaled) {  // (one that does not count makes the slots' scores NaN)
-            const bool counts = scale_counts(my_scales.y);
-            const int at = issued & (S::kAheadScales - 1);
-            if (lane < copies)
-              st->scales[at][lane % S::kPageScales] = make_float4(scale_counts(my_scales.x) ? my_scales.x : NAN, counts ? log2f(my_scales.y) : NAN,
-                                                                  counts ? 1.0f / my_scales.y : 1.0f, 0.0f);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_of(&st->scales_full[at]));
-          }
           if (lane == 0) mbar_expect(bar, S::kRing);
           __syncwarp();
           const uint32_t dst = base + (uint32_t)(ring - smem) + slot * S::kRing;
@@ -320,6 +300,43 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
       if (lane == 0) {
         st->copies[is_v] = issued;
         if (!is_v) st->queries = queries;
+      }
+    } else if (PAGES && warp == S::kScales) {
+      // ---- page scales of every tile, by a warp of their own: K's producer would bring 64 KB an SM later for them (64 x 7
+      // tokens, pages of 32: 236 us) ----
+      const int shift = P.cache.page_shift, box = min(1 << shift, kTileSlots), pages = kTileSlots / box;
+      int it = 0;
+      bool ok = true;
+      while (ok && walk.next(s)) {
+        const int32_t* table = P.batch.pages + (int64_t)s.b * P.batch.max_pages;
+        // a round of as many tiles as the warp has lanes for their pages (8 at most), scales a round ahead and pages two
+        const int round = min(32 / pages, 8), mine = lane / pages;
+        const auto page_of = [&](int first) {
+          const int tile = first + mine, at = tile * kTileSlots + lane % pages * box;
+          const int p = mine < round && tile < s.tile1 && at < s.end ? __ldg(table + (at >> shift)) : -1;
+          return p < P.cache.num_pages ? p : -1;
+        };
+        const auto scales_of = [&](int page) {  // of a page outside the pool, which reads as zeros, 1
+          const int64_t at = (int64_t)page * P.heads + s.head;
+          return page >= 0 ? make_float2(P.scales.k[at], P.scales.v[at]) : make_float2(1.0f, 1.0f);
+        };
+        int far_page = page_of(s.tile0 + round);
+        float2 next = scales_of(page_of(s.tile0));
+        for (int first = s.tile0; ok && first < s.tile1; first += round) {
+          const float2 x = next;
+          next = scales_of(far_page);
+          far_page = page_of(first + 2 * round);
+          const bool counts = scale_counts(x.y);  // one that does not makes the slots' scores NaN
+          const float4 told = make_float4(scale_counts(x.x) ? x.x : NAN, counts ? log2f(x.y) : NAN, counts ? 1.0f / x.y : 1.0f, 0.0f);
+          for (int i = 0; i < min(round, s.tile1 - first); ++i, ++it) {
+            const int at = it & (S::kAheadScales - 1);
+            ok = mbar_wait_warp(smem_addr(&st->scales_empty[at]), ((it / S::kAheadScales) & 1) ^ 1, dead);
+            if (!ok) break;
+            if (mine == i) st->scales[at][lane % pages % S::kPageScales] = told;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&st->scales_full[at]));
+          }
+        }
       }
     } else if (warp == kIssuer) {
       // ---- matrix products: weighted values of a tile or scores of the next, as either is ready ----
@@ -548,6 +565,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
           k_factor = x.x, v_log2 = x.y, v_inverse = x.z;
         }
         __syncwarp();
+        if (PAGES && lane == 0) mbar_arrive(smem_addr(&st->scales_empty[it & (S::kAheadScales - 1)]));
         tc_fence_after();
 
         const auto weigh = [&](auto tag) {

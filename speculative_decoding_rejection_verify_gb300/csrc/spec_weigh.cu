@@ -35,6 +35,17 @@ struct WeighParams {
   float scale_log2;          // scale * log2(e)
 };
 
+// The waits of this kernel.  A limit of 0, which a test sets, does not let the first try suspend.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const Patience& w) {
+  if (w.limit > 0) return mbar_wait(bar, parity, w);
+  if (mbar_test(bar, parity)) return true;
+  *w.dead = 1;
+  return false;
+}
+__device__ __forceinline__ bool wait_for_warp(uint32_t bar, uint32_t parity, const Patience& w) {
+  return __all_sync(~0u, wait_for(bar, parity, w));
+}
+
 template <int D, bool F8, int NT>
 struct WeighShape {
   static constexpr int kHalves = D / 64;
@@ -161,7 +172,7 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
           if (other) continue;
           const int my_page = next_page;
           if (tile + 2 < tile1) next_page = entry(tile + 2);
-          ok = mbar_wait_warp(bar_of(&st->ring_empty[at_slot]), at_phase ^ 1, dead);
+          ok = wait_for_warp(bar_of(&st->ring_empty[at_slot]), at_phase ^ 1, dead);
           if (!ok) break;
           const uint32_t bar = bar_of(&st->ring_full[at_slot]);
           if (lane == 0) mbar_expect(bar, S::kRing);
@@ -206,11 +217,11 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
       const int tiles = uniform(s.tile1 - s.tile0), passes = uniform(passes_of(s)), first = uniform(owner(s, s.tile0));
       for (int pass = 0; ok && pass < passes; ++pass, ++nth) {
         const int qb = nth & 1;
-        ok = mbar_wait_warp(bar_of(F8 ? &st->q_full[qb] : &st->q_loaded[qb]), (nth >> 1) & 1, dead);
+        ok = wait_for_warp(bar_of(F8 ? &st->q_full[qb] : &st->q_loaded[qb]), (nth >> 1) & 1, dead);
         for (int tile = 0; ok && tile < tiles; ++tile) {
           const int buffer = (first + tile) & (S::kGroups - 1);
-          ok = mbar_wait_warp(bar_of(&st->ring_full[slot]), phase, dead) &&
-               mbar_wait_warp(bar_of(&st->s_empty[buffer]), ((s_phase >> buffer) & 1) ^ 1, dead);
+          ok = wait_for_warp(bar_of(&st->ring_full[slot]), phase, dead) &&
+               wait_for_warp(bar_of(&st->s_empty[buffer]), ((s_phase >> buffer) & 1) ^ 1, dead);
           if (!ok) break;
           tc_fence_after();
           const uint64_t a = k_desc + ahead(slot * S::kRing), b = q_desc + ahead(qb * S::kQ);
@@ -249,7 +260,7 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
       for (int pass = 0; ok && pass < passes; ++pass, ++nth) {
         const int qb = nth & 1, t0 = pass * P.tokens, rows = min(s.tokens - t0, P.tokens) * P.group;
         if (me == 0) {
-          ok = mbar_wait_warp(bar_of(&st->q_empty[qb]), ((nth >> 1) & 1) ^ 1, dead);
+          ok = wait_for_warp(bar_of(&st->q_empty[qb]), ((nth >> 1) & 1) ^ 1, dead);
           if (!ok) break;
           const uint32_t bar = bar_of(&st->q_loaded[qb]);
           if (lane == 0) mbar_expect(bar, P.rows * D * 2), st->queries = nth + 1;
@@ -258,7 +269,7 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
           for (int h = 0; h < S::kHalves; ++h)
             tma_load(base + qb * S::kQ + h * NT * 128, &P.q_map, h * 64, uniform(s.head) * P.group, uniform(t0), uniform(s.b), bar);
         }
-        ok = mbar_wait_warp(smem_addr(&st->rows_empty[qb]), ((nth >> 1) & 1) ^ 1, dead);
+        ok = wait_for_warp(smem_addr(&st->rows_empty[qb]), ((nth >> 1) & 1) ^ 1, dead);
         if (!ok) break;
         for (int r0 = me * 32; r0 < NT; r0 += kCount) {
           const int r = r0 + lane;
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
         for (int t = tid; t < min(P.tokens, s.tokens - t0); t += kCount)
           st->rule[qb][t] = P.mask ? (uint64_t)__ldg(P.mask + (int64_t)s.b * P.batch.T + t0 + t) : t0 + t >= 63 ? ~0ull : (2ull << (t0 + t)) - 1;
         if constexpr (F8) {
-          ok = mbar_wait_warp(smem_addr(&st->q_loaded[qb]), (nth >> 1) & 1, dead);
+          ok = wait_for_warp(smem_addr(&st->q_loaded[qb]), (nth >> 1) & 1, dead);
           if (!ok) break;
           const float c = P.scale_log2 * (!PAGES && P.cache.k_scale ? __ldg(P.cache.k_scale + s.head) : 1.0f);
           split_queries<D, NT, kCount>(q_buf + qb * S::kQ, tid, (rows + 15) & ~15, c, st->mult[qb]);
@@ -309,7 +320,7 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
       };
       for (int pass = 0; pass < passes; ++pass, ++nth) {
         const int qb = nth & 1, t0 = pass * P.tokens, rows = min(s.tokens - t0, P.tokens) * P.group;
-        ok = ok && mbar_wait(smem_addr(&st->rows_full[qb]), (nth >> 1) & 1, dead);
+        ok = ok && wait_for(smem_addr(&st->rows_full[qb]), (nth >> 1) & 1, dead);
         __syncwarp();
         bool plain = true;  // every row has a part
 #pragma unroll
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
           look(tile + S::kGroups);
           next_page = page_of(tile + 2 * S::kGroups);
 
-          ok = ok && mbar_wait(smem_addr(&st->s_full[wg]), parity, dead);
+          ok = ok && wait_for(smem_addr(&st->s_full[wg]), parity, dead);
           parity ^= 1;
           __syncwarp();
           tc_fence_after();

@@ -451,3 +451,72 @@ def test_eviction_captured_and_replayed():
         assert m.tolist() == [64, 100]
         for x, y in zip(dev, twin):
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_weigh_waits_that_give_up_leave_nan(kind):
+    import speculative_decoding_rejection_verify_gb300 as sv
+    d = build(kind, 3, 4, 8, 2, 128, 16, [700, 1900, 300])
+    want = weigh(d)[0]
+    sv.set_test_hooks(2)
+    try:
+        got = weigh(d)[0]
+    finally:
+        sv.set_test_hooks(0)
+    same = torch.nan_to_num(got, nan=-1.0) == torch.nan_to_num(want, nan=-1.0)
+    assert (same | torch.isnan(got)).all() and (torch.isnan(got) & ~torch.isnan(want)).any()
+    assert torch.equal(torch.nan_to_num(weigh(d)[0]), torch.nan_to_num(want))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_weigh_queries_of_a_projection(kind):
+    """q with its heads between others' and its tokens in front of its requests."""
+    d = build(kind, 3, 4, 8, 2, 64, 16, [5, 130, 60])
+    wide = torch.full((4, 3, 14, 64), float("nan"), dtype=BF).transpose(0, 1)
+    wide[:, :, 3:11] = d["q"]
+    q = wide.transpose(0, 1).contiguous().cuda().transpose(0, 1)[:, :, 3:11]
+    import speculative_decoding_rejection_verify_gb300 as sv
+    w, p = d["weight"].cuda(), d["position"].cuda()
+    sv.kv_weigh(q, R.to_cuda(d["k"]), d["pages"].cuda(), i32(d["ctx"]), d["lse"].cuda(), w, p, scale=d["scale"], k_scale=R.to_cuda(d["ks"]))
+    want, want_p = weigh(d)
+    assert torch.equal(torch.nan_to_num(w.cpu()), torch.nan_to_num(want)) and torch.equal(p.cpu(), want_p)
+
+
+def test_eviction_on_another_stream():
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(5)
+    w, pos, pages = record(2, 2, 16, 300, g)
+    stream = torch.cuda.Stream()
+    w, pos, t = w.cuda(), pos.cuda(), pages.cuda()
+    k, v = (torch.randn((w.shape[0], 16, 2, 64), device="cuda").to(BF) for _ in range(2))
+    results = []
+    for s in (None, stream):
+        x = [y.clone() for y in (k, v, w, pos)]
+        stream.wait_stream(torch.cuda.current_stream())
+        src, dst, n, m = sv.kv_select(x[2], x[3], t, i32([300, 222]), i32([100, 90]), recent=30, stream=s)
+        sv.kv_move(x[0], x[1], t, m, src, dst, n, weight=x[2], position=x[3], stream=s)
+        torch.cuda.synchronize()
+        results.append(x)
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def test_empty_batches_and_tables():
+    """No request, no token, no page: nothing is written, and the lists are empty."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    k = torch.zeros((3, 16, 2, 64), dtype=BF, device="cuda")
+    w, pos = torch.ones((3, 2, 16), device="cuda"), torch.zeros((3, 2, 16), dtype=torch.int32, device="cuda")
+    none = torch.zeros((0, 2), dtype=torch.int32, device="cuda")
+    q = torch.zeros((0, 1, 4, 64), dtype=BF, device="cuda")
+    sv.kv_weigh(q, k, none, i32([]).int(), torch.zeros((0, 1, 4), device="cuda"), w, pos)
+    out = sv.kv_select(w, pos, none, i32([]).int(), i32([]).int())
+    assert [tuple(x.shape) for x in out] == [(0, 2, 16), (0, 2, 16), (0, 2), (0,)]
+    sv.kv_move(k, k, none, out[3], *out[:3])
+    tables = torch.zeros((2, 0), dtype=torch.int32, device="cuda")
+    out = sv.kv_select(w, pos, tables, i32([5, 0]), i32([3, 3]))
+    assert out[2].tolist() == [[0, 0], [0, 0]] and out[3].tolist() == [0, 0]
+    sv.kv_move(k, k, tables, out[3], *out[:3])
+    q = torch.zeros((2, 1, 4, 64), dtype=BF, device="cuda")
+    sv.kv_weigh(q, k, tables, i32([5, 0]), torch.zeros((2, 1, 4), device="cuda"), w, pos)
+    torch.cuda.synchronize()
+    assert (w == 1).all() and (k == 0).all()

@@ -481,3 +481,59 @@ def test_on_another_stream():
     stream.wait_stream(torch.cuda.current_stream())
     got, again = call(d, stream=stream)
     assert torch.equal(got, want) and torch.equal(sums, again)
+
+
+def test_waits_that_give_up_leave_nan():
+    """The waits' limit is set to one try: rows and their sums come out as NaN where a wait ran out, and later calls are whole."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    d = build(3, 4, 8, 2, 128, 16, [700, 1900, 300])
+    want, sums = call(d)
+    sv.set_test_hooks(2)
+    try:
+        out, lse = call(d)
+    finally:
+        sv.set_test_hooks(0)
+    lost = torch.isnan(out).any(-1)
+    assert lost.any()
+    again, sums2 = call(d)
+    assert torch.equal(again, want) and torch.equal(sums2, sums)
+
+
+# ------------------------------------------------------------------------------------------------
+# strides
+# ------------------------------------------------------------------------------------------------
+def far(x, stride):
+    """x [pages, ...] with its pages `stride` bytes apart, so that offsets pass 32 bits."""
+    n = x.shape[0]
+    raw = torch.zeros(stride * (n - 1) + x[0].numel(), dtype=torch.uint8, device="cuda")
+    y = raw.as_strided(x.shape, (stride,) + tuple(x.contiguous().stride()[1:])).view(R.F8)
+    y.view(torch.uint8).copy_(x.view(torch.uint8))
+    return y
+
+
+def test_offsets_beyond_32_bits():
+    """Append, attention, weigh, keep and move over pages 600 MB apart give what they give over adjacent ones."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    B, T, Hq, H, D, page = 1, 5, 8, 2, 64, 16
+    c = Cache(B, H, D, page, 96)
+    ctx, pages = i32([70]), c.pages.cuda()
+    qkv = torch.randn((B, T, Hq + 2 * H, D), generator=c.g).to(BF).cuda()
+    stride = 600 << 20
+    results = []
+    for pool in (c.dev[:2], [far(x, stride) for x in c.dev[:2]]):
+        k, v, ks, vs = *pool, c.dev[2].clone(), c.dev[3].clone()
+        if pool is c.dev[:2]:
+            k, v = k.clone(), v.clone()
+        q = sv.kv_append(qkv[:, :, :Hq], qkv[:, :, Hq:Hq + H], qkv[:, :, Hq + H:], k, v, pages, ctx, k_scale=ks, v_scale=vs)
+        lse = torch.zeros((B, T, Hq), device="cuda")
+        o = sv.paged_attention(q, k, v, pages, ctx, k_scale=ks, v_scale=vs, lse=lse)
+        w, p = torch.zeros((k.shape[0], H, page), device="cuda"), torch.zeros((k.shape[0], H, page), dtype=torch.int32, device="cuda")
+        sv.kv_weigh(q, k, pages, ctx, lse, w, p, k_scale=ks)
+        sv.kv_keep(k, v, pages, ctx, i32([[0, 3, 4]]), i32([3]), k_scale=ks, v_scale=vs, weight=w, position=p)
+        src, dst, n, m = sv.kv_select(w, p, pages, ctx + 3, i32([40]), recent=8)
+        sv.kv_move(k, v, pages, m, src, dst, n, k_scale=ks, v_scale=vs, weight=w, position=p)
+        torch.cuda.synchronize()
+        results.append([o, lse, k.contiguous().view(torch.uint8), v.contiguous().view(torch.uint8), ks, vs, w, p, n, m])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert int(results[0][8].sum()) > 0
