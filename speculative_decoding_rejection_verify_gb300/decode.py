@@ -191,10 +191,11 @@ def _cache(k_cache, v_cache, k_scale, v_scale, layered):
     layers, layer = (1, 0) if len(shape) == 4 else (shape[0], st[0])
     num_pages, page, heads, D = shape[-4:]
     scales, ks, vs = None, 0, 0
-    if (k_scale is not None and k_scale.dim() > 1) or (v_scale is not None and v_scale.dim() > 1):
-        scales = _page_scales(k_scale, v_scale, shape[:-3] + (heads,), index)
-    else:
-        ks, vs = _maybe(k_scale, "k_scale", (heads,), _torch.float32, index), _maybe(v_scale, "v_scale", (heads,), _torch.float32, index)
+    if k_scale is not None or v_scale is not None:
+        if (v_scale if k_scale is None else k_scale).dim() > 1:
+            scales = _page_scales(k_scale, v_scale, (num_pages, heads) if len(shape) == 4 else (layers, num_pages, heads), index)
+        else:
+            ks, vs = _maybe(k_scale, "k_scale", (heads,), _torch.float32, index), _maybe(v_scale, "v_scale", (heads,), _torch.float32, index)
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), layer, st[-4], st[-3], st[-2], layers, num_pages, page,
                        heads, D, dt, ks, vs), heads, D, index, scales
 
@@ -336,19 +337,18 @@ def kv_keep(k_cache, v_cache, pages, ctx_len, path, n_keep, stream=None, k_scale
     to; ``weight`` and ``position`` move with the entries (spec_kv_keep_ex)."""
     torch, lib = _load()
     c, heads, _, index, scales = _cache(k_cache, v_cache, k_scale, v_scale, True)
-    if scales is None and (k_scale is not None or v_scale is not None):
-        raise ValueError("k_scale and v_scale of kv_keep are scales per page: a scale per head moves with nothing")
     if path.dim() != 2:
         raise ValueError("path must be [B, max_keep]")
     B, most = path.shape
     b = _batch(pages, ctx_len, None, B, 0, index)
-    r = _record(weight, position, _record_shape(k_cache), index)
     p, n = _fits(path, "path", (B, most), torch.int32, index), _fits(n_keep, "n_keep", (B,), torch.int32, index)
     handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    if scales is None and r is None:
+    if k_scale is None and v_scale is None and weight is None and position is None:
         rc = lib.spec_kv_keep(c, b, p, n, most, handle)
     else:
-        rc = lib.spec_kv_keep_ex(c, scales, r, b, p, n, most, handle)
+        if scales is None and (k_scale is not None or v_scale is not None):
+            raise ValueError("k_scale and v_scale of kv_keep are scales per page: a scale per head moves with nothing")
+        rc = lib.spec_kv_keep_ex(c, scales, _record(weight, position, _record_shape(k_cache), index), b, p, n, most, handle)
     if rc != sv.SPEC_OK:
         raise sv.SpecVerifyError(rc, "spec_kv_keep")
 
@@ -389,6 +389,8 @@ def kv_select(weight, position, pages, ctx_len, budget, seen=None, first: int = 
     them.  Returns ``(source, target, moves, new_len)`` for ``kv_move``: lists ``[(layers,) B, heads, slots // 2]`` of which
     the first ``moves [(layers,) B, heads]`` count, and the context's new lengths ``[B]`` (``out``: such tensors to write to)."""
     torch, lib = _load()
+    if not (0 <= first < 1 << 31 and 0 <= recent < 1 << 31):
+        raise ValueError("first and recent must lie in [0, 2^31)")
     if weight.dim() not in (3, 4):
         raise ValueError("weight must be [num_pages, heads, page_size], or with layers in front of it")
     index = weight.get_device()

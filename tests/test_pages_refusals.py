@@ -112,7 +112,7 @@ def test_weigh_arguments(lib):  # noqa: F811
 def test_select_arguments(lib):  # noqa: F811
     assert select(lib, r=None) == INVALID
     for bad in (dict(weight=None), dict(weight=4097), dict(position=4098), dict(layers=0), dict(num_pages=-1), dict(heads=0), dict(page_size=0),
-                dict(layer_stride=-4)):
+                dict(layer_stride=-4), dict(weight=4100), dict(position=4104), dict(layer_stride=6)):
         assert select(lib, r=record(**bad)) == INVALID, bad
     assert select(lib, r=record(page_size=4)) == UNSUPPORTED
     assert select(lib, r=record(heads=65536)) == UNSUPPORTED
@@ -166,8 +166,8 @@ def test_structs_match_the_header(tmp_path):
         assert [getattr(s, f[0]) for f in cls._fields_] == values
 
 
-def test_the_binding_refuses(lib, monkeypatch):  # noqa: F811
-    """Host tensors, and scales that are neither per head nor per page (with the device's part stood in for)."""
+def test_the_binding_refuses(lib):  # noqa: F811
+    """Host tensors, numbers that C would cut, and a scale per page without the other."""
     c = torch.zeros((2, 16, 2, 64), dtype=torch.float8_e4m3fn)
     i, n = torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     x, w = torch.zeros((1, 1, 2, 64), dtype=torch.bfloat16), torch.zeros((2, 2, 16))
@@ -176,6 +176,9 @@ def test_the_binding_refuses(lib, monkeypatch):  # noqa: F811
             call()
     with pytest.raises(ValueError, match="layers"):
         sv.kv_select(torch.zeros((2, 2)), None, i, n, n)
+    for wrong in (dict(first=-1), dict(recent=-1), dict(first=1 << 31), dict(recent=1 << 40)):
+        with pytest.raises(ValueError, match="first and recent"):
+            sv.kv_select(w, w.int(), i, n, n, **wrong)
     decode._load()
     with pytest.raises(ValueError, match="both"):
         decode._page_scales(torch.zeros((2, 2)), None, (2, 2), -1)
