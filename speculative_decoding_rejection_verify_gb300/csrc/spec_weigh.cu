@@ -32,7 +32,7 @@ struct WeighParams {
   const float* lse;
   const int32_t* positions;
   int heads, group;
-  int tokens, passes;        // tokens per pass
+  int tokens;                // of a pass
   int rows;                  // group * tokens
   int row_groups;            // of the line's items: 1
   int item_cost;             // an item's beginning, in tiles
@@ -504,7 +504,8 @@ extern "C" spec_status_t spec_kv_weigh(const spec_heads_t* q, int32_t q_heads, c
   P.mask = mask, P.lse = lse, P.positions = positions;
   const int D = cache->head_dim;
   P.heads = cache->heads, P.group = q_heads / cache->heads;
-  row_groups(batch->T, P.group, &P.tokens, &P.passes);
+  int passes;
+  row_groups(batch->T, P.group, &P.tokens, &passes);
   P.rows = P.group * P.tokens;
   P.row_groups = 1;
   P.scale_log2 = scale * kLog2e;

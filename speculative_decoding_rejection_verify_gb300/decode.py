@@ -192,30 +192,31 @@ def _cache(k_cache, v_cache, k_scale, v_scale, layered):
     num_pages, page, heads, D = shape[-4:]
     scales, ks, vs = None, 0, 0
     if k_scale is not None or v_scale is not None:
+        f32 = _torch.float32
         if (v_scale if k_scale is None else k_scale).dim() > 1:
-            scales = _page_scales(k_scale, v_scale, (num_pages, heads) if len(shape) == 4 else (layers, num_pages, heads), index)
+            if k_scale is None or v_scale is None:
+                raise ValueError("k_scale and v_scale must both have a scale per page, or neither")
+            at = (num_pages, heads) if len(shape) == 4 else (layers, num_pages, heads)
+            scales = _pack_scales(_fits(k_scale, "k_scale", at, f32, index), _fits(v_scale, "v_scale", at, f32, index), num_pages * heads)
         else:
-            ks, vs = _maybe(k_scale, "k_scale", (heads,), _torch.float32, index), _maybe(v_scale, "v_scale", (heads,), _torch.float32, index)
+            ks, vs = _maybe(k_scale, "k_scale", (heads,), f32, index), _maybe(v_scale, "v_scale", (heads,), f32, index)
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), layer, st[-4], st[-3], st[-2], layers, num_pages, page,
                        heads, D, dt, ks, vs), heads, D, index, scales
-
-
-def _page_scales(k_scale, v_scale, shape, index):
-    """Scales per page and head, [num_pages, heads] (with the cache's layers in front)."""
-    if k_scale is None or v_scale is None:
-        raise ValueError("k_scale and v_scale must both have a scale per page, or neither")
-    k, v = (_fits(x, name, shape, _torch.float32, index) for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")))
-    return _pack_scales(k, v, shape[-2] * shape[-1] if len(shape) == 3 else 0)
 
 
 def _record(weight, position, shape, index):
     """The struct of weights and positions [num_pages, heads, page_size] (with layers in front), either of which may be None."""
     if weight is None and position is None:
         return None
-    w, p = _maybe(weight, "weight", shape, _torch.float32, index), _maybe(position, "position", shape, _torch.int32, index)
     num_pages, heads, page = shape[-3:]
-    return _pack_record(w, p, num_pages * heads * page if len(shape) == 4 else 0, 1 if len(shape) == 3 else shape[0], num_pages,
-                        page, heads)
+    return _pack_record(_maybe(weight, "weight", shape, _torch.float32, index), _maybe(position, "position", shape, _torch.int32, index),
+                        num_pages * heads * page, 1 if len(shape) == 3 else shape[0], num_pages, page, heads)
+
+
+def _record_shape(cache):
+    """The shape of what is recorded of a cache's entries."""
+    s = tuple(cache.shape)
+    return (s[0], s[2], s[1]) if len(s) == 4 else (s[0], s[1], s[3], s[2])
 
 
 def _batch(pages, ctx_len, t_per_row, B, T, index):
@@ -353,11 +354,6 @@ def kv_keep(k_cache, v_cache, pages, ctx_len, path, n_keep, stream=None, k_scale
         raise sv.SpecVerifyError(rc, "spec_kv_keep")
 
 
-def _record_shape(k_cache):
-    s = k_cache.shape
-    return s[:-3] + (s[-2], s[-3])
-
-
 def kv_weigh(q, k_cache, pages, ctx_len, lse, weight, position=None, t_per_row=None, mask=None, positions=None,
              scale: Optional[float] = None, k_scale=None, stream=None) -> None:
     """Add up what the new tokens' attention gives every entry (spec_kv_weigh): ``weight [num_pages, heads, page_size]``
@@ -398,15 +394,15 @@ def kv_select(weight, position, pages, ctx_len, budget, seen=None, first: int = 
         raise ValueError("weight must be a CUDA tensor")
     if index != _current_device():
         sv._launches_on(index)
-    shape = weight.shape
+    shape = tuple(weight.shape)
     r = _record(weight, position, shape, index)
     if pages.dim() != 2:
         raise ValueError("pages must be [B, max_pages]")
-    B, max_pages = pages.shape
+    B = pages.shape[0]
     b = _batch(pages, ctx_len, None, B, 0, index)
-    lists = shape[:-3] + (B, shape[-2])
-    most = max_pages * shape[-1] // 2
+    lists = (B, shape[1]) if len(shape) == 3 else (shape[0], B, shape[2])
     if out is None:
+        most = pages.shape[1] * shape[-1] // 2
         new = lambda size: torch.empty(size, dtype=torch.int32, device=weight.device)  # noqa: E731
         if stream is None:
             out = new(lists + (most,)), new(lists + (most,)), new(lists), new((B,))
@@ -415,9 +411,9 @@ def kv_select(weight, position, pages, ctx_len, budget, seen=None, first: int = 
                 out = new(lists + (most,)), new(lists + (most,)), new(lists), new((B,))
     source, target, moves, new_len = out
     most = source.shape[-1] if source.dim() else 0
-    i32 = torch.int32
+    i32, full = torch.int32, lists + (most,)
     rc = lib.spec_kv_select(r, b, _fits(budget, "budget", (B,), i32, index), _maybe(seen, "seen", (B,), i32, index), first, recent,
-                            _fits(source, "source", lists + (most,), i32, index), _fits(target, "target", lists + (most,), i32, index),
+                            _fits(source, "source", full, i32, index), _fits(target, "target", full, i32, index),
                             most, _fits(moves, "moves", lists, i32, index), _fits(new_len, "new_len", (B,), i32, index),
                             _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != sv.SPEC_OK:
@@ -438,9 +434,10 @@ def kv_move(k_cache, v_cache, pages, new_len, source, target, moves, k_scale=Non
         raise ValueError("pages must be [B, max_pages], and source [B, heads, n]")
     B, most = pages.shape[0], source.shape[-1]
     b = _batch(pages, new_len, None, B, 0, index)
-    lists, i32 = k_cache.shape[:-4] + (B, heads), torch.int32
-    rc = lib.spec_kv_move(c, scales, _record(weight, position, _record_shape(k_cache), index), b,
-                          _fits(source, "source", lists + (most,), i32, index), _fits(target, "target", lists + (most,), i32, index),
+    lists, i32 = (B, heads) if k_cache.dim() == 4 else (k_cache.shape[0], B, heads), torch.int32
+    full = lists + (most,)
+    r = None if weight is None and position is None else _record(weight, position, _record_shape(k_cache), index)
+    rc = lib.spec_kv_move(c, scales, r, b, _fits(source, "source", full, i32, index), _fits(target, "target", full, i32, index),
                           _fits(moves, "moves", lists, i32, index), most, _raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != sv.SPEC_OK:
         raise sv.SpecVerifyError(rc, "spec_kv_move")

@@ -179,6 +179,3 @@ def test_the_binding_refuses(lib):  # noqa: F811
     for wrong in (dict(first=-1), dict(recent=-1), dict(first=1 << 31), dict(recent=1 << 40)):
         with pytest.raises(ValueError, match="first and recent"):
             sv.kv_select(w, w.int(), i, n, n, **wrong)
-    decode._load()
-    with pytest.raises(ValueError, match="both"):
-        decode._page_scales(torch.zeros((2, 2)), None, (2, 2), -1)
