@@ -41,15 +41,17 @@ constexpr int kMaxCluster = 8;
 constexpr uint32_t kNoKey = 0x007FFFFFu;  // of -infinity
 
 struct SelectState {
-  alignas(16) int bins[kBins];
+  union {
+    alignas(16) int bins[kBins];
+    alignas(16) uint32_t turned[kSelectWarps][kRun];  // keys of a warp's run that the block does not hold (after the histograms)
+  };
   int warp_sum[kSelectWarps];
   int digit, above, whole;
   alignas(16) int counts[4];                    // of the block: larger, equal; and of those the ones below m
   int warp_counts[2][kSelectWarps];
-  alignas(16) uint32_t turned[kSelectWarps][kRun];  // keys of a warp's run that the block does not hold
 };
 
-__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_constant__ SelectParams P) {
+__global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(const __grid_constant__ SelectParams P) {
   extern __shared__ __align__(16) uint32_t keys[];  // [held]
   __shared__ SelectState st;
   pdl_launch_next();
@@ -144,13 +146,17 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_
     cluster.sync();
     // this thread's four bins, from the top, over all blocks
     const int top = kBins - 4 - threadIdx.x * 4;
-    int4 sum = make_int4(0, 0, 0, 0), of_block[kMaxCluster];
+    int4 sum = make_int4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int r0 = 0; r0 < blocks; r0 += 4) {  // four in flight: more take registers that a third block an SM needs
+      int4 of_block[4];
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)  // all in flight
-      if (r < blocks) of_block[r] = *reinterpret_cast<const int4*>(cluster.map_shared_rank(&st.bins[top], r));
+      for (int r = 0; r < 4; ++r)
+        if (r0 + r < blocks) of_block[r] = *reinterpret_cast<const int4*>(cluster.map_shared_rank(&st.bins[top], r0 + r));
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r)
-      if (r < blocks) sum.x += of_block[r].x, sum.y += of_block[r].y, sum.z += of_block[r].z, sum.w += of_block[r].w;
+      for (int r = 0; r < 4; ++r)
+        if (r0 + r < blocks) sum.x += of_block[r].x, sum.y += of_block[r].y, sum.z += of_block[r].z, sum.w += of_block[r].w;
+    }
     const int mine = sum.x + sum.y + sum.z + sum.w;
     int before = mine;
 #pragma unroll
