@@ -2,7 +2,8 @@
 // their values, with the queries rotated on the way) and spec_kv_keep (the accepted branch moved up
 // behind the context).  Both are streams of 16-byte vectors, bound by memory traffic on large calls and
 // by their launch on small ones.  Measured: 4 x 2047 tokens of 32 + 2 x 8 heads of 128, half-split, bf16: 33 us,
-// 6.2 TB/s of the bytes read and written (0.92 of a copy's 6772 GB/s); 8 x 6 tokens: 2.8 us.  64 requests' 1 to 5
+// 6.2 TB/s of the bytes read and written (0.92 of a copy's 6772 GB/s); 8 x 6 tokens: 2.8 us.  With page scales, interleaved, pages of
+// 32: 28.5 us, 3.3 TB/s (0.49), bound by instructions; 8 x 6 tokens: 3.3 us.  64 requests' 1 to 5
 // entries in 32 layers: 5.0 us, 3.8 TB/s, bound by the chain of two dependent loads before the first entry.
 
 #include "decode_common.cuh"
@@ -182,7 +183,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 // 49 with 256; of 256: 106, 58, 43).
 constexpr int kPageThreadsMost = 256;
 static int page_threads(int tokens) { return tokens <= 32 ? 64 : tokens <= 128 ? 128 : 256; }
-constexpr int kPageHeld = 4;  // tokens a thread holds between the two passes
 
 struct PageAppendParams {
   Heads k, v;
@@ -201,6 +201,7 @@ struct PageAppendParams {
 // products of a rotation are rounded one by one, so the magnitude does not depend on how they are fused.
 template <int D, bool INTERLEAVED>
 __device__ __forceinline__ void append_page(const PageAppendParams& P, int index) {
+  constexpr int kHeld = INTERLEAVED ? 4 : 2;  // tokens that a thread holds between the two passes
   __shared__ float most_of[kPageThreadsMost / 32];
   const bool is_v = index & 1;
   index >>= 1;
@@ -228,7 +229,6 @@ __device__ __forceinline__ void append_page(const PageAppendParams& P, int index
   const Heads& in = is_v ? P.v : P.k;
   const char* src = in.data + b * in.row + head * in.head;
 
-  uint4 w0[kPageHeld], w1[kPageHeld];
   const auto load = [&](int t, uint4& a, uint4& c) {
     const char* p = src + t * in.token;
     a = *reinterpret_cast<const uint4*>(p + lo * 2);
@@ -258,26 +258,31 @@ __device__ __forceinline__ void append_page(const PageAppendParams& P, int index
   };
 
   float most = 0.0f;  // of the finite magnitudes
-  const auto look = [&](int t, const uint4& a, const uint4& c) {
-    float x[8], y[8];
-    turned(t, a, c, x, y);
+  const auto look = [&](const float (&x)[8], const float (&y)[8]) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if (fabsf(x[e]) < INFINITY) most = fmaxf(most, fabsf(x[e]));
-      if (pair && fabsf(y[e]) < INFINITY) most = fmaxf(most, fabsf(y[e]));
+      if (!INTERLEAVED && pair && fabsf(y[e]) < INFINITY) most = fmaxf(most, fabsf(y[e]));
     }
   };
+  float x[kHeld][8], y[kHeld][8];  // the first tokens, turned
   if (works) {
+    uint4 a[kHeld], c[kHeld];
 #pragma unroll
-    for (int i = 0; i < kPageHeld; ++i)
-      if (t0 + lane0 + i * lanes < t1) load(t0 + lane0 + i * lanes, w0[i], w1[i]);
+    for (int i = 0; i < kHeld; ++i)
+      if (t0 + lane0 + i * lanes < t1) load(t0 + lane0 + i * lanes, a[i], c[i]);
 #pragma unroll
-    for (int i = 0; i < kPageHeld; ++i)
-      if (t0 + lane0 + i * lanes < t1) look(t0 + lane0 + i * lanes, w0[i], w1[i]);
-    for (int t = t0 + lane0 + kPageHeld * lanes; t < t1; t += lanes) {
+    for (int i = 0; i < kHeld; ++i)
+      if (t0 + lane0 + i * lanes < t1) {
+        turned(t0 + lane0 + i * lanes, a[i], c[i], x[i], y[i]);
+        look(x[i], y[i]);
+      }
+    for (int t = t0 + lane0 + kHeld * lanes; t < t1; t += lanes) {
       uint4 a, c;
+      float x[8], y[8];
       load(t, a, c);
-      look(t, a, c);
+      turned(t, a, c, x, y);
+      look(x, y);
     }
   }
 #pragma unroll
@@ -301,9 +306,7 @@ __device__ __forceinline__ void append_page(const PageAppendParams& P, int index
     }
   }
   if (!works) return;
-  const auto store = [&](int t, const uint4& a, const uint4& c) {
-    float x[8], y[8];
-    turned(t, a, c, x, y);
+  const auto store = [&](int t, const float (&x)[8], const float (&y)[8]) {
     char* p = out + (int64_t)(ctx + t - from) * P.cache.slot;
     const auto put = [&](char* at, const float (&z)[8]) {
       float c[8];
@@ -312,15 +315,17 @@ __device__ __forceinline__ void append_page(const PageAppendParams& P, int index
       *reinterpret_cast<uint2*>(at) = make_uint2(pack_e4m3(c[0], c[1], c[2], c[3]), pack_e4m3(c[4], c[5], c[6], c[7]));
     };
     put(p + lo, x);
-    if (pair) put(p + lo + far, y);
+    if (!INTERLEAVED && pair) put(p + lo + far, y);
   };
 #pragma unroll
-  for (int i = 0; i < kPageHeld; ++i)
-    if (t0 + lane0 + i * lanes < t1) store(t0 + lane0 + i * lanes, w0[i], w1[i]);
-  for (int t = t0 + lane0 + kPageHeld * lanes; t < t1; t += lanes) {
+  for (int i = 0; i < kHeld; ++i)
+    if (t0 + lane0 + i * lanes < t1) store(t0 + lane0 + i * lanes, x[i], y[i]);
+  for (int t = t0 + lane0 + kHeld * lanes; t < t1; t += lanes) {
     uint4 a, c;
+    float x[8], y[8];
     load(t, a, c);
-    store(t, a, c);
+    turned(t, a, c, x, y);
+    store(t, x, y);
   }
 }
 
@@ -331,9 +336,9 @@ struct PageStepParams {
 };
 
 // The pages' blocks, then the tokens' that rotate the queries: in one launch they run beside one another (4 x 2047 tokens of 32 +
-// 2 x 8 heads, pages of 32: 30 us, 31 in two; 8 x 6 tokens: a launch less).
+// 2 x 8 heads, pages of 32: 30 us, 31 in two; 8 x 6 tokens: a launch less).  Four blocks of 256 threads an SM: 28.5 us instead of 30.6.
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kPageThreadsMost) page_append_kernel(const __grid_constant__ PageStepParams P) {
+__global__ void __launch_bounds__(kPageThreadsMost, 4) page_append_kernel(const __grid_constant__ PageStepParams P) {
   pdl_launch_next();
   pdl_wait();
   if (blockIdx.x < P.page_blocks) append_page<D, INTERLEAVED>(P.pages, blockIdx.x);

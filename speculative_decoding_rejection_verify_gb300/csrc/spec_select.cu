@@ -8,9 +8,9 @@
 // A cluster of 1 to 8 blocks per (layer, request, head), each with a stretch of the slots, whose keys it holds in shared
 // memory as far as they fit: weights and positions are read once.
 //
-// Measured: 4 layers x 16 requests x 8 heads of 30000 to 65003 entries, 16384 kept: 198 us, 1.2 TB/s of the bytes read and
-// written (0.18 of a copy's 6749 GB/s).  A block's 16000 keys take about 35000 cycles: 9000 to read and count, 3500 to exchange bins for
-// each digit, 3000 to count each, 15000 to number and list; two blocks an SM issue in 58 % of the cycles.  One layer of 8 requests of
+// Measured: 4 layers x 16 requests x 8 heads of 30000 to 65003 entries, 16384 kept: 177 us, 1.3 TB/s of the bytes read and
+// written (0.20 of a copy's 6749 GB/s).  A block's 16000 keys take about 35000 cycles: 9000 to read and count, 3500 to exchange bins for
+// each digit, 3000 to count each, 15000 to number and list; three blocks an SM.  One layer of 8 requests of
 // about 1000 entries: 10.5 us, the call's host part.
 
 #include <cooperative_groups.h>
@@ -301,9 +301,9 @@ extern "C" spec_status_t spec_kv_select(const spec_kv_record_t* record, const sp
   while ((1 << P.page_shift) < record->page_size) ++P.page_shift;
 
   // Blocks a list: more while they fit the GPU beside one another, as an exchange costs a block what 2000 keys do (8 lists of
-  // 65000: 117 us with 1, 55 with 2, 25 with 4 or 8; 512 of 9000: 39, 54, 108, 344), and as many as hold the keys (512 of 65000, two
-  // blocks an SM: 272 with 1, 200 with 2, 209 with 4).
-  constexpr int kMostHeld = 24576;  // 96 KB: two blocks an SM
+  // 65000: 117 us with 1, 55 with 2, 25 with 4 or 8; 512 of 9000: 39, 54, 108, 344), and as many as hold the keys (512 of 65000, with
+  // two blocks an SM: 272 with 1, 200 with 2, 209 with 4; with three 177 with 4).
+  constexpr int kMostHeld = 24576;  // 96 KB
   int blocks = 1;
   int dev = 0, sms = 0;
   if (device_sms(&dev, &sms) != cudaSuccess) return SPEC_ERR_CUDA;
