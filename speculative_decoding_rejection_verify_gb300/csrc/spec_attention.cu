@@ -781,23 +781,23 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
       const bool whole = s.tile0 == 0 && s.tile1 == s.tiles;
       // parts: slot 0 for an item that an earlier CTA began, slot 1 for one that a later one ends
       const int64_t part_row = ((int64_t)blockIdx.x * 2 + (s.tile0 == 0)) * P.rows;
-      float lse = -INFINITY;
+      float lse = -INFINITY, sum = 0.0f;
       if (wtid < S::kOwn) {
         float f = 0.0f;
         if (my_row < rows) {
-          const float sum = st->red[0][my_row] + st->red[1][my_row] + st->red[2][my_row] + st->red[3][my_row];
+          sum = st->red[0][my_row] + st->red[1][my_row] + st->red[2][my_row] + st->red[3][my_row];
           f = sum == 0.0f ? 0.0f : v_scale / sum;
-          if (!whole) P.part_ml[part_row + my_row] = make_float2(st->top[my_row], sum);
-          else if (P.lse) lse = row_lse(st->top[my_row], kLift, sum);
+          if (whole && P.lse) lse = row_lse(st->top[my_row], kLift, sum);
         }
         st->factor[my_row] = f;
       }
       mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
       __syncwarp();
       tc_fence_after();
-      group_sync(bar);
+      const bool lost = group_any(bar, *dead.dead != 0);  // one answer for the warpgroup's rows
       const bool bad = st->bad_value[seg & 3] == (uint32_t)seg + 1;
-      const bool lost = *dead.dead != 0;
+      // (a lost part's sum is NaN, which the join makes the row's output and lse; a NaN maximum it would pass over)
+      if (!whole && wtid < S::kOwn && my_row < rows) P.part_ml[part_row + my_row] = make_float2(st->top[my_row], lost ? NAN : sum);
       char* out = P.out.data + s.b * P.out.row + (int64_t)t0 * P.out.token + (int64_t)s.head * P.group * P.out.head + key * 2;
       float* part = P.part + part_row * D + key;
       const int rows_all = min(P.rows, (P.batch.T - t0) * P.group);
