@@ -248,6 +248,7 @@ spec_status_t spec_kv_weigh(const spec_heads_t* q, int32_t q_heads, const spec_k
  *   source, likewise: the slots >= m that do, in ascending order.  There are as many of each: moves [layers, B, heads],
  *   at most half of the page table's slots, and max_moves is that half at least.  Elements past them are not written;
  *   new_len [B]: m;  budget [B] int32 (a negative one counts as 0);  seen [B] int32: tokens so far, NULL: ctx_len.
+ *   new_len may be ctx_len, budget or seen itself, which it then replaces (SPEC_ERR_INVALID_ARG where it overlaps one otherwise).
  *   record->position may be NULL where first and recent are 0; weight and position are 16-byte aligned and layer_stride a
  *   multiple of 4.  batch->T and t_per_row are not used.
  */

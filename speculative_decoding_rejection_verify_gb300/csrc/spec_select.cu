@@ -29,7 +29,7 @@ struct SelectParams {
   int32_t* source;
   int32_t* target;
   int32_t* moves;
-  int32_t* new_len;
+  int32_t* new_len;  // null: lengths_kernel writes it
   int heads, num_pages, page_shift, first, recent, max_moves;
   int held;  // keys that a block holds
 };
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(const __grid_
   const int list = blockIdx.x / blocks, head = list % P.heads, rest = list / P.heads, b = rest % P.batch.B, layer = rest / P.batch.B;
   const int ctx = batch_context(P.batch, b), m = min(ctx, max(__ldg(P.budget + b), 0));
   const bool tells = rank == 0 && threadIdx.x == 0;
-  if (tells && head == 0 && layer == 0) P.new_len[b] = m;
+  if (tells && head == 0 && layer == 0 && P.new_len) P.new_len[b] = m;
   if (m == ctx || m == 0) {  // the whole cluster
     if (tells) P.moves[list] = 0;
     return;
@@ -269,6 +269,20 @@ __global__ void __launch_bounds__(kSelectThreads, 3) select_kernel(const __grid_
   cluster.sync();  // no block leaves while its counts are read
 }
 
+struct LengthsParams {
+  Batch batch;
+  const int32_t* budget;
+  int32_t* new_len;
+};
+
+// The new lengths where they replace an input that the selection's blocks read until their end: behind all of them.
+__global__ void __launch_bounds__(128) lengths_kernel(const __grid_constant__ LengthsParams P) {
+  pdl_launch_next();
+  pdl_wait();
+  const int b = blockIdx.x * 128 + threadIdx.x;
+  if (b < P.batch.B) P.new_len[b] = min(min(max(P.batch.ctx_len[b], 0), P.batch.slots), max(P.budget[b], 0));
+}
+
 }  // namespace sv
 
 using namespace sv;
@@ -292,11 +306,19 @@ extern "C" spec_status_t spec_kv_select(const spec_kv_record_t* record, const sp
   const int64_t slots = (int64_t)batch->max_pages * record->page_size;
   if ((int64_t)max_moves < slots / 2) return SPEC_ERR_INVALID_ARG;
   if (!budget || !moves || !new_len || (max_moves > 0 && (!source || !target))) return SPEC_ERR_INVALID_ARG;
+  // new_len may be an input itself, and must not overlap one in another way
+  bool replaces = false;
+  for (const int32_t* input : {batch->ctx_len, budget, seen}) {
+    const uintptr_t a = (uintptr_t)input, n = (uintptr_t)new_len, bytes = (uintptr_t)batch->B * 4;
+    if (input && a != n && a < n + bytes && n < a + bytes) return SPEC_ERR_INVALID_ARG;
+    replaces |= a == n;
+  }
   SelectParams P = {};
   P.record = record_of(record);
   if (first == 0 && recent == 0) P.record.position = nullptr;
   P.batch = batch_of(batch, &sizes);
-  P.budget = budget, P.seen = seen, P.source = source, P.target = target, P.moves = moves, P.new_len = new_len;
+  P.budget = budget, P.seen = seen, P.source = source, P.target = target, P.moves = moves;
+  P.new_len = replaces ? nullptr : new_len;
   P.heads = record->heads, P.num_pages = record->num_pages, P.first = first, P.recent = recent, P.max_moves = max_moves;
   while ((1 << P.page_shift) < record->page_size) ++P.page_shift;
 
@@ -324,5 +346,8 @@ extern "C" spec_status_t spec_kv_select(const spec_kv_record_t* record, const sp
   at[1].id = cudaLaunchAttributeClusterDimension;
   at[1].val.clusterDim.x = blocks, at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at, cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_kernel, P) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, select_kernel, P) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (!replaces) return SPEC_OK;
+  const LengthsParams L = {P.batch, budget, new_len};
+  return launch_early(lengths_kernel, dim3((unsigned)((batch->B + 127) / 128)), dim3(128), 0, cfg.stream, L) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

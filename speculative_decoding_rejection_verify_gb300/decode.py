@@ -383,7 +383,8 @@ def kv_select(weight, position, pages, ctx_len, budget, seen=None, first: int = 
     ``weight`` and ``position [num_pages, heads, page_size]``, or with layers in front.  Entries at positions ``< first`` or
     ``>= seen[b] - recent`` (``seen [B]``: tokens so far, None: ``ctx_len``) go before all others; ``position`` may be None without
     them.  Returns ``(source, target, moves, new_len)`` for ``kv_move``: lists ``[(layers,) B, heads, slots // 2]`` of which
-    the first ``moves [(layers,) B, heads]`` count, and the context's new lengths ``[B]`` (``out``: such tensors to write to)."""
+    the first ``moves [(layers,) B, heads]`` count, and the context's new lengths ``[B]`` (``out``: such tensors to write to, the
+    lengths' may be ``ctx_len`` itself)."""
     torch, lib = _load()
     if not (0 <= first < 1 << 31 and 0 <= recent < 1 << 31):
         raise ValueError("first and recent must lie in [0, 2^31)")

@@ -64,3 +64,85 @@ def test_sums_where_a_wait_gave_up_are_nan(kind, ctx, Hq):
     assert torch.equal(out[~lost], want[~lost]) and torch.equal(lse[~lost], sums[~lost])
     again, sums2 = call()
     assert torch.equal(again, want) and torch.equal(sums2, sums)
+
+
+# ------------------------------------------------------------------------------------------------
+# selection and moves
+# ------------------------------------------------------------------------------------------------
+def record(B, H, page, slots, g, layers=None):
+    maxp = -(-slots // page)
+    num = B * maxp + 2
+    shape = (() if layers is None else (layers,)) + (num, H, page)
+    return torch.rand(shape, generator=g) ** 8, torch.randint(0, 2 * slots, shape, generator=g).to(torch.int32), R.tables(B, maxp, num, g)
+
+
+def same_lists(a, b):
+    (s1, t1, n1, m1), (s2, t2, n2, m2) = a, b
+    assert torch.equal(n1, n2) and torch.equal(m1, m2)
+    counts = torch.arange(s1.shape[-1], device="cuda") < n1[..., None]
+    assert torch.equal(s1[counts], s2[counts]) and torch.equal(t1[counts], t2[counts])
+
+
+@pytest.mark.parametrize("layers,B,H,slots", [(None, 1, 1, 40000), (4, 16, 8, 3000), (2, 300, 2, 100)])
+@pytest.mark.parametrize("which", ["ctx", "budget", "seen"])
+def test_select_replaces_lengths_in_place(layers, B, H, slots, which):
+    """The new lengths go to an input that every list's blocks read: the lists are those of a call with a tensor of its own."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(2)
+    w, p, pages = (x.cuda() for x in record(B, H, 16, slots, g, layers))
+    ctx = torch.randint(slots // 2, slots + 1, (B,), generator=g)
+    given = dict(ctx=ctx, budget=torch.randint(0, slots // 2, (B,), generator=g), seen=ctx + 7)
+    given = {n: x.to(torch.int32).cuda() for n, x in given.items()}
+    want = sv.kv_select(w, p, pages, given["ctx"], given["budget"], seen=given["seen"], first=2, recent=30)
+    before = {n: x.clone() for n, x in given.items()}
+    for _ in range(3):
+        for n, x in given.items():
+            x.copy_(before[n])
+        out = tuple(torch.full_like(x, -1) for x in want[:3]) + (given[which],)
+        got = sv.kv_select(w, p, pages, given["ctx"], given["budget"], seen=given["seen"], first=2, recent=30, out=out)
+        assert got[3] is given[which]
+        same_lists(got, want)
+        for n, x in given.items():
+            assert torch.equal(x, want[3] if n == which else before[n])
+
+
+def test_a_loop_that_evicts_in_place_captured_and_replayed():
+    """Selection, move and the next tokens' lengths as one graph over the same ctx_len."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(6)
+    B, H, D, page, slots = 6, 4, 64, 16, 400
+    w, p, pages = record(B, H, page, slots, g)
+    k, v = (torch.randn((w.shape[0], page, H, D), generator=g).to(BF).cuda() for _ in range(2))
+    dev, pages, budget = [k, v, w.cuda(), p.cuda()], pages.cuda(), i32([100, 1, 0, 399, 64, 200])
+    start = [400, 300, 17, 400, 65, 399]
+
+    def step(x, ctx, out):
+        got = sv.kv_select(x[2], x[3], pages, ctx, budget, out=out)
+        sv.kv_move(x[0], x[1], pages, got[3], *got[:3], weight=x[2], position=x[3])
+        ctx += 3
+        return got
+
+    most = pages.shape[1] * page // 2
+    lists = lambda: [torch.zeros((B, H, most), dtype=torch.int32, device="cuda") for _ in range(2)] + [torch.zeros((B, H), dtype=torch.int32, device="cuda")]  # noqa: E731
+    ctx, mine = i32(start), lists()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        warm = i32(start)
+        step([x.clone() for x in dev], warm, (*lists(), warm))
+    torch.cuda.current_stream().wait_stream(side)
+    twin = [x.clone() for x in dev]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(dev, ctx, (*mine, ctx))
+    ctx.copy_(i32(start))
+    other = i32(start)
+    for _ in range(4):
+        graph.replay()
+        new = torch.zeros_like(other)
+        step(twin, other, (*lists(), new))  # lengths of their own
+        other = new + 3
+        torch.cuda.synchronize()
+        assert torch.equal(ctx, other)
+        for x, y in zip(dev, twin):
+            assert torch.equal(x, y)
