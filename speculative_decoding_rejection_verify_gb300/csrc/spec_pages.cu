@@ -534,9 +534,9 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 6) page_move_kernel(const __g
     const int last = m.end & mask ? m.end >> shift : -1;  // the page that the context ends in
     if (m.n == 0 || (P.last && last < 0)) continue;
     int begin = 0, stop = m.n;  // the moves that this launch takes
-    if (last >= 0) {            // the first move into the last page, among as many as the page has slots before the end
+    if (last >= 0) {            // the first move into the last page: any number that are left out may be behind the page's own
       int first = m.n;
-      for (int i = m.n - 1 - lane; first > m.n - (m.end & mask); i -= 32) {
+      for (int i = m.n - 1 - lane;; i -= 32) {
         const uint32_t in = __ballot_sync(~0u, i >= 0 && m.target[max(i, 0)] >> shift >= last);
         first -= in == ~0u ? 32 : __ffs(~in) - 1;
         if (in != ~0u) break;

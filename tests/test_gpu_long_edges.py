@@ -146,3 +146,38 @@ def test_a_loop_that_evicts_in_place_captured_and_replayed():
         assert torch.equal(ctx, other)
         for x, y in zip(dev, twin):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("end", [203, 201])
+@pytest.mark.parametrize("behind", [29, 33, 64, 150])
+def test_move_with_many_left_out_behind_the_last_page(end, behind):
+    """A short last page, whose rows behind the end go to other pages, and behind its own moves many that are left out for their
+    targets: every entry keeps its value, whatever the pages' scales."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(end + behind)
+    B, H, D, page, slots = 3, 2, 64, 8, 500
+    w, pos, pages = record(B, H, page, slots, g)
+    k, v, ks, vs = P.pool(w.shape[0], page, H, D, "slot", g)
+    ks, vs = (2.0 ** torch.randint(-20, 20, x.shape, generator=g).float() for x in (ks, vs))
+    last = end // 8 * 8
+    targets = sorted(torch.randperm(last, generator=g)[:90].tolist()) + list(range(last, end))
+    sources = list(range(end, end + 8)) + sorted((end + 8 + torch.randperm(slots - end - 8, generator=g)[:len(targets) + behind - 8]).tolist())
+    pairs = list(zip(sources, targets))
+    n = len(sources)
+    src, dst = (torch.tensor(x, dtype=torch.int32).expand(B, H, n).contiguous().cuda() for x in (sources, targets + list(range(end, end + behind))))
+    dev = [R.to_cuda(k), R.to_cuda(v), ks.cuda(), vs.cuda(), w.cuda(), pos.cuda()]
+    sv.kv_move(dev[0], dev[1], pages.cuda(), i32([end] * B), src, dst, torch.full((B, H), n, dtype=torch.int32, device="cuda"),
+               k_scale=dev[2], v_scale=dev[3], weight=dev[4], position=dev[5])
+    torch.cuda.synchronize()
+    at = lambda b, s: (int(pages[b, s // page]), s % page)  # noqa: E731
+    for b in range(B):
+        for h in range(H):
+            P.moved(k, ks, pages[b], pairs, h, end, page)
+            P.moved(v, vs, pages[b], pairs, h, end, page)
+            for s, t in pairs:
+                for x in (w, pos):
+                    x[at(b, t)[0], h, at(b, t)[1]] = x[at(b, s)[0], h, at(b, s)[1]]
+    for got, want in zip(dev, (k, v, ks, vs, w, pos)):
+        got = got.cpu()
+        got, want = (x.view(torch.uint8) if x.dtype == R.F8 else x for x in (got, want))
+        assert torch.equal(got, want), int((got != want).sum())
