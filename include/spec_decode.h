@@ -45,7 +45,8 @@ extern "C" {
                                        heads x row groups (of at most 128 rows) x (page table's slots /
                                        128 + 4) stay under 2^31                                      */
 #define SPEC_MAX_PAGE 4096          /* page_size: a power of two in [8, SPEC_MAX_PAGE]               */
-#define SPEC_MAX_SLOTS (1 << 30)    /* max_pages * page_size of one request                          */
+#define SPEC_MAX_SLOTS (1 << 30)    /* max_pages * page_size of one request, and the length of its lists:
+                                       max_keep, max_moves of spec_kv_move                           */
 #define SPEC_MAX_HISTORY 1048448    /* history entries of spec_process_logits                        */
 #define SPEC_MAX_BIAS 2046          /* bias entries per request of spec_process_logits               */
 

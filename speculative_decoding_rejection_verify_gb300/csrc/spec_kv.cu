@@ -510,6 +510,7 @@ spec_status_t spec_kv_keep(const spec_kv_cache_t* cache, const spec_decode_batch
   if (s == SPEC_OK) s = check_batch(batch, cache);
   if (s != SPEC_OK) return s;
   if (max_keep < 0) return SPEC_ERR_INVALID_ARG;
+  if (max_keep > SPEC_MAX_SLOTS) return SPEC_ERR_UNSUPPORTED;
   if (batch->B == 0 || max_keep == 0) return SPEC_OK;
   if (!path || !n_keep) return SPEC_ERR_INVALID_ARG;
   KeepParams P = {};

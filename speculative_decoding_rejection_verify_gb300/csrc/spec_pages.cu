@@ -631,7 +631,7 @@ spec_status_t spec_kv_keep_ex(const spec_kv_cache_t* cache, const spec_kv_page_s
   if (s == SPEC_OK) s = check_batch(batch, cache);
   if (s != SPEC_OK) return s;
   if (max_keep < 0) return SPEC_ERR_INVALID_ARG;
-  if (scales && max_keep > SPEC_MAX_NEW) return SPEC_ERR_UNSUPPORTED;
+  if (max_keep > (scales ? SPEC_MAX_NEW : SPEC_MAX_SLOTS)) return SPEC_ERR_UNSUPPORTED;
   const int64_t lists = (int64_t)cache->layers * batch->B * cache->heads;
   if ((int64_t)cache->layers * cache->heads > 0x3fffffffll || lists > 0x3fffffffll || batch->B > SPEC_MAX_BATCH) return SPEC_ERR_UNSUPPORTED;
   if (batch->B == 0 || max_keep == 0) return SPEC_OK;
@@ -668,7 +668,7 @@ spec_status_t spec_kv_move(const spec_kv_cache_t* cache, const spec_kv_page_scal
   if (s != SPEC_OK) return s;
   if (max_moves < 0) return SPEC_ERR_INVALID_ARG;
   const int64_t lists = (int64_t)cache->layers * batch->B * cache->heads;
-  if (lists > 0x3fffffffll || batch->B > SPEC_MAX_BATCH) return SPEC_ERR_UNSUPPORTED;
+  if (lists > 0x3fffffffll || batch->B > SPEC_MAX_BATCH || max_moves > SPEC_MAX_SLOTS) return SPEC_ERR_UNSUPPORTED;
   if (batch->B == 0 || max_moves == 0) return SPEC_OK;
   if (!source || !target || !moves) return SPEC_ERR_INVALID_ARG;
   MoveParams P = {};

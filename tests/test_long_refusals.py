@@ -1,13 +1,7 @@
 """More of what the long contexts' calls refuse before they touch the device (CPU only)."""
-import ctypes
-
-import pytest
-import torch
-
-import speculative_decoding_rejection_verify_gb300 as sv
-from speculative_decoding_rejection_verify_gb300 import decode
-from test_decode_refusals import INVALID, OK, UNSUPPORTED, batch, cache, lib  # noqa: F401
-from test_pages_refusals import record
+import test_decode_refusals as step
+from test_decode_refusals import INVALID, UNSUPPORTED, batch, lib  # noqa: F401
+from test_pages_refusals import keep, move, record
 
 
 def test_new_lengths_that_overlap_an_input(lib):  # noqa: F811
@@ -24,3 +18,13 @@ def test_new_lengths_that_overlap_an_input(lib):  # noqa: F811
         for off in (-16, 16, 0):
             assert select(start + off) != INVALID
     assert select(at["seen"] + 4, seen=None) != INVALID
+
+
+def test_lists_longer_than_any_context(lib):  # noqa: F811
+    """Longer than SPEC_MAX_SLOTS, where an index that goes on by a grid's stride would pass 31 bits."""
+    for n in ((1 << 30) + 1, (1 << 31) - 1):
+        assert move(lib, most=n) == UNSUPPORTED
+        assert move(lib, s=None, most=n) == UNSUPPORTED
+        assert keep(lib, m=n) == UNSUPPORTED
+        assert keep(lib, s=None, m=n) == UNSUPPORTED
+        assert step.keep(lib, m=n) == UNSUPPORTED
