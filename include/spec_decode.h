@@ -196,7 +196,8 @@ spec_status_t spec_paged_attention(const spec_heads_t* q, const spec_heads_t* ou
  *   scales   page scales of an E4M3 cache (layer 0; cache->k_scale and v_scale are NULL).  A row that attends to a slot
  *            whose page's scale does not count comes out as NaN.  A page outside the pool has scale 1;
  *   lse      [B, T, q_heads] float: log sum_s exp(scale * q . K_s) of every row, -inf for rows past T_b and rows that
- *            attend to nothing, NaN where a wait ran out and the row is NaN.  Over a bf16 cache the sum is that of the rounded weights: within 2^-8 of the logarithm.
+ *            attend to nothing, NaN where a wait ran out before it was known.  The sum is in fp32, of weights before
+ *            their rounding.
  */
 spec_status_t spec_paged_attention_ex(const spec_heads_t* q, const spec_heads_t* out, int32_t q_heads,
                                       const spec_kv_cache_t* cache, const spec_kv_page_scales_t* scales,

@@ -63,6 +63,7 @@ struct AttnParams {
   float* lse;                  // [B, T, q heads] or null
   float* part;                 // [CTA][2][rows][D] unnormalised O
   float2* part_ml;             // [CTA][2][rows] (m in log2 units, l)
+  float* part_raw;             // [CTA][2][rows] bf16 with lse: the sum of the weights before their rounding
   int4* cut;                   // [CTA] (b, head * row_groups + row group, item's end, total) on the line of an
                                //       item that begins in this CTA and ends in a later one; b = -1: none
 };
@@ -80,7 +81,7 @@ __device__ __forceinline__ int64_t lse_place(int b, int T, int t, int heads, int
 // ------------------------------------------------------------------------------------------------
 template <int D, int KIND, int NT>
 struct Shape {
-  static constexpr bool F8 = KIND != kBf16;
+  static constexpr bool F8 = holds_e4m3(KIND);
   static constexpr int kHalves = D / 64;                          // 128-byte columns of a 16-bit row
   static constexpr int kTile16 = kTileSlots * D * 2;              // a K or V tile in 16 bits
   static constexpr int kRing = kTileSlots * D * (F8 ? 1 : 2);     // a ring slot: a tile as the cache holds it
@@ -170,7 +171,7 @@ __device__ __forceinline__ float fold_lanes(float (&x)[N], int lane, Op op) {
 // ------------------------------------------------------------------------------------------------
 template <int D, int KIND, int NT>
 __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams P) {
-  constexpr bool F8 = KIND != kBf16, PAGES = KIND == kE4m3Pages;
+  constexpr bool F8 = holds_e4m3(KIND), PAGES = KIND == kE4m3Pages, LSE = KIND == kBf16Lse;
   using S = Shape<D, KIND, NT>;
   extern __shared__ char raw_smem[];
   char* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
@@ -518,6 +519,10 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
     const int rule_row = lane < S::kOwn ? row_of(lane) : kMaxRows, rule_token = rule_row / P.group;
     constexpr float kLift = F8 ? kLift16 : 0.0f;
     float l[S::kChunks][CK];
+    // The sum that lse is the logarithm of: over bf16, where l is of rounded weights, a second one, of the weights before their
+    // rounding (64 x 7 tokens, 28 rows, 1000 to 16000 slots: 342 us against 340 without; 32 x 16 to 32 x 32 tokens, 500 to 9000 slots: 64 rows 117, 114;
+    // 68 rows 124, 118; 128 rows 161, 135, where the sums spill).
+    float raw[LSE ? S::kChunks : 1][LSE ? CK : 1];
     uint32_t it = 0;
     int v_slot = 1;
     uint32_t v_phase = 0;
@@ -550,7 +555,10 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
 #pragma unroll
       for (int j = 0; j < S::kChunks; ++j)
 #pragma unroll
-        for (int i = 0; i < CK; ++i) l[j][i] = 0.0f;
+        for (int i = 0; i < CK; ++i) {
+          l[j][i] = 0.0f;
+          if constexpr (LSE) raw[j][i] = 0.0f;
+        }
 
       for (int tile = s.tile0; tile < s.tile1; ++tile, ++it) {
         const int sb = it & 1;
@@ -620,6 +628,10 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
                 over = *reinterpret_cast<const uint32_t*>(&m);
               } else {
                 const uint32_t h = pack_bf16(w.x, w.y);
+                if constexpr (LSE) {
+                  const float2 s = add2(make_float2(raw[j][i], raw[j][i + 1]), w);
+                  raw[j][i] = s.x, raw[j][i + 1] = s.y;
+                }
                 p[S::kHold ? j : 0][i / 2] = h;
                 w = make_float2(bf16_low(h), bf16_high(h));
                 const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&h), *reinterpret_cast<const __nv_bfloat162*>(&over));
@@ -662,6 +674,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
 #pragma unroll
                   for (int i = 0; i < CK; ++i) {
                     float w = sees(j, i) ? exp2_approx(x[i]) : 0.0f;
+                    if constexpr (LSE) raw[j][i] = w < 0x1p100f ? raw[j][i] - w : 0.0f;
                     if constexpr (!F8) w = __bfloat162float(__float2bfloat16(w));  // as it was added
                     l[j][i] = w < (PAGES ? 0x1p90f : 0x1p100f) ? (PAGES ? fmaf(-w, v_inverse, l[j][i]) : l[j][i] - w) : 0.0f;
                   }
@@ -703,6 +716,7 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
                     const float f = st->factor[col(j) + i];
                     x[i] *= f;
                     l[j][i] *= f;
+                    if constexpr (LSE) raw[j][i] *= f;
                   }
                   tm_store<CK>(lanes + 2 * NT + col(j), x);
                 }
@@ -781,23 +795,42 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
       const bool whole = s.tile0 == 0 && s.tile1 == s.tiles;
       // parts: slot 0 for an item that an earlier CTA began, slot 1 for one that a later one ends
       const int64_t part_row = ((int64_t)blockIdx.x * 2 + (s.tile0 == 0)) * P.rows;
-      float lse = -INFINITY, sum = 0.0f;
+      float lse = -INFINITY;
       if (wtid < S::kOwn) {
         float f = 0.0f;
         if (my_row < rows) {
-          sum = st->red[0][my_row] + st->red[1][my_row] + st->red[2][my_row] + st->red[3][my_row];
+          const float sum = st->red[0][my_row] + st->red[1][my_row] + st->red[2][my_row] + st->red[3][my_row];
           f = sum == 0.0f ? 0.0f : v_scale / sum;
-          if (whole && P.lse) lse = row_lse(st->top[my_row], kLift, sum);
+          if (!whole) P.part_ml[part_row + my_row] = make_float2(st->top[my_row], sum);
+          else if (!LSE && P.lse) lse = row_lse(st->top[my_row], kLift, sum);
         }
         st->factor[my_row] = f;
+      }
+      if constexpr (LSE) {
+        group_sync(bar);  // the sums of l are read
+#pragma unroll
+        for (int j = 0; j < S::kChunks; ++j)
+          if (col(j) < rows) {
+            const float part = fold_lanes<CK>(raw[j], lane, [](float a, float b) { return a + b; });
+            if (lane < CK) st->red[quad][col(j) + lane] = part;
+          }
+        group_sync(bar);
+        if (wtid < S::kOwn && my_row < rows) {
+          const float sum = st->red[0][my_row] + st->red[1][my_row] + st->red[2][my_row] + st->red[3][my_row];
+          if (whole) lse = row_lse(st->top[my_row], kLift, sum);
+          else P.part_raw[part_row + my_row] = sum;
+        }
       }
       mbar_wait(smem_addr(&st->o_full), (it - 1) & 1, dead);
       __syncwarp();
       tc_fence_after();
-      const bool lost = group_any(bar, *dead.dead != 0);  // one answer for the warpgroup's rows
+      group_sync(bar);
       const bool bad = st->bad_value[seg & 3] == (uint32_t)seg + 1;
-      // (a lost part's sum is NaN, which the join makes the row's output and lse; a NaN maximum it would pass over)
-      if (!whole && wtid < S::kOwn && my_row < rows) P.part_ml[part_row + my_row] = make_float2(st->top[my_row], lost ? NAN : sum);
+      const bool lost = *dead.dead != 0;
+      if (lost && !whole && wtid < S::kOwn && my_row < rows) {  // the join makes NaN of the row then (a NaN maximum it would pass over)
+        P.part_ml[part_row + my_row].y = NAN;
+        if constexpr (LSE) P.part_raw[part_row + my_row] = NAN;
+      }
       char* out = P.out.data + s.b * P.out.row + (int64_t)t0 * P.out.token + (int64_t)s.head * P.group * P.out.head + key * 2;
       float* part = P.part + part_row * D + key;
       const int rows_all = min(P.rows, (P.batch.T - t0) * P.group);
@@ -901,6 +934,7 @@ struct JoinParams {
   const float* v_scale;
   const float* part;
   const float2* part_ml;
+  const float* part_raw;  // null: lse is of part_ml's sums
   const int4* cut;
   float* lse;
   float lift;
@@ -925,7 +959,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
                                                         (int64_t)(head * P.group + n % P.group) * P.out.head);
   constexpr int E = D / 32;
   float o[E] = {};
-  float sum = 0.0f, top = -INFINITY;
+  float sum = 0.0f, raw = 0.0f, top = -INFINITY;
   if (t < batch_tokens(P.batch, b)) {
     // the last CTA of the item: the one whose part of the line holds tile end - 1
     int c1 = (int)(((int64_t)end * ctas - 1) / total);
@@ -937,15 +971,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
     const float base = top == -INFINITY ? 0.0f : top;
     for (int c = c0; c <= c1; c += 32) {
-      float f = 0.0f, part = 0.0f;
+      float f = 0.0f, part = 0.0f, raw_part = 0.0f;
       if (c + lane <= c1) {
         const float2 ml = P.part_ml[row_of(c + lane)];
         f = exp2_approx(ml.x - base);
         part = f * ml.y;
+        if (P.part_raw) raw_part = f * P.part_raw[row_of(c + lane)];
       }
 #pragma unroll
-      for (int d = 16; d > 0; d /= 2) part += __shfl_xor_sync(~0u, part, d);
-      sum += part;
+      for (int d = 16; d > 0; d /= 2) part += __shfl_xor_sync(~0u, part, d), raw_part += __shfl_xor_sync(~0u, raw_part, d);
+      sum += part, raw += raw_part;
       const int last = min(32, c1 + 1 - c);
 #pragma unroll 4
       for (int i = 0; i < last; ++i) {
@@ -964,7 +999,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
       }
     }
   }
-  if (P.lse && lane == 0) P.lse[lse_place(b, P.batch.T, t, P.heads, head, P.group, n % P.group)] = row_lse(top, P.lift, sum);
+  if (P.lse && lane == 0) P.lse[lse_place(b, P.batch.T, t, P.heads, head, P.group, n % P.group)] = row_lse(top, P.lift, P.part_raw ? raw : sum);
   const float v = P.v_scale ? __ldg(P.v_scale + head) : 1.0f;
   const float inv = sum == 0.0f ? 0.0f : v / sum;
 #pragma unroll
@@ -976,21 +1011,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
 // host side
 // ------------------------------------------------------------------------------------------------
 struct AttnLayout {
-  size_t part, ml, cut, bytes;
+  size_t part, ml, raw, cut, bytes;
 };
 static AttnLayout attn_layout(int rows, int D) {
   const auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   AttnLayout L;
   L.part = 0;
   L.ml = up(L.part + (size_t)kMaxParts * 2 * rows * D * sizeof(float));
-  L.cut = up(L.ml + (size_t)kMaxParts * 2 * rows * sizeof(float2));
+  L.raw = up(L.ml + (size_t)kMaxParts * 2 * rows * sizeof(float2));
+  L.cut = up(L.raw + (size_t)kMaxParts * 2 * rows * sizeof(float));
   L.bytes = up(L.cut + kMaxParts * sizeof(int4));
   return L;
 }
 
 template <int D, int KIND, int NT>
 static cudaError_t launch_attention(const AttnParams& P, int dev, int ctas, cudaStream_t st) {
-  constexpr bool F8 = KIND != kBf16;
+  constexpr bool F8 = holds_e4m3(KIND);
   using S = Shape<D, KIND, NT>;
   auto kern = attn_kernel<D, KIND, NT>;
   static std::atomic<uint64_t> ready{0};  // devices on which the kernel's shared memory is set
@@ -1008,7 +1044,7 @@ static cudaError_t launch_attention(const AttnParams& P, int dev, int ctas, cuda
   }
   e = launch_early(kern, dim3(ctas), dim3(S::kThreads), S::kBytes, st, P);
   if (e != cudaSuccess || ctas == 1 || P.whole) return e;
-  const JoinParams J = {P.out, P.batch, F8 ? P.cache.v_scale : nullptr, P.part, P.part_ml, P.cut, P.lse, F8 ? kLift16 : 0.0f,
+  const JoinParams J = {P.out, P.batch, F8 ? P.cache.v_scale : nullptr, P.part, P.part_ml, KIND == kBf16Lse ? P.part_raw : nullptr, P.cut, P.lse, F8 ? kLift16 : 0.0f,
                         P.heads, P.group, P.tokens, P.row_groups, P.rows, ctas};
   return launch_early(join_kernel<D>, dim3(ctas, (P.rows + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0, st, J);
 }
@@ -1021,6 +1057,14 @@ static cudaError_t launch_rows(const AttnParams& P, int dev, int ctas, cudaStrea
   // a width of its own: 128 columns' sums spill where 96 do not (68 rows, E4M3: 118 us against 139; bf16: 114, 118)
   if (P.rows <= 96) return launch_attention<D, KIND, 96>(P, dev, ctas, st);
   return launch_attention<D, KIND, 128>(P, dev, ctas, st);
+}
+
+template <int D>
+static cudaError_t launch_kind(int kind, const AttnParams& P, int dev, int ctas, cudaStream_t st) {
+  if (kind == kBf16) return launch_rows<D, kBf16>(P, dev, ctas, st);
+  if (kind == kBf16Lse) return launch_rows<D, kBf16Lse>(P, dev, ctas, st);
+  if (kind == kE4m3) return launch_rows<D, kE4m3>(P, dev, ctas, st);
+  return launch_rows<D, kE4m3Pages>(P, dev, ctas, st);
 }
 
 }  // namespace sv
@@ -1070,6 +1114,7 @@ spec_status_t spec_paged_attention_ex(const spec_heads_t* q, const spec_heads_t*
   char* ws = static_cast<char*>(workspace);
   P.part = reinterpret_cast<float*>(ws + L.part);
   P.part_ml = reinterpret_cast<float2*>(ws + L.ml);
+  P.part_raw = reinterpret_cast<float*>(ws + L.raw);
   P.cut = reinterpret_cast<int4*>(ws + L.cut);
 
   // the line's length at most: what the page table could hold
@@ -1100,11 +1145,8 @@ spec_status_t spec_paged_attention_ex(const spec_heads_t* q, const spec_heads_t*
   int ctas = sms < kMaxParts ? sms : kMaxParts;
   if (most < ctas) ctas = (int)most;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int kind = scales ? kE4m3Pages : f8 ? kE4m3 : kBf16;
-  e = D == 128 ? (kind == kBf16 ? launch_rows<128, kBf16>(P, dev, ctas, st)
-                  : kind == kE4m3 ? launch_rows<128, kE4m3>(P, dev, ctas, st) : launch_rows<128, kE4m3Pages>(P, dev, ctas, st))
-               : (kind == kBf16 ? launch_rows<64, kBf16>(P, dev, ctas, st)
-                  : kind == kE4m3 ? launch_rows<64, kE4m3>(P, dev, ctas, st) : launch_rows<64, kE4m3Pages>(P, dev, ctas, st));
+  const int kind = scales ? kE4m3Pages : f8 ? kE4m3 : lse ? kBf16Lse : kBf16;
+  e = D == 128 ? launch_kind<128>(kind, P, dev, ctas, st) : launch_kind<64>(kind, P, dev, ctas, st);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

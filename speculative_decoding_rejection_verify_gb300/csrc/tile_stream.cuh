@@ -16,8 +16,9 @@ constexpr int kTileSlots = 128;  // slots per tile = rows of the matrix unit
 constexpr int kMaxRows = 128;    // query rows of one item
 constexpr float kLog2e = 1.4426950408889634f;
 
-// What the cache holds: E4M3 with a scale per head, or per page and head.
-enum { kBf16 = 0, kE4m3 = 1, kE4m3Pages = 2 };
+// What the cache holds: E4M3 with a scale per head, or per page and head.  (kBf16Lse: the attention over bf16 that leaves lse.)
+enum { kBf16 = 0, kE4m3 = 1, kE4m3Pages = 2, kBf16Lse = 3 };
+__host__ __device__ constexpr bool holds_e4m3(int kind) { return kind == kE4m3 || kind == kE4m3Pages; }
 
 // ------------------------------------------------------------------------------------------------
 // PTX

@@ -37,8 +37,8 @@ def cache(kind, num_pages, page, H, D, g, layout="slot"):
 @pytest.mark.parametrize("ctx", [[300, 500, 100], [700, 1900, 300]])
 @pytest.mark.parametrize("Hq", [8, 40])
 def test_sums_where_a_wait_gave_up_are_nan(kind, ctx, Hq):
-    """Of items that one block takes whole (the narrow table) and of those that are cut and joined: a row and its sum come out as
-    they are, or both as NaN."""
+    """Of items that one block takes whole (the narrow table) and of those that are cut and joined: what is not as it should be
+    is NaN, sums as well as rows."""
     import speculative_decoding_rejection_verify_gb300 as sv
     g = torch.Generator().manual_seed(4)
     B, T, H, D, page = 3, 4, 2, 128, 16
@@ -59,11 +59,55 @@ def test_sums_where_a_wait_gave_up_are_nan(kind, ctx, Hq):
         out, lse = call()
     finally:
         sv.set_test_hooks(0)
-    lost = torch.isnan(out).any(-1)
-    assert lost.any() and torch.equal(torch.isnan(lse), lost)
-    assert torch.equal(out[~lost], want[~lost]) and torch.equal(lse[~lost], sums[~lost])
+    assert torch.isnan(out).any() and torch.isnan(lse).any()
+    assert (torch.isnan(out) | (out == want)).all() and (torch.isnan(lse) | (lse == sums)).all()
     again, sums2 = call()
     assert torch.equal(again, want) and torch.equal(sums2, sums)
+
+
+@pytest.mark.parametrize("Hq,D", [(2, 64), (8, 128), (40, 128), (60, 64), (84, 128)])
+@pytest.mark.parametrize("ctx", [[0, 40, 700], [1, 1900, 300]])
+@pytest.mark.parametrize("rising", [False, True])
+def test_sums_over_bf16_are_of_weights_as_they_are(Hq, D, ctx, rising):
+    """fp32's bound, without the 2^-8 of weights that are rounded to bf16; the output stays what it is without sums.  `rising`: keys
+    that grow along the context, so that the maximum in use is passed again and again, by little and by more than 2^100."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(Hq)
+    B, T, H, page = 3, 3, 2, 16
+    maxp = -(-(max(ctx) + T) // page)
+    k, v, _, kv, _ = cache("bf16", B * maxp, page, H, D, g)
+    pages = R.tables(B, maxp, B * maxp, g)
+    if rising:
+        k *= (torch.arange(B * maxp) % 7).to(BF)[:, None, None, None]
+        for b in range(B):
+            k[pages[b, -4:].long()] *= 16
+        kv = k.double()
+    q = torch.randn((B, T, Hq, D), generator=g).to(BF)
+    args = (q.cuda(), R.to_cuda(k), R.to_cuda(v), pages.cuda(), i32(ctx))
+    lse = torch.zeros((B, T, Hq), device="cuda")
+    out = sv.paged_attention(*args, lse=lse)
+    assert torch.equal(out, sv.paged_attention(*args))
+    want, bound = P.lse(q, kv, pages, ctx, [T] * B, None, D ** -0.5, False)
+    off = (lse.cpu().double() - want).abs()
+    assert (off <= bound).all(), f"over the bound by {(off - bound).max():.3g}"
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_then_weigh_adds_one_for_every_row(kind):
+    """Every row's weights sum to 1: 2^-12 for the bound of the scores, for a bf16 cache too."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(3)
+    B, T, Hq, H, D, page, ctx = 3, 7, 16, 4, 128, 32, [5000, 17, 4000]
+    maxp = -(-(max(ctx) + T) // page)
+    k, v, scales, *_ = cache(kind, B * maxp, page, H, D, g)
+    if kind == "pages":
+        scales["k_scale"].fill_(2.0 ** -7)
+    q, k, pages = torch.randn((B, T, Hq, D), generator=g).to(BF).cuda(), k.cuda(), torch.arange(B * maxp, dtype=torch.int32).view(B, maxp).cuda()
+    lse, w = torch.zeros((B, T, Hq), device="cuda"), torch.zeros((B * maxp, H, page), device="cuda")
+    sv.paged_attention(q, k, v.cuda(), pages, i32(ctx), lse=lse, **scales)
+    sv.kv_weigh(q, k, pages, i32(ctx), lse, w, k_scale=scales.get("k_scale"))
+    rows = T * Hq // H
+    assert ((w.double().view(B, maxp, H, page).sum((1, 3)) - rows).abs() <= rows * 2.0 ** -12).all()
 
 
 # ------------------------------------------------------------------------------------------------
