@@ -178,8 +178,8 @@ size_t spec_paged_attention_workspace_bytes(int32_t B, int32_t T, int32_t q_head
  * Slots that a row does not attend to have no part in it, whatever they hold (NaN and infinities
  * among them).  A page outside the pool reads as zeros; slots past the page table are dropped.
  * Scores, weights and sums are fp32; the weights are rounded where they multiply V (bf16 for a bf16 cache, whose
- * row's sum is that of the rounded ones; fp16 for E4M3).  Over an E4M3 cache a query row enters the scores as two E4M3 numbers
- * an element: exactly where the element reaches 2^-9 of the row's largest, within 2^-17 of that largest elsewhere; a row
+ * row's sum is that of the rounded ones; fp16 for E4M3).  Over an E4M3 cache a query row enters the scores as an E4M3 and an E5M2
+ * number an element: exactly where the element reaches 2^-13 of the row's largest, within 2^-21 of that largest elsewhere; a row
  * that holds an infinity gives NaN.
  * Each wait inside the kernel has a limit: should one run out, the rows that its block works on come
  * out as NaN, and the kernel ends.
@@ -234,7 +234,8 @@ spec_status_t spec_kv_keep_ex(const spec_kv_cache_t* cache, const spec_kv_page_s
  * attends to what, q, cache (v is not used), scales, batch and mask are as for spec_paged_attention_ex, and lse is what it
  * gave; a row whose lse is +inf or -inf has no part (a caller may set it, for rows of rejected drafts).
  * positions [B, T] int32 or NULL: ctx_len[b] + t.  Slots whose page lies outside the table or the pool are left out.
- * Two requests must not share a page.  Scores, weights and sums are fp32.  Each wait inside the kernel has a limit, as for
+ * Two requests must not share a page.  Scores, weights and sums are fp32, queries over an E4M3 cache those that the attention takes
+ * (within 2^-21 of a row's largest element).  Each wait inside the kernel has a limit, as for
  * spec_paged_attention: should one run out, weights that its block works on come out as NaN.
  */
 spec_status_t spec_kv_weigh(const spec_heads_t* q, int32_t q_heads, const spec_kv_cache_t* cache,

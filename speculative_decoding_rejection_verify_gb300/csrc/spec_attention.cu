@@ -394,9 +394,10 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               if constexpr (F8) {
-                // q = (its 4 upper bits) + (the others), each in E4M3: see the split below
+                // q = (its 4 upper bits, E4M3) + (the others, E5M2): see split_queries
                 const int part = k / (D / 32), in = (k % (D / 32)) * 32;
-                tc_mma<true>(cols + sb * NT, a + ahead(in), b + ahead(part * (D == 128 ? NT * 128 : 64) + in), s_idesc, k > 0);
+                tc_mma<true>(cols + sb * NT, a + ahead(in), b + ahead(part * (D == 128 ? NT * 128 : 64) + in),
+                             s_idesc | (part ? kSecondE5m2 : 0u), k > 0);
               } else {
                 const int half = k / 4, in = (k % 4) * 32;
                 tc_mma<false>(cols + sb * NT, a + ahead(half * (kTileSlots * 128) + in), b + ahead(half * (NT * 128) + in),

@@ -235,7 +235,8 @@ __global__ void __launch_bounds__(WeighShape<D, KIND != kBf16, NT>::kThreads, 1)
           for (int k = 0; k < D / 16; ++k) {
             if constexpr (F8) {
               const int part = k / (D / 32), in = (k % (D / 32)) * 32;  // of q: its 4 upper bits, then the others
-              tc_mma<true>(cols + buffer * NT, a + ahead(in), b + ahead(part * (D == 128 ? NT * 128 : 64) + in), idesc, k > 0);
+              tc_mma<true>(cols + buffer * NT, a + ahead(in), b + ahead(part * (D == 128 ? NT * 128 : 64) + in),
+                           idesc | (part ? kSecondE5m2 : 0u), k > 0);
             } else {
               const int half = k / 4, in = (k % 4) * 32;
               tc_mma<false>(cols + buffer * NT, a + ahead(half * (kTileSlots * 128) + in), b + ahead(half * (NT * 128) + in), idesc, k > 0);

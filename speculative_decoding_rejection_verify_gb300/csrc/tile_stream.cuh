@@ -110,7 +110,7 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
-// kind::f16 (fp16 or bf16 operands) or kind::f8f6f4 (E4M3)
+// kind::f16 (fp16 or bf16 operands) or kind::f8f6f4 (E4M3, and E5M2 as B)
 template <bool F8>
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   if constexpr (F8)
@@ -219,6 +219,9 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return r;
 }
 
+// In an instruction's descriptor: B is E5M2 (A and E4M3 are 0), for the remainders of split queries.
+constexpr uint32_t kSecondE5m2 = 1u << 10;
+
 // Shared-memory matrix descriptors: 128-byte swizzle (or 64-byte: E4M3 rows of 64), strides in bytes.  Along
 // a swizzled row lies the reduction (Q and K) or the free dimension (V^T and P^T, "transposed" in the
 // instruction).
@@ -228,10 +231,11 @@ __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lead, ui
          1ull << 46 | (ROW == 128 ? 2ull : 4ull) << 61;
 }
 
-// Over an E4M3 cache the queries are E4M3 too: a row is scaled by a power of two to a largest element in [128, 256), and
-// its 8-bit significands split into E4M3's 4 bits and a remainder of 4: exact but for elements under 2^-9 of the largest,
-// which are off by 2^-17 of it at most (q's own rounding to bf16 is 2^-8 of each element).  The scale goes into the row's
-// factor, beside `c`.  rows: a multiple of 16.  The split overwrites the row (a TMA-loaded [halves][NT][128 bytes]): no other row's lines.
+// Over an E4M3 cache the queries are 8-bit numbers too: a row is scaled by a power of two to a largest element in [128, 256), and
+// its 8-bit significands split into E4M3's 4 bits and a remainder of at most 8 units in the last place, which are E5M2's 3 bits.
+// That is exact where an element, scaled, is a normal E4M3 number, 2^-6 (2^-13 of the largest at least); below, what E4M3's step of
+// 2^-9 leaves is 2^-10 at most and off by 2^-14, 2^-21 of the largest.  (E4M3 has no finer steps for the remainder than for the number
+// itself: 2^-17.  One query channel that is 100 times the others is usual.)  The scale goes into the row's factor, beside `c`.  rows: a multiple of 16.  The split overwrites the row (a TMA-loaded [halves][NT][128 bytes]): no other row's lines.
 template <int D, int NT, int THREADS>
 __device__ __forceinline__ void split_queries(char* q, int tid, int rows, float c, float* mult) {
   constexpr int kLanes = D / 16;  // threads per row, 16 elements each
@@ -258,7 +262,7 @@ __device__ __forceinline__ void split_queries(char* q, int tid, int rows, float 
       for (int k = 0; k < 4; ++k) x[e + k] *= scale;
       hi[e / 4] = pack_e4m3(x[e], x[e + 1], x[e + 2], x[e + 3]);
       const float4 u = unpack_e4m3(hi[e / 4]);
-      lo[e / 4] = pack_e4m3(x[e] - u.x, x[e + 1] - u.y, x[e + 2] - u.z, x[e + 3] - u.w);
+      lo[e / 4] = pack_e5m2(x[e] - u.x, x[e + 1] - u.y, x[e + 2] - u.z, x[e + 3] - u.w);
     }
     __syncwarp();  // the row is read
     *reinterpret_cast<uint4*>(q + row * 128 + ((i ^ sw) * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);

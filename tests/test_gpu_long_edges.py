@@ -110,6 +110,48 @@ def test_attention_then_weigh_adds_one_for_every_row(kind):
     assert ((w.double().view(B, maxp, H, page).sum((1, 3)) - rows).abs() <= rows * 2.0 ** -12).all()
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "pages"])
+@pytest.mark.parametrize("Hq,D", [(2, 64), (8, 128), (40, 64), (64, 128)])
+@pytest.mark.parametrize("large", [100.0, 700.0])
+def test_weights_with_a_large_query_channel(kind, Hq, D, large):
+    """One channel that is far above the others, which is usual: over E4M3 keys an element is off by 2^-21 of its row's largest, and a
+    score by that times the sum of its key's elements; the sums of attention and the weights are held to it."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(Hq)
+    B, T, H, page, ctx = 2, 3, 2, 16, [40, 1900]
+    maxp = -(-(max(ctx) + T) // page)
+    k, v, scales, kv, _ = cache(kind, B * maxp, page, H, D, g)
+    if kind == "pages":  # so that scores of the usual size come out
+        scales["k_scale"].fill_(2.0 ** -7)
+        kv = P.values(k, scales["k_scale"].cpu())
+    q = torch.randn((B, T, Hq, D), generator=g)
+    q[..., 5] = large
+    q = q.to(BF)
+    k.view(torch.uint8)[..., 5] = 8 + torch.randint(0, 2, k.shape[:-1], generator=g).to(torch.uint8)  # 2^-6 and a step more
+    kv = P.values(k, scales["k_scale"].cpu()) if kind == "pages" else k.contiguous().view(torch.uint8).view(R.F8).double() * scales["k_scale"].cpu().double()[:, None]
+    pages, scale, tb = R.tables(B, maxp, B * maxp, g), D ** -0.5, [T] * B
+    lse = torch.zeros((B, T, Hq), device="cuda")
+    args = pages.cuda(), i32(ctx)
+    sv.paged_attention(q.cuda(), R.to_cuda(k), R.to_cuda(v), *args, lse=lse, **scales)
+    want, bound = P.lse(q, kv, pages, ctx, tb, None, scale, False)
+    extra = torch.zeros(kv.shape[:1] + (H, page), dtype=torch.float64)
+    for b, t, n, z, _ in P.scores(q, kv, pages, ctx, tb, None, scale, False):
+        kk = kv[pages[b].long()[n // page], n % page].transpose(0, 1)
+        top = q[b, t].double().abs().view(H, Hq // H, D).amax(-1)[..., None]
+        off = 2.0 ** -21 * top * kk.abs().sum(-1)[:, None] * scale
+        bound[b, t] += off.amax(-1).view(-1)
+        w = torch.exp(z - want[b, t].view(H, -1, 1))
+        extra[pages[b].long()[n // page], :, n % page] += (w * torch.expm1(off)).sum(1).T
+    off = (lse.cpu().double() - want).abs()
+    assert (off <= bound).all(), f"lse over the bound by {(off / bound).max():.3g} times"
+    given, weight = want.float(), torch.zeros(extra.shape)
+    w = weight.cuda()
+    sv.kv_weigh(q.cuda(), R.to_cuda(k), *args, given.cuda(), w, k_scale=scales["k_scale"])
+    want, _, bound = P.weigh(q, kv, pages, ctx, tb, None, scale, given, weight, torch.zeros(weight.shape, dtype=torch.int32), None, False)
+    off = (w.cpu().double() - want).abs()
+    assert (off <= bound + extra).all(), f"weights over the bound by {(off / (bound + extra)).nan_to_num().max():.3g} times"
+
+
 # ------------------------------------------------------------------------------------------------
 # selection and moves
 # ------------------------------------------------------------------------------------------------
