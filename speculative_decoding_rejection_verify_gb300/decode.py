@@ -12,7 +12,7 @@ Two ways to keep a long context small:
 
 * a float8_e4m3fn cache with a scale per page and head instead of one per head: pass ``k_scale`` and ``v_scale`` as
   ``[num_pages, heads]`` to every one of these calls; ``kv_append``, ``kv_keep`` and ``kv_move`` set them;
-* eviction: ``kv_weigh`` adds up the weight that attention gives every entry (``paged_attention`` leaves the rows' sums in ``lse``),
+* eviction: ``kv_weigh`` adds up the weight that the accepted tokens' attention gave every entry (``paged_attention`` leaves the rows' sums in ``lse``),
   ``kv_select`` picks the entries of every head that stay within a budget, ``kv_move`` brings them together.  Weights
   (float32) and positions (int32) of the entries are tensors ``[num_pages, heads, page_size]``.
 
@@ -359,7 +359,8 @@ def kv_weigh(q, k_cache, pages, ctx_len, lse, weight, position=None, t_per_row=N
     """Add up what the new tokens' attention gives every entry (spec_kv_weigh): ``weight [num_pages, heads, page_size]``
     float32 gains the weights that the rows of ``q`` (with the ``lse`` that ``paged_attention`` left, and its arguments) give the
     context's entries, and takes those that they give one another; ``position`` (int32, of weight's shape) takes the new tokens'
-    ``positions [B, T]`` (None: ``ctx_len[b] + t``).  A row whose ``lse`` is infinite has no part."""
+    ``positions [B, T]`` (None: ``ctx_len[b] + t``).  A row whose ``lse`` is infinite has no part.  Called after the verdict, with the
+    accepted tokens as ``t_per_row`` (a chain) or an infinite ``lse`` for the other rows (a tree, before ``kv_keep``), it leaves out rejected drafts."""
     torch, lib = _load()
     paged = k_scale is not None and k_scale.dim() > 1
     c, heads, D, index, scales = _cache(k_cache, k_cache, k_scale, k_scale if paged else None, False)
