@@ -17,7 +17,7 @@ The C ABI is declared in ``include/spec_verify.h``; the names here mirror it:
 * ``kv_append``, ``paged_attention``, ``kv_keep``, ``process_logits``: the operators of a decode step around
   the verify step (``decode.py``, ``include/spec_decode.h``, ``csrc/spec_kv.cu``, ``csrc/spec_attention.cu``,
   ``csrc/spec_pages.cu``, ``csrc/spec_logits.cu``), and ``kv_weigh``, ``kv_select``, ``kv_move``, which keep its cache
-  within a budget (``csrc/spec_evict.cu``, ``csrc/spec_pages.cu``);
+  within a budget (``csrc/spec_weigh.cu``, ``csrc/spec_select.cu``, ``csrc/spec_pages.cu``);
 * ``Controller(...)``: the host-side draft-length controller of ``include/spec_control.h``
   (2kiu.com/news/5895634 §4.4 and §7), fed with each batch's ``num_accepted``.
 
