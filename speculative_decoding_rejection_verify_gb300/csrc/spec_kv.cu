@@ -336,7 +336,9 @@ struct PageStepParams {
 };
 
 // The pages' blocks, then the tokens' that rotate the queries: in one launch they run beside one another (4 x 2047 tokens of 32 +
-// 2 x 8 heads, pages of 32: 30 us, 31 in two; 8 x 6 tokens: a launch less).  Four blocks of 256 threads an SM: 28.5 us instead of 30.6.
+// 2 x 8 heads, pages of 32: 30 us, 31 in two; 8 x 6 tokens: a launch less).  Four blocks of 256 threads an SM: 28 us
+// instead of 30.6 interleaved.  Half-split, with a few registers spilled: 30 us, 36 at pages of 256; 29 and 40 with three blocks, 36 and 53 with
+// two, which spill nothing.
 template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kPageThreadsMost, 4) page_append_kernel(const __grid_constant__ PageStepParams P) {
   pdl_launch_next();
