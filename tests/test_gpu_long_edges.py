@@ -120,10 +120,9 @@ def test_weights_with_a_large_query_channel(kind, Hq, D, large):
     g = torch.Generator().manual_seed(Hq)
     B, T, H, page, ctx = 2, 3, 2, 16, [40, 1900]
     maxp = -(-(max(ctx) + T) // page)
-    k, v, scales, kv, _ = cache(kind, B * maxp, page, H, D, g)
+    k, v, scales, *_ = cache(kind, B * maxp, page, H, D, g)
     if kind == "pages":  # so that scores of the usual size come out
         scales["k_scale"].fill_(2.0 ** -7)
-        kv = P.values(k, scales["k_scale"].cpu())
     q = torch.randn((B, T, Hq, D), generator=g)
     q[..., 5] = large
     q = q.to(BF)
@@ -150,6 +149,66 @@ def test_weights_with_a_large_query_channel(kind, Hq, D, large):
     want, _, bound = P.weigh(q, kv, pages, ctx, tb, None, scale, given, weight, torch.zeros(weight.shape, dtype=torch.int32), None, False)
     off = (w.cpu().double() - want).abs()
     assert (off <= bound + extra).all(), f"weights over the bound by {(off / (bound + extra)).nan_to_num().max():.3g} times"
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_and_weigh_captured_and_on_another_stream(kind):
+    """Both as one graph that is replayed on other queries, and on a stream of their own, give what the calls give."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(9)
+    B, T, Hq, H, D, page, ctx = 3, 4, 12, 2, 64, 16, [1500, 33, 700]
+    maxp = -(-(max(ctx) + T) // page)
+    k, v, scales, *_ = cache(kind, B * maxp, page, H, D, g)
+    k, v, pages, n = R.to_cuda(k), R.to_cuda(v), R.tables(B, maxp, B * maxp, g).cuda(), i32(ctx)
+    q = torch.zeros((B, T, Hq, D), dtype=BF, device="cuda")
+
+    def step(w, p, stream=None):
+        lse = torch.zeros((B, T, Hq), device="cuda")
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        out = sv.paged_attention(q, k, v, pages, n, lse=lse, stream=stream, **scales)
+        sv.kv_weigh(q, k, pages, n, lse, w, p, k_scale=scales.get("k_scale"), stream=stream)
+        return out, lse
+
+    record = lambda: (torch.zeros((B * maxp, H, page), device="cuda"), torch.zeros((B * maxp, H, page), dtype=torch.int32, device="cuda"))  # noqa: E731
+    side = torch.cuda.Stream()
+    mine, twin, third = record(), record(), record()
+    with torch.cuda.stream(side):
+        step(*record())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = step(*mine)
+    for seed in range(3):
+        q.copy_(torch.randn(q.shape, generator=g) * (1 + seed))
+        graph.replay()
+        want = step(*twin)
+        torch.cuda.synchronize()
+        other = step(*third, stream=side)
+        torch.cuda.synchronize()
+        for x, y, z in zip((out, lse, *mine), (*want, *twin), (*other, *third)):
+            assert torch.equal(x, y) and torch.equal(x, z)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq", [8, 84])
+def test_a_callers_workspace_of_just_the_size(kind, Hq):
+    """With sums, over a table that cuts items: nothing behind the workspace's bytes is written, and less is refused."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(1)
+    B, T, H, D, page, ctx = 2, 3, 2, 128, 16, [1900, 40]
+    maxp = -(-(max(ctx) + T) // page)
+    k, v, scales, *_ = cache(kind, B * maxp, page, H, D, g)
+    k, v, pages, n = R.to_cuda(k), R.to_cuda(v), R.tables(B, maxp, B * maxp, g).cuda(), i32(ctx)
+    q = torch.randn((B, T, Hq, D), generator=g).to(BF).cuda()
+    size = sv.load().spec_paged_attention_workspace_bytes(B, T, Hq, H, D)
+    raw = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    lse, mine = torch.zeros((B, T, Hq), device="cuda"), torch.zeros((B, T, Hq), device="cuda")
+    want = sv.paged_attention(q, k, v, pages, n, lse=lse, **scales)
+    got = sv.paged_attention(q, k, v, pages, n, lse=mine, workspace_tensor=raw[:size], **scales)
+    assert torch.equal(got, want) and torch.equal(mine, lse) and (raw[size:] == 0xA5).all()
+    with pytest.raises(sv.SpecVerifyError):
+        sv.paged_attention(q, k, v, pages, n, lse=mine, workspace_tensor=raw[:size - 256], **scales)
 
 
 # ------------------------------------------------------------------------------------------------
