@@ -152,6 +152,32 @@ def test_weights_with_a_large_query_channel(kind, Hq, D, large):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq", [2, 40])
+def test_a_sum_that_is_nan_shows_where_its_row_attends(kind, Hq):
+    """As after a wait that gave up: the row's weights are NaN, and slots that it does not attend to have none of it."""
+    import speculative_decoding_rejection_verify_gb300 as sv
+    g = torch.Generator().manual_seed(2)
+    B, T, H, D, page, ctx = 2, 3, 2, 64, 16, [30, 300]
+    maxp = -(-(max(ctx) + T) // page)
+    k, v, scales, *_ = cache(kind, B * maxp, page, H, D, g)
+    k, v, pages, n = R.to_cuda(k), R.to_cuda(v), R.tables(B, maxp, B * maxp, g), i32(ctx)
+    q, lse = torch.randn((B, T, Hq, D), generator=g).to(BF).cuda(), torch.zeros((B, T, Hq), device="cuda")
+    sv.paged_attention(q, k, v, pages.cuda(), n, lse=lse, **scales)
+    both = []
+    for bad in (False, True):
+        if bad:
+            lse[1, 1, 0] = math.nan  # request 1, head 0: the context, tokens 0 and 1
+        w = torch.zeros((B * maxp, H, page), device="cuda")
+        sv.kv_weigh(q, k, pages.cuda(), n, lse, w, k_scale=scales.get("k_scale"))
+        both.append(w.cpu())
+    lost = torch.zeros(both[0].shape, dtype=torch.bool)
+    for s in range(ctx[1] + 2):
+        p, r = R.at(pages, 1, s, page)
+        lost[p, 0, r] = True
+    assert torch.equal(torch.isnan(both[1]), lost) and torch.equal(both[0][~lost], both[1][~lost])
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_attention_and_weigh_captured_and_on_another_stream(kind):
     """Both as one graph that is replayed on other queries, and on a stream of their own, give what the calls give."""
     import speculative_decoding_rejection_verify_gb300 as sv
