@@ -2,8 +2,8 @@
 // their values, with the queries rotated on the way) and spec_kv_keep (the accepted branch moved up
 // behind the context).  Both are streams of 16-byte vectors, bound by memory traffic on large calls and
 // by their launch on small ones.  Measured: 4 x 2047 tokens of 32 + 2 x 8 heads of 128, half-split, bf16: 33 us,
-// 6.2 TB/s of the bytes read and written (0.92 of a copy's 6772 GB/s); 8 x 6 tokens: 2.8 us.  With page scales, interleaved, pages of
-// 32: 28.5 us, 3.3 TB/s (0.49), bound by instructions; 8 x 6 tokens: 3.3 us.  64 requests' 1 to 5
+// 6.2 TB/s of the bytes read and written (0.92 of a copy's 6772 GB/s); 8 x 6 tokens: 2.8 us.  With page scales, pages of 32:
+// 28 us interleaved, 3.3 TB/s (0.49), 30 half-split, bound by instructions; 8 x 6 tokens: 3.4 us.  64 requests' 1 to 5
 // entries in 32 layers: 5.0 us, 3.8 TB/s, bound by the chain of two dependent loads before the first entry.
 
 #include "decode_common.cuh"

@@ -4,10 +4,11 @@
 // then the page's other codes change with it; so a page's moves are one warp's work: their codes into registers, the largest
 // magnitude (only where a source's scale is above the target's: else nothing can grow it), the new scale, the codes.
 //
-// Measured: 32 requests x 8 heads of 128, 6000 of 8000 to 16000 entries kept, E4M3 with page scales: 147 us, 2.7 TB/s of the bytes
-// moved (0.40 of a copy's 6749 GB/s), bound by instructions and by the chain list -> page -> scale and codes -> store at 24 warps an
-// SM (two warps' work for keys and values: 225 us with both in one, which takes 162 registers); 317 us where two thirds of the
-// pages grow.  64 requests' 1 to 5 entries in 32 layers: 12 us.
+// Measured: 32 requests x 8 heads of 128, 6000 of 8000 to 16000 entries kept, E4M3 with page scales: 262 us on a new cache, two
+// thirds of whose pages grow, and 143 us where none does: 2.8 TB/s of the bytes moved (0.41 of a copy's 6749 GB/s), bound by
+// instructions and by the chain list -> page -> scale and codes -> store at 24 warps an SM (two warps' work for keys and values:
+// 225 us with both in one, which takes 162 registers).  A scale per head 88 us, bf16 149.  64 requests' 1 to 5 entries in 32 layers:
+// 29 us on a new cache, 12 where no page grows (17 with weights and positions); up to 31 entries 42 and 17, up to 61 132 and 150.
 
 #include "decode_common.cuh"
 

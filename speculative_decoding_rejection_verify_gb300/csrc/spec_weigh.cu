@@ -13,7 +13,7 @@
 // Measured (requests x tokens, 8 kv heads x 4 of 128, 1000 to 16000 slots; time; of the bytes' 6749 GB/s):
 //   64 x 7, E4M3 with page scales   105 us  0.84   memory; a launch's beginning and end are 10 us of it
 //   64 x 7, bf16                    179 us  0.95   memory
-//   64 x 17 (68 rows), E4M3         141 us  0.63   the sums: 68 columns of 128 slots a tile
+//   64 x 17 (68 rows), E4M3         139 us  0.64   the sums: 68 columns of 128 slots a tile (page scales: 143)
 //   8 x 6, 0 to 4001, bf16           11 us  0.45   the call's host part
 
 #include <type_traits>

@@ -1,5 +1,5 @@
 """Decoding with drafts within a budget, through verdicts: what rejected drafts looked at must not count, for a chain of drafts (as the
-README's loop has it) and for a tree."""
+documented loop has it) and for a tree."""
 import math
 import os
 import re
@@ -19,8 +19,8 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
-def test_the_readmes_loop_counts_accepted_tokens_only():
-    """The block as it stands in README.md, one step with drafts that are rejected: weights are those of the accepted rows."""
+def test_the_documented_loop_counts_accepted_tokens_only():
+    """The block as users read it, one step with drafts that are rejected: weights are those of the accepted rows."""
     import speculative_decoding_rejection_verify_gb300 as sv
     with open(os.path.join(ROOT, "README.md")) as f:
         blocks = [b for b in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "kv_weigh" in b]
