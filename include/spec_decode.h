@@ -232,8 +232,9 @@ spec_status_t spec_kv_keep_ex(const spec_kv_cache_t* cache, const spec_kv_page_s
  *                  of exp(scale * q[b, t, i] . K_s - lse[b, t, i])
  * for the context's slots and the T_b new tokens', whose positions are recorded too (record->position may be NULL).  Who
  * attends to what, q, cache (v is not used), scales, batch and mask are as for spec_paged_attention_ex, and lse is what it
- * gave; a row whose lse is +inf or -inf has no part, NaN makes NaN of what the row attends to.  So that rejected drafts do not count, a caller that has kept q and lse calls
- * after the verdict, with the accepted tokens of a chain as t_per_row, or with the lse of a tree's other rows set to +inf.
+ * gave; a row whose lse is +inf or -inf has no part, NaN makes NaN of what the row attends to.  So that rejected drafts do not
+ * count, a caller that has kept q and lse calls after the verdict, with the accepted tokens of a chain as t_per_row, or with the
+ * lse of a tree's other rows set to +inf.
  * positions [B, T] int32 or NULL: ctx_len[b] + t.  Slots whose page lies outside the table or the pool are left out.
  * Two requests must not share a page.  Scores, weights and sums are fp32, queries over an E4M3 cache those that the attention takes
  * (within 2^-21 of a row's largest element).  Each wait inside the kernel has a limit, as for

@@ -521,8 +521,8 @@ __global__ void __launch_bounds__(Shape<D, KIND, NT>::kThreads, 1) attn_kernel(c
     constexpr float kLift = F8 ? kLift16 : 0.0f;
     float l[S::kChunks][CK];
     // The sum that lse is the logarithm of: over bf16, where l is of rounded weights, a second one, of the weights before their
-    // rounding (64 x 7 tokens, 28 rows, 1000 to 16000 slots: 342 us against 340 without; 32 x 16 to 32 x 32 tokens, 500 to 9000 slots: 64 rows 117, 114;
-    // 68 rows 124, 118; 128 rows 161, 135, where the sums spill).
+    // rounding (64 x 7 tokens, 28 rows, 1000 to 16000 slots: 333 us against 332 without; 32 x 16 to 32 x 32 tokens, 500 to 9000 slots:
+    // 64 rows 115, 111; 68 rows 123, 116; 128 rows 162, 134, where the sums spill).
     float raw[LSE ? S::kChunks : 1][LSE ? CK : 1];
     uint32_t it = 0;
     int v_slot = 1;

@@ -8,7 +8,7 @@
 // thirds of whose pages grow, and 143 us where none does: 2.8 TB/s of the bytes moved (0.41 of a copy's 6749 GB/s), bound by
 // instructions and by the chain list -> page -> scale and codes -> store at 24 warps an SM (two warps' work for keys and values:
 // 225 us with both in one, which takes 162 registers).  A scale per head 88 us, bf16 149.  64 requests' 1 to 5 entries in 32 layers:
-// 29 us on a new cache, 12 where no page grows (17 with weights and positions); up to 31 entries 42 and 17, up to 61 132 and 150.
+// 29 us on a new cache, 12 where no page grows (17 with weights and positions); up to 31 entries 42 and 17, up to 61 171 and 150.
 
 #include "decode_common.cuh"
 

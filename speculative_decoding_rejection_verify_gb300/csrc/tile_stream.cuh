@@ -235,7 +235,8 @@ __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr, uint32_t lead, ui
 // its 8-bit significands split into E4M3's 4 bits and a remainder of at most 8 units in the last place, which are E5M2's 3 bits.
 // That is exact where an element, scaled, is a normal E4M3 number, 2^-6 (2^-13 of the largest at least); below, what E4M3's step of
 // 2^-9 leaves is 2^-10 at most and off by 2^-14, 2^-21 of the largest.  (E4M3 has no finer steps for the remainder than for the number
-// itself: 2^-17.  One query channel that is 100 times the others is usual.)  The scale goes into the row's factor, beside `c`.  rows: a multiple of 16.  The split overwrites the row (a TMA-loaded [halves][NT][128 bytes]): no other row's lines.
+// itself: 2^-17.  One query channel that is 100 times the others is usual.)  The scale goes into the row's factor, beside `c`.
+// rows: a multiple of 16.  The split overwrites the row (a TMA-loaded [halves][NT][128 bytes]): no other row's lines.
 template <int D, int NT, int THREADS>
 __device__ __forceinline__ void split_queries(char* q, int tid, int rows, float c, float* mult) {
   constexpr int kLanes = D / 16;  // threads per row, 16 elements each
